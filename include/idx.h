@@ -19,8 +19,10 @@
  *     library never allocates, frees or synchronises; it only enqueues
  *     kernels on `stream` (a cudaStream_t; NULL = the legacy default stream),
  *     so idx_dequant_nvfp4_pages, idx_score_pages, idx_topk16_select,
- *     idx_decode_step, idx_mtp_score_fp8, idx_prefill_index_step and
- *     idx_mxfp8_quantize can sit inside CUDA-graph capture.
+ *     idx_decode_step, idx_mtp_score_fp8, idx_prefill_index_step,
+ *     idx_mxfp8_quantize, idx_build_slots, idx_rope_append,
+ *     idx_tree_attention and idx_verify_drafts can sit inside CUDA-graph
+ *     capture.
  *   - Return value: IDX_OK (0) when the work was enqueued (or there was
  *     nothing to do), else a negative IDX_E_* code; on an error nothing is
  *     launched.  Argument checks are on the host and never touch the GPU.
@@ -59,6 +61,8 @@ extern "C" {
 #define IDX_ST_LEN_CLAMPED 2 /* a request held more pages than the table or buffer: clamped */
 #define IDX_ST_BAD_OUTPUT 4  /* an output page index outside the output buffer: skipped */
 #define IDX_ST_TIMEOUT 8     /* an internal pipeline wait gave up; that CTA's outputs are incomplete */
+#define IDX_ST_NO_BLOCKS 16  /* the free list ran out: block ids and slots of -1 */
+#define IDX_ST_BAD_TREE 32   /* a parent outside [-1, own index), or a drafted token past 64 in a tree */
 
 /* Fixed geometry. */
 #define IDX_PAGE_TOKENS 128
@@ -388,6 +392,235 @@ int idx_mxfp8_quantize(const uint16_t* x_bf16, int64_t rows, int64_t cols, int64
  *   status   optional; IDX_ST_TIMEOUT if the final wait gave up.
  */
 int idx_fp8_mma_probe(int32_t iters, float* check, double* flops, int32_t* status, void* stream);
+
+/* ======================================================================
+ * One step of decoding with drafted tokens, around the indexer:
+ *   idx_build_slots     where the step's tokens go: block tables, slots,
+ *                       positions and tree masks from the requests' lengths;
+ *   idx_rope_append     rotary positions of q and k; k and v into the cache;
+ *   (idx_decode_step    the pages that each drafted token looks at;)
+ *   idx_tree_attention  attention of the drafted tokens over the cache;
+ *   idx_verify_drafts   which drafted tokens stand, and the token after them.
+ *
+ * Tokens of all requests are packed: request r's are cu_tokens[r] ..
+ * cu_tokens[r+1]-1.  Token i of a request is stored at place seq_len - n + i
+ * of the request, n being its number of tokens of this step; its place is
+ * cache slot block_table[r][place / page_tokens] * page_tokens + place %
+ * page_tokens.  With a tree of drafts, node 0 is the last certain token and
+ * every node's parent has a lower index.  The pages of the indexer's sources
+ * end where these calls begin; their formulas stand here.
+ * ====================================================================== */
+
+/* Element types of q, k, v and the attention cache. */
+#define IDX_BF16 0
+#define IDX_F16 1
+#define IDX_F32 2
+
+/*
+ * Block tables, slot maps, positions and tree masks from request lengths.
+ * With ctx, new >= 0 (negative: 0), P = page_tokens and all sums in 64 bits:
+ *     need_r  = min(ceil((ctx_r + new_r) / P), max_blocks)
+ *     take_r  = max(0, need_r - owned_r)
+ *     first_r = *free_cursor + sum_{s < r} take_s
+ *     block_table[r][owned_r + i] = free_blocks[first_r + i], i < take_r,
+ *                                   or -1 from num_free on (IDX_ST_NO_BLOCKS)
+ *     cu_tokens[r] = min(sum_{s < r} new_s, num_tokens)   (IDX_ST_LEN_CLAMPED)
+ *     seq_lens[r]  = ctx_r + new_r
+ *     pages_out[r] = max(owned_r, need_r), less the blocks that were missing
+ *     *cursor_out  = min(*free_cursor + sum take, num_free)
+ * and for token t, the i-th of request r, at place ctx_r + i:
+ *     slots[t]     = block * P + place % P, block = block_table[r][place / P];
+ *                    -1 where the place has no page (IDX_ST_LEN_CLAMPED past
+ *                    max_blocks) or the block is outside [0, num_blocks)
+ *                    (IDX_ST_BLOCK_OOR unless it is -1)
+ *     positions[t] = ctx_r + i, or with parents ctx_r + the node's depth
+ *     tree_mask[t] = with parents: bit j set for j = i and each ancestor j of
+ *                    i; tokens from 64 on get mask 0 and position ctx_r + i
+ *                    (IDX_ST_BAD_TREE)
+ * Tokens from the last request's end to num_tokens (a padded batch) get slot
+ * -1, position 0 and mask 0.
+ *
+ *   ctx_lens, new_lens, owned_pages, seq_lens, pages_out   [num_reqs] int32
+ *   block_table   [num_reqs, bt_stride] int32, in and out: entries below
+ *                 owned_r are read, those taken are written
+ *   free_blocks   [num_free] int32: free block ids, taken in request order
+ *   free_cursor, cursor_out   int32 in device memory; different addresses (a
+ *                 program swaps the two, and owned_pages and pages_out,
+ *                 after the step)
+ *   parents       [num_tokens] int32 or NULL: index within the request of
+ *                 each token's parent, -1 for a root; one outside [-1, i)
+ *                 counts as -1 (IDX_ST_BAD_TREE)
+ *   cu_tokens     [num_reqs + 1] int32;  positions [num_tokens] int32
+ *   slots         [num_tokens] int64;  tree_mask [num_tokens] uint64 (with
+ *                 parents, else NULL)
+ */
+int idx_build_slots(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* owned_pages, int32_t num_reqs,
+                    int32_t* block_table, int64_t bt_stride, int32_t max_blocks, const int32_t* free_blocks,
+                    int32_t num_free, const int32_t* free_cursor, int64_t num_blocks, int32_t page_tokens,
+                    const int32_t* parents, int32_t num_tokens, int32_t* cu_tokens, int32_t* seq_lens,
+                    int32_t* pages_out, int32_t* cursor_out, int32_t* positions, int64_t* slots,
+                    uint64_t* tree_mask, int32_t* status, void* stream);
+
+/*
+ * Rotary frequencies, on the host (needs no GPU): inv_freq[i] for i in
+ * [0, rotary_dim / 2) and the magnitude to pass as mscale.
+ *     f_i = base^(-2i / rotary_dim)
+ *   IDX_ROPE_PLAIN   inv_freq = f_i, mscale 1
+ *   IDX_ROPE_LINEAR  inv_freq = f_i / factor, mscale 1 (positions interpolated)
+ *   IDX_ROPE_RAMP    frequencies turning more than beta_fast times within
+ *                    orig_len positions are kept, those turning less than
+ *                    beta_slow times are divided by factor, a linear ramp over
+ *                    the index between:  e(b) = rotary_dim ln(orig_len / (2 pi
+ *                    b)) / (2 ln base), lo = max(0, floor e(beta_fast)), hi =
+ *                    min(rotary_dim - 1, ceil e(beta_slow)), w_i = clamp((i -
+ *                    lo) / max(hi - lo, 1e-3), 0, 1), inv_freq = f_i (1 - w_i)
+ *                    + w_i f_i / factor; mscale 0.1 ln(factor) + 1 for factor
+ *                    > 1, else 1
+ */
+#define IDX_ROPE_PLAIN 0
+#define IDX_ROPE_LINEAR 1
+#define IDX_ROPE_RAMP 2
+int idx_rope_frequencies(int32_t rotary_dim, double base, int32_t kind, double factor, double orig_len,
+                         double beta_fast, double beta_slow, double* inv_freq, double* mscale);
+
+/*
+ * Rotary positions, and the paged cache's append.  For each token t, head,
+ * and pair i < rotary_dim / 2, with a = positions[t] * inv_freq[i]:
+ *     y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x2 cos a + x1 sin a)
+ * computed in 32 bits and rounded once; (x1, x2) are elements i and i +
+ * rotary_dim / 2 of the head, or 2i and 2i + 1 with IDX_ROPE_INTERLEAVED.
+ * Elements from rotary_dim on pass unchanged.  The angle is reduced exactly
+ * (as a 64-bit fraction of a turn), so positions up to 2^31 - 1 keep full
+ * precision.  Rotated queries go to q_out; rotated keys and unchanged values
+ * go to cache slot slots[t] (NULL: slot t); a negative slot is skipped, one
+ * past the cache is skipped with IDX_ST_BLOCK_OOR.  Two tokens of one call
+ * must not share a slot.
+ *
+ *   q, q_out      [num_tokens, q_heads, head_dim] with the given strides in
+ *                 elements; the head's elements contiguous; q_out may be q
+ *                 (with its strides).
+ *                 NULL (both) with q_heads 0.
+ *   k, v          [num_tokens, kv_heads, head_dim], NULL (both, and the
+ *                 caches) with kv_heads 0; v and v_cache alone may be NULL.
+ *   k_cache, v_cache   [num_blocks, page_tokens, kv_heads, head_dim] with the
+ *                 given strides in elements, the same for both
+ *   head_dim      1..512;  rotary_dim  even, 0..head_dim
+ *   inv_freq      [rotary_dim / 2] float64 in device memory, radians a
+ *                 position
+ *   dtype         IDX_BF16, IDX_F16 or IDX_F32, of all tensors
+ *   flags         0 or IDX_ROPE_INTERLEAVED
+ */
+#define IDX_ROPE_INTERLEAVED 1
+int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                    int64_t qo_token_stride, int64_t qo_head_stride, int32_t q_heads, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                    int64_t v_head_stride, int32_t kv_heads, int32_t num_tokens, int32_t head_dim, int32_t rotary_dim,
+                    const int32_t* positions, const double* inv_freq, float mscale, const int64_t* slots,
+                    void* k_cache, void* v_cache, int64_t num_blocks, int32_t page_tokens, int64_t c_block_stride,
+                    int64_t c_token_stride, int64_t c_head_stride, int32_t dtype, int32_t flags, int32_t* status,
+                    void* stream);
+
+/*
+ * Attention of a step's tokens over the paged cache.  Token t, the i-th of
+ * request r's n, sees the places p < ctx = seq_len - n, and of the places ctx
+ * + j those of the drafted tokens j in its mask (bit j of tree_mask[t], j <
+ * min(n, 64); with tree_mask NULL a chain: j <= i).  With pages, places
+ * outside the token's listed pages are not seen.  For query head h and KV
+ * head h / (q_heads / kv_heads), over the places seen,
+ *     s_p = scale (q . k_p),  out = sum_p e^(s_p - L) v_p,  L = ln sum_p e^s_p
+ * A token that sees nothing gets out 0 and L -inf (as does one whose scores
+ * are all -inf).  Scores, maxima, sums and outputs are held in fp32; e^(s_p -
+ * max) is rounded to the cache's type for the product with v.  What is stored
+ * at places that no token sees (unwritten slots of the last page, NaN and
+ * infinities among them) has no effect, and what a drafted token has stored
+ * reaches only the tokens that see it.
+ *
+ *   q, out        [num_tokens, q_heads, head_dim] with the given strides in
+ *                 elements (multiples of 8), 16-byte aligned
+ *   k_cache, v_cache   [num_blocks, page_tokens, kv_heads, head_dim] with the
+ *                 given strides in elements (multiples of 8, the same for
+ *                 both), 16-byte aligned
+ *   page_tokens   16, 32, 64, or a multiple of 128
+ *   head_dim      64 or 128;  q_heads a multiple of kv_heads, at most 128
+ *                 query heads a KV head
+ *   dtype         IDX_BF16 or IDX_F16 (q, caches, out)
+ *   block_table   [num_reqs, bt_stride] int32, entries [0, max_blocks) used;
+ *                 places past max_blocks pages are not seen
+ *                 (IDX_ST_LEN_CLAMPED), nor those of a block id outside
+ *                 [0, num_blocks) (IDX_ST_BLOCK_OOR)
+ *   seq_lens      [num_reqs] int32 tokens per request, this step's included
+ *   cu_tokens     [num_reqs + 1] int32, non-decreasing, from 0 to num_tokens
+ *   tree_mask     [num_tokens] uint64 or NULL
+ *   pages         [num_tokens, page_lists, pages_per_list] int32 or NULL: the
+ *                 logical pages of each token and list, as idx_decode_step
+ *                 gives them ([num_reqs, query_len, 4, 16]); KV head h uses
+ *                 list h / (kv_heads / page_lists); entries that are negative
+ *                 or past the request's pages are skipped; an entry's
+ *                 repetition within a list changes nothing.  kv_heads a
+ *                 multiple of page_lists, pages_per_list 1..64.
+ *   lse           [num_tokens, q_heads] float32 or NULL: L
+ *   workspace     >= idx_tree_attention_workspace_bytes(...) bytes, 256-byte
+ *                 aligned, no initialisation needed
+ */
+size_t idx_tree_attention_workspace_bytes(int32_t num_reqs, int32_t num_tokens, int32_t q_heads, int32_t kv_heads,
+                                          int32_t head_dim, int32_t page_lists, int32_t pages_per_list);
+int idx_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                       const void* v_cache, int64_t num_blocks, int32_t page_tokens, int64_t c_block_stride,
+                       int64_t c_token_stride, int64_t c_head_stride, const int32_t* block_table, int64_t bt_stride,
+                       int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_tokens, int32_t num_reqs,
+                       int32_t num_tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                       const uint64_t* tree_mask, const int32_t* pages, int32_t page_lists, int32_t pages_per_list,
+                       float scale, int32_t dtype, void* out, int64_t o_token_stride, int64_t o_head_stride,
+                       float* lse, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Verification of drafted tokens.  Row p = target[t] is the target's
+ * distribution of the token after node t, row q = draft[t] the one from which
+ * the children of node t were drawn.  From node 0 (the last certain token),
+ * with c = 0 and W = 1, the children x_1, x_2, ... of the node (those whose
+ * parent it is, by index) are tried in turn:
+ *     child x with random number u = accept_u[x's node] stands when
+ *         u W q(x) < max(p(x) - c q(x), 0);
+ *     the walk then goes on at that child with c = 0, W = 1;
+ *     otherwise  c <- c + W,  W <- sum_v max(p(v) - c q(v), 0).
+ * Where no child stands, the next token is drawn from the residual: the
+ * lowest v with  sum_{v' <= v} max(p(v') - c q(v'), 0) > sample_u[r] * W.
+ * (The residual after k refused children, normalised after each, is max(p -
+ * c_k q, 0) / W_k: normalising only moves c.)  With draft NULL the drafts
+ * are not random: child x stands when u W < p(x), p(x) taken as 0 if a
+ * refused sibling was the same token; otherwise W <- W - p(x), and the
+ * residual is p without the refused tokens.  A residual without mass falls
+ * back to p; p without mass gives token vocab - 1.
+ * Products are formed in 64-bit floating point; masses and cumulative sums
+ * are exact sums of terms cut to multiples of 2^-60, so they do not depend on
+ * the order of adding.  Entries are probabilities: a negative or
+ * NaN entry counts as 0, and a row's sum must stay below 8.
+ *
+ *   target, draft [num_tokens, vocab] float32, row strides in elements;
+ *                 draft may be NULL
+ *   tokens        [num_tokens] int32 drafted tokens (node 0's entry is not
+ *                 read); one outside [0, vocab) is not tried
+ *   parents       [num_tokens] int32 index within the request, or NULL for a
+ *                 chain; a node whose parent is outside [0, own index) is
+ *                 not tried
+ *   cu_tokens     [num_reqs + 1] int32, from 0 to num_tokens; at most
+ *                 IDX_VERIFY_MAX_NODES tokens a request (IDX_ST_BAD_TREE: the
+ *                 rest are not tried)
+ *   accept_u      [num_tokens] float32;  sample_u [num_reqs] float32, in [0, 1)
+ *   out_tokens    [num_reqs, max_out] int32: the tokens that stand, the drawn
+ *                 one, then -1
+ *   out_nodes     [num_reqs, max_out] int32: indices of the drafted tokens
+ *                 that stand, then -1
+ *   num_accepted  [num_reqs] int32: how many stand, at most max_out - 1 (a
+ *                 walk that got there draws from p)
+ * A request without tokens gets num_accepted 0 and rows of -1.
+ */
+#define IDX_VERIFY_MAX_NODES 1024
+int idx_verify_drafts(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                      int32_t vocab, const int32_t* tokens, const int32_t* parents, const int32_t* cu_tokens,
+                      int32_t num_reqs, int32_t num_tokens, const float* accept_u, const float* sample_u,
+                      int32_t* out_tokens, int32_t* out_nodes, int32_t max_out, int32_t* num_accepted,
+                      int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }
