@@ -316,56 +316,67 @@ def idx_fp8_mma_probe(iters: int, check=None, status=None, stream=None) -> float
 ROPE_PLAIN, ROPE_LINEAR, ROPE_RAMP = 0, 1, 2  # idx_rope_frequencies kinds
 VERIFY_MAX_NODES = 1024  # tokens a request of idx_verify_drafts
 _ROPE_INTERLEAVED = 1
-_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
-_code_of: dict = {}  # dtype object -> code
+_T = None  # torch's types and the raw stream getter, bound at the first call
 
 
-def _dtype_code(name: str, *tensors) -> int:
-    """The element type's code; all given tensors (None left out) must share it."""
-    first = None
+class _Torch:
+    def __init__(self):
+        import torch
+
+        self.i32, self.i64, self.f32, self.f64 = torch.int32, torch.int64, torch.float32, torch.float64
+        self.words = (torch.int64, torch.uint64)
+        self.codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        # the current stream's handle without a Stream object (3 us less a call)
+        self.raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _torch() -> _Torch:
+    global _T
+    if _T is None:
+        _T = _Torch()
+    return _T
+
+
+def _stream_on(stream, t) -> int | None:
+    """The given stream, or the current one of t's device."""
+    if stream is None:
+        return _T.raw(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _are(dtype, shape, *tensors) -> bool:
+    """Whether every given tensor (None left out) has the type and the sizes and is contiguous."""
     for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+            return False
+    return True
+
+
+# The checks below run as one expression a call; only where it fails does
+# _explain go through the tensors again to name the one that is wrong.
+def _explain(name: str, dense=(), **tensors) -> None:
+    """Raise for the first tensor that is not what is needed: each is (tensor, types, sizes with None for any); those
+    named in `dense` must be contiguous, the others in their last dimension."""
+    for arg, (t, dtypes, shape) in tensors.items():
         if t is None:
             continue
-        if first is None:
-            first = t.dtype
-        elif t.dtype != first:
-            raise ValueError(f"{name}: tensors of one element type are needed, got {first} and {t.dtype}")
-    code = _code_of.get(first)
-    if code is None:
-        code = _DTYPES.get(str(first))
-        if code is None:
-            raise ValueError(f"{name}: bfloat16, float16 or float32 is needed, got {first}")
-        _code_of[first] = code
-    return code
-
-
-def _want(name: str, **tensors) -> None:
-    """Each given tensor contiguous along its rows: (tensor, dtype name, dimensions, first sizes or None)."""
-    for arg, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if _names.setdefault(t.dtype, str(t.dtype)) not in dtype:
-            raise ValueError(f"{name}: {arg} has type {t.dtype}, {' or '.join(dtype)} is needed")
-        have = t.shape
-        if len(have) != len(shape) or any(w is not None and w != h for w, h in zip(shape, have)):
-            raise ValueError(f"{name}: {arg} has shape {tuple(have)}, {tuple('any' if w is None else w for w in shape)} is needed")
-
-
-_names: dict = {}  # dtype object -> its name
-_I32, _I64, _F32 = ("torch.int32",), ("torch.int64", "torch.uint64"), ("torch.float32",)
-_F64 = ("torch.float64",)
-
-
-def _packed(name: str, **tensors) -> None:
-    for arg, t in tensors.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name}: {arg} must be contiguous")
-
-
-def _inner(name: str, **tensors) -> None:
-    for arg, t in tensors.items():
-        if t is not None and t.stride(-1) != 1 and t.shape[-1] > 1:
+        dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: {arg} has type {t.dtype}, {' or '.join(map(str, dtypes))} is needed")
+        if t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):
+            need = tuple("any" if w is None else w for w in shape)
+            raise ValueError(f"{name}: {arg} has shape {tuple(t.shape)}, {need} is needed")
+        if arg in dense:
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: {arg} must be contiguous")
+        elif t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"{name}: the last dimension of {arg} must be contiguous")
+    raise ValueError(f"{name}: a tensor has the wrong type, shape or strides")
+
+
+def _rows_ok(t, dtype, shape) -> bool:
+    """Type and sizes, and the last dimension contiguous (the others may have any strides)."""
+    return t is None or (t.dtype is dtype and t.shape == shape and (t.stride(-1) == 1 or shape[-1] <= 1))
 
 
 def idx_build_slots(ctx_lens, new_lens, owned_pages, block_table, free_blocks, free_cursor, num_blocks: int,
@@ -373,22 +384,27 @@ def idx_build_slots(ctx_lens, new_lens, owned_pages, block_table, free_blocks, f
                     tree_mask=None, status=None, stream=None) -> int:
     """Block tables (block_table [R, maxb] i32, in place), slots [T] i64 and positions [T] i32 of a step's tokens
     from ctx_lens / new_lens / owned_pages [R] i32 and the free list; with parents [T] i32 also tree_mask [T] i64."""
-    lib = load_library()
-    fn = "idx_build_slots"
-    reqs, tokens = ctx_lens.shape[0], positions.shape[0]
-    _want(fn, ctx_lens=(ctx_lens, _I32, (reqs,)), new_lens=(new_lens, _I32, (reqs,)), owned_pages=(owned_pages, _I32, (reqs,)),
-          block_table=(block_table, _I32, (reqs, None)), free_blocks=(free_blocks, _I32, (None,)),
-          free_cursor=(free_cursor, _I32, (1,)), cu_tokens=(cu_tokens, _I32, (reqs + 1,)), seq_lens=(seq_lens, _I32, (reqs,)),
-          pages_out=(pages_out, _I32, (reqs,)), cursor_out=(cursor_out, _I32, (1,)), positions=(positions, _I32, (tokens,)),
-          slots=(slots, _I64, (tokens,)), parents=(parents, _I32, (tokens,)), tree_mask=(tree_mask, _I64, (tokens,)))
-    _packed(fn, ctx_lens=ctx_lens, new_lens=new_lens, owned_pages=owned_pages, free_blocks=free_blocks, cu_tokens=cu_tokens,
-            seq_lens=seq_lens, pages_out=pages_out, positions=positions, slots=slots, parents=parents, tree_mask=tree_mask)
-    _inner(fn, block_table=block_table)
+    lib, T, fn = load_library(), _torch(), "idx_build_slots"
+    i32 = T.i32
+    per_req, per_token = ctx_lens.shape, positions.shape
+    reqs, width, tokens, free = per_req[0], block_table.shape[-1], per_token[0], free_blocks.shape[0]
+    if not (_are(i32, (reqs,), ctx_lens, new_lens, owned_pages, seq_lens, pages_out) and _are(i32, (reqs + 1,), cu_tokens)
+            and _are(i32, (1,), free_cursor, cursor_out) and _are(i32, (free,), free_blocks)
+            and _are(i32, (tokens,), positions, parents) and slots.shape == per_token and slots.dtype in T.words
+            and slots.is_contiguous() and _rows_ok(block_table, i32, (reqs, width))
+            and (tree_mask is None or (tree_mask.shape == per_token and tree_mask.dtype in T.words and tree_mask.is_contiguous()))):
+        r, t, one = (reqs,), (tokens,), (1,)
+        _explain(fn, ("ctx_lens", "new_lens", "owned_pages", "free_blocks", "cu_tokens", "seq_lens", "pages_out", "positions", "slots",
+                      "parents", "tree_mask"), ctx_lens=(ctx_lens, i32, r), new_lens=(new_lens, i32, r),
+                 owned_pages=(owned_pages, i32, r), block_table=(block_table, i32, (reqs, None)), free_blocks=(free_blocks, i32, (None,)),
+                 free_cursor=(free_cursor, i32, one), cu_tokens=(cu_tokens, i32, (reqs + 1,)), seq_lens=(seq_lens, i32, r),
+                 pages_out=(pages_out, i32, r), cursor_out=(cursor_out, i32, one), positions=(positions, i32, t),
+                 slots=(slots, T.words, t), parents=(parents, i32, t), tree_mask=(tree_mask, T.words, t))
     return _check(fn, lib.idx_build_slots(
-        _ptr(ctx_lens), _ptr(new_lens), _ptr(owned_pages), reqs, _ptr(block_table), _row_stride(block_table),
-        block_table.shape[1], _ptr(free_blocks), free_blocks.shape[0], _ptr(free_cursor), int(num_blocks),
-        int(page_tokens), _ptr(parents), tokens, _ptr(cu_tokens), _ptr(seq_lens), _ptr(pages_out), _ptr(cursor_out),
-        _ptr(positions), _ptr(slots), _ptr(tree_mask), _ptr(status), _stream(stream)))
+        ctx_lens.data_ptr(), new_lens.data_ptr(), owned_pages.data_ptr(), reqs, block_table.data_ptr(), _row_stride(block_table),
+        width, free_blocks.data_ptr(), free, free_cursor.data_ptr(), num_blocks, page_tokens, _ptr(parents), tokens,
+        cu_tokens.data_ptr(), seq_lens.data_ptr(), pages_out.data_ptr(), cursor_out.data_ptr(), positions.data_ptr(),
+        slots.data_ptr(), _ptr(tree_mask), _ptr(status), _stream_on(stream, positions)))
 
 
 def idx_rope_frequencies(rotary_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -408,37 +424,38 @@ def idx_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slots
                     interleaved: bool = False, status=None, stream=None) -> int:
     """Rotate q [T,Hq,D] into q_out and k [T,Hk,D] into the cache [nb,P,Hk,D], v beside it, at slots [T] i64 (None:
     slot t).  q and q_out, or k, v and the caches, or v and v_cache may be None."""
-    lib = load_library()
-    fn = "idx_rope_append"
-    code = _dtype_code(fn, q, q_out, k, v, k_cache, v_cache)
-    for pair, x, y in (("q and q_out", q, q_out), ("k and k_cache", k, k_cache), ("v and v_cache", v, v_cache)):
-        if (x is None) != (y is None):
-            raise ValueError(f"{fn}: {pair} go together")
+    lib, T, fn = load_library(), _torch(), "idx_rope_append"
     some = q if q is not None else k
     if some is None or (v is not None and k is None):
         raise ValueError(f"{fn}: q, or k (with or without v), is needed")
+    if (q is None) != (q_out is None) or (k is None) != (k_cache is None) or (v is None) != (v_cache is None):
+        raise ValueError(f"{fn}: q and q_out, k and k_cache, v and v_cache go together")
+    kind = some.dtype
+    code = T.codes.get(kind)
+    if code is None:
+        raise ValueError(f"{fn}: bfloat16, float16 or float32 is needed, got {kind}")
     tokens, dim = some.shape[0], some.shape[-1]
     hq = 0 if q is None else q.shape[1]
-    hk = 0 if k is None else k.shape[1]
-    kind = (str(some.dtype),)
-    _want(fn, q=(q, kind, (tokens, hq, dim)), q_out=(q_out, kind, (tokens, hq, dim)), k=(k, kind, (tokens, hk, dim)),
-          v=(v, kind, (tokens, hk, dim)), k_cache=(k_cache, kind, (None, None, hk, dim)),
-          v_cache=(v_cache, kind, (None, None, hk, dim)), positions=(positions, _I32, (tokens,)),
-          inv_freq=(inv_freq, _F64, (None,)), slots=(slots, _I64, (tokens,)))
-    _inner(fn, q=q, q_out=q_out, k=k, v=v, k_cache=k_cache, v_cache=v_cache)
-    _packed(fn, positions=positions, inv_freq=inv_freq, slots=slots)
-    if v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride()):
-        raise ValueError(f"{fn}: k_cache and v_cache must have the same shape and strides")
-    qs = (0, 0, 0) if q is None else q.stride()
-    os_ = (0, 0, 0) if q is None else q_out.stride()
-    ks = (0, 0, 0) if k is None else k.stride()
-    vs = (0, 0, 0) if v is None else v.stride()
+    nb, page, hk = (0, 1, 0) if k is None else (k_cache.shape[0], k_cache.shape[1], k.shape[1])
+    qshape, kshape, cshape = (tokens, hq, dim), (tokens, hk, dim), (nb, page, hk, dim)
+    if not (_rows_ok(q, kind, qshape) and _rows_ok(q_out, kind, qshape) and _rows_ok(k, kind, kshape) and _rows_ok(v, kind, kshape)
+            and _rows_ok(k_cache, kind, cshape) and _rows_ok(v_cache, kind, cshape) and _are(T.i32, (tokens,), positions)
+            and _are(T.f64, inv_freq.shape[:1], inv_freq)
+            and (slots is None or (slots.dtype in T.words and slots.shape == positions.shape and slots.is_contiguous()))):
+        _explain(fn, ("positions", "inv_freq", "slots"), q=(q, kind, qshape), q_out=(q_out, kind, qshape), k=(k, kind, kshape),
+                 v=(v, kind, kshape), k_cache=(k_cache, kind, (None, None, hk, dim)), v_cache=(v_cache, kind, cshape),
+                 positions=(positions, T.i32, (tokens,)), inv_freq=(inv_freq, T.f64, (None,)), slots=(slots, T.words, (tokens,)))
     cs = (0, 0, 0, 0) if k is None else k_cache.stride()
-    nb, page = (0, 1) if k is None else k_cache.shape[:2]
+    if v_cache is not None and v_cache.stride() != cs:
+        raise ValueError(f"{fn}: k_cache and v_cache must have the same strides")
+    none = (0, 0, 0)
+    qs, os_ = (none, none) if q is None else (q.stride(), q_out.stride())
+    ks = none if k is None else k.stride()
+    vs = none if v is None else v.stride()
     return _check(fn, lib.idx_rope_append(
         _ptr(q), qs[0], qs[1], _ptr(q_out), os_[0], os_[1], hq, _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], hk, tokens, dim,
-        2 * inv_freq.shape[0], _ptr(positions), _ptr(inv_freq), float(mscale), _ptr(slots), _ptr(k_cache), _ptr(v_cache), nb,
-        page, cs[0], cs[1], cs[2], code, _ROPE_INTERLEAVED if interleaved else 0, _ptr(status), _stream(stream)))
+        2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr(), mscale, _ptr(slots), _ptr(k_cache), _ptr(v_cache), nb,
+        page, cs[0], cs[1], cs[2], code, _ROPE_INTERLEAVED if interleaved else 0, _ptr(status), _stream_on(stream, some)))
 
 
 def idx_tree_attention_workspace_bytes(num_reqs: int, num_tokens: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -451,53 +468,55 @@ def idx_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, ou
                        lse=None, workspace=None, status=None, stream=None) -> int:
     """q [T,Hq,D] over the cache [nb,P,Hk,D] of each token's request -> out [T,Hq,D] (+ lse [T,Hq] f32); tree_mask [T] i64
     (None: a chain); pages [T,lists,per] i32 (or idx_decode_step's [R,query_len,lists,per]): only those pages."""
-    lib = load_library()
-    fn = "idx_tree_attention"
-    code = _dtype_code(fn, q, k_cache, v_cache, out)
-    tokens, hq, dim = q.shape
-    nb, page, hk = k_cache.shape[:3]
-    reqs = seq_lens.shape[0]
-    kind = (str(q.dtype),)
+    lib, T, fn = load_library(), _torch(), "idx_tree_attention"
+    kind, shape, cshape = q.dtype, q.shape, k_cache.shape
+    code = T.codes.get(kind, 2)
+    if code == 2:
+        raise ValueError(f"{fn}: bfloat16 or float16 is needed, got {kind}")
+    tokens, hq, dim = shape
+    nb, page, hk, _ = cshape
+    reqs, width = block_table.shape
     lists = per = 0
     if pages is not None:
         lists, per = pages.shape[-2:]
-        _want(fn, pages=(pages, _I32, (tokens, lists, per) if pages.dim() == 3 else (None, None, lists, per)))
-        if pages.numel() != tokens * lists * per:
-            raise ValueError(f"{fn}: pages has {pages.numel()} entries, {tokens * lists * per} are needed")
-    _want(fn, out=(out, kind, (tokens, hq, dim)), k_cache=(k_cache, kind, (nb, page, hk, dim)),
-          v_cache=(v_cache, kind, (nb, page, hk, dim)), block_table=(block_table, _I32, (reqs, None)),
-          seq_lens=(seq_lens, _I32, (reqs,)), cu_tokens=(cu_tokens, _I32, (reqs + 1,)), tree_mask=(tree_mask, _I64, (tokens,)),
-          lse=(lse, _F32, (tokens, hq)))
-    _inner(fn, q=q, k_cache=k_cache, v_cache=v_cache, out=out, block_table=block_table)
-    _packed(fn, seq_lens=seq_lens, cu_tokens=cu_tokens, tree_mask=tree_mask, lse=lse, pages=pages)
+    if not (_rows_ok(q, kind, shape) and _rows_ok(out, kind, shape) and cshape[3] == dim and _rows_ok(k_cache, kind, cshape)
+            and _rows_ok(v_cache, kind, cshape) and _rows_ok(block_table, T.i32, (reqs, width)) and _are(T.i32, (reqs,), seq_lens)
+            and _are(T.i32, (reqs + 1,), cu_tokens) and _are(T.f32, (tokens, hq), lse)
+            and (tree_mask is None or (tree_mask.dtype in T.words and tree_mask.shape == (tokens,) and tree_mask.is_contiguous()))
+            and (pages is None or (pages.dtype is T.i32 and pages.is_contiguous() and pages.numel() == tokens * lists * per))):
+        _explain(fn, ("seq_lens", "cu_tokens", "tree_mask", "lse", "pages"), q=(q, kind, shape), out=(out, kind, shape),
+                 k_cache=(k_cache, kind, (nb, page, hk, dim)), v_cache=(v_cache, kind, (nb, page, hk, dim)),
+                 block_table=(block_table, T.i32, (reqs, None)), seq_lens=(seq_lens, T.i32, (reqs,)),
+                 cu_tokens=(cu_tokens, T.i32, (reqs + 1,)), tree_mask=(tree_mask, T.words, (tokens,)), lse=(lse, T.f32, (tokens, hq)),
+                 pages=(pages, T.i32, (tokens, lists, per)))
     cs = k_cache.stride()
     if v_cache.stride() != cs:
         raise ValueError(f"{fn}: k_cache and v_cache must have the same strides")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     qs, os_ = q.stride(), out.stride()
     return _check(fn, lib.idx_tree_attention(
-        _ptr(q), qs[0], qs[1], _ptr(k_cache), _ptr(v_cache), nb, page, cs[0], cs[1], cs[2], _ptr(block_table),
-        _row_stride(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(cu_tokens), reqs, tokens, hq, hk, dim,
-        _ptr(tree_mask), _ptr(pages), lists, per, float(scale), code, _ptr(out), os_[0], os_[1], _ptr(lse), _ptr(workspace),
-        ws_bytes, _ptr(status), _stream(stream)))
+        q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), nb, page, cs[0], cs[1], cs[2], block_table.data_ptr(),
+        _row_stride(block_table), width, seq_lens.data_ptr(), cu_tokens.data_ptr(), reqs, tokens, hq, hk, dim, _ptr(tree_mask),
+        _ptr(pages), lists, per, scale, code, out.data_ptr(), os_[0], os_[1], _ptr(lse), _ptr(workspace), ws_bytes, _ptr(status),
+        _stream_on(stream, q)))
 
 
 def idx_verify_drafts(target, draft, tokens, cu_tokens, accept_u, sample_u, out_tokens, out_nodes, num_accepted,
                       parents=None, status=None, stream=None) -> int:
     """Which of the drafted tokens [T] i32 stand: target [T,V] f32, draft [T,V] f32 (None: drafts without randomness),
     accept_u [T], sample_u [R] f32 -> out_tokens, out_nodes [R,max_out] i32, num_accepted [R] i32."""
-    lib = load_library()
-    fn = "idx_verify_drafts"
-    total, vocab = target.shape
-    reqs, max_out = out_tokens.shape
-    _want(fn, target=(target, _F32, (total, vocab)), draft=(draft, _F32, (total, vocab)), tokens=(tokens, _I32, (total,)),
-          parents=(parents, _I32, (total,)), cu_tokens=(cu_tokens, _I32, (reqs + 1,)), accept_u=(accept_u, _F32, (total,)),
-          sample_u=(sample_u, _F32, (reqs,)), out_tokens=(out_tokens, _I32, (reqs, max_out)),
-          out_nodes=(out_nodes, _I32, (reqs, max_out)), num_accepted=(num_accepted, _I32, (reqs,)))
-    _inner(fn, target=target, draft=draft)
-    _packed(fn, tokens=tokens, parents=parents, cu_tokens=cu_tokens, accept_u=accept_u, sample_u=sample_u,
-            out_tokens=out_tokens, out_nodes=out_nodes, num_accepted=num_accepted)
+    lib, T, fn = load_library(), _torch(), "idx_verify_drafts"
+    i32, f32 = T.i32, T.f32
+    total, vocab = rows = target.shape
+    reqs, max_out = out_shape = out_tokens.shape
+    if not (_rows_ok(target, f32, rows) and _rows_ok(draft, f32, rows) and _are(i32, (total,), tokens, parents)
+            and _are(i32, (reqs + 1,), cu_tokens) and _are(f32, (total,), accept_u) and _are(f32, (reqs,), sample_u)
+            and _are(i32, out_shape, out_tokens, out_nodes) and _are(i32, (reqs,), num_accepted)):
+        _explain(fn, ("tokens", "parents", "cu_tokens", "accept_u", "sample_u", "out_tokens", "out_nodes", "num_accepted"),
+                 target=(target, f32, rows), draft=(draft, f32, rows), tokens=(tokens, i32, (total,)), parents=(parents, i32, (total,)),
+                 cu_tokens=(cu_tokens, i32, (reqs + 1,)), accept_u=(accept_u, f32, (total,)), sample_u=(sample_u, f32, (reqs,)),
+                 out_tokens=(out_tokens, i32, out_shape), out_nodes=(out_nodes, i32, out_shape), num_accepted=(num_accepted, i32, (reqs,)))
     return _check(fn, lib.idx_verify_drafts(
-        _ptr(target), _row_stride(target), _ptr(draft), 0 if draft is None else _row_stride(draft), vocab, _ptr(tokens),
-        _ptr(parents), _ptr(cu_tokens), reqs, total, _ptr(accept_u), _ptr(sample_u), _ptr(out_tokens), _ptr(out_nodes),
-        max_out, _ptr(num_accepted), _ptr(status), _stream(stream)))
+        target.data_ptr(), _row_stride(target), _ptr(draft), 0 if draft is None else _row_stride(draft), vocab, tokens.data_ptr(),
+        _ptr(parents), cu_tokens.data_ptr(), reqs, total, accept_u.data_ptr(), sample_u.data_ptr(), out_tokens.data_ptr(),
+        out_nodes.data_ptr(), max_out, num_accepted.data_ptr(), _ptr(status), _stream_on(stream, target)))
