@@ -15,18 +15,27 @@
 // by a stretch's end leaves partial (O, M, l) in the workspace, which
 // k_tree_combine joins.
 //
-// Roles of a CTA (six warps):
-//   warps 0-3  one thread a row: scores from TMEM, softmax, weights back to
-//              TMEM, and at a segment's end the rows' results;
-//   warp 4     TMA: the queries, then key and value tiles through a ring of
-//              kStages, and a record of each tile (its places, what is masked);
-//   warp 5     one thread issues the MMAs: S = Q K^T (both from shared
-//              memory), O += P V (P in TMEM, V as it lies, places along K);
-//              S is doubled, so tile i+1's scores form during tile i's softmax.
+// Roles of a CTA (thirteen warps), which pass tiles on through mbarriers:
+//   warps 0-7  a row's scores of a tile go to two threads, one in warps 0-3
+//              for places 0-63 and one in warps 4-7 for places 64-127: scores
+//              from TMEM, softmax, weights back into the scores' columns, and
+//              at a segment's end the rows' results.  The two halves have
+//              their own (O, M, l), so no tile needs them to meet;
+//   warp 8     the plan: records of up to kChunk tiles at once, a lane a tile
+//              (block ids, places, what is masked), kSlots chunks ahead;
+//   warps 9-11 TMA: keys, values (through one ring of kStages tiles), queries;
+//   warp 12    MMA: S = Q K^T (both from shared memory), double buffered, so
+//              tile i+1's scores form during tile i's softmax, and O += P V
+//              (P in TMEM, V as it lies, places along K).  The warp waits as a
+//              whole and its first lane issues.
+// An instruction of a warp that works alone takes 10-30 cycles, a barrier's
+// test 200-300: with the plan made tile by tile by the warp that issues the
+// copies, that warp set the pace (5,300 cycles a tile against the 2,800 that
+// HBM needs; the softmax takes 1,400), hence the many small roles.
 // With at most 64 (32) live rows the queries stand two (four) times in the
 // 128 rows, and copy c of a row takes the softmax of the c-th part of each
-// tile's places, its weights for the others being zero: four warps share the
-// work that otherwise one would do, and the copies' (O, M, l) join at the end.
+// half tile, its weights for the others being zero: all warps share the work
+// that otherwise a few would do, and the copies' (O, M, l) join at the end.
 //
 // The bound is HBM for up to ~128 rows a KV head (4 D flops a row and key
 // against 4 D bytes a key: 128 flops a byte, below the ridge of ~280).
@@ -47,23 +56,28 @@ constexpr int kRowsA = 128;         // rows of an MMA
 constexpr int kTile = 128;          // places of a tile
 constexpr int kMaxCtas = 160;       // persistent CTAs at most (workspace sizes depend on it)
 constexpr int kStagesA = 5;         // key and value tiles in flight
-constexpr int kSoftWarps = 4;
-constexpr int kTmaWarp = 4, kMmaWarpA = 5;
-constexpr int kThreadsA = 6 * 32;
-constexpr int kRecs = 8;            // tile records (the producer leads by at most 3 tiles)
+constexpr int kSoftWarps = 8;
+constexpr int kPlanWarp = 8, kKeyTma = 9, kValueTma = 10, kQueryTma = 11, kMmaWarpA = 12;
+constexpr int kThreadsA = 13 * 32;
+constexpr int kHalf = kTile / 2;    // places of a half tile
+constexpr int kChunk = 16;          // tiles planned at once, all of one segment
+constexpr int kSlots = 4;           // chunks planned ahead
+constexpr int kSlotUsers = kSoftWarps + 4;  // warps that read a chunk
 constexpr int kRecWords = 32;
+constexpr int kSlotWords = (kChunk + 1) * kRecWords;  // a header, then the tiles
 constexpr int kGroup = 16;          // places of a record's group
 constexpr int kMaxListTokens = 32;  // tokens of a block with page lists (bits of a mask)
 constexpr float kRescale = 8.f;     // powers of two that a weight may exceed 1 before O is rescaled
 constexpr float kLog2e = 1.4426950408889634f;
 
-// TMEM columns
-constexpr uint32_t kColS = 0, kColO = 256, kColP = 384, kTmemColsA = 512;
+// TMEM columns: two score tiles, whose halves the weights overwrite (two to a
+// column), and the two halves' O.
+constexpr uint32_t kColS = 0, kColO = 256, kTmemColsA = 512;
 
-enum RecWord { kRFlags, kRTok0, kRTokens, kRHead, kRCtx, kRNew, kRNode0, kRLen, kRPos, kRMask = kRPos + 8, kROut = kRMask + 8,
-               kRReq, kRFirst, kREnd, kRList };
-static_assert(kRList < kRecWords, "a record fits");
-constexpr int kFlagFirst = 1, kFlagLast = 2, kKindShift = 2, kFoldShift = 4;
+// A chunk's header, and a tile's record.
+enum HeadWord { kHTiles, kHTok0, kHTokens, kHHead, kHCtx, kHNew, kHNode0, kHLen, kHOut, kHReq, kHFirst, kHEnd, kHList, kHFold };
+enum RecWord { kRFlags, kROffset, kRPos = 8, kRMask = 16, kRBox = 24 };
+constexpr int kFlagFirst = 1, kFlagLast = 2, kKindShift = 2;
 enum Kind { kFull = 0, kRowMask = 1, kGeneral = 2 };  // every row sees every place / whole rows do or do not / place by place
 
 struct ListEntry {
@@ -138,15 +152,38 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 16 consecutive 32-bit columns of this thread's TMEM lane from registers.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+// Two values at once: a * b + c, and a + b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// The four softmax warps of both halves, none of which can be missing here.
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // tcgen05 instruction descriptor, kind::f16: D f32, A and B both f16 (0) or
 // bf16 (1), A K-major, B K-major or (tb) N-major.
 __host__ __device__ constexpr uint32_t idesc_16(bool bf16, int m, int n, bool tb) {
@@ -225,26 +262,60 @@ struct Num<__half> {
 template <int D>
 struct Smem {
   static constexpr int kQ = kRowsA * D * 2, kKv = kTile * D * 2;
-  static constexpr int kScratchRow = 33;  // floats: 32 columns and one of padding
+  static constexpr int kScratchRow = 17;  // floats: 16 columns and one of padding
   static constexpr int kOffQ = 0;
   static constexpr int kOffKv = kOffQ + kQ;
   static constexpr int kOffScratch = kOffKv + kStagesA * kKv;
-  static constexpr int kOffStats = kOffScratch + kRowsA * kScratchRow * 4;
-  static constexpr int kOffRec = kOffStats + kRowsA * 8;
-  static constexpr int kOffBar = kOffRec + kRecs * kRecWords * 4;
+  static constexpr int kOffStats = kOffScratch + kSoftWarps * 32 * kScratchRow * 4;
+  static constexpr int kOffRec = kOffStats + kSoftWarps * 32 * 8;
+  static constexpr int kOffBar = kOffRec + kSlots * kSlotWords * 4;
   static constexpr int kOffMisc = kOffBar + 64 * 8;
   static constexpr int kBytes = kOffMisc + 64 + 1024;
 };
 enum BarsA { kKvFull = 0, kKvEmpty = kKvFull + kStagesA, kQFullA = kKvEmpty + kStagesA, kQEmptyA, kSFull, kPFull = kSFull + 2,
-             kPvDone, kOEmpty, kMerge, kRecFull, kDrainA = kRecFull + kRecs, kNumBarsA };
+             kPvDone = kPFull + 2, kOEmpty = kPvDone + 2, kMerge, kSlotFull, kSlotEmpty = kSlotFull + kSlots, kDrainA = kSlotEmpty + kSlots,
+             kNumBarsA };
 static_assert(kNumBarsA <= 64, "barriers fit");
 
 struct MiscA {
   uint32_t tmem_base;
   int abort_flag;
+  int soft_dead;  // a softmax warp gave up
+  int issued[2];  // key and value tiles whose copies were issued
   unsigned long long total;
-  unsigned long long rem0;
-  int r0;
+};
+
+// A warp's way through the planned tiles: all its lanes call next() for each
+// tile and done() after it.
+struct Walk {
+  uint32_t* recs;
+  uint64_t* bars;
+  volatile int* abort_flag;
+  int32_t* status;
+  uint32_t polls;
+  int chunk = -1, k = 0, n = 0;
+  const volatile uint32_t* head = nullptr;
+  const volatile uint32_t* rec = nullptr;
+  __device__ Walk(uint32_t* r, uint64_t* b, volatile int* f, int32_t* s, uint32_t p)
+      : recs(r), bars(b), abort_flag(f), status(s), polls(p) {}
+  __device__ bool next() {
+    if (k == n) {
+      ++chunk;
+      const int slot = chunk % kSlots;
+      const bool ok = timed_wait_flag(&bars[kSlotFull + slot], (uint32_t)(chunk / kSlots) & 1u, abort_flag, status, polls);
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+      head = recs + slot * kSlotWords;
+      rec = head;
+      n = (int)head[kHTiles], k = 0;
+    }
+    rec += kRecWords;
+    ++k;
+    return true;
+  }
+  __device__ void done() {
+    __syncwarp();
+    if (k == n && lane_id() == 0) mbar_arrive(&bars[kSlotEmpty + chunk % kSlots]);
+  }
 };
 
 // What a row's softmax needs of its segment.
@@ -266,92 +337,93 @@ __device__ __forceinline__ uint32_t group_bits(int pos, uint32_t tokens, const R
   return exist & (cached | (drafted & ~cached)) & 0xFFFFu;
 }
 
-// One tile's softmax for copies of 128 / F rows: scores in, weights out.
-// Returns through m, l the row's reference maximum (of raw scores) and sum.
+// One half tile's softmax for a thread whose row stands F times: kCols scores
+// in, their weights out.  Updates the row's reference maximum m (of raw
+// scores) and its sum l.
 template <typename T, int D, int F>
-__device__ __forceinline__ bool soft_tile(uint32_t tmem_row, uint32_t s_col, const volatile uint32_t* rec, const RowState& st,
-                                          bool tree, bool lists, float c, bool negate, int part, bool first, float& m, float& l,
-                                          uint64_t* pv_done, int prev, volatile int* abort_flag, int32_t* status, uint32_t polls) {
-  constexpr int kCols = kTile / F;
-  const uint32_t flags = rec[kRFlags];
-  const int kind = (flags >> kKindShift) & 3;
-  uint32_t v[kCols / 32][32];
+__device__ __forceinline__ bool soft_tile(uint32_t half_s, uint32_t half_o, const volatile uint32_t* rec, const RowState& st,
+                                          bool tree, bool lists, float c, bool negate, int col0, int copy, bool first, float& m,
+                                          float& l, uint64_t* pv_prev, uint32_t pv_parity, volatile int* abort_flag,
+                                          int32_t* status, uint32_t polls) {
+  constexpr int kCols = kHalf / F;
+  const int kind = (rec[kRFlags] >> kKindShift) & 3;
+  uint32_t v[kCols];
 #pragma unroll
-  for (int k = 0; k < kCols / 32; ++k) tmem_ld32(tmem_row + s_col + (uint32_t)(part * kCols + 32 * k), v[k]);
+  for (int k = 0; k < kCols; k += 16) tmem_ld16(half_s + (uint32_t)(copy * kCols + k), v + k);
   tmem_wait_ld();
   if (negate) {
 #pragma unroll
-    for (int k = 0; k < kCols / 32; ++k)
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[k][e] ^= 0x80000000u;
+    for (int e = 0; e < kCols; ++e) v[e] ^= 0x80000000u;
   }
   if (kind == kRowMask) {
     if (!((rec[kRMask] >> st.token) & 1u)) {
 #pragma unroll
-      for (int k = 0; k < kCols / 32; ++k)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[k][e] = 0xFF800000u;
+      for (int e = 0; e < kCols; ++e) v[e] = 0xFF800000u;
     }
   } else if (kind == kGeneral) {
 #pragma unroll
-    for (int k = 0; k < kCols / 32; ++k) {
-      const int g = part * (kCols / kGroup) + 2 * k;
-      const uint32_t bits = group_bits((int)rec[kRPos + g], rec[kRMask + g], st, tree, lists) |
-                            group_bits((int)rec[kRPos + g + 1], rec[kRMask + g + 1], st, tree, lists) << 16;
+    for (int k = 0; k < kCols; k += kGroup) {
+      const int g = (col0 + k) / kGroup;
+      const uint32_t bits = group_bits((int)rec[kRPos + g], rec[kRMask + g], st, tree, lists);
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!((bits >> e) & 1u)) v[k][e] = 0xFF800000u;
+      for (int e = 0; e < kGroup; ++e)
+        if (!((bits >> e) & 1u)) v[k + e] = 0xFF800000u;
     }
   }
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int k = 0; k < kCols / 32; ++k)
-#pragma unroll
-    for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(v[k][e]));
+  for (int e = 0; e < kCols; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(v[e]));
   const float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 
-  // O is complete up to the tile before, and its weights are free
-  bool ok = true;
-  if (prev >= 0) ok = timed_wait_flag(pv_done, (uint32_t)prev & 1u, abort_flag, status, polls);
-  if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-  tc_fence_after();
   float scale = 1.f;
   if (big > m && (m == -INFINITY || (big - m) * c > kRescale)) {
     scale = m == -INFINITY ? 1.f : ex2((m - big) * c);  // with no score so far O and l are zero
     m = big;
   }
-  l *= scale;
   if (!first && __any_sync(0xFFFFFFFFu, scale != 1.f)) {
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-      uint32_t o[32];
-      tmem_ld32(tmem_row + kColO + 32 * k, o);
+    // O is complete up to the tile before
+    const bool ok = timed_wait_flag(pv_prev, pv_parity, abort_flag, status, polls);
+    if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+    tc_fence_after();
+    l *= scale;
+#pragma unroll 1
+    for (int k = 0; k < D; k += 16) {
+      uint32_t o[16];
+      tmem_ld16(half_o + (uint32_t)k, o);
       tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
-      tmem_st32(tmem_row + kColO + 32 * k, o);
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+      tmem_st8(half_o + (uint32_t)k, o);
+      tmem_st8(half_o + (uint32_t)k + 8, o + 8);
     }
-  }
-  if (F > 1 && first) {
-    // the other copies' parts of the weights are zero throughout the segment
-    const uint32_t zero[16] = {};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) tmem_st16(tmem_row + kColP + 16 * k, zero);
   }
   const float mc = m == -INFINITY ? 0.f : m * c;
-  float sum[4] = {};
+  const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+  float2 sum[2] = {};
 #pragma unroll
-  for (int k = 0; k < kCols / 32; ++k) {
-    uint32_t w[16];
+  for (int k = 0; k < kCols; k += 16) {
+    uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const float x = ex2(fmaf(__uint_as_float(v[k][e]), c, -mc)), y = ex2(fmaf(__uint_as_float(v[k][e + 1]), c, -mc));
-      sum[(e >> 1) & 3] += x + y;
-      w[e >> 1] = Num<T>::pack(x, y);
+    for (int e = 0; e < 16; e += 2) {
+      const float2 x = fma2(make_float2(__uint_as_float(v[k + e]), __uint_as_float(v[k + e + 1])), c2, mc2);
+      const float2 y = make_float2(ex2(x.x), ex2(x.y));
+      sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+      w[e >> 1] = Num<T>::pack(y.x, y.y);
     }
-    tmem_st16(tmem_row + kColP + (uint32_t)(part * (kCols / 2) + 16 * k), w);
+    tmem_st8(half_s + (uint32_t)((copy * kCols + k) / 2), w);
   }
-  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  if (F > 1) {
+    // the places of the other copies
+    const uint32_t zero[8] = {};
+#pragma unroll
+    for (int k = 0; k < F; ++k)
+      if (k != copy) {
+#pragma unroll
+        for (int e = 0; e < kCols / 2; e += 8) tmem_st8(half_s + (uint32_t)(k * kCols / 2 + e), zero);
+      }
+  }
+  const float2 both = add2(sum[0], sum[1]);
+  l += both.x + both.y;
   return true;
 }
 
@@ -359,11 +431,11 @@ __device__ __forceinline__ bool soft_tile(uint32_t tmem_row, uint32_t s_col, con
 // does not see (or whose weight is zero) is an infinity or NaN.  The warp
 // forms the row's O again, place by place, from what the row sees alone.
 template <typename T, int D>
-__device__ __noinline__ void row_again(const TreeArgs& a, const volatile uint32_t* rec, int row, const RowState st, float m, float c,
+__device__ __noinline__ void row_again(const TreeArgs& a, const volatile uint32_t* head, int row, const RowState st, float m, float c,
                                        int col0, int col1, float* dst) {
   const int lane = (int)lane_id();
   constexpr int kE = D / 32;
-  const int t = (int)rec[kRTok0] + st.token, kvh = (int)rec[kRHead], r = (int)rec[kRReq];
+  const int t = (int)head[kHTok0] + st.token, kvh = (int)head[kHHead], r = (int)head[kHReq];
   const int h = kvh * a.group + row % a.group;
   const bool tree = a.mask != nullptr, lists = a.pages != nullptr;
   const float cs = a.scale < 0.f ? -c : c;
@@ -371,10 +443,10 @@ __device__ __noinline__ void row_again(const TreeArgs& a, const volatile uint32_
   const T* qp = static_cast<const T*>(a.q) + (int64_t)t * a.q_ts + (int64_t)h * a.q_hs + lane * kE;
 #pragma unroll
   for (int e = 0; e < kE; ++e) q[e] = (float)qp[e], o[e] = 0.f;
-  const int64_t list = (int64_t)rec[kRList];
+  const int64_t list = (int64_t)head[kHList];
   const int lh = lists ? kvh / (a.kv_heads / a.lists) : 0;
-  const int count = lists ? min(a.counts[(int64_t)rec[kRTok0] * a.lists + lh], (int)rec[kRTokens] * a.per) : 0;
-  for (int tile = (int)rec[kRFirst]; tile < (int)rec[kREnd]; ++tile)
+  const int count = lists ? min(a.counts[(int64_t)head[kHTok0] * a.lists + lh], (int)head[kHTokens] * a.per) : 0;
+  for (int tile = (int)head[kHFirst]; tile < (int)head[kHEnd]; ++tile)
     for (int col = col0; col < col1; ++col) {
       int64_t place = (int64_t)tile * kTile + col, blk = -1;
       uint32_t tokens = 0xFFFFFFFFu;
@@ -430,20 +502,26 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   if (tid == 0) {
     misc->total = 0;
     misc->abort_flag = 0;
+    misc->soft_dead = 0;
+    misc->issued[0] = misc->issued[1] = 0;
     for (int s = 0; s < kStagesA; ++s) {
       mbar_init(&bars[kKvFull + s], 1);
       mbar_init(&bars[kKvEmpty + s], 1);
     }
     mbar_init(&bars[kQFullA], 1);
     mbar_init(&bars[kQEmptyA], 1);
-    mbar_init(&bars[kSFull], 1);
-    mbar_init(&bars[kSFull + 1], 1);
-    mbar_init(&bars[kPFull], kSoftWarps);
-    mbar_init(&bars[kPvDone], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars[kSFull + s], 1);
+      mbar_init(&bars[kPFull + s], kSoftWarps);
+      mbar_init(&bars[kPvDone + s], 1);
+    }
     mbar_init(&bars[kOEmpty], kSoftWarps);
     mbar_init(&bars[kMerge], kSoftWarps);
-    for (int s = 0; s < kRecs; ++s) mbar_init(&bars[kRecFull + s], 1);
     mbar_init(&bars[kDrainA], 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&bars[kSlotFull + s], 1);
+      mbar_init(&bars[kSlotEmpty + s], kSlotUsers);
+    }
     fence_mbar_init();
   }
   __syncthreads();
@@ -453,6 +531,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     local = warp_sum_u64(local);
     if (lane == 0 && local) atomicAdd(&misc->total, local);
   }
+  __syncwarp();
   if (warp == 0) tmem_alloc(&misc->tmem_base, kTmemColsA);
   tc_fence_before();
   __syncthreads();
@@ -462,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   const unsigned long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
   const int count = (int)(w1 - w0);
 
-  if (warp == kTmaWarp && count > 0) {
+  if (warp == kPlanWarp && count > 0) {
     // the request of the stretch's first unit
     unsigned long long acc = 0;
     int r = 0;
@@ -508,130 +587,73 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     }
 
     const int bs = min(a.page, kTile), boxes = kTile / bs;  // places of a box, boxes of a tile
-    const uint32_t tile_bytes = (uint32_t)S::kKv;
-    int i = 0, seg = 0, piece_first = tile, items = 0, queries = 0;  // items, queries: copies issued
-    bool ok = true, bad_block = false;
-    bool fresh = true;  // the queries of the segment are still to load
-    // Block ids of the next 32 boxes, loaded together by the lanes.
-    int box_base = 0, ids = -1, id_page = 0;
-    uint32_t id_tokens = 0;
+    const int page_tiles = max(1, a.page / kTile);
+    int i = 0, seg = 0, piece_first = tile, chunk = 0;
+    bool bad_block = false;
     while (i < count) {
       const int len = plan.len(s), ctx = s - n;
       const int m = min(a.block_tokens, n - b * a.block_tokens), tok = t0 + b * a.block_tokens;
       const int rows = m * a.group;
-      const int fold = rows <= kRowsA / 4 ? 4 : rows <= kRowsA / 2 ? 2 : 1;
+      const int fold_code = rows <= kRowsA / 4 ? 2 : rows <= kRowsA / 2 ? 1 : 0;
       const int lh = lists ? kvh / per_list : 0;
       const int64_t list = ((int64_t)tok * a.lists + (int64_t)lh * m) * a.per;
       const int entries = lists ? min(a.counts[(int64_t)tok * a.lists + lh], m * a.per) : 0;
       const int piece_end = min(tiles, tile + (count - i));
-      if (fresh) {
-        if (seg > 0) ok = timed_wait_flag(&bars[kQEmptyA], (uint32_t)(seg - 1) & 1u, abort_flag, a.status, a.polls);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        const int loads = m * fold * (D / 64);
-        if (lane == 0) mbar_arrive_expect_tx(&bars[kQFullA], (uint32_t)(loads * a.group * 128));
-        ++queries;
-        __syncwarp();
-        for (int k = lane; k < loads; k += 32) {
-          const int sub = k % (D / 64), tk = k / (D / 64) % m, copy = k / (D / 64) / m;
-          tma_load_3d(smem + S::kOffQ + sub * (kRowsA * 128) + (copy * (kRowsA / fold) + tk * a.group) * 128, &qmap, sub * 64,
-                      kvh * a.group, tok + tk, &bars[kQFullA]);
-        }
-        fresh = false;
-        piece_first = tile;
-        box_base = -1;
+      const int here = min(kChunk, piece_end - tile);  // tiles of this chunk
+      const int slot = chunk % kSlots;
+      const bool ok =
+          timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag, a.status, a.polls);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      uint32_t* head = recs + slot * kSlotWords;
+      if (lane == 31) {
+        head[kHTiles] = (uint32_t)here, head[kHTok0] = (uint32_t)tok, head[kHTokens] = (uint32_t)m, head[kHHead] = (uint32_t)kvh;
+        head[kHCtx] = (uint32_t)ctx, head[kHNew] = (uint32_t)n, head[kHNode0] = (uint32_t)(b * a.block_tokens);
+        head[kHLen] = (uint32_t)len, head[kHReq] = (uint32_t)r, head[kHFirst] = (uint32_t)piece_first;
+        head[kHEnd] = (uint32_t)piece_end, head[kHList] = (uint32_t)list, head[kHFold] = (uint32_t)fold_code;
+        // partial results: slot 2x for the first segment of stretch x, 2x + 1 for the last; -1: the whole segment is here
+        head[kHOut] = piece_first == 0 && piece_end == tiles ? 0xFFFFFFFFu : (uint32_t)(2 * blockIdx.x + (seg > 0 ? 1 : 0));
       }
-      const int first_box = tile * boxes;
-      if (box_base < 0 || first_box >= box_base + 32) {
-        box_base = first_box;
-        const int64_t p = (int64_t)(box_base + lane) * bs;  // in the order of the list's or the table's places
-        ids = -1;
-        if (lists) {
-          const int64_t e = p / a.page;
-          if (e < entries) {
-            const ListEntry en = a.entries[list + e];
-            ids = en.block, id_page = en.page, id_tokens = en.tokens;
+      if (lane < here) {
+        const int my = tile + lane;
+        uint32_t* rec = head + (1 + lane) * kRecWords;
+        const uint32_t every = m >= 32 ? 0xFFFFFFFFu : (1u << m) - 1u;
+        const int page0 = boxes > 1 ? my * boxes : my / page_tiles, offset = boxes > 1 ? 0 : (my % page_tiles) * kTile;
+        bool all_cached = true, all_tokens = true;
+        for (int x = 0; x < boxes; ++x) {
+          int blk = -1, pg = page0 + x;
+          uint32_t tokens = 0xFFFFFFFFu;
+          if (lists) {
+            if (pg < entries) {
+              const ListEntry en = a.entries[list + pg];
+              blk = en.block, pg = en.page, tokens = en.tokens;
+            }
+          } else if ((int64_t)pg * a.page < len) {
+            blk = a.bt[r * a.bt_stride + pg];
+            if (blk < 0 || blk >= a.num_blocks) bad_block = true, blk = -1;
           }
-        } else if (p < len) {
-          id_page = (int)(p / a.page);
-          const int blk = a.bt[r * a.bt_stride + id_page];
-          if (blk >= 0 && blk < a.num_blocks) ids = blk;
-          else bad_block = true;
+          rec[kRBox + x] = (uint32_t)(blk < 0 ? (int)a.num_blocks : blk);  // a block outside the pool reads as zeros
+          const int pos = pg * a.page + offset;
+          all_cached = all_cached && blk >= 0 && (int64_t)pos + bs <= ctx && (int64_t)pos + bs <= len;
+          all_tokens = all_tokens && (tokens & every) == every;
+          for (int g = 0; g < bs / kGroup; ++g) {
+            rec[kRPos + x * (bs / kGroup) + g] = (uint32_t)(blk < 0 ? -1 : pos + g * kGroup);
+            rec[kRMask + x * (bs / kGroup) + g] = tokens;
+          }
         }
+        const int kind = all_cached && all_tokens ? kFull : all_cached && boxes == 1 ? kRowMask : kGeneral;
+        rec[kROffset] = (uint32_t)offset;
+        rec[kRFlags] = (uint32_t)((my == piece_first ? kFlagFirst : 0) | (my + 1 == piece_end ? kFlagLast : 0) | (kind << kKindShift));
       }
-      // this lane's box and group of the tile
-      const int my_box = first_box - box_base + lane % boxes, my_grp_box = first_box - box_base + (lane % 8) * kGroup / bs;
-      const int box_id = __shfl_sync(0xFFFFFFFFu, ids, my_box);
-      const int grp_id = __shfl_sync(0xFFFFFFFFu, ids, my_grp_box), grp_page = __shfl_sync(0xFFFFFFFFu, id_page, my_grp_box);
-      const uint32_t grp_tokens = lists ? __shfl_sync(0xFFFFFFFFu, id_tokens, my_grp_box) : 0xFFFFFFFFu;
-      const int in_order = (int)(((int64_t)tile * kTile) % a.page);  // offset of a whole-page tile within its page
-      const int off = bs < kTile ? ((lane % 8) * kGroup) % bs : in_order + (lane % 8) * kGroup;
-      const int pos = grp_id < 0 ? -1 : grp_page * a.page + off;
-      const uint32_t every = m >= 32 ? 0xFFFFFFFFu : (1u << m) - 1u;
-      const bool cached = pos >= 0 && pos + kGroup <= ctx && pos + kGroup <= len;
-      const bool all_cached = __all_sync(0xFFFFFFFFu, cached);
-      const bool all_tokens = !lists || __all_sync(0xFFFFFFFFu, (grp_tokens & every) == every);
-      const int kind = all_cached && all_tokens ? kFull : all_cached && boxes == 1 ? kRowMask : kGeneral;
-      const bool last = tile + 1 == piece_end;
-      uint32_t word = 0;
-      const int fold_code = fold == 4 ? 2 : fold == 2 ? 1 : 0;
-      // partial results: slot 2x for the first segment of stretch x, 2x + 1 for the last; -1: the whole segment is here
-      const bool whole = piece_first == 0 && piece_end == tiles;
-      switch (lane) {
-        case kRFlags:
-          word = (uint32_t)((tile == piece_first ? kFlagFirst : 0) | (last ? kFlagLast : 0) | (kind << kKindShift) |
-                            (fold_code << kFoldShift));
-          break;
-        case kRTok0: word = (uint32_t)tok; break;
-        case kRTokens: word = (uint32_t)m; break;
-        case kRHead: word = (uint32_t)kvh; break;
-        case kRCtx: word = (uint32_t)ctx; break;
-        case kRNew: word = (uint32_t)n; break;
-        case kRNode0: word = (uint32_t)(b * a.block_tokens); break;
-        case kRLen: word = (uint32_t)len; break;
-        case kROut: word = whole ? 0xFFFFFFFFu : (uint32_t)(2 * blockIdx.x + (seg > 0 ? 1 : 0)); break;
-        case kRReq: word = (uint32_t)r; break;
-        case kRFirst: word = (uint32_t)piece_first; break;
-        case kREnd: word = (uint32_t)piece_end; break;
-        case kRList: word = (uint32_t)list; break;
-        default: break;
-      }
-      {
-        const int g = lane >= kRMask ? lane - kRMask : lane - kRPos;
-        const uint32_t p = __shfl_sync(0xFFFFFFFFu, (uint32_t)pos, g & 7), k = __shfl_sync(0xFFFFFFFFu, grp_tokens, g & 7);
-        if (lane >= kRPos && lane < kRMask) word = p;
-        if (lane >= kRMask && lane < kROut) word = k;
-      }
-      // the record's slot was read at tile i - kRecs, whose value stage is free since tile i - 3
-      for (int half = 0; half < 2; ++half) {
-        const int item = 2 * i + half, stage = item % kStagesA;
-        if (ok) ok = timed_wait_flag(&bars[kKvEmpty + stage], ((uint32_t)(item / kStagesA) & 1u) ^ 1u, abort_flag, a.status, a.polls);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
-        if (half == 0) {
-          recs[(i % kRecs) * kRecWords + lane] = word;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kRecFull + i % kRecs]);
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&bars[kKvFull + stage], tile_bytes);
-        items = item + 1;
-        __syncwarp();
-        if (lane < boxes * (D / 64)) {
-          const int bx = lane % boxes, sub = lane / boxes;
-          const int c2 = boxes == 1 ? in_order : 0;
-          // a block outside the pool reads as zeros
-          tma_load_4d(smem + S::kOffKv + stage * S::kKv + sub * (kTile * 128) + bx * bs * 128, half == 0 ? &kmap : &vmap, sub * 64,
-                      kvh, c2, box_id < 0 ? (int)a.num_blocks : box_id, &bars[kKvFull + stage]);
-        }
-      }
-      if (!ok) break;
-      ++i;
-      if (++tile == tiles) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kSlotFull + slot]);
+      ++chunk;
+      i += here;
+      tile += here;
+      if (tile == tiles) {
         // next segment
         tile = 0;
+        piece_first = 0;
         ++seg;
-        fresh = true;
         if (++kvh == a.kv_heads) {
           kvh = 0;
           if (++b >= plan.blocks(n)) {
@@ -647,31 +669,73 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       }
     }
     if (bad_block) report(a.status, IDX_ST_BLOCK_OOR);
-    // never leave with a copy in flight
-    if (lane == 0) {
-      for (int k = max(0, items - kStagesA); k < items; ++k)
-        mbar_wait(&bars[kKvFull + k % kStagesA], (uint32_t)(k / kStagesA) & 1u, nullptr);
-      if (queries > 0) mbar_wait(&bars[kQFullA], (uint32_t)(queries - 1) & 1u, nullptr);
+  } else if ((warp == kKeyTma || warp == kValueTma) && count > 0) {
+    const bool keys = warp == kKeyTma;
+    const CUtensorMap* map = keys ? &kmap : &vmap;
+    const int bs = min(a.page, kTile), boxes = kTile / bs;
+    const int bx = lane % boxes, sub = lane / boxes;
+    const bool mine = lane < boxes * (D / 64);
+    uint8_t* dst = smem + S::kOffKv + sub * (kTile * 128) + bx * bs * 128;
+    Walk w(recs, bars, abort_flag, a.status, a.polls);
+    int issued = 0;
+    for (int i = 0; i < count; ++i) {
+      if (!w.next()) break;
+      const int kvh = (int)w.head[kHHead], offset = (int)w.rec[kROffset], box = (int)w.rec[kRBox + bx];
+      const int item = 2 * i + (keys ? 0 : 1), stage = item % kStagesA;
+      const bool ok =
+          timed_wait_flag(&bars[kKvEmpty + stage], ((uint32_t)(item / kStagesA) & 1u) ^ 1u, abort_flag, a.status, a.polls);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars[kKvFull + stage], (uint32_t)S::kKv);
+      __syncwarp();
+      if (mine) tma_load_4d(dst + stage * S::kKv, map, sub * 64, kvh, offset, box, &bars[kKvFull + stage]);
+      issued = i + 1;
+      w.done();
     }
+    if (lane == 0) misc->issued[keys ? 0 : 1] = issued;
+  } else if (warp == kQueryTma && count > 0) {
+    Walk w(recs, bars, abort_flag, a.status, a.polls);
+    int queries = 0;
+    for (int i = 0; i < count; ++i) {
+      if (!w.next()) break;
+      if (w.rec[kRFlags] & kFlagFirst) {
+        bool ok = true;
+        if (queries > 0) ok = timed_wait_flag(&bars[kQEmptyA], (uint32_t)(queries - 1) & 1u, abort_flag, a.status, a.polls);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        const int m = (int)w.head[kHTokens], fold = 1 << (int)w.head[kHFold], tok = (int)w.head[kHTok0], kvh = (int)w.head[kHHead];
+        const int loads = m * fold * (D / 64);
+        if (lane == 0) mbar_arrive_expect_tx(&bars[kQFullA], (uint32_t)(loads * a.group * 128));
+        __syncwarp();
+        for (int k = lane; k < loads; k += 32) {
+          const int sub = k % (D / 64), tk = k / (D / 64) % m, copy = k / (D / 64) / m;
+          tma_load_3d(smem + S::kOffQ + sub * (kRowsA * 128) + (copy * (kRowsA / fold) + tk * a.group) * 128, &qmap, sub * 64,
+                      kvh * a.group, tok + tk, &bars[kQFullA]);
+        }
+        ++queries;
+      }
+      w.done();
+    }
+    if (lane == 0 && queries > 0) mbar_wait(&bars[kQFullA], (uint32_t)(queries - 1) & 1u, nullptr);
   } else if (warp == kMmaWarpA && count > 0) {
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc_16(Num<T>::kBf16, kRowsA, kTile, false);
-      constexpr uint32_t kIdO = idesc_16(Num<T>::kBf16, kRowsA, D, true);
-      int seg = 0, done_seg = 0;
-      bool ok = true, issued = false;
-      uint32_t prev_flags = 0;
-      for (int i = 0; i <= count && ok; ++i) {
-        uint32_t flags = 0;
-        if (i < count) {
-          const int item = 2 * i, stage = item % kStagesA;
-          ok = spin_wait_flag(&bars[kKvFull + stage], (uint32_t)(item / kStagesA) & 1u, abort_flag, a.status, a.polls);
-          if (!ok) break;
-          flags = *reinterpret_cast<volatile uint32_t*>(recs + (i % kRecs) * kRecWords);
-          if (flags & kFlagFirst) {
-            ok = spin_wait_flag(&bars[kQFullA], (uint32_t)seg & 1u, abort_flag, a.status, a.polls);
-            if (!ok) break;
-          }
-          tc_fence_after();
+    constexpr uint32_t kIdS = idesc_16(Num<T>::kBf16, kRowsA, kTile, false);
+    constexpr uint32_t kIdO = idesc_16(Num<T>::kBf16, kRowsA, D, true);
+    Walk w(recs, bars, abort_flag, a.status, a.polls);
+    int seg_s = 0, seg_o = 0;  // segments whose scores, whose rows are complete
+    bool issued = false;
+    uint32_t prev = 0;  // flags of the tile before
+    auto wait = [&](int bar, int phase) { return spin_wait_flag(&bars[bar], (uint32_t)phase & 1u, abort_flag, a.status, a.polls); };
+    for (int i = 0; i <= count; ++i) {
+      uint32_t flags = 0;
+      if (i < count) {
+        if (!w.next()) break;
+        flags = w.rec[kRFlags];
+        w.done();
+        const int item = 2 * i, stage = item % kStagesA;
+        bool ok = wait(kKvFull + stage, item / kStagesA);
+        if (ok && (flags & kFlagFirst)) ok = wait(kQFullA, seg_s);
+        if (ok && i >= 2) ok = wait(kPvDone + (i & 1), (i >> 1) - 1);  // the weights of tile i - 2 have been read
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
+        if (lane == 0) {
           const uint64_t qd = sw128_desc(sbase + S::kOffQ), kd = sw128_desc(sbase + S::kOffKv + stage * S::kKv);
           const uint32_t d = tmem + kColS + (uint32_t)(i & 1) * kTile;
 #pragma unroll
@@ -679,42 +743,50 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             const uint64_t step = (uint64_t)((k / 4) * (kRowsA * 128 / 16) + (k % 4) * 2);
             mma_16(d, qd + step, kd + step, kIdS, k > 0 ? 1u : 0u);
           }
+          // a tile's stage is given back before anybody can learn that the
+          // tile is done: the ring's waits count on that order
+          mma_commit(&bars[kKvEmpty + stage]);
+          if (flags & kFlagLast) mma_commit(&bars[kQEmptyA]);
           mma_commit(&bars[kSFull + (i & 1)]);
-          mma_commit(&bars[kKvEmpty + stage]);
-          if (flags & kFlagLast) {
-            mma_commit(&bars[kQEmptyA]);
-            ++seg;
-          }
-          issued = true;
         }
-        if (i > 0) {
-          const int item = 2 * (i - 1) + 1, stage = item % kStagesA;
-          ok = spin_wait_flag(&bars[kKvFull + stage], (uint32_t)(item / kStagesA) & 1u, abort_flag, a.status, a.polls) &&
-               spin_wait_flag(&bars[kPFull], (uint32_t)(i - 1) & 1u, abort_flag, a.status, a.polls);
-          if (!ok) break;
-          if ((prev_flags & kFlagFirst) && done_seg > 0) {
-            ok = spin_wait_flag(&bars[kOEmpty], (uint32_t)(done_seg - 1) & 1u, abort_flag, a.status, a.polls);
-            if (!ok) break;
-          }
-          tc_fence_after();
+        __syncwarp();
+        if (flags & kFlagLast) ++seg_s;
+        issued = true;
+      }
+      if (i > 0) {
+        const int j = i - 1, item = 2 * j + 1, stage = item % kStagesA;
+        const bool first = (prev & kFlagFirst) != 0;
+        bool ok = wait(kKvFull + stage, item / kStagesA);
+        if (ok && first && seg_o > 0) ok = wait(kOEmpty, seg_o - 1);  // the rows of the segment before have been read
+        if (ok) ok = wait(kPFull + (j & 1), j >> 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
+        if (lane == 0) {
           const uint64_t vd = sw128_desc_nmajor(sbase + S::kOffKv + stage * S::kKv);
+          const uint32_t p = tmem + kColS + (uint32_t)(j & 1) * kTile;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_16_ta(tmem + kColO, tmem + kColP + 8 * k, vd + (uint64_t)(k * (2048 / 16)), kIdO,
-                      k > 0 || !(prev_flags & kFlagFirst) ? 1u : 0u);
-          mma_commit(&bars[kPvDone]);
+          for (int k = 0; k < kTile / 16; ++k) {
+            const int half = k / (kHalf / 16);
+            mma_16_ta(tmem + kColO + (uint32_t)(half * D), p + (uint32_t)(half * kHalf + 8 * (k % (kHalf / 16))),
+                      vd + (uint64_t)(k * (2048 / 16)), kIdO, k % (kHalf / 16) > 0 || !first ? 1u : 0u);
+          }
           mma_commit(&bars[kKvEmpty + stage]);
-          if (prev_flags & kFlagLast) ++done_seg;
+          mma_commit(&bars[kPvDone + (j & 1)]);
         }
-        prev_flags = flags;
+        __syncwarp();
+        if (prev & kFlagLast) ++seg_o;
       }
-      if (issued) {
-        mma_commit(&bars[kDrainA]);
-        mbar_wait(&bars[kDrainA], 0, nullptr);
-      }
+      prev = flags;
+    }
+    if (issued) {
+      if (lane == 0) mma_commit(&bars[kDrainA]);
+      __syncwarp();
+      mbar_wait(&bars[kDrainA], 0, nullptr);
     }
   } else if (warp < kSoftWarps) {
-    const uint32_t tmem_row = tmem + ((uint32_t)(warp * 32) << 16);
+    const int lane_row = tid & (kRowsA - 1), half = warp >> 2;
+    const uint32_t tmem_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t half_o = tmem_row + kColO + (uint32_t)(half * D);
     float* scratch = reinterpret_cast<float*>(smem + S::kOffScratch);
     float2* stats = reinterpret_cast<float2*>(smem + S::kOffStats);
     const bool negate = a.scale < 0.f;
@@ -722,60 +794,57 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
     float m = -INFINITY, l = 0.f;
     RowState st{};
-    uint32_t merges = 0;
-    int row = 0, part = 0, fold = 1;
-    auto meet = [&]() {  // the four warps
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kMerge]);
-      const bool ok = timed_wait_flag(&bars[kMerge], merges & 1u, abort_flag, a.status, a.polls);
-      ++merges;
-      return __all_sync(0xFFFFFFFFu, ok) != 0;
-    };
+    int seg = 0;
+    int row = 0, copy = 0, fold = 1, col0 = 0;
+    bool warp_live = true, done = count == 0;
+    Walk w(recs, bars, abort_flag, a.status, a.polls);
     for (int i = 0; i < count; ++i) {
-      bool ok_r, ok_s;
-      mbar_test2(&bars[kRecFull + i % kRecs], (uint32_t)(i / kRecs) & 1u, &bars[kSFull + (i & 1)], (uint32_t)(i >> 1) & 1u, ok_r, ok_s);
-      if (!ok_r) ok_r = timed_wait_flag(&bars[kRecFull + i % kRecs], (uint32_t)(i / kRecs) & 1u, abort_flag, a.status, a.polls);
-      if (!__all_sync(0xFFFFFFFFu, ok_r)) break;
-      const volatile uint32_t* rec = recs + (i % kRecs) * kRecWords;
+      if (!w.next()) break;
+      const uint32_t s_par = (uint32_t)(i >> 1) & 1u;
+      const volatile uint32_t *rec = w.rec, *head = w.head;
       const uint32_t flags = rec[kRFlags];
       const bool first = (flags & kFlagFirst) != 0;
+      const int rows = (int)head[kHTokens] * a.group;
       if (first) {
-        fold = 1 << ((flags >> kFoldShift) & 3);
-        row = tid & (kRowsA / fold - 1), part = tid / (kRowsA / fold);
+        fold = 1 << (int)head[kHFold];
+        row = lane_row & (kRowsA / fold - 1), copy = lane_row / (kRowsA / fold);
+        col0 = half * kHalf + copy * (kHalf / fold);
+        warp_live = (row & ~31) < rows;
         m = -INFINITY, l = 0.f;
-        st.token = min(row / a.group, (int)rec[kRTokens] - 1);  // rows past the block's compute on the last token's mask
-        st.ctx = (int)rec[kRCtx], st.len = (int)rec[kRLen];
-        const int n = (int)rec[kRNew];
-        st.chain_end = st.ctx + (int)rec[kRNode0] + st.token + 1;
-        st.tree = tree ? a.mask[(int)rec[kRTok0] + st.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
+        st.token = min(row / a.group, (int)head[kHTokens] - 1);  // rows past the block's compute on the last token's mask
+        st.ctx = (int)head[kHCtx], st.len = (int)head[kHLen];
+        const int n = (int)head[kHNew];
+        st.chain_end = st.ctx + (int)head[kHNode0] + st.token + 1;
+        st.tree = tree ? a.mask[(int)head[kHTok0] + st.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
       }
-      if (!ok_s) ok_s = timed_wait_flag(&bars[kSFull + (i & 1)], (uint32_t)(i >> 1) & 1u, abort_flag, a.status, a.polls);
-      if (!__all_sync(0xFFFFFFFFu, ok_s)) break;
+      bool ok = timed_wait_flag(&bars[kSFull + (i & 1)], s_par, abort_flag, a.status, a.polls);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
-      const uint32_t s_col = kColS + (uint32_t)(i & 1) * kTile;
-      bool ok;
-      if (fold == 4)
-        ok = soft_tile<T, D, 4>(tmem_row, s_col, rec, st, tree, lists, c, negate, part, first, m, l, &bars[kPvDone], i - 1, abort_flag,
-                                a.status, a.polls);
-      else if (fold == 2)
-        ok = soft_tile<T, D, 2>(tmem_row, s_col, rec, st, tree, lists, c, negate, part, first, m, l, &bars[kPvDone], i - 1, abort_flag,
-                                a.status, a.polls);
-      else
-        ok = soft_tile<T, D, 1>(tmem_row, s_col, rec, st, tree, lists, c, negate, part, first, m, l, &bars[kPvDone], i - 1, abort_flag,
-                                a.status, a.polls);
+      const uint32_t half_s = tmem_row + kColS + (uint32_t)((i & 1) * kTile + half * kHalf);
+      uint64_t* pv_prev = &bars[kPvDone + ((i + 1) & 1)];
+      const uint32_t pv_par = (uint32_t)((i - 1) >> 1) & 1u;
+      if (warp_live) {  // a warp without a live row leaves what lies there: its rows are not read
+        if (fold == 4)
+          ok = soft_tile<T, D, 4>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
+                                  a.status, a.polls);
+        else if (fold == 2)
+          ok = soft_tile<T, D, 2>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
+                                  a.status, a.polls);
+        else
+          ok = soft_tile<T, D, 1>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
+                                  a.status, a.polls);
+      }
       if (!ok) break;
-      if (((flags >> kKindShift) & 3) == kGeneral) {
+      if (((flags >> kKindShift) & 3) == kGeneral && half < D / 64) {
         // values at places that do not exist may be anything: zeros in their stead
-        const int pos = (int)rec[kRPos + tid / kGroup];
-        if (pos >= 0 && pos + tid % kGroup >= st.len) {
+        const int pos = (int)rec[kRPos + lane_row / kGroup];
+        if (pos >= 0 && pos + lane_row % kGroup >= st.len) {
           const int item = 2 * i + 1, stage = item % kStagesA;
           ok = timed_wait_flag(&bars[kKvFull + stage], (uint32_t)(item / kStagesA) & 1u, abort_flag, a.status, a.polls);
           if (ok) {
-            uint4* vrow = reinterpret_cast<uint4*>(smem + S::kOffKv + stage * S::kKv + tid * 128);
+            uint4* vrow = reinterpret_cast<uint4*>(smem + S::kOffKv + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
 #pragma unroll
-            for (int sub = 0; sub < D / 64; ++sub)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) vrow[sub * (kTile * 128 / 16) + e] = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 8; ++e) vrow[e] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -784,128 +853,128 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kPFull]);
-      if (!(flags & kFlagLast)) continue;
+      if (lane == 0) mbar_arrive(&bars[kPFull + (i & 1)]);
+      if (!(flags & kFlagLast)) {
+        w.done();
+        continue;
+      }
 
       // the segment's rows
-      ok = timed_wait_flag(&bars[kPvDone], (uint32_t)i & 1u, abort_flag, a.status, a.polls);
+      ok = timed_wait_flag(&bars[kPvDone + (i & 1)], s_par, abort_flag, a.status, a.polls);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
-      const int rows = (int)rec[kRTokens] * a.group;
       const bool live = row < rows;
       {
         float probe = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t o[32];
-          tmem_ld32(tmem_row + kColO + 32 * k, o);
+#pragma unroll 1
+        for (int k = 0; k < D; k += 16) {
+          uint32_t o[16];
+          tmem_ld16(half_o + (uint32_t)k, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) probe = fmaf(__uint_as_float(o[e]), 0.f, probe);
+          for (int e = 0; e < 16; ++e) probe = fmaf(__uint_as_float(o[e]), 0.f, probe);
         }
         uint32_t again = __ballot_sync(0xFFFFFFFFu, live && l > 0.f && l < INFINITY && probe != 0.f);
         while (again) {
           const int who = __ffs(again) - 1;
           again &= again - 1;
-          RowState w;
-          w.tree = __shfl_sync(0xFFFFFFFFu, st.tree, who);
-          w.ctx = st.ctx, w.len = st.len;
-          w.chain_end = __shfl_sync(0xFFFFFFFFu, st.chain_end, who);
-          w.token = __shfl_sync(0xFFFFFFFFu, st.token, who);
+          RowState x;
+          x.tree = __shfl_sync(0xFFFFFFFFu, st.tree, who);
+          x.ctx = st.ctx, x.len = st.len;
+          x.chain_end = __shfl_sync(0xFFFFFFFFu, st.chain_end, who);
+          x.token = __shfl_sync(0xFFFFFFFFu, st.token, who);
           float* dst = scratch + warp * 32 * S::kScratchRow;
-          row_again<T, D>(a, rec, __shfl_sync(0xFFFFFFFFu, row, who), w, __shfl_sync(0xFFFFFFFFu, m, who), c,
-                          __shfl_sync(0xFFFFFFFFu, part, who) * (kTile / fold),
-                          (__shfl_sync(0xFFFFFFFFu, part, who) + 1) * (kTile / fold), dst);
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[32];
-            tmem_ld32(tmem_row + kColO + 32 * k, o);
+          const int from = __shfl_sync(0xFFFFFFFFu, col0, who);
+          row_again<T, D>(a, head, __shfl_sync(0xFFFFFFFFu, row, who), x, __shfl_sync(0xFFFFFFFFu, m, who), c, from,
+                          from + kHalf / fold, dst);
+#pragma unroll 1
+          for (int k = 0; k < D; k += 16) {
+            uint32_t o[16];
+            tmem_ld16(half_o + (uint32_t)k, o);
             tmem_wait_ld();
             if (lane == who)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(dst[32 * k + e]);
-            tmem_st32(tmem_row + kColO + 32 * k, o);
-            tmem_wait_st();
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(dst[k + e]);
+            tmem_st8(half_o + (uint32_t)k, o);
+            tmem_st8(half_o + (uint32_t)k + 8, o + 8);
           }
+          tmem_wait_st();
           __syncwarp();
         }
       }
-      float big = m, factor = 1.f, whole_l = l;
-      if (fold > 1) {
-        stats[tid] = make_float2(m, l);
-        if (!meet()) break;
-        whole_l = 0.f;
-        for (int p = 0; p < fold; ++p) big = fmaxf(big, stats[p * (kRowsA / fold) + row].x);
-        for (int p = 0; p < fold; ++p) {
-          const float2 x = stats[p * (kRowsA / fold) + row];
-          if (x.x != -INFINITY) whole_l += x.y * ex2((x.x - big) * c);
-        }
-        factor = m == -INFINITY ? 0.f : ex2((m - big) * c);
+      stats[tid] = make_float2(m, l);
+      // All eight warps meet, those that gave up among them (see below); the
+      // wait ends for all or for none, so that no warp misses a later barrier.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kMerge]);
+      ok = mbar_wait(&bars[kMerge], (uint32_t)seg & 1u, nullptr);
+      ++seg;
+      if (!__all_sync(0xFFFFFFFFu, ok) || *reinterpret_cast<volatile int*>(&misc->soft_dead)) {
+        done = true;
+        break;
       }
-      const uint32_t slot = rec[kROut];
-      const int t = (int)rec[kRTok0] + st.token, h = (int)rec[kRHead] * a.group + row % a.group;
-      const bool direct = slot == 0xFFFFFFFFu;
-      const bool empty = whole_l == 0.f;
-      const float inv = direct ? (empty ? 0.f : 1.f / whole_l) : 1.f;
-      if (live && part == 0) {
+      // the row's parts: two halves of `fold` copies
+      const int parts = 2 * fold, my_part = half * fold + copy, per = kRowsA / fold;
+      auto part_at = [&](int p) { return (p / fold) * kRowsA + (p % fold) * per + row; };
+      float big = -INFINITY, sum_l = 0.f;
+      for (int p = 0; p < parts; ++p) big = fmaxf(big, stats[part_at(p)].x);
+      for (int p = 0; p < parts; ++p) {
+        const float2 x = stats[part_at(p)];
+        if (x.x != -INFINITY) sum_l += x.y * ex2((x.x - big) * c);
+      }
+      const float factor = m == -INFINITY ? 0.f : ex2((m - big) * c);
+      const uint32_t slot = head[kHOut];
+      const int t = (int)head[kHTok0] + st.token, h = (int)head[kHHead] * a.group + row % a.group;
+      const bool direct = slot == 0xFFFFFFFFu, empty = sum_l == 0.f;
+      const float inv = empty ? 0.f : direct ? 1.f / sum_l : 1.f;
+      if (live && my_part == 0) {
         if (direct) {
-          if (a.lse != nullptr) a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + log2f(whole_l)) * 0.6931471805599453f;
+          if (a.lse != nullptr) a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + log2f(sum_l)) * 0.6931471805599453f;
         } else {
-          reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : big * c, whole_l);
+          reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : big * c, sum_l);
         }
       }
       T* out = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs;
       float* part_o = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row) * D;
-      bool alive = true;
+      const int width = 16 / parts;  // columns of a round that this thread joins: 8, 4 or 2
 #pragma unroll 1
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t o[32];
-        tmem_ld32(tmem_row + kColO + 32 * k, o);
+      for (int k = 0; k < D; k += 16) {
+        uint32_t o[16];
+        tmem_ld16(half_o + (uint32_t)k, o);
         tmem_wait_ld();
-        const int width = 32 / fold;  // columns that this thread writes
-        float f[32];
-        if (fold == 1) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = empty ? 0.f : __uint_as_float(o[e]) * inv;
-        } else {
+        for (int e = 0; e < 16; ++e) scratch[tid * S::kScratchRow + e] = factor == 0.f ? 0.f : __uint_as_float(o[e]) * factor;
+        soft_sync();
+        const int col = my_part * width;
+        float f[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) scratch[tid * S::kScratchRow + e] = factor == 0.f ? 0.f : __uint_as_float(o[e]) * factor;
-          if (!meet()) {
-            alive = false;
-            break;
+        for (int e = 0; e < 8; ++e) {
+          f[e] = 0.f;
+          if (e < width) {
+            for (int p = 0; p < parts; ++p) f[e] += scratch[part_at(p) * S::kScratchRow + col + e];
+            f[e] = empty ? 0.f : f[e] * inv;
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < width) {
-              float sum = 0.f;
-              for (int p = 0; p < fold; ++p) sum += scratch[(p * (kRowsA / fold) + row) * S::kScratchRow + part * width + e];
-              f[e] = empty ? 0.f : sum * inv;
-            }
         }
         if (live) {
-          const int col = 32 * k + (fold == 1 ? 0 : part * width);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
+          for (int e = 0; e < 8; e += 2)
             if (e < width) {
-              if (direct) {
-                *reinterpret_cast<uint4*>(out + col + e) =
-                    make_uint4(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]), Num<T>::pack(f[e + 4], f[e + 5]),
-                               Num<T>::pack(f[e + 6], f[e + 7]));
-              } else {
-                reinterpret_cast<float4*>(part_o + col + e)[0] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-                reinterpret_cast<float4*>(part_o + col + e)[1] = make_float4(f[e + 4], f[e + 5], f[e + 6], f[e + 7]);
-              }
+              if (direct) *reinterpret_cast<uint32_t*>(out + k + col + e) = Num<T>::pack(f[e], f[e + 1]);
+              else *reinterpret_cast<float2*>(part_o + k + col + e) = make_float2(f[e], f[e + 1]);
             }
         }
-        if (fold > 1 && !meet()) {
-          alive = false;
-          break;
-        }
+        soft_sync();
       }
-      if (!alive) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kOEmpty]);
+      w.done();
+      done = i + 1 == count;  // the last tile ends a segment or the stretch's part of it
+    }
+    if (!done && lane == 0) {
+      // gave up: say so, then take this warp's place at the barrier that the others may wait at
+      *reinterpret_cast<volatile int*>(&misc->soft_dead) = 1;
+      mbar_arrive(&bars[kMerge]);
     }
   }
 
@@ -913,11 +982,24 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     if (count == 0) a.cuts[8 * blockIdx.x] = 0;
     if (blockIdx.x == 0) *reinterpret_cast<unsigned long long*>(a.cuts + 8 * kMaxCtas) = W;
   }
-  __syncthreads();
   // lengths that the table does not hold
   if (blockIdx.x == 0)
     for (int r = tid; r < a.num_reqs; r += kThreadsA)
       if (plan.ntok(r) > 0 && plan.len(plan.seq(r)) < plan.seq(r)) report(a.status, IDX_ST_LEN_CLAMPED);
+  __syncwarp();
+  __syncthreads();
+  if (*abort_flag) {
+    if (tid < kStagesA) {
+      // never leave with a copy in flight: the last one into each stage
+      int last = -1;
+      for (int k = 0; k < 2; ++k)
+        for (int i = max(0, misc->issued[k] - kStagesA); i < misc->issued[k]; ++i)
+          if ((2 * i + k) % kStagesA == tid) last = max(last, 2 * i + k);
+      if (last >= 0) mbar_wait(&bars[kKvFull + tid], (uint32_t)(last / kStagesA) & 1u, nullptr);
+    }
+    __syncwarp();
+    __syncthreads();
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemColsA);

@@ -31,13 +31,14 @@
 namespace idx {
 namespace {
 
-constexpr int kThreadsV = 512;
+constexpr int kThreadsV = 256;
 constexpr int kWarpsV = kThreadsV / 32;
 constexpr int kMaxNodes = IDX_VERIFY_MAX_NODES;
 constexpr int kMaxCluster = 8;
-constexpr int kUnrollV = 8;  // loads in flight a thread and row
-constexpr int kPieceV = 4;   // entries a thread takes in the draw's search
+constexpr int kUnrollV = 4;  // loads of four entries in flight a thread and row
 constexpr double kUnit = 1152921504606846976.0;  // 2^60
+constexpr double kUnitC = 4503599627370496.0;    // 2^52
+constexpr double kMostC = 4095.0;
 
 using u64 = unsigned long long;
 
@@ -90,14 +91,28 @@ __device__ __forceinline__ u64 fixed_of(float x) {
   return e == 0u || sh > 63u ? 0ull : m >> sh;
 }
 
-// The term of one vocabulary entry: max(p - c q, 0).
-__device__ __forceinline__ u64 term(float p, float q, double c, bool one) {
-  if (one) {
-    const long long d = (long long)(fixed_of(clean(p)) - fixed_of(clean(q)));
-    return d > 0 ? (u64)d : 0ull;
+// The term of one vocabulary entry, max(p - c q, 0), in multiples of 2^-60; c
+// in multiples of 2^-52 (`one`: c is 1, the first refusal of nearly all walks).
+__device__ __forceinline__ u64 term(float p, float q, u64 c52, bool one) {
+  const u64 f = fixed_of(clean(q));
+  u64 cq = f;
+  if (!one) {
+    const u64 hi = __umul64hi(f, c52);
+    cq = hi >> 52 ? ~0ull : hi << 12 | (f * c52) >> 52;
   }
-  const double d = __dsub_rn((double)clean(p), __dmul_rn(c, (double)clean(q)));
-  return d > 0.0 ? __double2ull_rz(fmin(d, 7.99) * kUnit) : 0ull;
+  const u64 fp = fixed_of(clean(p));
+  return fp > cq ? fp - cq : 0ull;
+}
+
+// Entries v .. v + 3 of a row, 0 outside it; `vec`: v is at an aligned address.
+__device__ __forceinline__ float4 quad_of(const float* row, int v, int vocab, bool vec) {
+  if (vec && v >= 0 && v + 4 <= vocab) return *reinterpret_cast<const float4*>(row + v);
+  float4 x;
+  x.x = v >= 0 && v < vocab ? row[v] : 0.f;
+  x.y = v + 1 >= 0 && v + 1 < vocab ? row[v + 1] : 0.f;
+  x.z = v + 2 >= 0 && v + 2 < vocab ? row[v + 2] : 0.f;
+  x.w = v + 3 < vocab ? row[v + 3] : 0.f;
+  return x;
 }
 
 struct Shared {
@@ -145,10 +160,22 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
   if (tid == 0) s.at = 0, s.next = 1, s.taken = 0, s.num_refused = 0, s.c = 0.0, s.w = 1.0;
   __syncthreads();
 
-  // this CTA's part of the vocabulary, and the warp's stretch of it
-  const int v_lo = (int)((int64_t)a.vocab * rank / cs), v_hi = (int)((int64_t)a.vocab * (rank + 1) / cs);
-  const int w_lo = v_lo + (int)((int64_t)(v_hi - v_lo) * warp / kWarpsV);
-  const int w_hi = v_lo + (int)((int64_t)(v_hi - v_lo) * (warp + 1) / kWarpsV);
+  // The vocabulary in quads of four entries that share an aligned 16-byte load
+  // of the target's row (the first and the last quad may be cut); this CTA's
+  // quads, and the warp's stretch of them.  `shift` entries lie before the row
+  // in its first quad.
+  struct Span {
+    int shift, lo, hi;  // quads [lo, hi) are this CTA's
+  };
+  auto span_of = [&](int at) {
+    Span w;
+    const float* p = a.target + (int64_t)(t0 + at) * a.target_stride;
+    w.shift = (int)((reinterpret_cast<uintptr_t>(p) >> 2) & 3);
+    const int64_t quads = ((int64_t)a.vocab + w.shift + 3) / 4;
+    w.lo = (int)(quads * rank / cs), w.hi = (int)(quads * (rank + 1) / cs);
+    return w;
+  };
+  auto stretch = [&](const Span& w, int k) { return w.lo + (int)((int64_t)(w.hi - w.lo) * k / kWarpsV); };
   int parity = 0;
   bool summed = false;  // a pass has run; with c != 0 it was the state's
   u64 total = 0;
@@ -158,26 +185,38 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
     const float* p = a.target + (int64_t)(t0 + at) * a.target_stride;
     const float* q = a.draft + (int64_t)(t0 + at) * a.draft_stride;
     const bool with_q = a.draft != nullptr && c != 0.0, one = c == 1.0;
+    const bool both = with_q && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    const u64 c52 = (u64)(fmin(c, kMostC) * kUnitC);
+    const Span w = span_of(at);
+    const int w_lo = stretch(w, warp), w_hi = stretch(w, warp + 1);
     u64 sum = 0;
-    for (int v = w_lo + lane; v < w_hi; v += 32 * kUnrollV) {
-      float pv[kUnrollV], qv[kUnrollV];
+    for (int k = w_lo + lane; k < w_hi; k += 32 * kUnrollV) {
+      float4 pv[kUnrollV], qv[kUnrollV];
 #pragma unroll
-      for (int e = 0; e < kUnrollV; ++e) pv[e] = v + 32 * e < w_hi ? p[v + 32 * e] : 0.f;
+      for (int e = 0; e < kUnrollV; ++e) {
+        pv[e] = qv[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k + 32 * e < w_hi) {
+          const int v = 4 * (k + 32 * e) - w.shift;
+          pv[e] = quad_of(p, v, a.vocab, true);
+          if (with_q) qv[e] = quad_of(q, v, a.vocab, both);
+        }
+      }
       if (with_q) {
 #pragma unroll
-        for (int e = 0; e < kUnrollV; ++e) qv[e] = v + 32 * e < w_hi ? q[v + 32 * e] : 0.f;
-#pragma unroll
-        for (int e = 0; e < kUnrollV; ++e) sum += term(pv[e], qv[e], c, one);
+        for (int e = 0; e < kUnrollV; ++e)
+          sum += (term(pv[e].x, qv[e].x, c52, one) + term(pv[e].y, qv[e].y, c52, one)) +
+                 (term(pv[e].z, qv[e].z, c52, one) + term(pv[e].w, qv[e].w, c52, one));
       } else {
 #pragma unroll
-        for (int e = 0; e < kUnrollV; ++e) sum += fixed_of(clean(pv[e]));
+        for (int e = 0; e < kUnrollV; ++e)
+          sum += (fixed_of(clean(pv[e].x)) + fixed_of(clean(pv[e].y))) + (fixed_of(clean(pv[e].z)) + fixed_of(clean(pv[e].w)));
       }
     }
     sum = warp_sum_u64(sum);
     if (subtract)  // the refused tokens of the warp's stretch (each listed once)
       for (int k = 0; k < s.num_refused; ++k) {
         const int x = s.refused[k];
-        if (x >= w_lo && x < w_hi) sum -= fixed_of(clean(p[x]));
+        if ((x + w.shift) / 4 >= w_lo && (x + w.shift) / 4 < w_hi) sum -= fixed_of(clean(p[x]));
       }
     if (lane == 0) s.warp_sum[warp] = sum;
     __syncthreads();
@@ -272,26 +311,24 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
   if (thr < before || thr - before >= s.cta_sum[parity][rank]) return;  // another CTA's
   int seg = 0;
   while (seg < kWarpsV - 1 && thr - before >= s.warp_sum[seg]) before += s.warp_sum[seg++];
-  const int lo = v_lo + (int)((int64_t)(v_hi - v_lo) * seg / kWarpsV);
-  const int hi = v_lo + (int)((int64_t)(v_hi - v_lo) * (seg + 1) / kWarpsV);
+  const Span span = span_of(at);
+  const int lo = stretch(span, seg), hi = stretch(span, seg + 1);
   const float* p = a.target + (int64_t)(t0 + at) * a.target_stride;
   const float* q = a.draft + (int64_t)(t0 + at) * a.draft_stride;
-  const bool with_q = a.draft != nullptr && last_c != 0.0;
-  for (int base = lo; base < hi; base += kThreadsV * kPieceV) {
-    const int v0 = base + tid * kPieceV;
-    u64 f[kPieceV], mine = 0;
-#pragma unroll
-    for (int e = 0; e < kPieceV; ++e) {
-      const int v = v0 + e;
-      f[e] = v >= hi ? 0ull : with_q ? term(p[v], q[v], last_c, last_c == 1.0) : fixed_of(clean(p[v]));
-    }
+  const bool with_q = a.draft != nullptr && last_c != 0.0, one = last_c == 1.0;
+  const u64 c52 = (u64)(fmin(last_c, kMostC) * kUnitC);
+  for (int base = lo; base < hi; base += kThreadsV) {
+    const int v0 = 4 * (base + tid) - span.shift;
+    const bool in = base + tid < hi;
+    const float4 pv = in ? quad_of(p, v0, a.vocab, true) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 qv = in && with_q ? quad_of(q, v0, a.vocab, false) : make_float4(0.f, 0.f, 0.f, 0.f);
+    u64 f[4] = {term(pv.x, qv.x, c52, one), term(pv.y, qv.y, c52, one), term(pv.z, qv.z, c52, one), term(pv.w, qv.w, c52, one)};
     if (last_excl)
       for (int k = 0; k < s.num_refused; ++k)
 #pragma unroll
-        for (int e = 0; e < kPieceV; ++e)
+        for (int e = 0; e < 4; ++e)
           if (s.refused[k] == v0 + e) f[e] = 0;
-#pragma unroll
-    for (int e = 0; e < kPieceV; ++e) mine += f[e];
+    const u64 mine = (f[0] + f[1]) + (f[2] + f[3]);
     u64 incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -309,7 +346,7 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
     u64 sum = at_warp + incl - mine;
     if (mine > 0 && thr >= sum && thr - sum < mine) {
 #pragma unroll
-      for (int e = 0; e < kPieceV; ++e) {
+      for (int e = 0; e < 4; ++e) {
         if (thr >= sum && thr - sum < f[e]) out_tokens[taken] = v0 + e;
         sum += f[e];
       }
@@ -324,7 +361,7 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
 // requests, stretches of at least a few loads a thread.
 int cluster_for(int32_t num_reqs, int32_t vocab) {
   (void)num_reqs, (void)vocab;
-  return 1;
+  return 8;
 }
 
 }  // namespace

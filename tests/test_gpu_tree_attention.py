@@ -328,3 +328,19 @@ def test_offsets_past_32_bits(lib):
     c["table"] = np.where(c["table"] >= 0, c["table"] + blocks - n, -1).astype(np.int32)
     out, L, st = run(lib, c)
     compare(c, out, L, want)
+
+
+def test_times_out_then_recovers(lib):
+    """With a budget of zero polls a wait is a single test, so the launch gives up, reports it and ends; the next is right."""
+    c = make(27, [9000, 500, 3000, 10], [8, 5, 1, 8], 64, 4, 128, 128, "bf16")
+    ref = reference(c)
+    for _ in range(3):
+        prev = lib.idx_set_wait_limit(0)
+        try:
+            _, _, st = run(lib, c)
+        finally:
+            assert lib.idx_set_wait_limit(prev) == 0
+        assert st & lib.ST_TIMEOUT
+        out, L, st = run(lib, c)
+        assert st == 0
+        compare(c, out, L, ref)
