@@ -10,9 +10,10 @@
 // the query heads of one KV head are the 128 rows of an MMA, so each key and
 // value tile is read once for all of them.  Its keys come in tiles of 128
 // places, gathered by TMA from the pages (several boxes a tile for pages
-// below 128 places).  All tiles of all segments form one line of units; each
-// of the persistent CTAs, one an SM, takes an equal stretch of it.  A segment cut
-// by a stretch's end leaves partial (O, M, l) in the workspace, which
+// below 128 places).  All segments form one line of units, kSegCost for a
+// segment's begin and end and one for each of its tiles; each of the
+// persistent CTAs, one an SM, takes an equal stretch of it.  A segment cut by a
+// stretch's end leaves partial (O, M, l) in the workspace, which
 // k_tree_combine joins.
 //
 // Roles of a CTA (thirteen warps), which pass tiles on through mbarriers:
@@ -23,7 +24,7 @@
 //              their own (O, M, l), so no tile needs them to meet;
 //   warp 8     the plan: records of up to kChunk tiles at once, a lane a tile
 //              (block ids, places, what is masked), kSlots chunks ahead;
-//   warps 9-11 TMA: keys, values (through one ring of kStages tiles), queries;
+//   warps 9-11 TMA: keys, values (a ring of tiles each), queries;
 //   warp 12    MMA: S = Q K^T (both from shared memory), double buffered, so
 //              tile i+1's scores form during tile i's softmax, and O += P V
 //              (P in TMEM, V as it lies, places along K).  The warp waits as a
@@ -55,7 +56,15 @@ namespace {
 constexpr int kRowsA = 128;         // rows of an MMA
 constexpr int kTile = 128;          // places of a tile
 constexpr int kMaxCtas = 160;       // persistent CTAs at most (workspace sizes depend on it)
-constexpr int kStagesA = 5;         // key and value tiles in flight
+// Key and value tiles in flight.  A key tile is held for its load and one MMA,
+// a value tile too where it does not come early; one ring for both would load
+// a value tile long before its softmax is done.
+template <int D>
+struct Ring {
+  static constexpr int kKeys = D == 128 ? 3 : 5, kValues = D == 128 ? 2 : 5;
+};
+constexpr int kMaxStages = 5;
+constexpr int kSegCost = 1;         // units of a segment's begin and end
 constexpr int kSoftWarps = 8;
 constexpr int kPlanWarp = 8, kKeyTma = 9, kValueTma = 10, kQueryTma = 11, kMmaWarpA = 12;
 constexpr int kThreadsA = 13 * 32;
@@ -137,11 +146,12 @@ struct Plan {
     if (a.mask == nullptr) lim = min(lim, max(0, s - n + min(n, (b + 1) * a.block_tokens)));
     return max(1, (int)(((int64_t)lim + kTile - 1) / kTile));
   }
+  // units of a request: for each segment kSegCost, then its tiles
   __device__ unsigned long long units(int r) const {
     const int n = ntok(r), t0 = tok0(r), s = seq(r), nl = a.pages != nullptr ? a.lists : 1;
     unsigned long long sum = 0;
     for (int b = 0; b < blocks(n); ++b)
-      for (int l = 0; l < nl; ++l) sum += (unsigned long long)tiles(s, n, t0, b, l);
+      for (int l = 0; l < nl; ++l) sum += (unsigned long long)(kSegCost + tiles(s, n, t0, b, l));
     return sum * (unsigned)(a.kv_heads / nl);
   }
 };
@@ -171,6 +181,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 // The four softmax warps of both halves, none of which can be missing here.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -265,14 +284,16 @@ struct Smem {
   static constexpr int kScratchRow = 17;  // floats: 16 columns and one of padding
   static constexpr int kOffQ = 0;
   static constexpr int kOffKv = kOffQ + kQ;
-  static constexpr int kOffScratch = kOffKv + kStagesA * kKv;
+  static constexpr int kOffV = kOffKv + Ring<D>::kKeys * kKv;
+  static constexpr int kOffScratch = kOffV + Ring<D>::kValues * kKv;
   static constexpr int kOffStats = kOffScratch + kSoftWarps * 32 * kScratchRow * 4;
   static constexpr int kOffRec = kOffStats + kSoftWarps * 32 * 8;
   static constexpr int kOffBar = kOffRec + kSlots * kSlotWords * 4;
   static constexpr int kOffMisc = kOffBar + 64 * 8;
   static constexpr int kBytes = kOffMisc + 64 + 1024;
 };
-enum BarsA { kKvFull = 0, kKvEmpty = kKvFull + kStagesA, kQFullA = kKvEmpty + kStagesA, kQEmptyA, kSFull, kPFull = kSFull + 2,
+enum BarsA { kKFullA = 0, kKEmptyA = kKFullA + kMaxStages, kVFullA = kKEmptyA + kMaxStages, kVEmptyA = kVFullA + kMaxStages,
+             kQFullA = kVEmptyA + kMaxStages, kQEmptyA, kSFull, kPFull = kSFull + 2,
              kPvDone = kPFull + 2, kOEmpty = kPvDone + 2, kMerge, kSlotFull, kSlotEmpty = kSlotFull + kSlots, kDrainA = kSlotEmpty + kSlots,
              kNumBarsA };
 static_assert(kNumBarsA <= 64, "barriers fit");
@@ -283,6 +304,7 @@ struct MiscA {
   int soft_dead;  // a softmax warp gave up
   int issued[2];  // key and value tiles whose copies were issued
   unsigned long long total;
+  uint32_t again[kRowsA / 32];  // rows to form again
 };
 
 // A warp's way through the planned tiles: all its lanes call next() for each
@@ -294,6 +316,7 @@ struct Walk {
   int32_t* status;
   uint32_t polls;
   int chunk = -1, k = 0, n = 0;
+  bool ended = false;
   const volatile uint32_t* head = nullptr;
   const volatile uint32_t* rec = nullptr;
   __device__ Walk(uint32_t* r, uint64_t* b, volatile int* f, int32_t* s, uint32_t p)
@@ -307,6 +330,10 @@ struct Walk {
       head = recs + slot * kSlotWords;
       rec = head;
       n = (int)head[kHTiles], k = 0;
+      if (n == 0) {  // the stretch's end
+        ended = true;
+        return false;
+      }
     }
     rec += kRecWords;
     ++k;
@@ -427,58 +454,58 @@ __device__ __forceinline__ bool soft_tile(uint32_t half_s, uint32_t half_o, cons
   return true;
 }
 
-// A row whose O is not finite although its scores are: some value that it
-// does not see (or whose weight is zero) is an infinity or NaN.  The warp
-// forms the row's O again, place by place, from what the row sees alone.
+// A row whose result is not finite although its scores are: some value that
+// it does not see (or whose weight is zero) is an infinity or NaN.  The warp
+// forms the row again, place by place, from what the row sees alone: o[e] for
+// element lane * D / 32 + e.
 template <typename T, int D>
 __device__ __noinline__ void row_again(const TreeArgs& a, const volatile uint32_t* head, int row, const RowState st, float m, float c,
-                                       int col0, int col1, float* dst) {
+                                       float inv, float (&o)[D / 32]) {
   const int lane = (int)lane_id();
   constexpr int kE = D / 32;
   const int t = (int)head[kHTok0] + st.token, kvh = (int)head[kHHead], r = (int)head[kHReq];
   const int h = kvh * a.group + row % a.group;
   const bool tree = a.mask != nullptr, lists = a.pages != nullptr;
   const float cs = a.scale < 0.f ? -c : c;
-  float q[kE], o[kE];
+  float q[kE];
   const T* qp = static_cast<const T*>(a.q) + (int64_t)t * a.q_ts + (int64_t)h * a.q_hs + lane * kE;
 #pragma unroll
   for (int e = 0; e < kE; ++e) q[e] = (float)qp[e], o[e] = 0.f;
   const int64_t list = (int64_t)head[kHList];
   const int lh = lists ? kvh / (a.kv_heads / a.lists) : 0;
   const int count = lists ? min(a.counts[(int64_t)head[kHTok0] * a.lists + lh], (int)head[kHTokens] * a.per) : 0;
-  for (int tile = (int)head[kHFirst]; tile < (int)head[kHEnd]; ++tile)
-    for (int col = col0; col < col1; ++col) {
-      int64_t place = (int64_t)tile * kTile + col, blk = -1;
-      uint32_t tokens = 0xFFFFFFFFu;
-      if (lists) {
-        const int64_t e = place / a.page;
-        if (e >= count) continue;
-        const ListEntry en = a.entries[list + e];
-        blk = en.block, tokens = en.tokens;
-        place = (int64_t)en.page * a.page + place % a.page;
-      } else if (place < st.len) {
-        blk = a.bt[r * a.bt_stride + place / a.page];
-      }
-      if (blk < 0 || blk >= a.num_blocks || place >= st.len) continue;
-      const int pos = (int)(place / kGroup * kGroup);
-      if (!((group_bits(pos, tokens, st, tree, lists) >> (int)(place - pos)) & 1u)) continue;
-      const int64_t at = blk * a.c_bs + place % a.page * a.c_ts + (int64_t)kvh * a.c_hs + lane * kE;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) s = fmaf(q[e], (float)static_cast<const T*>(a.kc)[at + e], s);
-#pragma unroll
-      for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-      const float p = ex2(s * cs - m * c);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const float vv = (float)static_cast<const T*>(a.vc)[at + e];
-        // a weight below the smallest number still carries an infinity's sign
-        o[e] = fmaf(p == 0.f && isinf(vv) ? 1.f : p, vv, o[e]);
-      }
+  const int64_t end = (int64_t)(int)head[kHEnd] * kTile;
+  for (int64_t at = (int64_t)(int)head[kHFirst] * kTile; at < end; ++at) {
+    int64_t place = at, blk = -1;
+    uint32_t tokens = 0xFFFFFFFFu;
+    if (lists) {
+      const int64_t e = at / a.page;
+      if (e >= count) break;
+      const ListEntry en = a.entries[list + e];
+      blk = en.block, tokens = en.tokens;
+      place = (int64_t)en.page * a.page + at % a.page;
+    } else if (place < st.len) {
+      blk = a.bt[r * a.bt_stride + place / a.page];
     }
+    if (blk < 0 || blk >= a.num_blocks || place >= st.len) continue;
+    const int pos = (int)(place / kGroup * kGroup);
+    if (!((group_bits(pos, tokens, st, tree, lists) >> (int)(place - pos)) & 1u)) continue;
+    const int64_t from = blk * a.c_bs + place % a.page * a.c_ts + (int64_t)kvh * a.c_hs + lane * kE;
+    float s = 0.f;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) dst[lane * kE + e] = o[e];
-  __syncwarp();
+    for (int e = 0; e < kE; ++e) s = fmaf(q[e], (float)static_cast<const T*>(a.kc)[from + e], s);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
+    const float p = ex2(s * cs - m * c);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const float vv = (float)static_cast<const T*>(a.vc)[from + e];
+      // a weight below the smallest number still carries an infinity's sign
+      o[e] = fmaf(p == 0.f && isinf(vv) ? 1.f : p, vv, o[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] *= inv;
 }
 
 template <typename T, int D>
@@ -504,10 +531,13 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     misc->abort_flag = 0;
     misc->soft_dead = 0;
     misc->issued[0] = misc->issued[1] = 0;
-    for (int s = 0; s < kStagesA; ++s) {
-      mbar_init(&bars[kKvFull + s], 1);
-      mbar_init(&bars[kKvEmpty + s], 1);
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&bars[kKFullA + s], 1);
+      mbar_init(&bars[kKEmptyA + s], 1);
+      mbar_init(&bars[kVFullA + s], 1);
+      mbar_init(&bars[kVEmptyA + s], 1);
     }
+    for (int s = 0; s < kRowsA / 32; ++s) misc->again[s] = 0;
     mbar_init(&bars[kQFullA], 1);
     mbar_init(&bars[kQEmptyA], 1);
     for (int s = 0; s < 2; ++s) {
@@ -539,9 +569,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   const uint32_t tmem = misc->tmem_base;
   const unsigned long long W = misc->total;
   const unsigned long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
-  const int count = (int)(w1 - w0);
 
-  if (warp == kPlanWarp && count > 0) {
+  if (warp == kPlanWarp) {
     // the request of the stretch's first unit
     unsigned long long acc = 0;
     int r = 0;
@@ -565,20 +594,23 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       acc += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
     // and its block, head and tile; all lanes hold the same cursor
-    int n = plan.ntok(r), t0 = plan.tok0(r), s = plan.seq(r), b = 0, kvh = 0;
+    const bool some = w0 < w1;
+    int n = some ? plan.ntok(r) : 0, t0 = some ? plan.tok0(r) : 0, s = some ? plan.seq(r) : 0, b = 0, kvh = 0;
     const int per_list = lists ? a.kv_heads / a.lists : a.kv_heads;
-    int tiles = plan.tiles(s, n, t0, 0, 0);
-    while (rem >= (unsigned)tiles) {
-      rem -= (unsigned)tiles;
+    int tiles = some ? plan.tiles(s, n, t0, 0, 0) : 0;
+    while (some && rem >= (unsigned)(kSegCost + tiles)) {
+      rem -= (unsigned)(kSegCost + tiles);
       if (++kvh == a.kv_heads) kvh = 0, ++b;
       tiles = plan.tiles(s, n, t0, b, kvh / per_list);
     }
-    int tile = (int)rem;
+    // the segment's units begin at u0; the stretch's part of it are the tiles from `tile` on
+    unsigned long long u0 = w0 - rem;
+    int tile = max(0, (int)rem - kSegCost);
     if (lane == 0) {
       // where this stretch begins inside a segment, the segment's units
       int32_t* cut = a.cuts + 8 * blockIdx.x;
-      const unsigned long long u0 = w0 - rem, u1 = u0 + tiles;
-      cut[0] = rem > 0 ? 1 : 0;
+      const unsigned long long u1 = u0 + kSegCost + tiles;
+      cut[0] = some && tile > 0 ? 1 : 0;
       cut[1] = t0 + b * a.block_tokens;
       cut[2] = min(a.block_tokens, n - b * a.block_tokens);
       cut[3] = kvh;
@@ -588,9 +620,12 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 
     const int bs = min(a.page, kTile), boxes = kTile / bs;  // places of a box, boxes of a tile
     const int page_tiles = max(1, a.page / kTile);
-    int i = 0, seg = 0, piece_first = tile, chunk = 0;
-    bool bad_block = false;
-    while (i < count) {
+    int seg = 0, piece_first = tile, chunk = 0;
+    bool bad_block = false, gave_up = false;
+    while (some && u0 < w1) {
+      // tiles of the segment up to the stretch's end
+      const int piece_end = (int)min((unsigned long long)tiles, w1 > u0 + kSegCost ? w1 - u0 - kSegCost : 0ull);
+      if (tile >= piece_end) break;  // the stretch ends before the segment's first tile
       const int len = plan.len(s), ctx = s - n;
       const int m = min(a.block_tokens, n - b * a.block_tokens), tok = t0 + b * a.block_tokens;
       const int rows = m * a.group;
@@ -598,12 +633,14 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       const int lh = lists ? kvh / per_list : 0;
       const int64_t list = ((int64_t)tok * a.lists + (int64_t)lh * m) * a.per;
       const int entries = lists ? min(a.counts[(int64_t)tok * a.lists + lh], m * a.per) : 0;
-      const int piece_end = min(tiles, tile + (count - i));
       const int here = min(kChunk, piece_end - tile);  // tiles of this chunk
       const int slot = chunk % kSlots;
       const bool ok =
           timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag, a.status, a.polls);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        gave_up = true;
+        break;
+      }
       uint32_t* head = recs + slot * kSlotWords;
       if (lane == 31) {
         head[kHTiles] = (uint32_t)here, head[kHTok0] = (uint32_t)tok, head[kHTokens] = (uint32_t)m, head[kHHead] = (uint32_t)kvh;
@@ -647,10 +684,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kSlotFull + slot]);
       ++chunk;
-      i += here;
       tile += here;
       if (tile == tiles) {
         // next segment
+        u0 += (unsigned)(kSegCost + tiles);
         tile = 0;
         piece_first = 0;
         ++seg;
@@ -665,38 +702,49 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             if (r < a.num_reqs) t0 = plan.tok0(r), s = plan.seq(r);
           }
         }
-        if (i < count) tiles = plan.tiles(s, n, t0, b, kvh / per_list);
+        if (u0 < w1) tiles = plan.tiles(s, n, t0, b, kvh / per_list);
+      } else if (tile == piece_end) {
+        break;
       }
     }
+    if (!gave_up) {
+      const int slot = chunk % kSlots;
+      const bool ok =
+          timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag, a.status, a.polls);
+      if (__all_sync(0xFFFFFFFFu, ok) && lane == 0) {
+        recs[slot * kSlotWords + kHTiles] = 0;  // the end
+        mbar_arrive(&bars[kSlotFull + slot]);
+      }
+      __syncwarp();
+    }
     if (bad_block) report(a.status, IDX_ST_BLOCK_OOR);
-  } else if ((warp == kKeyTma || warp == kValueTma) && count > 0) {
+  } else if (warp == kKeyTma || warp == kValueTma) {
     const bool keys = warp == kKeyTma;
     const CUtensorMap* map = keys ? &kmap : &vmap;
     const int bs = min(a.page, kTile), boxes = kTile / bs;
     const int bx = lane % boxes, sub = lane / boxes;
     const bool mine = lane < boxes * (D / 64);
-    uint8_t* dst = smem + S::kOffKv + sub * (kTile * 128) + bx * bs * 128;
+    const int stages = keys ? Ring<D>::kKeys : Ring<D>::kValues;
+    uint64_t *full = &bars[keys ? kKFullA : kVFullA], *empty = &bars[keys ? kKEmptyA : kVEmptyA];
+    uint8_t* dst = smem + (keys ? S::kOffKv : S::kOffV) + sub * (kTile * 128) + bx * bs * 128;
     Walk w(recs, bars, abort_flag, a.status, a.polls);
-    int issued = 0;
-    for (int i = 0; i < count; ++i) {
-      if (!w.next()) break;
+    int i = 0, stage = 0;
+    uint32_t phase = 0;
+    for (; w.next(); ++i) {
       const int kvh = (int)w.head[kHHead], offset = (int)w.rec[kROffset], box = (int)w.rec[kRBox + bx];
-      const int item = 2 * i + (keys ? 0 : 1), stage = item % kStagesA;
-      const bool ok =
-          timed_wait_flag(&bars[kKvEmpty + stage], ((uint32_t)(item / kStagesA) & 1u) ^ 1u, abort_flag, a.status, a.polls);
+      const bool ok = timed_wait_flag(&empty[stage], phase ^ 1u, abort_flag, a.status, a.polls);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&bars[kKvFull + stage], (uint32_t)S::kKv);
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)S::kKv);
       __syncwarp();
-      if (mine) tma_load_4d(dst + stage * S::kKv, map, sub * 64, kvh, offset, box, &bars[kKvFull + stage]);
-      issued = i + 1;
+      if (mine) tma_load_4d(dst + stage * S::kKv, map, sub * 64, kvh, offset, box, &full[stage]);
       w.done();
+      if (++stage == stages) stage = 0, phase ^= 1u;
     }
-    if (lane == 0) misc->issued[keys ? 0 : 1] = issued;
-  } else if (warp == kQueryTma && count > 0) {
+    if (lane == 0) misc->issued[keys ? 0 : 1] = i;
+  } else if (warp == kQueryTma) {
     Walk w(recs, bars, abort_flag, a.status, a.polls);
     int queries = 0;
-    for (int i = 0; i < count; ++i) {
-      if (!w.next()) break;
+    while (w.next()) {
       if (w.rec[kRFlags] & kFlagFirst) {
         bool ok = true;
         if (queries > 0) ok = timed_wait_flag(&bars[kQEmptyA], (uint32_t)(queries - 1) & 1u, abort_flag, a.status, a.polls);
@@ -715,7 +763,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       w.done();
     }
     if (lane == 0 && queries > 0) mbar_wait(&bars[kQFullA], (uint32_t)(queries - 1) & 1u, nullptr);
-  } else if (warp == kMmaWarpA && count > 0) {
+  } else if (warp == kMmaWarpA) {
     constexpr uint32_t kIdS = idesc_16(Num<T>::kBf16, kRowsA, kTile, false);
     constexpr uint32_t kIdO = idesc_16(Num<T>::kBf16, kRowsA, D, true);
     Walk w(recs, bars, abort_flag, a.status, a.polls);
@@ -723,14 +771,15 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     bool issued = false;
     uint32_t prev = 0;  // flags of the tile before
     auto wait = [&](int bar, int phase) { return spin_wait_flag(&bars[bar], (uint32_t)phase & 1u, abort_flag, a.status, a.polls); };
-    for (int i = 0; i <= count; ++i) {
+    for (int i = 0;; ++i) {
       uint32_t flags = 0;
-      if (i < count) {
-        if (!w.next()) break;
+      const bool more = w.next();
+      if (!more && !w.ended) break;
+      if (more) {
         flags = w.rec[kRFlags];
         w.done();
-        const int item = 2 * i, stage = item % kStagesA;
-        bool ok = wait(kKvFull + stage, item / kStagesA);
+        const int stage = i % Ring<D>::kKeys;
+        bool ok = wait(kKFullA + stage, i / Ring<D>::kKeys);
         if (ok && (flags & kFlagFirst)) ok = wait(kQFullA, seg_s);
         if (ok && i >= 2) ok = wait(kPvDone + (i & 1), (i >> 1) - 1);  // the weights of tile i - 2 have been read
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
@@ -745,7 +794,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           }
           // a tile's stage is given back before anybody can learn that the
           // tile is done: the ring's waits count on that order
-          mma_commit(&bars[kKvEmpty + stage]);
+          mma_commit(&bars[kKEmptyA + stage]);
           if (flags & kFlagLast) mma_commit(&bars[kQEmptyA]);
           mma_commit(&bars[kSFull + (i & 1)]);
         }
@@ -754,15 +803,15 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         issued = true;
       }
       if (i > 0) {
-        const int j = i - 1, item = 2 * j + 1, stage = item % kStagesA;
+        const int j = i - 1, stage = j % Ring<D>::kValues;
         const bool first = (prev & kFlagFirst) != 0;
-        bool ok = wait(kKvFull + stage, item / kStagesA);
+        bool ok = wait(kVFullA + stage, j / Ring<D>::kValues);
         if (ok && first && seg_o > 0) ok = wait(kOEmpty, seg_o - 1);  // the rows of the segment before have been read
         if (ok) ok = wait(kPFull + (j & 1), j >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t vd = sw128_desc_nmajor(sbase + S::kOffKv + stage * S::kKv);
+          const uint64_t vd = sw128_desc_nmajor(sbase + S::kOffV + stage * S::kKv);
           const uint32_t p = tmem + kColS + (uint32_t)(j & 1) * kTile;
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k) {
@@ -770,12 +819,13 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             mma_16_ta(tmem + kColO + (uint32_t)(half * D), p + (uint32_t)(half * kHalf + 8 * (k % (kHalf / 16))),
                       vd + (uint64_t)(k * (2048 / 16)), kIdO, k % (kHalf / 16) > 0 || !first ? 1u : 0u);
           }
-          mma_commit(&bars[kKvEmpty + stage]);
+          mma_commit(&bars[kVEmptyA + stage]);
           mma_commit(&bars[kPvDone + (j & 1)]);
         }
         __syncwarp();
         if (prev & kFlagLast) ++seg_o;
       }
+      if (!more) break;
       prev = flags;
     }
     if (issued) {
@@ -796,10 +846,9 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     RowState st{};
     int seg = 0;
     int row = 0, copy = 0, fold = 1, col0 = 0;
-    bool warp_live = true, done = count == 0;
+    bool warp_live = true, met = false;
     Walk w(recs, bars, abort_flag, a.status, a.polls);
-    for (int i = 0; i < count; ++i) {
-      if (!w.next()) break;
+    for (int i = 0; w.next(); ++i) {
       const uint32_t s_par = (uint32_t)(i >> 1) & 1u;
       const volatile uint32_t *rec = w.rec, *head = w.head;
       const uint32_t flags = rec[kRFlags];
@@ -839,10 +888,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         // values at places that do not exist may be anything: zeros in their stead
         const int pos = (int)rec[kRPos + lane_row / kGroup];
         if (pos >= 0 && pos + lane_row % kGroup >= st.len) {
-          const int item = 2 * i + 1, stage = item % kStagesA;
-          ok = timed_wait_flag(&bars[kKvFull + stage], (uint32_t)(item / kStagesA) & 1u, abort_flag, a.status, a.polls);
+          const int stage = i % Ring<D>::kValues;
+          ok = timed_wait_flag(&bars[kVFullA + stage], (uint32_t)(i / Ring<D>::kValues) & 1u, abort_flag, a.status, a.polls);
           if (ok) {
-            uint4* vrow = reinterpret_cast<uint4*>(smem + S::kOffKv + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
+            uint4* vrow = reinterpret_cast<uint4*>(smem + S::kOffV + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e) vrow[e] = make_uint4(0, 0, 0, 0);
           }
@@ -864,44 +913,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const bool live = row < rows;
-      {
-        float probe = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < D; k += 16) {
-          uint32_t o[16];
-          tmem_ld16(half_o + (uint32_t)k, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) probe = fmaf(__uint_as_float(o[e]), 0.f, probe);
-        }
-        uint32_t again = __ballot_sync(0xFFFFFFFFu, live && l > 0.f && l < INFINITY && probe != 0.f);
-        while (again) {
-          const int who = __ffs(again) - 1;
-          again &= again - 1;
-          RowState x;
-          x.tree = __shfl_sync(0xFFFFFFFFu, st.tree, who);
-          x.ctx = st.ctx, x.len = st.len;
-          x.chain_end = __shfl_sync(0xFFFFFFFFu, st.chain_end, who);
-          x.token = __shfl_sync(0xFFFFFFFFu, st.token, who);
-          float* dst = scratch + warp * 32 * S::kScratchRow;
-          const int from = __shfl_sync(0xFFFFFFFFu, col0, who);
-          row_again<T, D>(a, head, __shfl_sync(0xFFFFFFFFu, row, who), x, __shfl_sync(0xFFFFFFFFu, m, who), c, from,
-                          from + kHalf / fold, dst);
-#pragma unroll 1
-          for (int k = 0; k < D; k += 16) {
-            uint32_t o[16];
-            tmem_ld16(half_o + (uint32_t)k, o);
-            tmem_wait_ld();
-            if (lane == who)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(dst[k + e]);
-            tmem_st8(half_o + (uint32_t)k, o);
-            tmem_st8(half_o + (uint32_t)k + 8, o + 8);
-          }
-          tmem_wait_st();
-          __syncwarp();
-        }
-      }
       stats[tid] = make_float2(m, l);
       // All eight warps meet, those that gave up among them (see below); the
       // wait ends for all or for none, so that no warp misses a later barrier.
@@ -910,7 +921,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       ok = mbar_wait(&bars[kMerge], (uint32_t)seg & 1u, nullptr);
       ++seg;
       if (!__all_sync(0xFFFFFFFFu, ok) || *reinterpret_cast<volatile int*>(&misc->soft_dead)) {
-        done = true;
+        met = true;
         break;
       }
       // the row's parts: two halves of `fold` copies
@@ -922,7 +933,9 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         const float2 x = stats[part_at(p)];
         if (x.x != -INFINITY) sum_l += x.y * ex2((x.x - big) * c);
       }
-      const float factor = m == -INFINITY ? 0.f : ex2((m - big) * c);
+      // what this lane's two halves weigh in the row
+      const float m0 = stats[lane_row].x, m1 = stats[kRowsA + lane_row].x;
+      const float f0 = m0 == -INFINITY ? 0.f : ex2((m0 - big) * c), f1 = m1 == -INFINITY ? 0.f : ex2((m1 - big) * c);
       const uint32_t slot = head[kHOut];
       const int t = (int)head[kHTok0] + st.token, h = (int)head[kHHead] * a.group + row % a.group;
       const bool direct = slot == 0xFFFFFFFFu, empty = sum_l == 0.f;
@@ -936,42 +949,89 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       }
       T* out = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs;
       float* part_o = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row) * D;
-      const int width = 16 / parts;  // columns of a round that this thread joins: 8, 4 or 2
+      // Warps w and w + 4 reach the same TMEM lanes: each takes half of the
+      // columns of both halves' O.  Copies of a row lie in other lanes and
+      // meet through shared memory, 16 columns a round.
+      float probe = 0.f;
 #pragma unroll 1
-      for (int k = 0; k < D; k += 16) {
-        uint32_t o[16];
-        tmem_ld16(half_o + (uint32_t)k, o);
+      for (int k = 0; k < D / 2; k += 16) {
+        const int col = half * (D / 2) + k;
+        uint32_t x[16], y[16];
+        tmem_ld16(tmem_row + kColO + (uint32_t)col, x);
+        tmem_ld16(tmem_row + kColO + (uint32_t)(D + col), y);
         tmem_wait_ld();
+        float f[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) scratch[tid * S::kScratchRow + e] = factor == 0.f ? 0.f : __uint_as_float(o[e]) * factor;
-        soft_sync();
-        const int col = my_part * width;
-        float f[8];
+        for (int e = 0; e < 16; ++e)
+          f[e] = (f0 == 0.f ? 0.f : __uint_as_float(x[e]) * f0) + (f1 == 0.f ? 0.f : __uint_as_float(y[e]) * f1);
+        int width = 16, at = 0;  // columns of the 16 that this thread joins and writes
+        if (fold > 1) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] = 0.f;
-          if (e < width) {
-            for (int p = 0; p < parts; ++p) f[e] += scratch[part_at(p) * S::kScratchRow + col + e];
-            f[e] = empty ? 0.f : f[e] * inv;
-          }
+          for (int e = 0; e < 16; ++e) scratch[tid * S::kScratchRow + e] = f[e];
+          soft_sync();
+          width = 16 / fold, at = copy * width;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < width) {
+              f[e] = 0.f;
+              for (int p = 0; p < fold; ++p) f[e] += scratch[(half * kRowsA + p * per + row) * S::kScratchRow + at + e];
+            }
+          soft_sync();
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < width) {
+            f[e] = empty ? 0.f : f[e] * inv;
+            probe = fmaf(f[e], 0.f, probe);
+          }
         if (live) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2)
+          for (int e = 0; e < 16; e += 4)
             if (e < width) {
-              if (direct) *reinterpret_cast<uint32_t*>(out + k + col + e) = Num<T>::pack(f[e], f[e + 1]);
-              else *reinterpret_cast<float2*>(part_o + k + col + e) = make_float2(f[e], f[e + 1]);
+              if (direct)
+                *reinterpret_cast<uint2*>(out + col + at + e) = make_uint2(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]));
+              else *reinterpret_cast<float4*>(part_o + col + at + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
             }
         }
+      }
+      // rows to form again, rare: see row_again
+      if (soft_any(live && probe != 0.f && sum_l > 0.f && sum_l < INFINITY)) {
+        if (live && probe != 0.f && sum_l > 0.f && sum_l < INFINITY) atomicOr(&misc->again[row >> 5], 1u << (row & 31));
+        soft_sync();
+        for (int x = warp; x < rows; x += kSoftWarps) {
+          if (!((*reinterpret_cast<volatile uint32_t*>(&misc->again[x >> 5]) >> (x & 31)) & 1u)) continue;
+          RowState z = st;
+          z.token = x / a.group;
+          z.chain_end = st.ctx + (int)head[kHNode0] + z.token + 1;
+          const int n = (int)head[kHNew];
+          z.tree = tree ? a.mask[(int)head[kHTok0] + z.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
+          float zm = -INFINITY, zl = 0.f, o[D / 32];
+          auto part_of = [&](int p) { return (p / fold) * kRowsA + (p % fold) * per + x; };
+          for (int p = 0; p < parts; ++p) zm = fmaxf(zm, stats[part_of(p)].x);
+          for (int p = 0; p < parts; ++p) {
+            const float2 v = stats[part_of(p)];
+            if (v.x != -INFINITY) zl += v.y * ex2((v.x - zm) * c);
+          }
+          row_again<T, D>(a, head, x, z, zm, c, direct ? 1.f / zl : 1.f, o);
+          const int zt = (int)head[kHTok0] + z.token, zh = (int)head[kHHead] * a.group + x % a.group;
+          T* zo = static_cast<T*>(a.out) + (int64_t)zt * a.o_ts + (int64_t)zh * a.o_hs;
+          float* zp = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + x) * D;
+#pragma unroll
+          for (int e = 0; e < D / 32; e += 2) {
+            if (direct) *reinterpret_cast<uint32_t*>(zo + lane * (D / 32) + e) = Num<T>::pack(o[e], o[e + 1]);
+            else *reinterpret_cast<float2*>(zp + lane * (D / 32) + e) = make_float2(o[e], o[e + 1]);
+          }
+        }
+        soft_sync();
+        if (tid < kRowsA / 32) misc->again[tid] = 0;
         soft_sync();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kOEmpty]);
       w.done();
-      done = i + 1 == count;  // the last tile ends a segment or the stretch's part of it
     }
-    if (!done && lane == 0) {
+    if (!w.ended && !met && lane == 0) {
       // gave up: say so, then take this warp's place at the barrier that the others may wait at
       *reinterpret_cast<volatile int*>(&misc->soft_dead) = 1;
       mbar_arrive(&bars[kMerge]);
@@ -979,7 +1039,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   }
 
   if (tid == 0) {
-    if (count == 0) a.cuts[8 * blockIdx.x] = 0;
     if (blockIdx.x == 0) *reinterpret_cast<unsigned long long*>(a.cuts + 8 * kMaxCtas) = W;
   }
   // lengths that the table does not hold
@@ -989,13 +1048,11 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   __syncwarp();
   __syncthreads();
   if (*abort_flag) {
-    if (tid < kStagesA) {
-      // never leave with a copy in flight: the last one into each stage
-      int last = -1;
-      for (int k = 0; k < 2; ++k)
-        for (int i = max(0, misc->issued[k] - kStagesA); i < misc->issued[k]; ++i)
-          if ((2 * i + k) % kStagesA == tid) last = max(last, 2 * i + k);
-      if (last >= 0) mbar_wait(&bars[kKvFull + tid], (uint32_t)(last / kStagesA) & 1u, nullptr);
+    if (tid < 2) {
+      // never leave with a copy in flight: the last ones of each ring
+      const int stages = tid == 0 ? Ring<D>::kKeys : Ring<D>::kValues;
+      for (int i = max(0, misc->issued[tid] - stages); i < misc->issued[tid]; ++i)
+        mbar_wait(&bars[(tid == 0 ? kKFullA : kVFullA) + i % stages], (uint32_t)(i / stages) & 1u, nullptr);
     }
     __syncwarp();
     __syncthreads();
@@ -1024,7 +1081,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_tree_combine(const __grid_c
   auto start = [&](int y) { return W * (u64)y / (u64)ctas; };
   auto cta_of = [&](u64 u) { return (int)(((u + 1) * (u64)ctas - 1) / W); };
   const int from = cta_of(start(x) - 1), to = cta_of(u1 - 1);
-  if (start(from) > u0) return;  // an earlier block joins this segment
+  if (start(from) > u0 + kSegCost) return;  // an earlier block joins this segment
   const int row = blockIdx.y * kJoinWarps + warp, rows = cut[2] * a.group;
   if (row >= rows) return;
   // slot 2y, but 2y + 1 where the segment is not its stretch's first
