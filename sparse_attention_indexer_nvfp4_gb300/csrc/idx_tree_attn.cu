@@ -64,7 +64,7 @@ struct Ring {
   static constexpr int kKeys = D == 128 ? 3 : 5, kValues = D == 128 ? 2 : 5;
 };
 constexpr int kMaxStages = 5;
-constexpr int kSegCost = 1;         // units of a segment's begin and end
+constexpr int kSegCost = 4;         // units of a segment's begin and end
 constexpr int kSoftWarps = 8;
 constexpr int kPlanWarp = 8, kKeyTma = 9, kValueTma = 10, kQueryTma = 11, kMmaWarpA = 12;
 constexpr int kThreadsA = 13 * 32;
@@ -83,6 +83,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // column), and the two halves' O.
 constexpr uint32_t kColS = 0, kColO = 256, kTmemColsA = 512;
 
+// A segment that several stretches share, noted by the one that cuts it first:
+// its rows (0: none), first token, KV head, the stretches' first and last, the
+// first one's partial slot, and whether some stretch between may be empty.
+enum CutWord { kCRows, kCTok0, kCHead, kCFrom, kCTo, kCSlot, kCHoles };
 // A chunk's header, and a tile's record.
 enum HeadWord { kHTiles, kHTok0, kHTokens, kHHead, kHCtx, kHNew, kHNode0, kHLen, kHOut, kHReq, kHFirst, kHEnd, kHList, kHFold };
 enum RecWord { kRFlags, kROffset, kRPos = 8, kRMask = 16, kRBox = 24 };
@@ -116,7 +120,7 @@ struct TreeArgs {
   float* lse;
   int32_t* status;
   // workspace
-  int32_t* cuts;       // [kMaxCtas][8]: the segment that each CTA's stretch begins inside
+  int32_t* cuts;       // [kMaxCtas][8]: the segment to join that was cut first at each stretch's begin (see CutWord)
   float* part_ml;      // [2 * kMaxCtas][128][2]
   float* part_o;       // [2 * kMaxCtas][128][D]
   int32_t* counts;     // [num_tokens * lists], at a block's first token
@@ -607,15 +611,22 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     unsigned long long u0 = w0 - rem;
     int tile = max(0, (int)rem - kSegCost);
     if (lane == 0) {
-      // where this stretch begins inside a segment, the segment's units
       int32_t* cut = a.cuts + 8 * blockIdx.x;
-      const unsigned long long u1 = u0 + kSegCost + tiles;
-      cut[0] = some && tile > 0 ? 1 : 0;
-      cut[1] = t0 + b * a.block_tokens;
-      cut[2] = min(a.block_tokens, n - b * a.block_tokens);
-      cut[3] = kvh;
-      reinterpret_cast<unsigned long long*>(cut)[2] = u0;
-      reinterpret_cast<unsigned long long*>(cut)[3] = u1;
+      int rows = 0;
+      if (some && tile > 0) {
+        // stretch y begins at unit W y / ctas and holds unit u for y = ((u + 1) ctas - 1) / W
+        const unsigned long long ctas = gridDim.x, u1 = u0 + kSegCost + tiles;
+        const int from = (int)((w0 * ctas - 1) / W), to = (int)((u1 * ctas - 1) / W);
+        const unsigned long long begin = W * from / ctas;
+        if (begin <= u0 + kSegCost) {  // else the segment was cut before
+          rows = min(a.block_tokens, n - b * a.block_tokens) * a.group;
+          cut[kCTok0] = t0 + b * a.block_tokens, cut[kCHead] = kvh, cut[kCFrom] = from, cut[kCTo] = to;
+          // slot 2y, but 2y + 1 where the segment is not its stretch's first
+          cut[kCSlot] = 2 * from + (u0 > begin ? 1 : 0);
+          cut[kCHoles] = W < ctas ? 1 : 0;
+        }
+      }
+      cut[kCRows] = rows;
     }
 
     const int bs = min(a.page, kTile), boxes = kTile / bs;  // places of a box, boxes of a tile
@@ -1038,9 +1049,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     }
   }
 
-  if (tid == 0) {
-    if (blockIdx.x == 0) *reinterpret_cast<unsigned long long*>(a.cuts + 8 * kMaxCtas) = W;
-  }
+  if (tid == 0 && blockIdx.x == 0) *reinterpret_cast<unsigned long long*>(a.cuts + 8 * kMaxCtas) = W;
   // lengths that the table does not hold
   if (blockIdx.x == 0)
     for (int r = tid; r < a.num_reqs; r += kThreadsA)
@@ -1063,58 +1072,64 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   }
 }
 
-// Joins the partial rows of the segments that the stretches cut.  Block x
-// acts where stretch x + 1 begins inside a segment that the stretch before it
-// began; a warp joins a row: the largest reference maximum, then the weighted
-// sums.
+// Joins the partial rows of the segments that the stretches share: block
+// (x, y) those that stretch x + 1 cut first, a warp a row: the largest
+// reference maximum, then the weighted sums.
 constexpr int kJoinWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_tree_combine(const __grid_constant__ TreeArgs a, int ctas) {
   pdl_enter();
   __shared__ float weight[kJoinWarps][kMaxCtas];
-  using u64 = unsigned long long;
-  const int x = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t* cut = a.cuts + 8 * x;
-  if (cut[0] == 0) return;
-  const u64 W = *reinterpret_cast<const u64*>(a.cuts + 8 * kMaxCtas);
-  const u64 u0 = reinterpret_cast<const u64*>(cut)[2], u1 = reinterpret_cast<const u64*>(cut)[3];
-  auto start = [&](int y) { return W * (u64)y / (u64)ctas; };
-  auto cta_of = [&](u64 u) { return (int)(((u + 1) * (u64)ctas - 1) / W); };
-  const int from = cta_of(start(x) - 1), to = cta_of(u1 - 1);
-  if (start(from) > u0 + kSegCost) return;  // an earlier block joins this segment
-  const int row = blockIdx.y * kJoinWarps + warp, rows = cut[2] * a.group;
-  if (row >= rows) return;
-  // slot 2y, but 2y + 1 where the segment is not its stretch's first
-  const int first_slot = 2 * from + (u0 > start(from) ? 1 : 0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 c0 = *reinterpret_cast<const int4*>(a.cuts + 8 * (blockIdx.x + 1));
+  const int4 c1 = *reinterpret_cast<const int4*>(a.cuts + 8 * (blockIdx.x + 1) + 4);
+  const int row = blockIdx.y * kJoinWarps + warp;
+  if (row >= c0.x) return;
+  const int from = c0.w, to = c1.x, first_slot = c1.y;
+  const bool holes = c1.z != 0;
+  const unsigned long long W = holes ? *reinterpret_cast<const unsigned long long*>(a.cuts + 8 * kMaxCtas) : 0ull;
+  auto there = [&](int y) {  // stretch y has units
+    return !holes || W * (unsigned)y / (unsigned)ctas < W * (unsigned)(y + 1) / (unsigned)ctas;
+  };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  constexpr int kMost = (kMaxCtas + 31) / 32;
+  float2 part[kMost];
   float big = -INFINITY;
-  for (int y = from + lane; y <= to; y += 32)
-    if (start(y) < start(y + 1)) big = fmaxf(big, ml[(int64_t)(y == from ? first_slot : 2 * y) * kRowsA + row].x);
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int y = from + 32 * k + lane;
+    part[k] = y <= to && there(y) ? ml[(int64_t)(y == from ? first_slot : 2 * y) * kRowsA + row] : make_float2(-INFINITY, 0.f);
+    big = fmaxf(big, part[k].x);
+  }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
   float sum = 0.f;
-  for (int y = from + lane; y <= to; y += 32) {
-    float w = 0.f;
-    if (start(y) < start(y + 1)) {
-      const float2 p = ml[(int64_t)(y == from ? first_slot : 2 * y) * kRowsA + row];
-      if (p.x != -INFINITY) w = ex2(p.x - big), sum += w * p.y;
-    }
-    weight[warp][y - from] = w;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const float w = part[k].x != -INFINITY ? ex2(part[k].x - big) : 0.f;
+    sum += w * part[k].y;
+    if (from + 32 * k + lane <= to) weight[warp][32 * k + lane] = w;
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   __syncwarp();
   constexpr int kE = D / 32;
   float acc[kE] = {};
-#pragma unroll 4
-  for (int y = from; y <= to; ++y) {
-    const float w = weight[warp][y - from];
-    if (w == 0.f) continue;
-    const float* o = a.part_o + ((int64_t)(y == from ? first_slot : 2 * y) * kRowsA + row) * D + lane * kE;
+  for (int y = from; y <= to; y += 4) {
+    float w[4], o[4][kE];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+    for (int k = 0; k < 4; ++k) {
+      w[k] = y + k <= to ? weight[warp][y + k - from] : 0.f;
+      const float* src = a.part_o + ((int64_t)(y + k == from ? first_slot : 2 * (y + k)) * kRowsA + row) * D + lane * kE;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[k][e] = w[k] != 0.f ? src[e] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] = fmaf(w[k], o[k][e], acc[e]);
   }
-  const int t = cut[1] + row / a.group, h = cut[3] * a.group + row % a.group;
+  const int t = c0.y + row / a.group, h = c0.z * a.group + row % a.group;
   const bool empty = sum == 0.f;
   const float inv = empty ? 0.f : 1.f / sum;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs + lane * kE);
@@ -1123,66 +1138,66 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_tree_combine(const __grid_c
   if (lane == 0 && a.lse != nullptr) a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big + log2f(sum)) * 0.6931471805599453f;
 }
 
-// The union of a block's page lists.  One CTA per (token, list) looks whether
-// the token begins a block, gathers the lists of the block's tokens, and keeps
-// of each page its first appearance with the tokens that list it.
+// The union of a block's page lists: of each page its first appearance, with
+// the tokens that list it.  A CTA takes the blocks of a request (every
+// gridDim.z-th) and a list; a thread compares its entries with all of the
+// block's, four at a time from shared memory.
 constexpr int kUnionThreads = 128;
 __global__ void __launch_bounds__(kUnionThreads) k_list_pages(const __grid_constant__ TreeArgs a) {
   pdl_enter();
-  __shared__ int page_s[kMaxListTokens * 64];
-  __shared__ int kept, warp_kept[kUnionThreads / 32];
-  const int t = blockIdx.x, lh = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  __shared__ __align__(16) int page_s[kMaxListTokens * 64];
+  __shared__ int warp_kept[2][kUnionThreads / 32];
+  const int r = blockIdx.x, lh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Plan plan(a);
-  // the request: the last one whose tokens begin at or before t (a probe of 32 places a step)
-  int lo = 0, hi = a.num_reqs;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + lane * step;
-    const uint32_t ok = __ballot_sync(0xFFFFFFFFu, at < hi && plan.tok0(at) <= t);
-    const int k = 31 - __clz(ok | 1u);
-    const int nlo = lo + k * step;
-    hi = min(hi, nlo + step);
-    lo = nlo;
-  }
-  const int r = lo, t0 = plan.tok0(r), n = plan.ntok(r), node = t - t0;
-  if (node < 0 || node >= n || node % a.block_tokens != 0) return;
-  const int m = min(a.block_tokens, n - node), total = m * a.per;
-  const int len = plan.len(plan.seq(r)), used = (int)(((int64_t)len + a.page - 1) / a.page);
-  for (int e = tid; e < total; e += kUnionThreads) {
-    const int p = a.pages[((int64_t)(t + e / a.per) * a.lists + lh) * a.per + e % a.per];
-    page_s[e] = p >= 0 && p < used ? p : -1;
-  }
-  if (tid == 0) kept = 0;
-  __syncthreads();
-  ListEntry* out = a.entries + ((int64_t)t * a.lists + (int64_t)lh * m) * a.per;
+  const int t0 = plan.tok0(r), n = plan.ntok(r), s = plan.seq(r);
+  const int len = plan.len(s), used = (int)(((int64_t)len + a.page - 1) / a.page);
+  const int per4 = (a.per + 3) / 4 * 4;  // entries a token in shared memory
   bool bad = false;
-  for (int base = 0; base < total; base += kUnionThreads) {
-    const int e = base + tid;
-    const int p = e < total ? page_s[e] : -1;
-    uint32_t tokens = 0;
-    bool take = p >= 0;
-    int blk = -1;
-    if (take) {
-      blk = a.bt[r * a.bt_stride + p];
-      for (int f = 0; f < total; ++f)
-        if (page_s[f] == p) {
-          if (f < e) take = false;
-          tokens |= 1u << (f / a.per);
-        }
-      if (blk < 0 || blk >= a.num_blocks) bad = true, take = false;
+  for (int node = blockIdx.z * a.block_tokens; node < n; node += gridDim.z * a.block_tokens) {
+    const int m = min(a.block_tokens, n - node), t = t0 + node, total = m * per4;
+    for (int e = tid; e < total; e += kUnionThreads) {
+      const int tk = e / per4, j = e - tk * per4;
+      const int p = j < a.per ? a.pages[((int64_t)(t + tk) * a.lists + lh) * a.per + j] : -1;
+      page_s[e] = p >= 0 && p < used ? p : -1;
     }
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, take);
-    if (lane == 0) warp_kept[tid >> 5] = __popc(b);
     __syncthreads();
-    int at = kept;
-    for (int w = 0; w < tid >> 5; ++w) at += warp_kept[w];
-    if (take) out[at + __popc(b & ((1u << lane) - 1u))] = ListEntry{blk, p, tokens, 0};
-    __syncthreads();
-    if (tid == 0)
-      for (int w = 0; w < kUnionThreads / 32; ++w) kept += warp_kept[w];
-    __syncthreads();
+    ListEntry* out = a.entries + ((int64_t)t * a.lists + (int64_t)lh * m) * a.per;
+    int kept = 0;
+    for (int base = 0, round = 0; base < total; base += kUnionThreads, ++round) {
+      const int e = base + tid;
+      const int p = e < total ? page_s[e] : -1;
+      const int blk = p >= 0 ? a.bt[r * a.bt_stride + p] : -1;
+      uint32_t tokens = 0;
+      int first = total;
+      for (int tk = m - 1; tk >= 0; --tk) {
+        const int4* row = reinterpret_cast<const int4*>(page_s + tk * per4);
+        uint32_t hit = 0;
+        for (int j = 0; j < per4 / 4; ++j) {
+          const int4 x = row[j];
+          const int k = x.x == p ? 0 : x.y == p ? 1 : x.z == p ? 2 : x.w == p ? 3 : -1;
+          if (k >= 0) {
+            if (!hit) first = tk * per4 + 4 * j + k;
+            hit = 1;
+          }
+        }
+        tokens |= hit << tk;
+      }
+      bool take = p >= 0 && first == e;
+      if (p >= 0 && (blk < 0 || blk >= a.num_blocks)) bad = true, take = false;
+      const uint32_t b = __ballot_sync(0xFFFFFFFFu, take);
+      if (lane == 0) warp_kept[round & 1][warp] = __popc(b);
+      __syncthreads();
+      int at = kept;
+#pragma unroll
+      for (int w = 0; w < kUnionThreads / 32; ++w) {
+        if (w < warp) at += warp_kept[round & 1][w];
+        kept += warp_kept[round & 1][w];
+      }
+      if (take) out[at + __popc(b & ((1u << lane) - 1u))] = ListEntry{blk, p, tokens, 0};
+    }
+    if (tid == 0) a.counts[(int64_t)t * a.lists + lh] = kept;
+    __syncthreads();  // page_s is used up
   }
-  if (tid == 0) a.counts[(int64_t)t * a.lists + lh] = kept;
   if (bad) report(a.status, IDX_ST_BLOCK_OOR);
 }
 
@@ -1235,7 +1250,9 @@ int launch_tree(const TreeArgs& a, cudaStream_t s) {
       return IDX_E_BAD_SHAPE;
   }
   if (a.pages != nullptr) {
-    launch_pdl(k_list_pages, dim3((unsigned)a.num_tokens, (unsigned)a.lists), dim3(kUnionThreads), 0, s, a);
+    const int64_t blocks = ((int64_t)a.num_tokens + a.block_tokens - 1) / a.block_tokens;
+    const unsigned z = (unsigned)std::max<int64_t>(1, std::min<int64_t>(64, blocks / a.num_reqs));  // CTAs a request and list
+    launch_pdl(k_list_pages, dim3((unsigned)a.num_reqs, (unsigned)a.lists, z), dim3(kUnionThreads), 0, s, a);
     if (const int rc = launch_result()) return rc;
   }
   launch_pdl(k_tree_attention<T, D>, dim3(ctas), dim3(kThreadsA), Smem<D>::kBytes, s, qmap, kmap, vmap, a);
