@@ -78,6 +78,7 @@ constexpr int kGroup = 16;          // places of a record's group
 constexpr int kMaxListTokens = 32;  // tokens of a block with page lists (bits of a mask)
 constexpr float kRescale = 8.f;     // powers of two that a weight may exceed 1 before O is rescaled
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kScratchRow = 17;     // floats: 16 columns and one of padding
 
 // TMEM columns: two score tiles, whose halves the weights overwrite (two to a
 // column), and the two halves' O.
@@ -185,6 +186,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 // The four softmax warps of both halves, none of which can be missing here.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The four softmax warps of one half.
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(2 + half) : "memory"); }
 __device__ __forceinline__ bool soft_any(bool x) {
   uint32_t r;
   asm volatile(
@@ -285,7 +288,6 @@ struct Num<__half> {
 template <int D>
 struct Smem {
   static constexpr int kQ = kRowsA * D * 2, kKv = kTile * D * 2;
-  static constexpr int kScratchRow = 17;  // floats: 16 columns and one of padding
   static constexpr int kOffQ = 0;
   static constexpr int kOffKv = kOffQ + kQ;
   static constexpr int kOffV = kOffKv + Ring<D>::kKeys * kKv;
@@ -294,7 +296,7 @@ struct Smem {
   static constexpr int kOffRec = kOffStats + kSoftWarps * 32 * 8;
   static constexpr int kOffBar = kOffRec + kSlots * kSlotWords * 4;
   static constexpr int kOffMisc = kOffBar + 64 * 8;
-  static constexpr int kBytes = kOffMisc + 64 + 1024;
+  static constexpr int kBytes = kOffMisc + 64 + 4 * 384 + 1024;
 };
 enum BarsA { kKFullA = 0, kKEmptyA = kKFullA + kMaxStages, kVFullA = kKEmptyA + kMaxStages, kVEmptyA = kVFullA + kMaxStages,
              kQFullA = kVEmptyA + kMaxStages, kQEmptyA, kSFull, kPFull = kSFull + 2,
@@ -302,6 +304,7 @@ enum BarsA { kKFullA = 0, kKEmptyA = kKFullA + kMaxStages, kVFullA = kKEmptyA + 
              kNumBarsA };
 static_assert(kNumBarsA <= 64, "barriers fit");
 
+constexpr int kKeptUnits = 384;
 struct MiscA {
   uint32_t tmem_base;
   int abort_flag;
@@ -309,6 +312,7 @@ struct MiscA {
   int issued[2];  // key and value tiles whose copies were issued
   unsigned long long total;
   uint32_t again[kRowsA / 32];  // rows to form again
+  uint32_t units[kKeptUnits];   // of the first requests
 };
 
 // A warp's way through the planned tiles: all its lanes call next() for each
@@ -458,6 +462,70 @@ __device__ __forceinline__ bool soft_tile(uint32_t half_s, uint32_t half_o, cons
   return true;
 }
 
+// The rows of a segment whose row stands F times: this warp's half of the
+// columns of both halves' O, weighed by g0 and g1, summed over the copies and
+// written, 16 columns a round.  Warps w and w + 4 reach the same TMEM lanes, so
+// the halves join in registers; copies lie in other lanes and join through
+// shared memory, which also turns the rows so that four lanes write one row's
+// columns (row by row a thread would write pieces of 32 rows at a time: 4 us a
+// segment against 1).  Sets `again` for rows with a value that is not finite.
+template <typename T, int D, int F>
+__device__ __forceinline__ bool write_rows(const TreeArgs& a, uint32_t tmem_o, float* scratch, uint32_t* again, int half, float g0,
+                                           float g1, int rows, int tok0, int kvh, uint32_t slot) {
+  constexpr int kPer = kRowsA / F, kItems = 4 / F;  // rows, items (a row's four columns) of a thread
+  const int tid = threadIdx.x, lane = tid & 31, in_half = tid & (kRowsA - 1);
+  const bool direct = slot == 0xFFFFFFFFu;
+  float* own = scratch + tid * kScratchRow;
+  const float* base = scratch + half * kRowsA * kScratchRow;
+  T* out[kItems];
+  float* part[kItems];
+  int row[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    row[i] = F == 1 ? (in_half & ~31) + 8 * i + (lane >> 2) : 32 * i + (in_half >> 2);
+    const int t = tok0 + row[i] / a.group, h = kvh * a.group + row[i] % a.group;
+    const int col = half * (D / 2) + 4 * (lane & 3);
+    out[i] = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs + col;
+    part[i] = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row[i]) * D + col;
+  }
+  bool odd = false;
+#pragma unroll 1
+  for (int k = 0; k < D / 2; k += 16) {
+    const uint32_t col = tmem_o + (uint32_t)(half * (D / 2) + k);
+    uint32_t x[16], y[16];
+    tmem_ld16(col, x);
+    tmem_ld16(col + D, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      own[e] = (g0 == 0.f ? 0.f : __uint_as_float(x[e]) * g0) + (g1 == 0.f ? 0.f : __uint_as_float(y[e]) * g1);
+    if (F == 1) __syncwarp();
+    else half_sync(half);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const float* src = base + row[i] * kScratchRow + 4 * (lane & 3);
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = src[e];
+#pragma unroll
+        for (int c = 1; c < F; ++c) f[e] += src[c * kPer * kScratchRow + e];
+      }
+      if (row[i] < rows) {
+        if (!(fabsf(f[0]) + fabsf(f[1]) + fabsf(f[2]) + fabsf(f[3]) < INFINITY)) {
+          atomicOr(&again[row[i] >> 5], 1u << (row[i] & 31));
+          odd = true;
+        }
+        if (direct) *reinterpret_cast<uint2*>(out[i] + k) = make_uint2(Num<T>::pack(f[0], f[1]), Num<T>::pack(f[2], f[3]));
+        else *reinterpret_cast<float4*>(part[i] + k) = make_float4(f[0], f[1], f[2], f[3]);
+      }
+    }
+    if (F == 1) __syncwarp();
+    else half_sync(half);
+  }
+  return odd;
+}
+
 // A row whose result is not finite although its scores are: some value that
 // it does not see (or whose weight is zero) is an infinity or NaN.  The warp
 // forms the row again, place by place, from what the row sees alone: o[e] for
@@ -561,7 +629,11 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   __syncthreads();
   {
     unsigned long long local = 0;
-    for (int r = tid; r < a.num_reqs; r += kThreadsA) local += plan.units(r);
+    for (int r = tid; r < a.num_reqs; r += kThreadsA) {
+      const unsigned long long u = plan.units(r);
+      if (r < kKeptUnits) misc->units[r] = (uint32_t)min(u, 0xFFFFFFFFull);
+      local += u;
+    }
     local = warp_sum_u64(local);
     if (lane == 0 && local) atomicAdd(&misc->total, local);
   }
@@ -572,7 +644,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
   const unsigned long long W = misc->total;
-  const unsigned long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
+  // (64-bit divisions take some hundred cycles each)
+  const bool small = W < (1u << 23);
+  const unsigned long long w0 = small ? (uint32_t)W * blockIdx.x / gridDim.x : W * blockIdx.x / gridDim.x;
+  const unsigned long long w1 = small ? (uint32_t)W * (blockIdx.x + 1) / gridDim.x : W * (blockIdx.x + 1) / gridDim.x;
 
   if (warp == kPlanWarp) {
     // the request of the stretch's first unit
@@ -580,7 +655,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     int r = 0;
     unsigned long long rem = 0;
     for (int base = 0; base < a.num_reqs; base += 32) {
-      const unsigned long long n = base + lane < a.num_reqs ? plan.units(base + lane) : 0ull;
+      unsigned long long n = base + lane >= a.num_reqs ? 0ull : base + lane < kKeptUnits ? misc->units[base + lane] : plan.units(base + lane);
+      if (n == 0xFFFFFFFFull) n = plan.units(base + lane);
       unsigned long long incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -610,27 +686,12 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     // the segment's units begin at u0; the stretch's part of it are the tiles from `tile` on
     unsigned long long u0 = w0 - rem;
     int tile = max(0, (int)rem - kSegCost);
-    if (lane == 0) {
-      int32_t* cut = a.cuts + 8 * blockIdx.x;
-      int rows = 0;
-      if (some && tile > 0) {
-        // stretch y begins at unit W y / ctas and holds unit u for y = ((u + 1) ctas - 1) / W
-        const unsigned long long ctas = gridDim.x, u1 = u0 + kSegCost + tiles;
-        const int from = (int)((w0 * ctas - 1) / W), to = (int)((u1 * ctas - 1) / W);
-        const unsigned long long begin = W * from / ctas;
-        if (begin <= u0 + kSegCost) {  // else the segment was cut before
-          rows = min(a.block_tokens, n - b * a.block_tokens) * a.group;
-          cut[kCTok0] = t0 + b * a.block_tokens, cut[kCHead] = kvh, cut[kCFrom] = from, cut[kCTo] = to;
-          // slot 2y, but 2y + 1 where the segment is not its stretch's first
-          cut[kCSlot] = 2 * from + (u0 > begin ? 1 : 0);
-          cut[kCHoles] = W < ctas ? 1 : 0;
-        }
-      }
-      cut[kCRows] = rows;
-    }
-
     const int bs = min(a.page, kTile), boxes = kTile / bs;  // places of a box, boxes of a tile
     const int page_tiles = max(1, a.page / kTile);
+    // the segment that the stretch begins in, for its note below
+    const int tile0 = tile, tiles0 = tiles, rows0 = min(a.block_tokens, n - b * a.block_tokens) * a.group, kvh0 = kvh;
+    const int tok00 = t0 + b * a.block_tokens;
+    const unsigned long long u00 = u0;
     int seg = 0, piece_first = tile, chunk = 0;
     bool bad_block = false, gave_up = false;
     while (some && u0 < w1) {
@@ -727,6 +788,24 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         mbar_arrive(&bars[kSlotFull + slot]);
       }
       __syncwarp();
+    }
+    if (lane == 0) {
+      int32_t* cut = a.cuts + 8 * blockIdx.x;
+      int rows = 0;
+      if (some && tile0 > 0) {
+        // stretch y begins at unit W y / ctas and holds unit u for y = ((u + 1) ctas - 1) / W
+        const unsigned long long ctas = gridDim.x, u1 = u00 + kSegCost + tiles0;
+        const int from = (int)((w0 * ctas - 1) / W), to = (int)((u1 * ctas - 1) / W);
+        const unsigned long long begin = W * from / ctas;
+        if (begin <= u00 + kSegCost) {  // else the segment was cut before
+          rows = rows0;
+          cut[kCTok0] = tok00, cut[kCHead] = kvh0, cut[kCFrom] = from, cut[kCTo] = to;
+          // slot 2y, but 2y + 1 where the segment is not its stretch's first
+          cut[kCSlot] = 2 * from + (u00 > begin ? 1 : 0);
+          cut[kCHoles] = W < ctas ? 1 : 0;
+        }
+      }
+      cut[kCRows] = rows;
     }
     if (bad_block) report(a.status, IDX_ST_BLOCK_OOR);
   } else if (warp == kKeyTma || warp == kValueTma) {
@@ -923,7 +1002,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       ok = timed_wait_flag(&bars[kPvDone + (i & 1)], s_par, abort_flag, a.status, a.polls);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
-      const bool live = row < rows;
       stats[tid] = make_float2(m, l);
       // All eight warps meet, those that gave up among them (see below); the
       // wait ends for all or for none, so that no warp misses a later barrier.
@@ -936,79 +1014,34 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         break;
       }
       // the row's parts: two halves of `fold` copies
-      const int parts = 2 * fold, my_part = half * fold + copy, per = kRowsA / fold;
-      auto part_at = [&](int p) { return (p / fold) * kRowsA + (p % fold) * per + row; };
+      const int parts = 2 * fold, per = kRowsA / fold;
+      auto part_at = [&](int p, int x) { return (p >= fold ? kRowsA + (p - fold) * per : p * per) + x; };
       float big = -INFINITY, sum_l = 0.f;
-      for (int p = 0; p < parts; ++p) big = fmaxf(big, stats[part_at(p)].x);
+#pragma unroll 1
+      for (int p = 0; p < parts; ++p) big = fmaxf(big, stats[part_at(p, row)].x);
+#pragma unroll 1
       for (int p = 0; p < parts; ++p) {
-        const float2 x = stats[part_at(p)];
+        const float2 x = stats[part_at(p, row)];
         if (x.x != -INFINITY) sum_l += x.y * ex2((x.x - big) * c);
       }
-      // what this lane's two halves weigh in the row
-      const float m0 = stats[lane_row].x, m1 = stats[kRowsA + lane_row].x;
-      const float f0 = m0 == -INFINITY ? 0.f : ex2((m0 - big) * c), f1 = m1 == -INFINITY ? 0.f : ex2((m1 - big) * c);
       const uint32_t slot = head[kHOut];
-      const int t = (int)head[kHTok0] + st.token, h = (int)head[kHHead] * a.group + row % a.group;
       const bool direct = slot == 0xFFFFFFFFu, empty = sum_l == 0.f;
-      const float inv = empty ? 0.f : direct ? 1.f / sum_l : 1.f;
-      if (live && my_part == 0) {
-        if (direct) {
-          if (a.lse != nullptr) a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + log2f(sum_l)) * 0.6931471805599453f;
-        } else {
-          reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : big * c, sum_l);
-        }
+      // what this lane's two halves weigh in the row
+      const float inv = empty ? 0.f : direct ? 1.f / sum_l : 1.f, m0 = stats[lane_row].x, m1 = stats[kRowsA + lane_row].x;
+      const float g0 = m0 == -INFINITY ? 0.f : ex2((m0 - big) * c) * inv, g1 = m1 == -INFINITY ? 0.f : ex2((m1 - big) * c) * inv;
+      const int tok0 = (int)head[kHTok0], kvh = (int)head[kHHead];
+      if (row < rows && half == 0 && copy == 0) {
+        const int t = tok0 + row / a.group, h = kvh * a.group + row % a.group;
+        if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : big * c, sum_l);
+        else if (a.lse != nullptr)
+          a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + __log2f(sum_l)) * 0.6931471805599453f;
       }
-      T* out = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs;
-      float* part_o = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row) * D;
-      // Warps w and w + 4 reach the same TMEM lanes: each takes half of the
-      // columns of both halves' O.  Copies of a row lie in other lanes and
-      // meet through shared memory, 16 columns a round.
-      float probe = 0.f;
-#pragma unroll 1
-      for (int k = 0; k < D / 2; k += 16) {
-        const int col = half * (D / 2) + k;
-        uint32_t x[16], y[16];
-        tmem_ld16(tmem_row + kColO + (uint32_t)col, x);
-        tmem_ld16(tmem_row + kColO + (uint32_t)(D + col), y);
-        tmem_wait_ld();
-        float f[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          f[e] = (f0 == 0.f ? 0.f : __uint_as_float(x[e]) * f0) + (f1 == 0.f ? 0.f : __uint_as_float(y[e]) * f1);
-        int width = 16, at = 0;  // columns of the 16 that this thread joins and writes
-        if (fold > 1) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) scratch[tid * S::kScratchRow + e] = f[e];
-          soft_sync();
-          width = 16 / fold, at = copy * width;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < width) {
-              f[e] = 0.f;
-              for (int p = 0; p < fold; ++p) f[e] += scratch[(half * kRowsA + p * per + row) * S::kScratchRow + at + e];
-            }
-          soft_sync();
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (e < width) {
-            f[e] = empty ? 0.f : f[e] * inv;
-            probe = fmaf(f[e], 0.f, probe);
-          }
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            if (e < width) {
-              if (direct)
-                *reinterpret_cast<uint2*>(out + col + at + e) = make_uint2(Num<T>::pack(f[e], f[e + 1]), Num<T>::pack(f[e + 2], f[e + 3]));
-              else *reinterpret_cast<float4*>(part_o + col + at + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-            }
-        }
-      }
+      bool odd;
+      if (fold == 4) odd = write_rows<T, D, 4>(a, tmem_row + kColO, scratch, misc->again, half, g0, g1, rows, tok0, kvh, slot);
+      else if (fold == 2) odd = write_rows<T, D, 2>(a, tmem_row + kColO, scratch, misc->again, half, g0, g1, rows, tok0, kvh, slot);
+      else odd = write_rows<T, D, 1>(a, tmem_row + kColO, scratch, misc->again, half, g0, g1, rows, tok0, kvh, slot);
       // rows to form again, rare: see row_again
-      if (soft_any(live && probe != 0.f && sum_l > 0.f && sum_l < INFINITY)) {
-        if (live && probe != 0.f && sum_l > 0.f && sum_l < INFINITY) atomicOr(&misc->again[row >> 5], 1u << (row & 31));
-        soft_sync();
+      if (soft_any(odd)) {
         for (int x = warp; x < rows; x += kSoftWarps) {
           if (!((*reinterpret_cast<volatile uint32_t*>(&misc->again[x >> 5]) >> (x & 31)) & 1u)) continue;
           RowState z = st;
@@ -1017,14 +1050,14 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           const int n = (int)head[kHNew];
           z.tree = tree ? a.mask[(int)head[kHTok0] + z.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
           float zm = -INFINITY, zl = 0.f, o[D / 32];
-          auto part_of = [&](int p) { return (p / fold) * kRowsA + (p % fold) * per + x; };
-          for (int p = 0; p < parts; ++p) zm = fmaxf(zm, stats[part_of(p)].x);
+          for (int p = 0; p < parts; ++p) zm = fmaxf(zm, stats[part_at(p, x)].x);
           for (int p = 0; p < parts; ++p) {
-            const float2 v = stats[part_of(p)];
+            const float2 v = stats[part_at(p, x)];
             if (v.x != -INFINITY) zl += v.y * ex2((v.x - zm) * c);
           }
+          if (!(zl > 0.f && zl < INFINITY)) continue;  // its scores are not finite either
           row_again<T, D>(a, head, x, z, zm, c, direct ? 1.f / zl : 1.f, o);
-          const int zt = (int)head[kHTok0] + z.token, zh = (int)head[kHHead] * a.group + x % a.group;
+          const int zt = tok0 + z.token, zh = kvh * a.group + x % a.group;
           T* zo = static_cast<T*>(a.out) + (int64_t)zt * a.o_ts + (int64_t)zh * a.o_hs;
           float* zp = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + x) * D;
 #pragma unroll
