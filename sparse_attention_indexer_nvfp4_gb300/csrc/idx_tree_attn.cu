@@ -585,7 +585,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     k_tree_attention(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeArgs a) {
   using S = Smem<D>;
-  pdl_enter();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -626,9 +625,21 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     }
     fence_mbar_init();
   }
+  if (tid == 32) {  // a cold descriptor costs a copy a microsecond
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+  }
+  __syncwarp();
+  if (warp == 0) tmem_alloc(&misc->tmem_base, kTmemColsA);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem_base;
+  pdl_enter();  // before any global-memory access
   {
     unsigned long long local = 0;
+#pragma unroll 1
     for (int r = tid; r < a.num_reqs; r += kThreadsA) {
       const unsigned long long u = plan.units(r);
       if (r < kKeptUnits) misc->units[r] = (uint32_t)min(u, 0xFFFFFFFFull);
@@ -637,12 +648,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     local = warp_sum_u64(local);
     if (lane == 0 && local) atomicAdd(&misc->total, local);
   }
-  __syncwarp();
-  if (warp == 0) tmem_alloc(&misc->tmem_base, kTmemColsA);
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = misc->tmem_base;
   const unsigned long long W = misc->total;
   // (64-bit divisions take some hundred cycles each)
   const bool small = W < (1u << 23);
@@ -654,11 +660,12 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     unsigned long long acc = 0;
     int r = 0;
     unsigned long long rem = 0;
+#pragma unroll 1
     for (int base = 0; base < a.num_reqs; base += 32) {
       unsigned long long n = base + lane >= a.num_reqs ? 0ull : base + lane < kKeptUnits ? misc->units[base + lane] : plan.units(base + lane);
       if (n == 0xFFFFFFFFull) n = plan.units(base + lane);
       unsigned long long incl = n;
-#pragma unroll
+#pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += y;
@@ -1014,16 +1021,22 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         break;
       }
       // the row's parts: two halves of `fold` copies
-      const int parts = 2 * fold, per = kRowsA / fold;
-      auto part_at = [&](int p, int x) { return (p >= fold ? kRowsA + (p - fold) * per : p * per) + x; };
-      float big = -INFINITY, sum_l = 0.f;
+      const int per = kRowsA / fold;
+      auto row_of = [&](int x, float& sum) {  // the row's largest maximum, and its sum
+        float top = -INFINITY;
+        sum = 0.f;
 #pragma unroll 1
-      for (int p = 0; p < parts; ++p) big = fmaxf(big, stats[part_at(p, row)].x);
+        for (int p = x; p < kRowsA; p += per) top = fmaxf(top, fmaxf(stats[p].x, stats[kRowsA + p].x));
 #pragma unroll 1
-      for (int p = 0; p < parts; ++p) {
-        const float2 x = stats[part_at(p, row)];
-        if (x.x != -INFINITY) sum_l += x.y * ex2((x.x - big) * c);
-      }
+        for (int p = x; p < kRowsA; p += per) {
+          const float2 u = stats[p], v = stats[kRowsA + p];
+          if (u.x != -INFINITY) sum += u.y * ex2((u.x - top) * c);
+          if (v.x != -INFINITY) sum += v.y * ex2((v.x - top) * c);
+        }
+        return top;
+      };
+      float sum_l;
+      const float big = row_of(row, sum_l);
       const uint32_t slot = head[kHOut];
       const bool direct = slot == 0xFFFFFFFFu, empty = sum_l == 0.f;
       // what this lane's two halves weigh in the row
@@ -1049,12 +1062,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           z.chain_end = st.ctx + (int)head[kHNode0] + z.token + 1;
           const int n = (int)head[kHNew];
           z.tree = tree ? a.mask[(int)head[kHTok0] + z.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
-          float zm = -INFINITY, zl = 0.f, o[D / 32];
-          for (int p = 0; p < parts; ++p) zm = fmaxf(zm, stats[part_at(p, x)].x);
-          for (int p = 0; p < parts; ++p) {
-            const float2 v = stats[part_at(p, x)];
-            if (v.x != -INFINITY) zl += v.y * ex2((v.x - zm) * c);
-          }
+          float zl, o[D / 32];
+          const float zm = row_of(x, zl);
           if (!(zl > 0.f && zl < INFINITY)) continue;  // its scores are not finite either
           row_again<T, D>(a, head, x, z, zm, c, direct ? 1.f / zl : 1.f, o);
           const int zt = tok0 + z.token, zh = kvh * a.group + x % a.group;
@@ -1108,7 +1117,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 // Joins the partial rows of the segments that the stretches share: block
 // (x, y) those that stretch x + 1 cut first, a warp a row: the largest
 // reference maximum, then the weighted sums.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_tree_combine(const __grid_constant__ TreeArgs a, int ctas) {
   pdl_enter();
