@@ -592,8 +592,8 @@ int idx_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_str
  * residual is p without the refused tokens.  A residual without mass falls
  * back to p; p without mass gives token vocab - 1.
  * Tests of children are made in 64-bit floating point; masses and cumulative
- * sums are exact sums of terms cut to multiples of 2^-60 (c to 2^-52), so
- * they do not depend on the order of adding.  Entries are probabilities: a negative or
+ * sums are good to about 2^-45 of the mass and do not depend on anything but
+ * the inputs and the sizes of the call.  Entries are probabilities: a negative or
  * NaN entry counts as 0, and a row's sum must stay below 8.
  *
  *   target, draft [num_tokens, vocab] float32, row strides in elements;

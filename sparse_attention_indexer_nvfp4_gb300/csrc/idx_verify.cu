@@ -11,12 +11,15 @@
 // c_0 = 0, W_0 = 1: a refusal changes one number, and one pass over p and q
 // gives the next mass.  No residual row is stored.
 //
-// Masses and cumulative sums are exact: each term becomes an integer multiple
-// of 2^-60 (probabilities sum to about 1, so 63 bits hold a row), and integer
-// sums do not depend on the order of adding.  The drawn token is therefore
-// that of the definition in 64 bits whatever the split over warps and CTAs;
-// fp32 sums over 200,000 terms would move about one draw in 200.  (fp64 adds
-// would do too, but at 2 a clock and SM they, not HBM, would set the pace.)
+// A drawn token must be that of the definition in 64 bits: fp32 sums over
+// 200,000 terms would move about one draw in 200.  fp64 would do, but at 2 adds
+// a clock and SM it, not HBM, would set the pace.  So a thread adds its terms
+// in pairs of fp32 numbers (each difference and each addition with its exact
+// error, about 2^-45 of the sum), 12 instructions a term where 64-bit integers
+// took 54 and the call on 64 rows 49 us; the threads' sums become integer
+// multiples of 2^-60, which add up the same in any order.  Sums of p alone are
+// formed of such integers from the start, since refused tokens are taken off
+// them exactly.
 //
 // One cluster of CTAs a request.  Each CTA gathers the nodes' probabilities
 // and walks the tree by itself (the same numbers in each); a mass is summed
@@ -78,6 +81,34 @@ __device__ __forceinline__ void st_cluster(u64* p, uint32_t rank, u64 v) {
       : "memory");
 }
 
+// Two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
+
 // A probability: negative and NaN count as 0.
 __device__ __forceinline__ float clean(float x) { return fmaxf(x, 0.f); }
 
@@ -113,6 +144,39 @@ __device__ __forceinline__ float4 quad_of(const float* row, int v, int vocab, bo
   x.z = v + 2 >= 0 && v + 2 < vocab ? row[v + 2] : 0.f;
   x.w = v + 3 < vocab ? row[v + 3] : 0.f;
   return x;
+}
+
+// A sum of non-negative numbers as hi + lo, two sums side by side.
+struct Sum2 {
+  float2 hi = make_float2(0.f, 0.f), lo = make_float2(0.f, 0.f);
+  // x and an error term that comes with it
+  __device__ __forceinline__ void add(float2 x, float2 err) {
+    // two numbers' sum and its exact error, whichever is larger
+    const float2 t = add2(hi, x), b = sub2(t, hi);
+    const float2 e = add2(sub2(hi, sub2(t, b)), sub2(x, b));
+    hi = t;
+    lo = add2(lo, add2(e, err));
+  }
+  __device__ __forceinline__ u64 fixed() const {
+    const double v = ((double)hi.x + (double)lo.x) + ((double)hi.y + (double)lo.y);
+    return v > 0.0 ? __double2ull_rn(fmin(v, 15.0) * kUnit) : 0ull;
+  }
+};
+
+// Adds max(p - c q, 0) of two entries, c = ch + cl (kOne: c = 1).  Where p > c q
+// the error of the difference is (p - d) - c q exactly.
+template <bool kOne>
+__device__ __forceinline__ void add_terms(Sum2& s, float2 p, float2 q, float2 ch, float2 cl) {
+  p = make_float2(clean(p.x), clean(p.y)), q = make_float2(clean(q.x), clean(q.y));
+  float2 cq = q, low = make_float2(0.f, 0.f);
+  if (!kOne) {
+    cq = mul2(ch, q);
+    low = fma2(cl, q, fma2(ch, q, neg2(cq)));  // the product's error and the small part of c
+  }
+  const float2 d = sub2(p, cq);
+  float2 e = sub2(sub2(p, d), cq);
+  if (!kOne) e = sub2(e, low);
+  s.add(make_float2(fmaxf(d.x, 0.f), fmaxf(d.y, 0.f)), make_float2(d.x > 0.f ? e.x : 0.f, d.y > 0.f ? e.y : 0.f));
 }
 
 struct Shared {
@@ -186,7 +250,9 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
     const float* q = a.draft + (int64_t)(t0 + at) * a.draft_stride;
     const bool with_q = a.draft != nullptr && c != 0.0, one = c == 1.0;
     const bool both = with_q && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
-    const u64 c52 = (u64)(fmin(c, kMostC) * kUnitC);
+    const float ch1 = (float)c, cl1 = (float)(c - (double)ch1);
+    const float2 ch = make_float2(ch1, ch1), cl = make_float2(cl1, cl1);
+    Sum2 pair;
     const Span w = span_of(at);
     const int w_lo = stretch(w, warp), w_hi = stretch(w, warp + 1);
     u64 sum = 0;
@@ -203,15 +269,19 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
       }
       if (with_q) {
 #pragma unroll
-        for (int e = 0; e < kUnrollV; ++e)
-          sum += (term(pv[e].x, qv[e].x, c52, one) + term(pv[e].y, qv[e].y, c52, one)) +
-                 (term(pv[e].z, qv[e].z, c52, one) + term(pv[e].w, qv[e].w, c52, one));
+        for (int e = 0; e < kUnrollV; ++e) {
+          const float2 p0 = make_float2(pv[e].x, pv[e].y), p1 = make_float2(pv[e].z, pv[e].w);
+          const float2 q0 = make_float2(qv[e].x, qv[e].y), q1 = make_float2(qv[e].z, qv[e].w);
+          if (one) add_terms<true>(pair, p0, q0, ch, cl), add_terms<true>(pair, p1, q1, ch, cl);
+          else add_terms<false>(pair, p0, q0, ch, cl), add_terms<false>(pair, p1, q1, ch, cl);
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < kUnrollV; ++e)
           sum += (fixed_of(clean(pv[e].x)) + fixed_of(clean(pv[e].y))) + (fixed_of(clean(pv[e].z)) + fixed_of(clean(pv[e].w)));
       }
     }
+    if (with_q) sum = pair.fixed();
     sum = warp_sum_u64(sum);
     if (subtract)  // the refused tokens of the warp's stretch (each listed once)
       for (int k = 0; k < s.num_refused; ++k) {
@@ -317,6 +387,8 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
   const float* q = a.draft + (int64_t)(t0 + at) * a.draft_stride;
   const bool with_q = a.draft != nullptr && last_c != 0.0, one = last_c == 1.0;
   const u64 c52 = (u64)(fmin(last_c, kMostC) * kUnitC);
+  int last = -1;  // this thread's last entry with a term
+  if (tid == 0) s.next = -1;
   for (int base = lo; base < hi; base += kThreadsV) {
     const int v0 = 4 * (base + tid) - span.shift;
     const bool in = base + tid < hi;
@@ -328,6 +400,9 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (s.refused[k] == v0 + e) f[e] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (f[e] > 0) last = v0 + e;
     const u64 mine = (f[0] + f[1]) + (f[2] + f[3]);
     u64 incl = mine;
 #pragma unroll
@@ -355,6 +430,10 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
     before += whole;
     __syncthreads();
   }
+  // the sum above was larger by a rounding than these terms: the last of them
+  if (last >= 0) atomicMax(&s.next, last);
+  __syncthreads();
+  if (tid == 0) out_tokens[taken] = s.next >= 0 ? s.next : a.vocab - 1;
 }
 
 // CTAs a request: enough clusters to fill the GPU when there are few
