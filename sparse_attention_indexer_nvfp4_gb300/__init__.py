@@ -374,9 +374,12 @@ def _explain(name: str, dense=(), **tensors) -> None:
     raise ValueError(f"{name}: a tensor has the wrong type, shape or strides")
 
 
-def _rows_ok(t, dtype, shape) -> bool:
+def _rows_ok(dtype, shape, *tensors) -> bool:
     """Type and sizes, and the last dimension contiguous (the others may have any strides)."""
-    return t is None or (t.dtype is dtype and t.shape == shape and (t.stride(-1) == 1 or shape[-1] <= 1))
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or (t.stride(-1) != 1 and shape[-1] > 1)):
+            return False
+    return True
 
 
 def idx_build_slots(ctx_lens, new_lens, owned_pages, block_table, free_blocks, free_cursor, num_blocks: int,
@@ -391,7 +394,7 @@ def idx_build_slots(ctx_lens, new_lens, owned_pages, block_table, free_blocks, f
     if not (_are(i32, (reqs,), ctx_lens, new_lens, owned_pages, seq_lens, pages_out) and _are(i32, (reqs + 1,), cu_tokens)
             and _are(i32, (1,), free_cursor, cursor_out) and _are(i32, (free,), free_blocks)
             and _are(i32, (tokens,), positions, parents) and slots.shape == per_token and slots.dtype in T.words
-            and slots.is_contiguous() and _rows_ok(block_table, i32, (reqs, width))
+            and slots.is_contiguous() and _rows_ok(i32, (reqs, width), block_table)
             and (tree_mask is None or (tree_mask.shape == per_token and tree_mask.dtype in T.words and tree_mask.is_contiguous()))):
         r, t, one = (reqs,), (tokens,), (1,)
         _explain(fn, ("ctx_lens", "new_lens", "owned_pages", "free_blocks", "cu_tokens", "seq_lens", "pages_out", "positions", "slots",
@@ -400,11 +403,12 @@ def idx_build_slots(ctx_lens, new_lens, owned_pages, block_table, free_blocks, f
                  free_cursor=(free_cursor, i32, one), cu_tokens=(cu_tokens, i32, (reqs + 1,)), seq_lens=(seq_lens, i32, r),
                  pages_out=(pages_out, i32, r), cursor_out=(cursor_out, i32, one), positions=(positions, i32, t),
                  slots=(slots, T.words, t), parents=(parents, i32, t), tree_mask=(tree_mask, T.words, t))
-    return _check(fn, lib.idx_build_slots(
+    rc = lib.idx_build_slots(
         ctx_lens.data_ptr(), new_lens.data_ptr(), owned_pages.data_ptr(), reqs, block_table.data_ptr(), _row_stride(block_table),
-        width, free_blocks.data_ptr(), free, free_cursor.data_ptr(), num_blocks, page_tokens, _ptr(parents), tokens,
+        width, free_blocks.data_ptr(), free, free_cursor.data_ptr(), num_blocks, page_tokens, None if parents is None else parents.data_ptr(), tokens,
         cu_tokens.data_ptr(), seq_lens.data_ptr(), pages_out.data_ptr(), cursor_out.data_ptr(), positions.data_ptr(),
-        slots.data_ptr(), _ptr(tree_mask), _ptr(status), _stream_on(stream, positions)))
+        slots.data_ptr(), None if tree_mask is None else tree_mask.data_ptr(), None if status is None else status.data_ptr(), _stream_on(stream, positions))
+    return rc if rc >= 0 else _check(fn, rc)
 
 
 def idx_rope_frequencies(rotary_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -438,8 +442,7 @@ def idx_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slots
     hq = 0 if q is None else q.shape[1]
     nb, page, hk = (0, 1, 0) if k is None else (k_cache.shape[0], k_cache.shape[1], k.shape[1])
     qshape, kshape, cshape = (tokens, hq, dim), (tokens, hk, dim), (nb, page, hk, dim)
-    if not (_rows_ok(q, kind, qshape) and _rows_ok(q_out, kind, qshape) and _rows_ok(k, kind, kshape) and _rows_ok(v, kind, kshape)
-            and _rows_ok(k_cache, kind, cshape) and _rows_ok(v_cache, kind, cshape) and _are(T.i32, (tokens,), positions)
+    if not (_rows_ok(kind, qshape, q, q_out) and _rows_ok(kind, kshape, k, v) and _rows_ok(kind, cshape, k_cache, v_cache) and _are(T.i32, (tokens,), positions)
             and _are(T.f64, inv_freq.shape[:1], inv_freq)
             and (slots is None or (slots.dtype in T.words and slots.shape == positions.shape and slots.is_contiguous()))):
         _explain(fn, ("positions", "inv_freq", "slots"), q=(q, kind, qshape), q_out=(q_out, kind, qshape), k=(k, kind, kshape),
@@ -452,10 +455,11 @@ def idx_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slots
     qs, os_ = (none, none) if q is None else (q.stride(), q_out.stride())
     ks = none if k is None else k.stride()
     vs = none if v is None else v.stride()
-    return _check(fn, lib.idx_rope_append(
-        _ptr(q), qs[0], qs[1], _ptr(q_out), os_[0], os_[1], hq, _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], hk, tokens, dim,
-        2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr(), mscale, _ptr(slots), _ptr(k_cache), _ptr(v_cache), nb,
-        page, cs[0], cs[1], cs[2], code, _ROPE_INTERLEAVED if interleaved else 0, _ptr(status), _stream_on(stream, some)))
+    rc = lib.idx_rope_append(
+        None if q is None else q.data_ptr(), qs[0], qs[1], None if q_out is None else q_out.data_ptr(), os_[0], os_[1], hq, None if k is None else k.data_ptr(), ks[0], ks[1], None if v is None else v.data_ptr(), vs[0], vs[1], hk, tokens, dim,
+        2 * inv_freq.shape[0], positions.data_ptr(), inv_freq.data_ptr(), mscale, None if slots is None else slots.data_ptr(), None if k_cache is None else k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), nb,
+        page, cs[0], cs[1], cs[2], code, _ROPE_INTERLEAVED if interleaved else 0, None if status is None else status.data_ptr(), _stream_on(stream, some))
+    return rc if rc >= 0 else _check(fn, rc)
 
 
 def idx_tree_attention_workspace_bytes(num_reqs: int, num_tokens: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -479,8 +483,8 @@ def idx_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, ou
     lists = per = 0
     if pages is not None:
         lists, per = pages.shape[-2:]
-    if not (_rows_ok(q, kind, shape) and _rows_ok(out, kind, shape) and cshape[3] == dim and _rows_ok(k_cache, kind, cshape)
-            and _rows_ok(v_cache, kind, cshape) and _rows_ok(block_table, T.i32, (reqs, width)) and _are(T.i32, (reqs,), seq_lens)
+    if not (_rows_ok(kind, shape, q, out) and cshape[3] == dim and _rows_ok(kind, cshape, k_cache, v_cache)
+            and _rows_ok(T.i32, (reqs, width), block_table) and _are(T.i32, (reqs,), seq_lens)
             and _are(T.i32, (reqs + 1,), cu_tokens) and _are(T.f32, (tokens, hq), lse)
             and (tree_mask is None or (tree_mask.dtype in T.words and tree_mask.shape == (tokens,) and tree_mask.is_contiguous()))
             and (pages is None or (pages.dtype is T.i32 and pages.is_contiguous() and pages.numel() == tokens * lists * per))):
@@ -494,11 +498,12 @@ def idx_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, ou
         raise ValueError(f"{fn}: k_cache and v_cache must have the same strides")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     qs, os_ = q.stride(), out.stride()
-    return _check(fn, lib.idx_tree_attention(
+    rc = lib.idx_tree_attention(
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), nb, page, cs[0], cs[1], cs[2], block_table.data_ptr(),
-        _row_stride(block_table), width, seq_lens.data_ptr(), cu_tokens.data_ptr(), reqs, tokens, hq, hk, dim, _ptr(tree_mask),
-        _ptr(pages), lists, per, scale, code, out.data_ptr(), os_[0], os_[1], _ptr(lse), _ptr(workspace), ws_bytes, _ptr(status),
-        _stream_on(stream, q)))
+        _row_stride(block_table), width, seq_lens.data_ptr(), cu_tokens.data_ptr(), reqs, tokens, hq, hk, dim, None if tree_mask is None else tree_mask.data_ptr(),
+        None if pages is None else pages.data_ptr(), lists, per, scale, code, out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes, None if status is None else status.data_ptr(),
+        _stream_on(stream, q))
+    return rc if rc >= 0 else _check(fn, rc)
 
 
 def idx_verify_drafts(target, draft, tokens, cu_tokens, accept_u, sample_u, out_tokens, out_nodes, num_accepted,
@@ -509,14 +514,15 @@ def idx_verify_drafts(target, draft, tokens, cu_tokens, accept_u, sample_u, out_
     i32, f32 = T.i32, T.f32
     total, vocab = rows = target.shape
     reqs, max_out = out_shape = out_tokens.shape
-    if not (_rows_ok(target, f32, rows) and _rows_ok(draft, f32, rows) and _are(i32, (total,), tokens, parents)
+    if not (_rows_ok(f32, rows, target, draft) and _are(i32, (total,), tokens, parents)
             and _are(i32, (reqs + 1,), cu_tokens) and _are(f32, (total,), accept_u) and _are(f32, (reqs,), sample_u)
             and _are(i32, out_shape, out_tokens, out_nodes) and _are(i32, (reqs,), num_accepted)):
         _explain(fn, ("tokens", "parents", "cu_tokens", "accept_u", "sample_u", "out_tokens", "out_nodes", "num_accepted"),
                  target=(target, f32, rows), draft=(draft, f32, rows), tokens=(tokens, i32, (total,)), parents=(parents, i32, (total,)),
                  cu_tokens=(cu_tokens, i32, (reqs + 1,)), accept_u=(accept_u, f32, (total,)), sample_u=(sample_u, f32, (reqs,)),
                  out_tokens=(out_tokens, i32, out_shape), out_nodes=(out_nodes, i32, out_shape), num_accepted=(num_accepted, i32, (reqs,)))
-    return _check(fn, lib.idx_verify_drafts(
-        target.data_ptr(), _row_stride(target), _ptr(draft), 0 if draft is None else _row_stride(draft), vocab, tokens.data_ptr(),
-        _ptr(parents), cu_tokens.data_ptr(), reqs, total, accept_u.data_ptr(), sample_u.data_ptr(), out_tokens.data_ptr(),
-        out_nodes.data_ptr(), max_out, num_accepted.data_ptr(), _ptr(status), _stream_on(stream, target)))
+    rc = lib.idx_verify_drafts(
+        target.data_ptr(), _row_stride(target), None if draft is None else draft.data_ptr(), 0 if draft is None else _row_stride(draft), vocab, tokens.data_ptr(),
+        None if parents is None else parents.data_ptr(), cu_tokens.data_ptr(), reqs, total, accept_u.data_ptr(), sample_u.data_ptr(), out_tokens.data_ptr(),
+        out_nodes.data_ptr(), max_out, num_accepted.data_ptr(), None if status is None else status.data_ptr(), _stream_on(stream, target))
+    return rc if rc >= 0 else _check(fn, rc)

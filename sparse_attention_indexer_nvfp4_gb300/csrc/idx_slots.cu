@@ -37,6 +37,7 @@ struct SlotArgs {
   int64_t* slots;
   uint64_t* mask;
   int32_t* status;
+  bool wide;  // the tokens' outputs are 16-byte aligned
 };
 
 // Greatest i in [0, n) with key[i] <= x; key[0] <= x, key non-decreasing.
@@ -50,6 +51,8 @@ __device__ __forceinline__ int last_le(const long long* key, int n, long long x)
   return lo;
 }
 
+// kPer: consecutive tokens a thread takes at a time
+template <int kPer>
 __global__ void __launch_bounds__(kThreadsS) k_build_slots(const __grid_constant__ SlotArgs a) {
   pdl_enter();
   __shared__ long long tok0[kChunk];  // first token of each request of the chunk
@@ -58,7 +61,9 @@ __global__ void __launch_bounds__(kThreadsS) k_build_slots(const __grid_constant
   __shared__ long long warp_tok[kThreadsS / 32], warp_blk[kThreadsS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long cap = a.num_tokens;
-  const long long t_lo = cap * blockIdx.x / gridDim.x, t_hi = cap * (blockIdx.x + 1) / gridDim.x;
+  // slices of whole kPer
+  const long long pers = (cap + kPer - 1) / kPer;
+  const long long t_lo = kPer * (pers * blockIdx.x / gridDim.x), t_hi = min(cap, kPer * (pers * (blockIdx.x + 1) / gridDim.x));
   const int cursor = min(max(*a.cursor, 0), a.num_free);
   long long tok_sum = 0, blk_sum = 0;  // of the chunks before
   int bits = 0;
@@ -125,44 +130,79 @@ __global__ void __launch_bounds__(kThreadsS) k_build_slots(const __grid_constant
       const long long src = cursor + at;
       a.bt[(base + i) * a.bt_stride + col] = src < a.num_free ? a.free_blocks[src] : -1;
     }
-    // the tokens of this CTA's slice
+    // the tokens of this CTA's slice, kPer a thread: one search, and a load of
+    // a block id where the page changes
     const long long lo = max(t_lo, tok_sum), hi = min(t_hi, tok_sum + tok_all);
-    for (long long t = lo + tid; t < hi; t += kThreadsS) {
-      const int i = last_le(tok0, n, t);
-      const int r = base + i, node = (int)(t - tok0[i]);
-      const long long place = (long long)ctx_s[i] + node;
-      const long long pg = place / a.page;
+    for (long long t4 = lo / kPer * kPer + kPer * tid; t4 < hi; t4 += kPer * kThreadsS) {
+      const long long from = max(t4, lo);
+      int i = last_le(tok0, n, from), r_at = -1;
+      uint32_t pg_at = 0;
       int64_t block = -1;
-      if (pg < own_s[i]) {
-        block = a.bt[(int64_t)r * a.bt_stride + pg];
-      } else if (pg < need_s[i]) {
-        const long long src = cursor + blk0[i] + (pg - own_s[i]);
-        if (src < a.num_free) block = a.free_blocks[src];
-      }
-      if (block < -1 || block >= a.num_blocks) {
-        bits |= IDX_ST_BLOCK_OOR;
-        block = -1;
-      }
-      a.slots[t] = block < 0 ? -1 : block * a.page + place % a.page;
-      int depth = node;
-      if (a.parents != nullptr) {
-        // up the tree: a parent below its child's index, so the walk ends
-        uint64_t m = 0;
-        if (node < kTreeNodes) {
-          depth = -1;
-          for (int j = node; j >= 0;) {
-            m |= 1ull << j;
-            ++depth;
-            const int up = a.parents[tok0[i] + j];
-            if (up < -1 || up >= j) bits |= IDX_ST_BAD_TREE;
-            j = up >= -1 && up < j ? up : -1;
+      int64_t slot[kPer] = {};
+      int pos[kPer] = {};
+      uint64_t mask[kPer] = {};
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const long long t = t4 + e;
+        if (t < lo || t >= hi) continue;
+        while (i + 1 < n && tok0[i + 1] <= t) ++i;
+        const int node = (int)(t - tok0[i]);
+        const uint32_t place = (uint32_t)ctx_s[i] + (uint32_t)node;  // below 2^32
+        const uint32_t pg = place / (uint32_t)a.page;
+        if (i != r_at || pg != pg_at) {
+          r_at = i, pg_at = pg, block = -1;
+          if (pg < (uint32_t)own_s[i]) {
+            block = a.bt[(int64_t)(base + i) * a.bt_stride + pg];
+          } else if (pg < (uint32_t)need_s[i]) {
+            const long long src = cursor + blk0[i] + (pg - (uint32_t)own_s[i]);
+            if (src < a.num_free) block = a.free_blocks[src];
           }
-        } else {
-          bits |= IDX_ST_BAD_TREE;
+          if (block < -1 || block >= a.num_blocks) {
+            bits |= IDX_ST_BLOCK_OOR;
+            block = -1;
+          }
         }
-        a.mask[t] = m;
+        slot[e] = block < 0 ? -1 : block * a.page + (place - pg * (uint32_t)a.page);
+        int depth = node;
+        if (a.parents != nullptr) {
+          // up the tree: a parent below its child's index, so the walk ends
+          uint64_t m = 0;
+          if (node < kTreeNodes) {
+            depth = -1;
+            for (int j = node; j >= 0;) {
+              m |= 1ull << j;
+              ++depth;
+              const int up = a.parents[tok0[i] + j];
+              if (up < -1 || up >= j) bits |= IDX_ST_BAD_TREE;
+              j = up >= -1 && up < j ? up : -1;
+            }
+          } else {
+            bits |= IDX_ST_BAD_TREE;
+          }
+          mask[e] = m;
+        }
+        pos[e] = (int)min((long long)ctx_s[i] + depth, 0x7FFFFFFFll);
       }
-      a.pos[t] = (int)min((long long)ctx_s[i] + depth, 0x7FFFFFFFll);
+      bool written = false;
+      if (kPer == 4 && a.wide && t4 >= lo && t4 + 4 <= hi) {
+        written = true;
+        *reinterpret_cast<int4*>(a.pos + t4) = make_int4(pos[0], pos[1 % kPer], pos[2 % kPer], pos[3 % kPer]);
+        reinterpret_cast<longlong2*>(a.slots + t4)[0] = make_longlong2(slot[0], slot[1 % kPer]);
+        reinterpret_cast<longlong2*>(a.slots + t4)[1] = make_longlong2(slot[2 % kPer], slot[3 % kPer]);
+        if (a.mask != nullptr) {
+          reinterpret_cast<ulonglong2*>(a.mask + t4)[0] = make_ulonglong2(mask[0], mask[1 % kPer]);
+          reinterpret_cast<ulonglong2*>(a.mask + t4)[1] = make_ulonglong2(mask[2 % kPer], mask[3 % kPer]);
+        }
+      }
+      if (!written) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const long long t = t4 + e;
+          if (t < lo || t >= hi) continue;
+          a.pos[t] = pos[e], a.slots[t] = slot[e];
+          if (a.mask != nullptr) a.mask[t] = mask[e];
+        }
+      }
     }
     tok_sum += tok_all, blk_sum += blk_all;
     __syncthreads();  // the chunk's arrays are used up
@@ -215,10 +255,15 @@ extern "C" int idx_build_slots(const int32_t* ctx_lens, const int32_t* new_lens,
   if ((rc = check_device()) != IDX_OK) return rc;
   SlotArgs a{ctx_lens,  new_lens, owned_pages, num_reqs,   block_table, bt_stride, max_blocks, free_blocks,
              num_free,  free_cursor, num_blocks, page_tokens, parents,  num_tokens, cu_tokens, seq_lens,
-             pages_out, cursor_out,  positions,  slots,       tree_mask, status};
-  // one token a thread as long as one wave of CTAs takes them
-  const int sms = device_sms();
-  const int grid = max(1, min((num_tokens + kThreadsS - 1) / kThreadsS, 4 * (sms > 0 ? sms : 1)));
-  launch_pdl(k_build_slots, dim3(grid), dim3(kThreadsS), 0, (cudaStream_t)stream, a);
+             pages_out, cursor_out,  positions,  slots,       tree_mask, status,
+             aligned(positions, 16) && aligned(slots, 16) && aligned(tree_mask, 16)};
+  // a wave of CTAs (four an SM), a token a thread as long as that takes them
+  // all, else four (a million tokens: 12.7 us against 16.5, and 6.2 against 4.6
+  // for 512, whose loads follow one another)
+  const int wave = 4 * max(device_sms(), 1);
+  if (num_tokens <= wave * kThreadsS)
+    launch_pdl(k_build_slots<1>, dim3(max(1, (num_tokens + kThreadsS - 1) / kThreadsS)), dim3(kThreadsS), 0, (cudaStream_t)stream, a);
+  else
+    launch_pdl(k_build_slots<4>, dim3(wave), dim3(kThreadsS), 0, (cudaStream_t)stream, a);
   return launch_result();
 }
