@@ -78,7 +78,7 @@ constexpr int kGroup = 16;          // places of a record's group
 constexpr int kMaxListTokens = 32;  // tokens of a block with page lists (bits of a mask)
 constexpr float kRescale = 8.f;     // powers of two that a weight may exceed 1 before O is rescaled
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kScratchRow = 17;     // floats: 16 columns and one of padding
+constexpr int kScratchRow = 20;     // floats: 16 columns, and 4 that keep rows on different banks
 
 // TMEM columns: two score tiles, whose halves the weights overwrite (two to a
 // column), and the two halves' O.
@@ -112,6 +112,7 @@ struct TreeArgs {
   int32_t max_blocks;
   const int32_t *seq_lens, *cu;
   int32_t num_reqs, num_tokens, q_heads, kv_heads, group;
+  uint32_t group_inv;  // ceil(2^16 / group): x / group for rows x < 128
   const uint64_t* mask;
   const int32_t* pages;
   int32_t lists, per;
@@ -129,6 +130,9 @@ struct TreeArgs {
   int32_t block_tokens;
   uint32_t polls;
 };
+
+// The token of a block's row.
+__device__ __forceinline__ int token_of(const TreeArgs& a, int row) { return (int)(((uint32_t)row * a.group_inv) >> 16); }
 
 // The cut of all requests into segments and tiles.
 struct Plan {
@@ -152,8 +156,8 @@ struct Plan {
     return max(1, (int)(((int64_t)lim + kTile - 1) / kTile));
   }
   // units of a request: for each segment kSegCost, then its tiles
-  __device__ unsigned long long units(int r) const {
-    const int n = ntok(r), t0 = tok0(r), s = seq(r), nl = a.pages != nullptr ? a.lists : 1;
+  __device__ unsigned long long units(int n, int t0, int s) const {
+    const int nl = a.pages != nullptr ? a.lists : 1;
     unsigned long long sum = 0;
     for (int b = 0; b < blocks(n); ++b)
       for (int l = 0; l < nl; ++l) sum += (unsigned long long)(kSegCost + tiles(s, n, t0, b, l));
@@ -296,7 +300,7 @@ struct Smem {
   static constexpr int kOffRec = kOffStats + kSoftWarps * 32 * 8;
   static constexpr int kOffBar = kOffRec + kSlots * kSlotWords * 4;
   static constexpr int kOffMisc = kOffBar + 64 * 8;
-  static constexpr int kBytes = kOffMisc + 64 + 4 * 384 + 1024;
+  static constexpr int kBytes = kOffMisc + 256 + 1024;
 };
 enum BarsA { kKFullA = 0, kKEmptyA = kKFullA + kMaxStages, kVFullA = kKEmptyA + kMaxStages, kVEmptyA = kVFullA + kMaxStages,
              kQFullA = kVEmptyA + kMaxStages, kQEmptyA, kSFull, kPFull = kSFull + 2,
@@ -304,15 +308,15 @@ enum BarsA { kKFullA = 0, kKEmptyA = kKFullA + kMaxStages, kVFullA = kKEmptyA + 
              kNumBarsA };
 static_assert(kNumBarsA <= 64, "barriers fit");
 
-constexpr int kKeptUnits = 384;
 struct MiscA {
   uint32_t tmem_base;
   int abort_flag;
   int soft_dead;  // a softmax warp gave up
   int issued[2];  // key and value tiles whose copies were issued
-  unsigned long long total;
+  int begin[4];   // the request of the stretch's first unit: number, tokens, first token, length
+  unsigned long long rem;
+  unsigned long long warp_units[kThreadsA / 32];
   uint32_t again[kRowsA / 32];  // rows to form again
-  uint32_t units[kKeptUnits];   // of the first requests
 };
 
 // A warp's way through the planned tiles: all its lanes call next() for each
@@ -352,6 +356,8 @@ struct Walk {
     if (k == n && lane_id() == 0) mbar_arrive(&bars[kSlotEmpty + chunk % kSlots]);
   }
 };
+
+static_assert(sizeof(MiscA) <= 256, "fits its place");
 
 // What a row's softmax needs of its segment.
 struct RowState {
@@ -475,54 +481,72 @@ __device__ __forceinline__ bool write_rows(const TreeArgs& a, uint32_t tmem_o, f
   constexpr int kPer = kRowsA / F, kItems = 4 / F;  // rows, items (a row's four columns) of a thread
   const int tid = threadIdx.x, lane = tid & 31, in_half = tid & (kRowsA - 1);
   const bool direct = slot == 0xFFFFFFFFu;
-  float* own = scratch + tid * kScratchRow;
-  const float* base = scratch + half * kRowsA * kScratchRow;
+  float4* own = reinterpret_cast<float4*>(scratch + tid * kScratchRow);
+  const float* base = scratch + half * kRowsA * kScratchRow + 4 * (lane & 3);
+  const uint32_t tmem = tmem_o + (uint32_t)(half * (D / 2));
+  uint32_t x[16], y[16];
+  tmem_ld16(tmem, x);
+  tmem_ld16(tmem + D, y);
   T* out[kItems];
   float* part[kItems];
   int row[kItems];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
     row[i] = F == 1 ? (in_half & ~31) + 8 * i + (lane >> 2) : 32 * i + (in_half >> 2);
-    const int t = tok0 + row[i] / a.group, h = kvh * a.group + row[i] % a.group;
+    const int tk = token_of(a, row[i]), t = tok0 + tk, h = kvh * a.group + row[i] - tk * a.group;
     const int col = half * (D / 2) + 4 * (lane & 3);
     out[i] = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs + col;
     part[i] = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row[i]) * D + col;
   }
-  bool odd = false;
+  float worst[kItems] = {};  // sums of magnitudes: not finite where a value is not
 #pragma unroll 1
   for (int k = 0; k < D / 2; k += 16) {
-    const uint32_t col = tmem_o + (uint32_t)(half * (D / 2) + k);
-    uint32_t x[16], y[16];
-    tmem_ld16(col, x);
-    tmem_ld16(col + D, y);
     tmem_wait_ld();
+    float4 f[4];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      own[e] = (g0 == 0.f ? 0.f : __uint_as_float(x[e]) * g0) + (g1 == 0.f ? 0.f : __uint_as_float(y[e]) * g1);
+    for (int e = 0; e < 4; ++e) {
+      float* v = reinterpret_cast<float*>(&f[e]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = (g0 == 0.f ? 0.f : __uint_as_float(x[4 * e + j]) * g0) + (g1 == 0.f ? 0.f : __uint_as_float(y[4 * e + j]) * g1);
+    }
+    if (k + 16 < D / 2) {  // the next round's columns, meanwhile
+      tmem_ld16(tmem + (uint32_t)(k + 16), x);
+      tmem_ld16(tmem + (uint32_t)(D + k + 16), y);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) own[e] = f[e];
     if (F == 1) __syncwarp();
     else half_sync(half);
+    // all loads before any store, so that none waits for another
+    float4 z[kItems][F];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+      for (int c = 0; c < F; ++c) z[i][c] = *reinterpret_cast<const float4*>(base + (row[i] + c * kPer) * kScratchRow);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+      for (int c = 1; c < F; ++c) z[i][0].x += z[i][c].x, z[i][0].y += z[i][c].y, z[i][0].z += z[i][c].z, z[i][0].w += z[i][c].w;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const float* src = base + row[i] * kScratchRow + 4 * (lane & 3);
-      float f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[e] = src[e];
-#pragma unroll
-        for (int c = 1; c < F; ++c) f[e] += src[c * kPer * kScratchRow + e];
-      }
+      const float4 u = z[i][0];
+      worst[i] += (fabsf(u.x) + fabsf(u.y)) + (fabsf(u.z) + fabsf(u.w));
       if (row[i] < rows) {
-        if (!(fabsf(f[0]) + fabsf(f[1]) + fabsf(f[2]) + fabsf(f[3]) < INFINITY)) {
-          atomicOr(&again[row[i] >> 5], 1u << (row[i] & 31));
-          odd = true;
-        }
-        if (direct) *reinterpret_cast<uint2*>(out[i] + k) = make_uint2(Num<T>::pack(f[0], f[1]), Num<T>::pack(f[2], f[3]));
-        else *reinterpret_cast<float4*>(part[i] + k) = make_float4(f[0], f[1], f[2], f[3]);
+        if (direct) *reinterpret_cast<uint2*>(out[i] + k) = make_uint2(Num<T>::pack(u.x, u.y), Num<T>::pack(u.z, u.w));
+        else *reinterpret_cast<float4*>(part[i] + k) = u;
       }
     }
     if (F == 1) __syncwarp();
     else half_sync(half);
   }
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if (row[i] < rows && !(worst[i] < INFINITY)) {
+      atomicOr(&again[row[i] >> 5], 1u << (row[i] & 31));
+      odd = true;
+    }
   return odd;
 }
 
@@ -598,7 +622,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   const bool lists = a.pages != nullptr, tree = a.mask != nullptr;
 
   if (tid == 0) {
-    misc->total = 0;
     misc->abort_flag = 0;
     misc->soft_dead = 0;
     misc->issued[0] = misc->issued[1] = 0;
@@ -637,52 +660,62 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   tc_fence_after();
   const uint32_t tmem = misc->tmem_base;
   pdl_enter();  // before any global-memory access
+  // The line of units, cut into stretches [w0, w1): who holds unit w0, and the
+  // units before it in that request.
+  unsigned long long W = 0, w0 = 0, w1 = 0;
+  auto cut = [&](unsigned long long all) {  // (64-bit divisions take some hundred cycles each)
+    const uint32_t x = blockIdx.x, g = gridDim.x;
+    W = all;
+    if (W < (1u << 23)) w0 = (uint32_t)W * x / g, w1 = (uint32_t)W * (x + 1) / g;
+    else w0 = W * x / g, w1 = W * (x + 1) / g;
+  };
   {
-    unsigned long long local = 0;
+    // a request a thread, or a run of them
+    const int run = (a.num_reqs + kThreadsA - 1) / kThreadsA, r0 = tid * run;
+    unsigned long long mine = 0;
+    int n = 0, t0 = 0, s = 0;
 #pragma unroll 1
-    for (int r = tid; r < a.num_reqs; r += kThreadsA) {
-      const unsigned long long u = plan.units(r);
-      if (r < kKeptUnits) misc->units[r] = (uint32_t)min(u, 0xFFFFFFFFull);
-      local += u;
+    for (int r = r0; r < min(r0 + run, a.num_reqs); ++r) {
+      n = plan.ntok(r), t0 = plan.tok0(r), s = plan.seq(r);
+      mine += plan.units(n, t0, s);
     }
-    local = warp_sum_u64(local);
-    if (lane == 0 && local) atomicAdd(&misc->total, local);
+    unsigned long long incl = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) misc->warp_units[warp] = incl;
+    __syncthreads();
+    unsigned long long all = 0, before = incl - mine;
+#pragma unroll 1
+    for (int k = 0; k < kThreadsA / 32; ++k) {
+      const unsigned long long y = misc->warp_units[k];
+      if (k < warp) before += y;
+      all += y;
+    }
+    cut(all);
+    if (w0 < w1 && before <= w0 && w0 < before + mine) {
+      int r = min(r0 + run, a.num_reqs) - 1;
+      if (run > 1)  // which of the run
+        for (r = r0;; ++r) {
+          n = plan.ntok(r), t0 = plan.tok0(r), s = plan.seq(r);
+          const unsigned long long u = plan.units(n, t0, s);
+          if (w0 < before + u) break;
+          before += u;
+        }
+      misc->begin[0] = r, misc->begin[1] = n, misc->begin[2] = t0, misc->begin[3] = s;
+      misc->rem = w0 - before;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const unsigned long long W = misc->total;
-  // (64-bit divisions take some hundred cycles each)
-  const bool small = W < (1u << 23);
-  const unsigned long long w0 = small ? (uint32_t)W * blockIdx.x / gridDim.x : W * blockIdx.x / gridDim.x;
-  const unsigned long long w1 = small ? (uint32_t)W * (blockIdx.x + 1) / gridDim.x : W * (blockIdx.x + 1) / gridDim.x;
 
   if (warp == kPlanWarp) {
-    // the request of the stretch's first unit
-    unsigned long long acc = 0;
-    int r = 0;
-    unsigned long long rem = 0;
-#pragma unroll 1
-    for (int base = 0; base < a.num_reqs; base += 32) {
-      unsigned long long n = base + lane >= a.num_reqs ? 0ull : base + lane < kKeptUnits ? misc->units[base + lane] : plan.units(base + lane);
-      if (n == 0xFFFFFFFFull) n = plan.units(base + lane);
-      unsigned long long incl = n;
-#pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned long long excl = acc + incl - n;
-      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, n > 0 && excl <= w0 && w0 < excl + n);
-      if (hit) {
-        const int who = __ffs(hit) - 1;
-        r = base + who;
-        rem = w0 - __shfl_sync(0xFFFFFFFFu, excl, who);
-        break;
-      }
-      acc += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    }
-    // and its block, head and tile; all lanes hold the same cursor
     const bool some = w0 < w1;
-    int n = some ? plan.ntok(r) : 0, t0 = some ? plan.tok0(r) : 0, s = some ? plan.seq(r) : 0, b = 0, kvh = 0;
+    int r = some ? misc->begin[0] : 0, n = some ? misc->begin[1] : 0, t0 = some ? misc->begin[2] : 0, s = some ? misc->begin[3] : 0;
+    unsigned long long rem = some ? misc->rem : 0;
+    // and its block, head and tile; all lanes hold the same cursor
+    int b = 0, kvh = 0;
     const int per_list = lists ? a.kv_heads / a.lists : a.kv_heads;
     int tiles = some ? plan.tiles(s, n, t0, 0, 0) : 0;
     while (some && rem >= (unsigned)(kSegCost + tiles)) {
@@ -714,8 +747,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       const int entries = lists ? min(a.counts[(int64_t)tok * a.lists + lh], m * a.per) : 0;
       const int here = min(kChunk, piece_end - tile);  // tiles of this chunk
       const int slot = chunk % kSlots;
-      const bool ok =
-          timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag, a.status, a.polls);
+      const bool ok = chunk < kSlots || timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag,
+                                                        a.status, a.polls);
       if (!__all_sync(0xFFFFFFFFu, ok)) {
         gave_up = true;
         break;
@@ -843,6 +876,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     int queries = 0;
     while (w.next()) {
       if (w.rec[kRFlags] & kFlagFirst) {
+        for (int k = lane; k < (int)w.head[kHTokens] * (D / 64); k += 32)  // into L2 while the queries before are in use
+          asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(&qmap), "r"(k % (D / 64) * 64),
+                       "r"((int)w.head[kHHead] * a.group), "r"((int)w.head[kHTok0] + k / (D / 64))
+                       : "memory");
         bool ok = true;
         if (queries > 0) ok = timed_wait_flag(&bars[kQEmptyA], (uint32_t)(queries - 1) & 1u, abort_flag, a.status, a.polls);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
@@ -957,7 +994,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         col0 = half * kHalf + copy * (kHalf / fold);
         warp_live = (row & ~31) < rows;
         m = -INFINITY, l = 0.f;
-        st.token = min(row / a.group, (int)head[kHTokens] - 1);  // rows past the block's compute on the last token's mask
+        st.token = min(token_of(a, row), (int)head[kHTokens] - 1);  // rows past the block's compute on the last token's mask
         st.ctx = (int)head[kHCtx], st.len = (int)head[kHLen];
         const int n = (int)head[kHNew];
         st.chain_end = st.ctx + (int)head[kHNode0] + st.token + 1;
@@ -1044,7 +1081,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       const float g0 = m0 == -INFINITY ? 0.f : ex2((m0 - big) * c) * inv, g1 = m1 == -INFINITY ? 0.f : ex2((m1 - big) * c) * inv;
       const int tok0 = (int)head[kHTok0], kvh = (int)head[kHHead];
       if (row < rows && half == 0 && copy == 0) {
-        const int t = tok0 + row / a.group, h = kvh * a.group + row % a.group;
+        const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
         if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : big * c, sum_l);
         else if (a.lse != nullptr)
           a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + __log2f(sum_l)) * 0.6931471805599453f;
@@ -1357,6 +1394,7 @@ extern "C" int idx_tree_attention(const void* q, int64_t q_token_stride, int64_t
   a.num_blocks = num_blocks, a.page = page_tokens, a.c_bs = c_block_stride, a.c_ts = c_token_stride, a.c_hs = c_head_stride;
   a.bt = block_table, a.bt_stride = bt_stride, a.max_blocks = max_blocks, a.seq_lens = seq_lens, a.cu = cu_tokens;
   a.num_reqs = num_reqs, a.num_tokens = num_tokens, a.q_heads = q_heads, a.kv_heads = kv_heads, a.group = q_heads / kv_heads;
+  a.group_inv = (65536u + a.group - 1) / a.group;
   a.mask = tree_mask, a.pages = pages, a.lists = page_lists, a.per = pages_per_list, a.scale = scale;
   a.out = out, a.o_ts = o_token_stride, a.o_hs = o_head_stride, a.lse = lse, a.status = status;
   a.cuts = reinterpret_cast<int32_t*>(ws);
