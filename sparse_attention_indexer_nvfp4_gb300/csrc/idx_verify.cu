@@ -26,8 +26,14 @@
 // over the cluster, each warp over its own stretch of the vocabulary, and the
 // totals go to every CTA through distributed shared memory.  The draw finds
 // CTA and warp from the totals, and the owning CTA reads that one stretch again.
+//
 // The floor is the HBM read of one target row and, where a token was refused,
-// one draft row a request.
+// one draft row a request.  What bounds it is the chain of passes: a fixed ~8
+// us of latency (launch, gather of the nodes' probabilities, walk, one pass, the
+// draw's second look), then a refused token's pass or two a request.  64 chains
+// of 8 over 200,003 entries: 28.8 us with clusters of 8 CTAs of 256 threads (of
+// 4 and 2 CTAs: 33.5 and 48.9; of 512 and 128 threads: 43 and 40); 48 trees of
+// 24 over 128,000: 32 us; a chain of 4 over 32,000: 8.6 us.
 #include "idx_common.cuh"
 #include "idx_internal.h"
 
@@ -37,7 +43,7 @@ namespace {
 constexpr int kThreadsV = 256;
 constexpr int kWarpsV = kThreadsV / 32;
 constexpr int kMaxNodes = IDX_VERIFY_MAX_NODES;
-constexpr int kMaxCluster = 8;
+constexpr int kCluster = 8;
 constexpr int kUnrollV = 4;  // loads of four entries in flight a thread and row
 constexpr double kUnit = 1152921504606846976.0;  // 2^60
 constexpr double kUnitC = 4503599627370496.0;    // 2^52
@@ -185,7 +191,7 @@ struct Shared {
   int path[kMaxNodes];
   int refused[kMaxNodes];
   u64 warp_sum[kWarpsV];
-  u64 cta_sum[2][kMaxCluster];
+  u64 cta_sum[2][kCluster];
   u64 scan[kWarpsV];
   int at, next, taken, num_refused, more;
   double c, w;
@@ -436,13 +442,6 @@ __global__ void __launch_bounds__(kThreadsV) k_verify(const __grid_constant__ Ve
   if (tid == 0) out_tokens[taken] = s.next >= 0 ? s.next : a.vocab - 1;
 }
 
-// CTAs a request: enough clusters to fill the GPU when there are few
-// requests, stretches of at least a few loads a thread.
-int cluster_for(int32_t num_reqs, int32_t vocab) {
-  (void)num_reqs, (void)vocab;
-  return 8;
-}
-
 }  // namespace
 }  // namespace idx
 
@@ -467,16 +466,15 @@ extern "C" int idx_verify_drafts(const float* target, int64_t target_stride, con
   if ((rc = check_device()) != IDX_OK) return rc;
   const VerifyArgs a{target,  target_stride, draft,    draft_stride, vocab,      tokens,    parents, cu_tokens,   num_reqs,
                      num_tokens, accept_u,   sample_u, out_tokens,   out_nodes,  max_out,   num_accepted, status};
-  const int cs = cluster_for(num_reqs, vocab);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_reqs * cs);
+  cfg.gridDim = dim3((unsigned)num_reqs * kCluster);
   cfg.blockDim = dim3(kThreadsV);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cs, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  attr[1].val.clusterDim.x = kCluster, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cudaLaunchKernelEx(&cfg, k_verify, a);
