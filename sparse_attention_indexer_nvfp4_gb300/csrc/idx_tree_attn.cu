@@ -41,8 +41,11 @@
 //
 // The bound is HBM for up to ~128 rows a KV head (4 D flops a row and key
 // against 4 D bytes a key: 128 flops a byte, below the ridge of ~280); beyond,
-// the blocks of a KV head read its keys again, from L2 where they come close
-// together.  Measured with 64 query and 4 KV heads of 128 in bf16:
+// each block of a request goes through its tiles again and a CTA's pace a tile,
+// ~2,600 cycles with 128 live rows, is the bound (blocks taken side by side by
+// neighbouring CTAs, so that the second read comes from L2: 163 us for 169 on 5
+// requests of up to 61 tokens, but 58.6 for 55.7 on 64 tokens over 16,384
+// places).  Measured with 64 query and 4 KV heads of 128 in bf16:
 //     64 requests, 8 tokens each over 1,024 to 16,384 places   213 us, 5.9 TB/s
 //     one request, 8 tokens over 500,000 places                169 us, 6.1 TB/s
 //     64 requests, one token each over 8,192 places            178 us, 6.0 TB/s

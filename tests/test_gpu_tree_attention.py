@@ -344,3 +344,21 @@ def test_times_out_then_recovers(lib):
         out, L, st = run(lib, c)
         assert st == 0
         compare(c, out, L, ref)
+
+
+@pytest.mark.parametrize("tree", ["tree", "none"])
+@pytest.mark.parametrize("ctx,new,hq,hk", [([3000], [64], 64, 4), ([0], [64], 64, 4), ([1500] * 4, [16] * 4, 64, 4),
+                                           ([2000, 900, 2500, 10], [16, 24, 8, 40], 64, 4), ([1200, 700], [56, 48], 64, 4),
+                                           ([2500, 0, 1800], [61, 1, 33], 32, 8), ([700], [11], 100, 1), ([600, 600], [9, 10], 128, 1),
+                                           ([5000, 130], [2, 64], 128, 2)])
+def test_requests_of_several_blocks(lib, ctx, new, hq, hk, tree):
+    """Two to eight blocks of rows a request, and numbers that only single CTAs take; requests of one size and of several."""
+    c = make(sum(ctx) + sum(new), ctx, new, hq, hk, 128, 128, "bf16", tree=tree)
+    first = check(lib, c)
+    again, _, _ = run(lib, c)
+    assert torch.equal(first, again)
+
+
+def test_long_chain_in_blocks(lib):
+    """A prompt's chunk: 300 tokens, 38 blocks of 8, each seeing less than the next."""
+    check(lib, make(5, [513, 0], [300, 17], 64, 4, 64, 32, "fp16", tree="none"))
