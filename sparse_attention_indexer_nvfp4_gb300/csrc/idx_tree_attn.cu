@@ -59,6 +59,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "idx_common.cuh"
 #include "idx_internal.h"
@@ -103,7 +104,7 @@ constexpr uint32_t kColS = 0, kColO = 256, kTmemColsA = 512;
 // first one's partial slot, and whether some stretch between may be empty.
 enum CutWord { kCRows, kCTok0, kCHead, kCFrom, kCTo, kCSlot, kCHoles };
 // A chunk's header, and a tile's record.
-enum HeadWord { kHTiles, kHTok0, kHTokens, kHHead, kHCtx, kHNew, kHNode0, kHLen, kHOut, kHReq, kHFirst, kHEnd, kHList, kHFold };
+enum HeadWord { kHTiles, kHTok0, kHTokens, kHHead, kHCtx, kHNew, kHNode0, kHLen, kHOut, kHFold };
 enum RecWord { kRFlags, kROffset, kRPos = 8, kRMask = 16, kRBox = 24 };
 constexpr int kFlagFirst = 1, kFlagLast = 2, kKindShift = 2;
 enum Kind { kFull = 0, kRowMask = 1, kGeneral = 2 };  // every row sees every place / whole rows do or do not / place by place
@@ -303,6 +304,7 @@ struct Num<__half> {
 };
 
 // Shared memory
+constexpr int kBarSet = 64;  // barriers of a run over the stretch
 template <int D>
 struct Smem {
   static constexpr int kQ = kRowsA * D * 2, kKv = kTile * D * 2;
@@ -313,24 +315,29 @@ struct Smem {
   static constexpr int kOffStats = kOffScratch + kSoftWarps * 32 * kScratchRow * 4;
   static constexpr int kOffRec = kOffStats + kSoftWarps * 32 * 8;
   static constexpr int kOffBar = kOffRec + kSlots * kSlotWords * 4;
-  static constexpr int kOffMisc = kOffBar + 64 * 8;
+  static constexpr int kOffMisc = kOffBar + 2 * kBarSet * 8;
   static constexpr int kBytes = kOffMisc + 256 + 1024;
+  // in a careful run (see take_out) the scratch holds marks between segments' ends
+  static constexpr int kMarkWords = D / 16;  // of a place or row
+  static_assert(2 * 128 * kMarkWords <= kSoftWarps * 32 * kScratchRow, "places' and rows' marks fit");
 };
 enum BarsA { kKFullA = 0, kKEmptyA = kKFullA + kMaxStages, kVFullA = kKEmptyA + kMaxStages, kVEmptyA = kVFullA + kMaxStages,
              kQFullA = kVEmptyA + kMaxStages, kQEmptyA, kSFull, kPFull = kSFull + 2,
              kPvDone = kPFull + 2, kOEmpty = kPvDone + 2, kMerge, kSlotFull, kSlotEmpty = kSlotFull + kSlots, kDrainA = kSlotEmpty + kSlots,
              kNumBarsA };
-static_assert(kNumBarsA <= 64, "barriers fit");
+static_assert(kNumBarsA <= kBarSet, "barriers fit");
 
 struct MiscA {
   uint32_t tmem_base;
   int abort_flag;
   int soft_dead;  // a softmax warp gave up
+  int careful;    // some row's result is not finite though its scores are
+  int bad[2];     // (careful) whether a tile has a value that is not finite
   int issued[2];  // key and value tiles whose copies were issued
   int begin[4];   // the request of the stretch's first unit: number, tokens, first token, length
   unsigned long long rem;
   unsigned long long warp_units[kThreadsA / 32];
-  uint32_t again[kRowsA / 32];  // rows to form again
+  uint32_t odd[kRowsA / 32];  // rows whose result is not finite
 };
 
 // A warp's way through the planned tiles: all its lanes call next() for each
@@ -372,6 +379,31 @@ struct Walk {
 };
 
 static_assert(sizeof(MiscA) <= 256, "fits its place");
+
+// The barriers of a run over the stretch, by one thread.
+__device__ __forceinline__ void init_bars(uint64_t* bars) {
+  for (int s = 0; s < kMaxStages; ++s) {
+    mbar_init(&bars[kKFullA + s], 1);
+    mbar_init(&bars[kKEmptyA + s], 1);
+    mbar_init(&bars[kVFullA + s], 1);
+    mbar_init(&bars[kVEmptyA + s], 1);
+  }
+  mbar_init(&bars[kQFullA], 1);
+  mbar_init(&bars[kQEmptyA], 1);
+  for (int s = 0; s < 2; ++s) {
+    mbar_init(&bars[kSFull + s], 1);
+    mbar_init(&bars[kPFull + s], kSoftWarps);
+    mbar_init(&bars[kPvDone + s], 1);
+  }
+  mbar_init(&bars[kOEmpty], kSoftWarps);
+  mbar_init(&bars[kMerge], kSoftWarps);
+  mbar_init(&bars[kDrainA], 1);
+  for (int s = 0; s < kSlots; ++s) {
+    mbar_init(&bars[kSlotFull + s], 1);
+    mbar_init(&bars[kSlotEmpty + s], kSlotUsers);
+  }
+  fence_mbar_init();
+}
 
 // What a row's softmax needs of its segment.
 struct RowState {
@@ -488,9 +520,9 @@ __device__ __forceinline__ bool soft_tile(uint32_t half_s, uint32_t half_o, cons
 // the halves join in registers; copies lie in other lanes and join through
 // shared memory, which also turns the rows so that four lanes write one row's
 // columns (row by row a thread would write pieces of 32 rows at a time: 4 us a
-// segment against 1).  Sets `again` for rows with a value that is not finite.
+// segment against 1).  Sets `odd` for rows with a value that is not finite.
 template <typename T, int D, int F>
-__device__ __forceinline__ bool write_rows(const TreeArgs& a, uint32_t tmem_o, float* scratch, uint32_t* again, int half, float g0,
+__device__ __forceinline__ bool write_rows(const TreeArgs& a, uint32_t tmem_o, float* scratch, uint32_t* odd_rows, int half, float g0,
                                            float g1, int rows, int tok0, int kvh, uint32_t slot) {
   constexpr int kPer = kRowsA / F, kItems = 4 / F;  // rows, items (a row's four columns) of a thread
   const int tid = threadIdx.x, lane = tid & 31, in_half = tid & (kRowsA - 1);
@@ -558,64 +590,51 @@ __device__ __forceinline__ bool write_rows(const TreeArgs& a, uint32_t tmem_o, f
 #pragma unroll
   for (int i = 0; i < kItems; ++i)
     if (row[i] < rows && !(worst[i] < INFINITY)) {
-      atomicOr(&again[row[i] >> 5], 1u << (row[i] & 31));
+      atomicOr(&odd_rows[row[i] >> 5], 1u << (row[i] & 31));
       odd = true;
     }
   return odd;
 }
 
-// A row whose result is not finite although its scores are: some value that
-// it does not see (or whose weight is zero) is an infinity or NaN.  The warp
-// forms the row again, place by place, from what the row sees alone: o[e] for
-// element lane * D / 32 + e.
-template <typename T, int D>
-__device__ __noinline__ void row_again(const TreeArgs& a, const volatile uint32_t* head, int row, const RowState st, float m, float c,
-                                       float inv, float (&o)[D / 32]) {
-  const int lane = (int)lane_id();
-  constexpr int kE = D / 32;
-  const int t = (int)head[kHTok0] + st.token, kvh = (int)head[kHHead], r = (int)head[kHReq];
-  const int h = kvh * a.group + row % a.group;
-  const bool tree = a.mask != nullptr, lists = a.pages != nullptr;
-  const float cs = a.scale < 0.f ? -c : c;
-  float q[kE];
-  const T* qp = static_cast<const T*>(a.q) + (int64_t)t * a.q_ts + (int64_t)h * a.q_hs + lane * kE;
+// Values that are not finite.  A weight of zero does not take an infinity or
+// NaN out of the tensor core's sum, so a row can come out not finite because of
+// a value that it does not see.  That shows at the segment's end; the CTA then
+// goes through its stretch a second time, carefully: it takes such values out
+// of each value tile before the product, marks their places' columns, and adds
+// up for each row the marks of the places that it sees, which say what those
+// columns are.  That costs a CTA's stretch two to three times its usual time,
+// more where nearly every place holds one (64 requests of 8 tokens over 8,192
+// places: 219 us, 690 with one such value a request, 3.1 ms with one a place).
+
+// 64 columns of a place, as they lie in shared memory (16-byte pieces in the
+// order of the 128-byte swizzle): zeros in the stead of infinities and NaN,
+// marked in pos (+inf), neg (-inf) or both (NaN).
+template <typename T>
+__device__ __forceinline__ bool take_out(uint4* v, int place, uint32_t (&pos)[2], uint32_t (&neg)[2]) {
+  constexpr uint32_t kExp = Num<T>::kBf16 ? 0x7F80u : 0x7C00u;
+  pos[0] = pos[1] = neg[0] = neg[1] = 0u;
+  bool any = false;
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    uint4 x = v[k];
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+    bool here = false;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) q[e] = (float)qp[e], o[e] = 0.f;
-  const int64_t list = (int64_t)head[kHList];
-  const int lh = lists ? kvh / (a.kv_heads / a.lists) : 0;
-  const int count = lists ? min(a.counts[(int64_t)head[kHTok0] * a.lists + lh], (int)head[kHTokens] * a.per) : 0;
-  const int64_t end = (int64_t)(int)head[kHEnd] * kTile;
-  for (int64_t at = (int64_t)(int)head[kHFirst] * kTile; at < end; ++at) {
-    int64_t place = at, blk = -1;
-    uint32_t tokens = 0xFFFFFFFFu;
-    if (lists) {
-      const int64_t e = at / a.page;
-      if (e >= count) break;
-      const ListEntry en = a.entries[list + e];
-      blk = en.block, tokens = en.tokens;
-      place = (int64_t)en.page * a.page + at % a.page;
-    } else if (place < st.len) {
-      blk = a.bt[r * a.bt_stride + place / a.page];
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+      if ((h & kExp) == kExp) {
+        const int col = 8 * (k ^ (place & 7)) + e;
+        const uint32_t bit = 1u << (col & 31);
+        const bool nan = (h & 0x7FFFu) != kExp;
+        if (nan || !(h & 0x8000u)) pos[col >> 5] |= bit;
+        if (nan || (h & 0x8000u)) neg[col >> 5] |= bit;
+        w[e >> 1] &= ~(0xFFFFu << (16 * (e & 1)));
+        here = true;
+      }
     }
-    if (blk < 0 || blk >= a.num_blocks || place >= st.len) continue;
-    const int pos = (int)(place / kGroup * kGroup);
-    if (!((group_bits(pos, tokens, st, tree, lists) >> (int)(place - pos)) & 1u)) continue;
-    const int64_t from = blk * a.c_bs + place % a.page * a.c_ts + (int64_t)kvh * a.c_hs + lane * kE;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) s = fmaf(q[e], (float)static_cast<const T*>(a.kc)[from + e], s);
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    const float p = ex2(s * cs - m * c);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const float vv = (float)static_cast<const T*>(a.vc)[from + e];
-      // a weight below the smallest number still carries an infinity's sign
-      o[e] = fmaf(p == 0.f && isinf(vv) ? 1.f : p, vv, o[e]);
-    }
+    if (here) v[k] = x, any = true;
   }
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] *= inv;
+  return any;
 }
 
 template <typename T, int D>
@@ -639,28 +658,9 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     misc->abort_flag = 0;
     misc->soft_dead = 0;
     misc->issued[0] = misc->issued[1] = 0;
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&bars[kKFullA + s], 1);
-      mbar_init(&bars[kKEmptyA + s], 1);
-      mbar_init(&bars[kVFullA + s], 1);
-      mbar_init(&bars[kVEmptyA + s], 1);
-    }
-    for (int s = 0; s < kRowsA / 32; ++s) misc->again[s] = 0;
-    mbar_init(&bars[kQFullA], 1);
-    mbar_init(&bars[kQEmptyA], 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars[kSFull + s], 1);
-      mbar_init(&bars[kPFull + s], kSoftWarps);
-      mbar_init(&bars[kPvDone + s], 1);
-    }
-    mbar_init(&bars[kOEmpty], kSoftWarps);
-    mbar_init(&bars[kMerge], kSoftWarps);
-    mbar_init(&bars[kDrainA], 1);
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&bars[kSlotFull + s], 1);
-      mbar_init(&bars[kSlotEmpty + s], kSlotUsers);
-    }
-    fence_mbar_init();
+    misc->careful = misc->bad[0] = misc->bad[1] = 0;
+    for (int s = 0; s < kRowsA / 32; ++s) misc->odd[s] = 0;
+    init_bars(bars);
   }
   if (tid == 32) {  // a cold descriptor costs a copy a microsecond
     asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
@@ -724,295 +724,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     __syncthreads();
   }
 
-  if (warp == kPlanWarp) {
-    const bool some = w0 < w1;
-    int r = some ? misc->begin[0] : 0, n = some ? misc->begin[1] : 0, t0 = some ? misc->begin[2] : 0, s = some ? misc->begin[3] : 0;
-    unsigned long long rem = some ? misc->rem : 0;
-    // and its block, head and tile; all lanes hold the same cursor
-    int b = 0, kvh = 0;
-    const int per_list = lists ? a.kv_heads / a.lists : a.kv_heads;
-    int tiles = some ? plan.tiles(s, n, t0, 0, 0) : 0;
-    while (some && rem >= (unsigned)(kSegCost + tiles)) {
-      rem -= (unsigned)(kSegCost + tiles);
-      if (++kvh == a.kv_heads) kvh = 0, ++b;
-      tiles = plan.tiles(s, n, t0, b, kvh / per_list);
-    }
-    // the segment's units begin at u0; the stretch's part of it are the tiles from `tile` on
-    unsigned long long u0 = w0 - rem;
-    int tile = max(0, (int)rem - kSegCost);
-    const int bs = min(a.page, kTile), boxes = kTile / bs;  // places of a box, boxes of a tile
-    const int page_tiles = max(1, a.page / kTile);
-    // the segment that the stretch begins in, for its note below
-    const int tile0 = tile, tiles0 = tiles, rows0 = min(a.block_tokens, n - b * a.block_tokens) * a.group, kvh0 = kvh;
-    const int tok00 = t0 + b * a.block_tokens;
-    const unsigned long long u00 = u0;
-    int seg = 0, piece_first = tile, chunk = 0;
-    bool bad_block = false, gave_up = false;
-    while (some && u0 < w1) {
-      // tiles of the segment up to the stretch's end
-      const int piece_end = (int)min((unsigned long long)tiles, w1 > u0 + kSegCost ? w1 - u0 - kSegCost : 0ull);
-      if (tile >= piece_end) break;  // the stretch ends before the segment's first tile
-      const int len = plan.len(s), ctx = s - n;
-      const int m = min(a.block_tokens, n - b * a.block_tokens), tok = t0 + b * a.block_tokens;
-      const int rows = m * a.group;
-      const int fold_code = rows <= kRowsA / 4 ? 2 : rows <= kRowsA / 2 ? 1 : 0;
-      const int lh = lists ? kvh / per_list : 0;
-      const int64_t list = ((int64_t)tok * a.lists + (int64_t)lh * m) * a.per;
-      const int entries = lists ? min(a.counts[(int64_t)tok * a.lists + lh], m * a.per) : 0;
-      const int here = min(kChunk, piece_end - tile);  // tiles of this chunk
-      const int slot = chunk % kSlots;
-      const bool ok = chunk < kSlots || timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag,
-                                                        a.status, a.polls);
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        gave_up = true;
-        break;
-      }
-      uint32_t* head = recs + slot * kSlotWords;
-      if (lane == 31) {
-        head[kHTiles] = (uint32_t)here, head[kHTok0] = (uint32_t)tok, head[kHTokens] = (uint32_t)m, head[kHHead] = (uint32_t)kvh;
-        head[kHCtx] = (uint32_t)ctx, head[kHNew] = (uint32_t)n, head[kHNode0] = (uint32_t)(b * a.block_tokens);
-        head[kHLen] = (uint32_t)len, head[kHReq] = (uint32_t)r, head[kHFirst] = (uint32_t)piece_first;
-        head[kHEnd] = (uint32_t)piece_end, head[kHList] = (uint32_t)list, head[kHFold] = (uint32_t)fold_code;
-        // partial results: slot 2x for the first segment of stretch x, 2x + 1 for the last; -1: the whole segment is here
-        head[kHOut] = piece_first == 0 && piece_end == tiles ? 0xFFFFFFFFu : (uint32_t)(2 * blockIdx.x + (seg > 0 ? 1 : 0));
-      }
-      if (lane < here) {
-        const int my = tile + lane;
-        uint32_t* rec = head + (1 + lane) * kRecWords;
-        const uint32_t every = m >= 32 ? 0xFFFFFFFFu : (1u << m) - 1u;
-        const int page0 = boxes > 1 ? my * boxes : my / page_tiles, offset = boxes > 1 ? 0 : (my % page_tiles) * kTile;
-        bool all_cached = true, all_tokens = true;
-        for (int x = 0; x < boxes; ++x) {
-          int blk = -1, pg = page0 + x;
-          uint32_t tokens = 0xFFFFFFFFu;
-          if (lists) {
-            if (pg < entries) {
-              const ListEntry en = a.entries[list + pg];
-              blk = en.block, pg = en.page, tokens = en.tokens;
-            }
-          } else if ((int64_t)pg * a.page < len) {
-            blk = a.bt[r * a.bt_stride + pg];
-            if (blk < 0 || blk >= a.num_blocks) bad_block = true, blk = -1;
-          }
-          rec[kRBox + x] = (uint32_t)(blk < 0 ? (int)a.num_blocks : blk);  // a block outside the pool reads as zeros
-          const int pos = pg * a.page + offset;
-          all_cached = all_cached && blk >= 0 && (int64_t)pos + bs <= ctx && (int64_t)pos + bs <= len;
-          all_tokens = all_tokens && (tokens & every) == every;
-          for (int g = 0; g < bs / kGroup; ++g) {
-            rec[kRPos + x * (bs / kGroup) + g] = (uint32_t)(blk < 0 ? -1 : pos + g * kGroup);
-            rec[kRMask + x * (bs / kGroup) + g] = tokens;
-          }
-        }
-        const int kind = all_cached && all_tokens ? kFull : all_cached && boxes == 1 ? kRowMask : kGeneral;
-        rec[kROffset] = (uint32_t)offset;
-        rec[kRFlags] = (uint32_t)((my == piece_first ? kFlagFirst : 0) | (my + 1 == piece_end ? kFlagLast : 0) | (kind << kKindShift));
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kSlotFull + slot]);
-      ++chunk;
-      tile += here;
-      if (tile == tiles) {
-        // next segment
-        u0 += (unsigned)(kSegCost + tiles);
-        tile = 0;
-        piece_first = 0;
-        ++seg;
-        if (++kvh == a.kv_heads) {
-          kvh = 0;
-          if (++b >= plan.blocks(n)) {
-            b = 0;
-            do {
-              ++r;
-              n = r < a.num_reqs ? plan.ntok(r) : 0;
-            } while (r < a.num_reqs && n == 0);
-            if (r < a.num_reqs) t0 = plan.tok0(r), s = plan.seq(r);
-          }
-        }
-        if (u0 < w1) tiles = plan.tiles(s, n, t0, b, kvh / per_list);
-      } else if (tile == piece_end) {
-        break;
-      }
-    }
-    if (!gave_up) {
-      const int slot = chunk % kSlots;
-      const bool ok =
-          timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag, a.status, a.polls);
-      if (__all_sync(0xFFFFFFFFu, ok) && lane == 0) {
-        recs[slot * kSlotWords + kHTiles] = 0;  // the end
-        mbar_arrive(&bars[kSlotFull + slot]);
-      }
-      __syncwarp();
-    }
-    if (lane == 0) {
-      int32_t* cut = a.cuts + 8 * blockIdx.x;
-      int rows = 0;
-      if (some && tile0 > 0) {
-        // stretch y begins at unit W y / ctas and holds unit u for y = ((u + 1) ctas - 1) / W
-        const unsigned long long ctas = gridDim.x, u1 = u00 + kSegCost + tiles0;
-        const int from = (int)((w0 * ctas - 1) / W), to = (int)((u1 * ctas - 1) / W);
-        const unsigned long long begin = W * from / ctas;
-        if (begin <= u00 + kSegCost) {  // else the segment was cut before
-          rows = rows0;
-          cut[kCTok0] = tok00, cut[kCHead] = kvh0, cut[kCFrom] = from, cut[kCTo] = to;
-          // slot 2y, but 2y + 1 where the segment is not its stretch's first
-          cut[kCSlot] = 2 * from + (u00 > begin ? 1 : 0);
-          cut[kCHoles] = W < ctas ? 1 : 0;
-        }
-      }
-      cut[kCRows] = rows;
-    }
-    if (bad_block) report(a.status, IDX_ST_BLOCK_OOR);
-  } else if (warp == kKeyTma || warp == kValueTma) {
-    const bool keys = warp == kKeyTma;
-    const CUtensorMap* map = keys ? &kmap : &vmap;
-    const int bs = min(a.page, kTile), boxes = kTile / bs;
-    const int bx = lane % boxes, sub = lane / boxes;
-    const bool mine = lane < boxes * (D / 64);
-    const int stages = keys ? Ring<D>::kKeys : Ring<D>::kValues;
-    uint64_t *full = &bars[keys ? kKFullA : kVFullA], *empty = &bars[keys ? kKEmptyA : kVEmptyA];
-    uint8_t* dst = smem + (keys ? S::kOffKv : S::kOffV) + sub * (kTile * 128) + bx * bs * 128;
-    Walk w(recs, bars, abort_flag, a.status, a.polls);
-    int i = 0, stage = 0;
-    uint32_t phase = 0;
-    for (; w.next(); ++i) {
-      const int kvh = (int)w.head[kHHead], offset = (int)w.rec[kROffset], box = (int)w.rec[kRBox + bx];
-      const bool ok = timed_wait_flag(&empty[stage], phase ^ 1u, abort_flag, a.status, a.polls);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)S::kKv);
-      __syncwarp();
-      if (mine) tma_load_4d(dst + stage * S::kKv, map, sub * 64, kvh, offset, box, &full[stage]);
-      w.done();
-      if (++stage == stages) stage = 0, phase ^= 1u;
-    }
-    if (lane == 0) misc->issued[keys ? 0 : 1] = i;
-  } else if (warp == kQueryTma) {
-    Walk w(recs, bars, abort_flag, a.status, a.polls);
-    int queries = 0;
-    while (w.next()) {
-      if (w.rec[kRFlags] & kFlagFirst) {
-        for (int k = lane; k < (int)w.head[kHTokens] * (D / 64); k += 32)  // into L2 while the queries before are in use
-          asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(&qmap), "r"(k % (D / 64) * 64),
-                       "r"((int)w.head[kHHead] * a.group), "r"((int)w.head[kHTok0] + k / (D / 64))
-                       : "memory");
-        bool ok = true;
-        if (queries > 0) ok = timed_wait_flag(&bars[kQEmptyA], (uint32_t)(queries - 1) & 1u, abort_flag, a.status, a.polls);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        const int m = (int)w.head[kHTokens], fold = 1 << (int)w.head[kHFold], tok = (int)w.head[kHTok0], kvh = (int)w.head[kHHead];
-        const int loads = m * fold * (D / 64);
-        if (lane == 0) mbar_arrive_expect_tx(&bars[kQFullA], (uint32_t)(loads * a.group * 128));
-        __syncwarp();
-        for (int k = lane; k < loads; k += 32) {
-          const int sub = k % (D / 64), tk = k / (D / 64) % m, copy = k / (D / 64) / m;
-          tma_load_3d(smem + S::kOffQ + sub * (kRowsA * 128) + (copy * (kRowsA / fold) + tk * a.group) * 128, &qmap, sub * 64,
-                      kvh * a.group, tok + tk, &bars[kQFullA]);
-        }
-        ++queries;
-      }
-      w.done();
-    }
-    if (lane == 0 && queries > 0) mbar_wait(&bars[kQFullA], (uint32_t)(queries - 1) & 1u, nullptr);
-  } else if (warp == kMmaWarpA) {
-    constexpr uint32_t kIdS = idesc_16(Num<T>::kBf16, kRowsA, kTile, false);
-    constexpr uint32_t kIdO = idesc_16(Num<T>::kBf16, kRowsA, D, true);
-    Walk w(recs, bars, abort_flag, a.status, a.polls);
-    // A barrier's test takes 200-300 cycles even where the phase is long
-    // complete; one after another this warp's tests (up to six a tile) set the
-    // pace, 2,850 cycles a tile.  So its lanes test all that the next scores (of
-    // tile i) and the next rows (of tile j) wait for at once, a barrier a lane,
-    // and whatever is ready is issued (64 drafted tokens over 65,536 places:
-    // 168 -> 161 us; one token over 5,000: 16.5 -> 16.1).
-    int i = 0, j = 0;              // tiles whose scores, whose rows have been issued
-    int seg_s = 0, seg_o = 0;      // segments whose scores, whose rows have been issued
-    uint32_t flags[3] = {};        // of tiles i, i - 1, i - 2
-    int k_stage = 0, v_stage = 0;
-    uint32_t k_phase = 0, v_phase = 0;
-    bool issued = false;
-    bool more = w.next();
-    if (more) flags[0] = w.rec[kRFlags], w.done();
-    const uint64_t limit = a.polls == 0 ? 1ull : (uint64_t)a.polls << 10;
-    uint64_t idle = 0;  // tests since the last issue
-    while (more || j < i) {
-      const uint32_t row_flags = i - j == 2 ? flags[2] : flags[1];  // of tile j
-      int bar = -1;       // nothing to wait for
-      uint32_t phase = 0;
-      if (lane == 0) bar = kKFullA + k_stage, phase = k_phase;
-      if (lane == 1 && i >= 2) bar = kPvDone + (i & 1), phase = (uint32_t)((i >> 1) - 1) & 1u;  // the weights of tile i - 2 are read
-      if (lane == 2 && (flags[0] & kFlagFirst)) bar = kQFullA, phase = (uint32_t)seg_s & 1u;
-      if (lane == 3) bar = kVFullA + v_stage, phase = v_phase;
-      if (lane == 4) bar = kPFull + (j & 1), phase = (uint32_t)(j >> 1) & 1u;
-      if (lane == 5 && (row_flags & kFlagFirst) && seg_o > 0) bar = kOEmpty, phase = (uint32_t)(seg_o - 1) & 1u;  // the rows before are read
-      const bool ready = bar < 0 || mbar_try_wait_nosuspend(&bars[bar], phase);
-      const uint32_t got = __ballot_sync(0xFFFFFFFFu, ready);
-      const bool do_scores = more && (got & 7u) == 7u;
-      // scores come first: rows wait while all that scores lack is the end of
-      // the product just issued, or the next softmax would wait instead
-      const bool hold = more && i - j == 1 && (got & 7u) == 5u;
-      const bool do_rows = j < i && (got & 0x38u) == 0x38u && !hold;
-      if (!do_rows && !do_scores) {
-        const bool stop = ++idle >= limit || ((idle & 63u) == 0 && *abort_flag);
-        if (__any_sync(0xFFFFFFFFu, stop)) {
-          if (lane == 0 && !*abort_flag) {
-            *abort_flag = 1;
-            report(a.status, IDX_ST_TIMEOUT);
-          }
-          break;
-        }
-        continue;
-      }
-      idle = 0;
-      __syncwarp();  // what each lane has seen complete is so for the lane that issues
-      tc_fence_after();
-      if (lane == 0) {
-        if (do_scores) {
-          const uint64_t qd = sw128_desc(sbase + S::kOffQ), kd = sw128_desc(sbase + S::kOffKv + k_stage * S::kKv);
-          const uint32_t d = tmem + kColS + (uint32_t)(i & 1) * kTile;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t step = (uint64_t)((k / 4) * (kRowsA * 128 / 16) + (k % 4) * 2);
-            mma_16(d, qd + step, kd + step, kIdS, k > 0 ? 1u : 0u);
-          }
-          // a tile's stage is given back before anybody can learn that the
-          // tile is done: the ring's waits count on that order
-          mma_commit(&bars[kKEmptyA + k_stage]);
-          if (flags[0] & kFlagLast) mma_commit(&bars[kQEmptyA]);
-          mma_commit(&bars[kSFull + (i & 1)]);
-        }
-        if (do_rows) {
-          const uint64_t vd = sw128_desc_nmajor(sbase + S::kOffV + v_stage * S::kKv);
-          const uint32_t p = tmem + kColS + (uint32_t)(j & 1) * kTile, old = row_flags & kFlagFirst ? 0u : 1u;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) {
-            const int half = k / (kHalf / 16);
-            mma_16_ta(tmem + kColO + (uint32_t)(half * D), p + (uint32_t)(half * kHalf + 8 * (k % (kHalf / 16))),
-                      vd + (uint64_t)(k * (2048 / 16)), kIdO, k % (kHalf / 16) > 0 ? 1u : old);
-          }
-          mma_commit(&bars[kVEmptyA + v_stage]);
-          mma_commit(&bars[kPvDone + (j & 1)]);
-        }
-      }
-      __syncwarp();
-      issued = true;
-      if (do_rows) {
-        if (row_flags & kFlagLast) ++seg_o;
-        if (++v_stage == Ring<D>::kValues) v_stage = 0, v_phase ^= 1u;
-        ++j;
-      }
-      if (do_scores) {
-        if (flags[0] & kFlagLast) ++seg_s;
-        if (++k_stage == Ring<D>::kKeys) k_stage = 0, k_phase ^= 1u;
-        ++i;
-        flags[2] = flags[1], flags[1] = flags[0];
-        more = w.next();
-        if (more) flags[0] = w.rec[kRFlags], w.done();
-        else if (!w.ended) break;
-      }
-    }
-    if (issued) {
-      if (lane == 0) mma_commit(&bars[kDrainA]);
-      __syncwarp();
-      mbar_wait(&bars[kDrainA], 0, nullptr);
-    }
-  } else if (warp < kSoftWarps) {
+  // The softmax warps' part of a run.  A careful run is code of its own, so that
+  // the usual one has none of it in its loop.
+  auto softmax_role = [&](auto how) {
+    constexpr bool kCareful = decltype(how)::value;
     const int lane_row = tid & (kRowsA - 1), half = warp >> 2;
     const uint32_t tmem_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t half_o = tmem_row + kColO + (uint32_t)(half * D);
@@ -1023,9 +738,23 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
     float m = -INFINITY, l = 0.f;
     RowState st{};
-    int seg = 0;
+    int meets = 0;
     int row = 0, copy = 0, fold = 1, col0 = 0, rows = 0;
     bool warp_live = true, met = false;
+    // All eight warps meet, those that gave up among them (see below); the wait
+    // ends for all or for none, so that no warp misses a later barrier.  False:
+    // one gave up.
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kMerge]);
+      const bool all = mbar_wait(&bars[kMerge], (uint32_t)meets & 1u, nullptr);
+      ++meets;
+      return __all_sync(0xFFFFFFFFu, all) && !*reinterpret_cast<volatile int*>(&misc->soft_dead);
+    };
+    uint32_t* place_marks = reinterpret_cast<uint32_t*>(scratch);  // [place][+ columns, - columns]
+    uint32_t* row_marks = place_marks + kTile * S::kMarkWords;
+    if (kCareful)
+      for (int k = tid; k < kRowsA * S::kMarkWords; k += kSoftWarps * 32) row_marks[k] = 0;
     Walk w(recs, bars, abort_flag, a.status, a.polls);
     for (int i = 0; w.next(); ++i) {
       const uint32_t s_par = (uint32_t)(i >> 1) & 1u;
@@ -1078,6 +807,41 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         }
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
       }
+      if constexpr (kCareful) {
+        const int stage = i % Ring<D>::kValues;
+        ok = timed_wait_flag(&bars[kVFullA + stage], (uint32_t)(i / Ring<D>::kValues) & 1u, abort_flag, a.status, a.polls);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if (half < D / 64) {
+          uint32_t pos[2], neg[2];
+          uint4* v = reinterpret_cast<uint4*>(smem + S::kOffV + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
+          if (take_out<T>(v, lane_row, pos, neg)) misc->bad[i & 1] = 1;
+          uint32_t* mark = place_marks + lane_row * S::kMarkWords + 2 * half;
+          mark[0] = pos[0], mark[1] = pos[1], mark[D / 32] = neg[0], mark[D / 32 + 1] = neg[1];
+          fence_proxy_async_smem();
+        }
+        if (!meet()) {
+          met = true;
+          break;
+        }
+        if (*reinterpret_cast<volatile int*>(&misc->bad[i & 1]) && row < rows) {
+          // the marks of this thread's places that the row sees
+          const int kind = (flags >> kKindShift) & 3;
+          for (int p = col0; p < col0 + kHalf / fold; ++p) {
+            bool seen = kind == kFull || (kind == kRowMask && ((rec[kRMask] >> st.token) & 1u));
+            if (kind == kGeneral)
+              seen = (group_bits((int)rec[kRPos + p / kGroup], rec[kRMask + p / kGroup], st, tree, lists) >> (p % kGroup)) & 1u;
+            for (int k = 0; seen && k < S::kMarkWords; ++k) {
+              const uint32_t x = place_marks[p * S::kMarkWords + k];
+              if (x) atomicOr(&row_marks[row * S::kMarkWords + k], x);
+            }
+          }
+        }
+        if (tid == 0) misc->bad[(i + 1) & 1] = 0;
+        if (!meet()) {
+          met = true;
+          break;
+        }
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -1092,13 +856,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       stats[tid] = make_float2(m, l);
-      // All eight warps meet, those that gave up among them (see below); the
-      // wait ends for all or for none, so that no warp misses a later barrier.
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kMerge]);
-      ok = mbar_wait(&bars[kMerge], (uint32_t)seg & 1u, nullptr);
-      ++seg;
-      if (!__all_sync(0xFFFFFFFFu, ok) || *reinterpret_cast<volatile int*>(&misc->soft_dead)) {
+      if (!meet()) {
         met = true;
         break;
       }
@@ -1131,34 +889,41 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         else if (a.lse != nullptr)
           a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + __log2f(sum_l)) * 0.6931471805599453f;
       }
-      bool odd;
-      if (fold == 4) odd = write_rows<T, D, 4>(a, tmem_row + kColO, scratch, misc->again, half, g0, g1, rows, tok0, kvh, slot);
-      else if (fold == 2) odd = write_rows<T, D, 2>(a, tmem_row + kColO, scratch, misc->again, half, g0, g1, rows, tok0, kvh, slot);
-      else odd = write_rows<T, D, 1>(a, tmem_row + kColO, scratch, misc->again, half, g0, g1, rows, tok0, kvh, slot);
-      // rows to form again, rare: see row_again
-      if (soft_any(odd)) {
-        for (int x = warp; x < rows; x += kSoftWarps) {
-          if (!((*reinterpret_cast<volatile uint32_t*>(&misc->again[x >> 5]) >> (x & 31)) & 1u)) continue;
-          RowState z = st;
-          z.token = x / a.group;
-          z.chain_end = st.ctx + (int)head[kHNode0] + z.token + 1;
-          const int n = (int)head[kHNew];
-          z.tree = tree ? a.mask[(int)head[kHTok0] + z.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
-          float zl, o[D / 32];
-          const float zm = row_of(x, zl);
-          if (!(zl > 0.f && zl < INFINITY)) continue;  // its scores are not finite either
-          row_again<T, D>(a, head, x, z, zm, c, direct ? 1.f / zl : 1.f, o);
-          const int zt = tok0 + z.token, zh = kvh * a.group + x % a.group;
-          T* zo = static_cast<T*>(a.out) + (int64_t)zt * a.o_ts + (int64_t)zh * a.o_hs;
-          float* zp = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + x) * D;
+      const bool sum_ok = sum_l > 0.f && sum_l < INFINITY;  // else its scores are not finite, or it sees nothing
+      uint32_t pos[D / 64] = {}, neg[D / 64] = {};  // marks of the row's columns of this half
+      if constexpr (kCareful) {
+        if (row < rows && copy == 0 && sum_ok) {
 #pragma unroll
-          for (int e = 0; e < D / 32; e += 2) {
-            if (direct) *reinterpret_cast<uint32_t*>(zo + lane * (D / 32) + e) = Num<T>::pack(o[e], o[e + 1]);
-            else *reinterpret_cast<float2*>(zp + lane * (D / 32) + e) = make_float2(o[e], o[e + 1]);
+          for (int k = 0; k < D / 64; ++k) {
+            pos[k] = row_marks[row * S::kMarkWords + half * (D / 64) + k];
+            neg[k] = row_marks[row * S::kMarkWords + D / 32 + half * (D / 64) + k];
           }
         }
+        soft_sync();  // the scratch is free
+      }
+      bool odd;
+      if (fold == 4) odd = write_rows<T, D, 4>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
+      else if (fold == 2) odd = write_rows<T, D, 2>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
+      else odd = write_rows<T, D, 1>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
+      if constexpr (kCareful) {
+        soft_sync();  // the rows are written
+        const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
+        T* to = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs + half * (D / 2);
+        float* part = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row) * D + half * (D / 2);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          for (uint32_t left = pos[k] | neg[k]; left; left &= left - 1u) {
+            const int e = __ffs((int)left) - 1;
+            const bool up = (pos[k] >> e) & 1u, down = (neg[k] >> e) & 1u;
+            const float x = up && down ? NAN : up ? INFINITY : -INFINITY;
+            if (direct) to[32 * k + e] = (T)x;
+            else part[32 * k + e] = x;
+          }
+        for (int k = tid; k < kRowsA * S::kMarkWords; k += kSoftWarps * 32) row_marks[k] = 0;
+      } else if (soft_any(odd)) {  // rare
+        if (row < rows && sum_ok && ((*reinterpret_cast<volatile uint32_t*>(&misc->odd[row >> 5]) >> (row & 31)) & 1u)) misc->careful = 1;
         soft_sync();
-        if (tid < kRowsA / 32) misc->again[tid] = 0;
+        if (tid < kRowsA / 32) misc->odd[tid] = 0;
         soft_sync();
       }
       tc_fence_before();
@@ -1171,6 +936,314 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       *reinterpret_cast<volatile int*>(&misc->soft_dead) = 1;
       mbar_arrive(&bars[kMerge]);
     }
+  };
+
+  // once, or a second time where some value was not finite (see take_out)
+  bool careful = false;
+#pragma unroll 1
+  for (;;) {
+    if (warp == kPlanWarp) {
+      const bool some = w0 < w1;
+      int r = some ? misc->begin[0] : 0, n = some ? misc->begin[1] : 0, t0 = some ? misc->begin[2] : 0, s = some ? misc->begin[3] : 0;
+      unsigned long long rem = some ? misc->rem : 0;
+      // and its block, head and tile; all lanes hold the same cursor
+      int b = 0, kvh = 0;
+      const int per_list = lists ? a.kv_heads / a.lists : a.kv_heads;
+      int tiles = some ? plan.tiles(s, n, t0, 0, 0) : 0;
+      while (some && rem >= (unsigned)(kSegCost + tiles)) {
+        rem -= (unsigned)(kSegCost + tiles);
+        if (++kvh == a.kv_heads) kvh = 0, ++b;
+        tiles = plan.tiles(s, n, t0, b, kvh / per_list);
+      }
+      // the segment's units begin at u0; the stretch's part of it are the tiles from `tile` on
+      unsigned long long u0 = w0 - rem;
+      int tile = max(0, (int)rem - kSegCost);
+      const int bs = min(a.page, kTile), boxes = kTile / bs;  // places of a box, boxes of a tile
+      const int page_tiles = max(1, a.page / kTile);
+      // the segment that the stretch begins in, for its note below
+      const int tile0 = tile, tiles0 = tiles, rows0 = min(a.block_tokens, n - b * a.block_tokens) * a.group, kvh0 = kvh;
+      const int tok00 = t0 + b * a.block_tokens;
+      const unsigned long long u00 = u0;
+      int seg = 0, piece_first = tile, chunk = 0;
+      bool bad_block = false, gave_up = false;
+      while (some && u0 < w1) {
+        // tiles of the segment up to the stretch's end
+        const int piece_end = (int)min((unsigned long long)tiles, w1 > u0 + kSegCost ? w1 - u0 - kSegCost : 0ull);
+        if (tile >= piece_end) break;  // the stretch ends before the segment's first tile
+        const int len = plan.len(s), ctx = s - n;
+        const int m = min(a.block_tokens, n - b * a.block_tokens), tok = t0 + b * a.block_tokens;
+        const int rows = m * a.group;
+        const int fold_code = rows <= kRowsA / 4 ? 2 : rows <= kRowsA / 2 ? 1 : 0;
+        const int lh = lists ? kvh / per_list : 0;
+        const int64_t list = ((int64_t)tok * a.lists + (int64_t)lh * m) * a.per;
+        const int entries = lists ? min(a.counts[(int64_t)tok * a.lists + lh], m * a.per) : 0;
+        const int here = min(kChunk, piece_end - tile);  // tiles of this chunk
+        const int slot = chunk % kSlots;
+        const bool ok = chunk < kSlots || timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag,
+                                                          a.status, a.polls);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          gave_up = true;
+          break;
+        }
+        uint32_t* head = recs + slot * kSlotWords;
+        if (lane == 31) {
+          head[kHTiles] = (uint32_t)here, head[kHTok0] = (uint32_t)tok, head[kHTokens] = (uint32_t)m, head[kHHead] = (uint32_t)kvh;
+          head[kHCtx] = (uint32_t)ctx, head[kHNew] = (uint32_t)n, head[kHNode0] = (uint32_t)(b * a.block_tokens);
+          head[kHLen] = (uint32_t)len, head[kHFold] = (uint32_t)fold_code;
+          // partial results: slot 2x for the first segment of stretch x, 2x + 1 for the last; -1: the whole segment is here
+          head[kHOut] = piece_first == 0 && piece_end == tiles ? 0xFFFFFFFFu : (uint32_t)(2 * blockIdx.x + (seg > 0 ? 1 : 0));
+        }
+        if (lane < here) {
+          const int my = tile + lane;
+          uint32_t* rec = head + (1 + lane) * kRecWords;
+          const uint32_t every = m >= 32 ? 0xFFFFFFFFu : (1u << m) - 1u;
+          const int page0 = boxes > 1 ? my * boxes : my / page_tiles, offset = boxes > 1 ? 0 : (my % page_tiles) * kTile;
+          bool all_cached = true, all_tokens = true;
+          for (int x = 0; x < boxes; ++x) {
+            int blk = -1, pg = page0 + x;
+            uint32_t tokens = 0xFFFFFFFFu;
+            if (lists) {
+              if (pg < entries) {
+                const ListEntry en = a.entries[list + pg];
+                blk = en.block, pg = en.page, tokens = en.tokens;
+              }
+            } else if ((int64_t)pg * a.page < len) {
+              blk = a.bt[r * a.bt_stride + pg];
+              if (blk < 0 || blk >= a.num_blocks) bad_block = true, blk = -1;
+            }
+            rec[kRBox + x] = (uint32_t)(blk < 0 ? (int)a.num_blocks : blk);  // a block outside the pool reads as zeros
+            const int pos = pg * a.page + offset;
+            all_cached = all_cached && blk >= 0 && (int64_t)pos + bs <= ctx && (int64_t)pos + bs <= len;
+            all_tokens = all_tokens && (tokens & every) == every;
+            for (int g = 0; g < bs / kGroup; ++g) {
+              rec[kRPos + x * (bs / kGroup) + g] = (uint32_t)(blk < 0 ? -1 : pos + g * kGroup);
+              rec[kRMask + x * (bs / kGroup) + g] = tokens;
+            }
+          }
+          const int kind = all_cached && all_tokens ? kFull : all_cached && boxes == 1 ? kRowMask : kGeneral;
+          rec[kROffset] = (uint32_t)offset;
+          rec[kRFlags] = (uint32_t)((my == piece_first ? kFlagFirst : 0) | (my + 1 == piece_end ? kFlagLast : 0) | (kind << kKindShift));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kSlotFull + slot]);
+        ++chunk;
+        tile += here;
+        if (tile == tiles) {
+          // next segment
+          u0 += (unsigned)(kSegCost + tiles);
+          tile = 0;
+          piece_first = 0;
+          ++seg;
+          if (++kvh == a.kv_heads) {
+            kvh = 0;
+            if (++b >= plan.blocks(n)) {
+              b = 0;
+              do {
+                ++r;
+                n = r < a.num_reqs ? plan.ntok(r) : 0;
+              } while (r < a.num_reqs && n == 0);
+              if (r < a.num_reqs) t0 = plan.tok0(r), s = plan.seq(r);
+            }
+          }
+          if (u0 < w1) tiles = plan.tiles(s, n, t0, b, kvh / per_list);
+        } else if (tile == piece_end) {
+          break;
+        }
+      }
+      if (!gave_up) {
+        const int slot = chunk % kSlots;
+        const bool ok =
+            timed_wait_flag(&bars[kSlotEmpty + slot], ((uint32_t)(chunk / kSlots) & 1u) ^ 1u, abort_flag, a.status, a.polls);
+        if (__all_sync(0xFFFFFFFFu, ok) && lane == 0) {
+          recs[slot * kSlotWords + kHTiles] = 0;  // the end
+          mbar_arrive(&bars[kSlotFull + slot]);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) {
+        int32_t* cut = a.cuts + 8 * blockIdx.x;
+        int rows = 0;
+        if (some && tile0 > 0) {
+          // stretch y begins at unit W y / ctas and holds unit u for y = ((u + 1) ctas - 1) / W
+          const unsigned long long ctas = gridDim.x, u1 = u00 + kSegCost + tiles0;
+          const int from = (int)((w0 * ctas - 1) / W), to = (int)((u1 * ctas - 1) / W);
+          const unsigned long long begin = W * from / ctas;
+          if (begin <= u00 + kSegCost) {  // else the segment was cut before
+            rows = rows0;
+            cut[kCTok0] = tok00, cut[kCHead] = kvh0, cut[kCFrom] = from, cut[kCTo] = to;
+            // slot 2y, but 2y + 1 where the segment is not its stretch's first
+            cut[kCSlot] = 2 * from + (u00 > begin ? 1 : 0);
+            cut[kCHoles] = W < ctas ? 1 : 0;
+          }
+        }
+        cut[kCRows] = rows;
+      }
+      if (bad_block) report(a.status, IDX_ST_BLOCK_OOR);
+    } else if (warp == kKeyTma || warp == kValueTma) {
+      const bool keys = warp == kKeyTma;
+      const CUtensorMap* map = keys ? &kmap : &vmap;
+      const int bs = min(a.page, kTile), boxes = kTile / bs;
+      const int bx = lane % boxes, sub = lane / boxes;
+      const bool mine = lane < boxes * (D / 64);
+      const int stages = keys ? Ring<D>::kKeys : Ring<D>::kValues;
+      uint64_t *full = &bars[keys ? kKFullA : kVFullA], *empty = &bars[keys ? kKEmptyA : kVEmptyA];
+      uint8_t* dst = smem + (keys ? S::kOffKv : S::kOffV) + sub * (kTile * 128) + bx * bs * 128;
+      Walk w(recs, bars, abort_flag, a.status, a.polls);
+      int i = 0, stage = 0;
+      uint32_t phase = 0;
+      for (; w.next(); ++i) {
+        const int kvh = (int)w.head[kHHead], offset = (int)w.rec[kROffset], box = (int)w.rec[kRBox + bx];
+        const bool ok = timed_wait_flag(&empty[stage], phase ^ 1u, abort_flag, a.status, a.polls);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)S::kKv);
+        __syncwarp();
+        if (mine) tma_load_4d(dst + stage * S::kKv, map, sub * 64, kvh, offset, box, &full[stage]);
+        w.done();
+        if (++stage == stages) stage = 0, phase ^= 1u;
+      }
+      if (lane == 0) misc->issued[keys ? 0 : 1] = i;
+    } else if (warp == kQueryTma) {
+      Walk w(recs, bars, abort_flag, a.status, a.polls);
+      int queries = 0;
+      while (w.next()) {
+        if (w.rec[kRFlags] & kFlagFirst) {
+          for (int k = lane; k < (int)w.head[kHTokens] * (D / 64); k += 32)  // into L2 while the queries before are in use
+            asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(&qmap), "r"(k % (D / 64) * 64),
+                         "r"((int)w.head[kHHead] * a.group), "r"((int)w.head[kHTok0] + k / (D / 64))
+                         : "memory");
+          bool ok = true;
+          if (queries > 0) ok = timed_wait_flag(&bars[kQEmptyA], (uint32_t)(queries - 1) & 1u, abort_flag, a.status, a.polls);
+          if (!__all_sync(0xFFFFFFFFu, ok)) break;
+          const int m = (int)w.head[kHTokens], fold = 1 << (int)w.head[kHFold], tok = (int)w.head[kHTok0], kvh = (int)w.head[kHHead];
+          const int loads = m * fold * (D / 64);
+          if (lane == 0) mbar_arrive_expect_tx(&bars[kQFullA], (uint32_t)(loads * a.group * 128));
+          __syncwarp();
+          for (int k = lane; k < loads; k += 32) {
+            const int sub = k % (D / 64), tk = k / (D / 64) % m, copy = k / (D / 64) / m;
+            tma_load_3d(smem + S::kOffQ + sub * (kRowsA * 128) + (copy * (kRowsA / fold) + tk * a.group) * 128, &qmap, sub * 64,
+                        kvh * a.group, tok + tk, &bars[kQFullA]);
+          }
+          ++queries;
+        }
+        w.done();
+      }
+      if (lane == 0 && queries > 0) mbar_wait(&bars[kQFullA], (uint32_t)(queries - 1) & 1u, nullptr);
+    } else if (warp == kMmaWarpA) {
+      constexpr uint32_t kIdS = idesc_16(Num<T>::kBf16, kRowsA, kTile, false);
+      constexpr uint32_t kIdO = idesc_16(Num<T>::kBf16, kRowsA, D, true);
+      Walk w(recs, bars, abort_flag, a.status, a.polls);
+      // A barrier's test takes 200-300 cycles even where the phase is long
+      // complete; one after another this warp's tests (up to six a tile) set the
+      // pace, 2,850 cycles a tile.  So its lanes test all that the next scores (of
+      // tile i) and the next rows (of tile j) wait for at once, a barrier a lane,
+      // and whatever is ready is issued (64 drafted tokens over 65,536 places:
+      // 168 -> 161 us; one token over 5,000: 16.5 -> 16.1).
+      int i = 0, j = 0;              // tiles whose scores, whose rows have been issued
+      int seg_s = 0, seg_o = 0;      // segments whose scores, whose rows have been issued
+      uint32_t flags[3] = {};        // of tiles i, i - 1, i - 2
+      int k_stage = 0, v_stage = 0;
+      uint32_t k_phase = 0, v_phase = 0;
+      bool issued = false;
+      bool more = w.next();
+      if (more) flags[0] = w.rec[kRFlags], w.done();
+      const uint64_t limit = a.polls == 0 ? 1ull : (uint64_t)a.polls << 10;
+      uint64_t idle = 0;  // tests since the last issue
+      while (more || j < i) {
+        const uint32_t row_flags = i - j == 2 ? flags[2] : flags[1];  // of tile j
+        int bar = -1;       // nothing to wait for
+        uint32_t phase = 0;
+        if (lane == 0) bar = kKFullA + k_stage, phase = k_phase;
+        if (lane == 1 && i >= 2) bar = kPvDone + (i & 1), phase = (uint32_t)((i >> 1) - 1) & 1u;  // the weights of tile i - 2 are read
+        if (lane == 2 && (flags[0] & kFlagFirst)) bar = kQFullA, phase = (uint32_t)seg_s & 1u;
+        if (lane == 3) bar = kVFullA + v_stage, phase = v_phase;
+        if (lane == 4) bar = kPFull + (j & 1), phase = (uint32_t)(j >> 1) & 1u;
+        if (lane == 5 && (row_flags & kFlagFirst) && seg_o > 0) bar = kOEmpty, phase = (uint32_t)(seg_o - 1) & 1u;  // the rows before are read
+        const bool ready = bar < 0 || mbar_try_wait_nosuspend(&bars[bar], phase);
+        const uint32_t got = __ballot_sync(0xFFFFFFFFu, ready);
+        const bool do_scores = more && (got & 7u) == 7u;
+        // scores come first: rows wait while all that scores lack is the end of
+        // the product just issued, or the next softmax would wait instead
+        const bool hold = more && i - j == 1 && (got & 7u) == 5u;
+        const bool do_rows = j < i && (got & 0x38u) == 0x38u && !hold;
+        if (!do_rows && !do_scores) {
+          const bool stop = ++idle >= limit || ((idle & 63u) == 0 && *abort_flag);
+          if (__any_sync(0xFFFFFFFFu, stop)) {
+            if (lane == 0 && !*abort_flag) {
+              *abort_flag = 1;
+              report(a.status, IDX_ST_TIMEOUT);
+            }
+            break;
+          }
+          continue;
+        }
+        idle = 0;
+        __syncwarp();  // what each lane has seen complete is so for the lane that issues
+        tc_fence_after();
+        if (lane == 0) {
+          if (do_scores) {
+            const uint64_t qd = sw128_desc(sbase + S::kOffQ), kd = sw128_desc(sbase + S::kOffKv + k_stage * S::kKv);
+            const uint32_t d = tmem + kColS + (uint32_t)(i & 1) * kTile;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t step = (uint64_t)((k / 4) * (kRowsA * 128 / 16) + (k % 4) * 2);
+              mma_16(d, qd + step, kd + step, kIdS, k > 0 ? 1u : 0u);
+            }
+            // a tile's stage is given back before anybody can learn that the
+            // tile is done: the ring's waits count on that order
+            mma_commit(&bars[kKEmptyA + k_stage]);
+            if (flags[0] & kFlagLast) mma_commit(&bars[kQEmptyA]);
+            mma_commit(&bars[kSFull + (i & 1)]);
+          }
+          if (do_rows) {
+            const uint64_t vd = sw128_desc_nmajor(sbase + S::kOffV + v_stage * S::kKv);
+            const uint32_t p = tmem + kColS + (uint32_t)(j & 1) * kTile, old = row_flags & kFlagFirst ? 0u : 1u;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k) {
+              const int half = k / (kHalf / 16);
+              mma_16_ta(tmem + kColO + (uint32_t)(half * D), p + (uint32_t)(half * kHalf + 8 * (k % (kHalf / 16))),
+                        vd + (uint64_t)(k * (2048 / 16)), kIdO, k % (kHalf / 16) > 0 ? 1u : old);
+            }
+            mma_commit(&bars[kVEmptyA + v_stage]);
+            mma_commit(&bars[kPvDone + (j & 1)]);
+          }
+        }
+        __syncwarp();
+        issued = true;
+        if (do_rows) {
+          if (row_flags & kFlagLast) ++seg_o;
+          if (++v_stage == Ring<D>::kValues) v_stage = 0, v_phase ^= 1u;
+          ++j;
+        }
+        if (do_scores) {
+          if (flags[0] & kFlagLast) ++seg_s;
+          if (++k_stage == Ring<D>::kKeys) k_stage = 0, k_phase ^= 1u;
+          ++i;
+          flags[2] = flags[1], flags[1] = flags[0];
+          more = w.next();
+          if (more) flags[0] = w.rec[kRFlags], w.done();
+          else if (!w.ended) break;
+        }
+      }
+      if (issued) {
+        if (lane == 0) mma_commit(&bars[kDrainA]);
+        __syncwarp();
+        mbar_wait(&bars[kDrainA], 0, nullptr);
+      }
+    } else if (warp < kSoftWarps) {
+      if (careful) softmax_role(std::true_type{});
+      else softmax_role(std::false_type{});
+    }
+
+    __syncwarp();
+    __syncthreads();  // all copies have landed, all products are done
+    if (careful || *abort_flag || !*reinterpret_cast<volatile int*>(&misc->careful)) break;
+    careful = true;
+    bars += kBarSet;  // barriers of its own: no arrival of the first run can reach them
+    if (tid == 0) {
+      misc->issued[0] = misc->issued[1] = 0;
+      init_bars(bars);
+    }
+    __syncthreads();
   }
 
   if (tid == 0 && blockIdx.x == 0) *reinterpret_cast<unsigned long long*>(a.cuts + 8 * kMaxCtas) = W;
@@ -1178,8 +1251,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   if (blockIdx.x == 0)
     for (int r = tid; r < a.num_reqs; r += kThreadsA)
       if (plan.ntok(r) > 0 && plan.len(plan.seq(r)) < plan.seq(r)) report(a.status, IDX_ST_LEN_CLAMPED);
-  __syncwarp();
-  __syncthreads();
   if (*abort_flag) {
     if (tid < 2) {
       // never leave with a copy in flight: the last ones of each ring
@@ -1230,7 +1301,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_tree_combine(const __grid_c
   float sum = 0.f;
 #pragma unroll
   for (int k = 0; k < kMost; ++k) {
-    const float w = part[k].x != -INFINITY ? ex2(part[k].x - big) : 0.f;
+    float w = part[k].x != -INFINITY ? ex2(part[k].x - big) : 0.f;
+    if (w == 0.f && part[k].x != -INFINITY) w = 1e-45f;  // an infinity that is seen keeps its place in the sum
     sum += w * part[k].y;
     if (from + 32 * k + lane <= to) weight[warp][32 * k + lane] = w;
   }
