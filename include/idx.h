@@ -489,9 +489,9 @@ int idx_rope_frequencies(int32_t rotary_dim, double base, int32_t kind, double f
  *     y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x2 cos a + x1 sin a)
  * computed in 32 bits and rounded once; (x1, x2) are elements i and i +
  * rotary_dim / 2 of the head, or 2i and 2i + 1 with IDX_ROPE_INTERLEAVED.
- * Elements from rotary_dim on pass unchanged.  The angle is reduced exactly
- * (as a 64-bit fraction of a turn), so positions up to 2^31 - 1 keep full
- * precision.  Rotated queries go to q_out; rotated keys and unchanged values
+ * Elements from rotary_dim on pass unchanged.  The angle is reduced as a
+ * 64-bit fraction of a turn: at positions up to 2^31 - 1 it is off by at most
+ * 2^-33 turns (and fp32's rounding of the fraction).  Rotated queries go to q_out; rotated keys and unchanged values
  * go to cache slot slots[t] (NULL: slot t); a negative slot is skipped, one
  * past the cache is skipped with IDX_ST_BLOCK_OOR.  Two tokens of one call
  * must not share a slot.

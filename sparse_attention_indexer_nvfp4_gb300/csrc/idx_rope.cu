@@ -2,14 +2,15 @@
 // paged cache.
 //
 // Each pair (x1, x2) of a head turns by a = position * inv_freq: y1 = m (x1
-// cos a - x2 sin a), y2 = m (x2 cos a + x1 sin a).  The angle is reduced
-// exactly: inv_freq / 2 pi becomes a 64-bit fraction of a turn (a multiple of
-// 2^-63), and position * fraction in 64-bit integer arithmetic drops the
-// whole turns by itself; what remains is a signed fraction in [-1/2, 1/2)
+// cos a - x2 sin a), y2 = m (x2 cos a + x1 sin a).  inv_freq / 2 pi becomes a
+// 64-bit fraction of a turn (to the nearest 2^-64: a product rounded to one
+// double is off by up to 2^-55.7, 2^-24.7 turns at a position of 2^31), and
+// position * fraction in 64-bit integer arithmetic drops the whole turns by
+// itself; what remains is a signed fraction in [-1/2, 1/2)
 // turns whose sine and cosine CUDA's sincospif gives.  A position of 2^31
-// leaves an error of 2^-33 turns, where a product in fp32 would be off by
-// whole turns; no table of positions is read (one of fp32 pairs would add 8
-// bytes a pair and token to the traffic).
+// leaves an error of 2^-34 turns and fp32's rounding of the fraction, where a
+// product in fp32 would be off by whole turns; no table of positions is read
+// (one of fp32 pairs would add 8 bytes a pair and token to the traffic).
 //
 // The kernels are bound by HBM: every element is read once and written once.
 // k_rope_rows, for heads of at most 32 pieces (of up to 16 bytes, as the
@@ -77,17 +78,27 @@ struct alignas(sizeof(T) * V) Piece {
   T e[V];
 };
 
-// Turns a position, modulo 1, as a multiple of 2^-63 in the upper bits.
+// Turns a position, modulo 1, in units of 2^-64: |freq| = m 2^-s times 2^64 / (2
+// pi), whose first 128 bits are kHi and kLo, in whole numbers (64-bit floating
+// point is slow here: 5.9 us against 5.3 for 512 tokens of 64 + 4 heads).
 __device__ __forceinline__ unsigned long long step_of(double freq) {
-  double turns = freq * 0.15915494309189535;  // 1 / (2 pi)
-  turns -= rint(turns);
-  return (unsigned long long)__double2ll_rn(turns * 9223372036854775808.0) << 1;
+  constexpr unsigned long long kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;
+  const unsigned long long bits = (unsigned long long)__double_as_longlong(freq);
+  const int e = (int)(bits >> 52) & 0x7FF, s = 1075 - max(e, 1);
+  const unsigned long long m = (bits & 0xFFFFFFFFFFFFFull) | (e > 0 ? 1ull << 52 : 0ull);
+  const unsigned long long carry = __umul64hi(m, kLo), low = m * kHi + carry;
+  const unsigned long long high = __umul64hi(m, kHi) + (low < carry ? 1ull : 0ull);
+  auto shifted = [&](int n) {  // bits n .. n + 63 of the product
+    return n >= 128 ? 0ull : n >= 64 ? high >> (n - 64) : n > 0 ? low >> n | high << (64 - n) : n > -64 ? low << -n : 0ull;
+  };
+  const unsigned long long step = s > 0 ? shifted(s) + (shifted(s - 1) & 1ull) : shifted(s);
+  return bits >> 63 ? 0ull - step : step;
 }
 
 // The cosine and sine of position * step, times m.
 __device__ __forceinline__ float2 turn_of(int position, unsigned long long step, float m) {
   const unsigned long long phase = step * (unsigned long long)(long long)position;
-  const float half_turns = (float)(int)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31: signed, in half turns
+  const float half_turns = (float)(long long)phase * 1.0842021724855044e-19f;  // 2^-63: signed, in half turns
   float s, c;
   sincospif(half_turns, &s, &c);
   return make_float2(c * m, s * m);
