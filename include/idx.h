@@ -530,7 +530,7 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  *     s_p = scale (q . k_p),  out = sum_p e^(s_p - L) v_p,  L = ln sum_p e^s_p
  * (scale finite; negative and zero ones too).
  * A token that sees nothing gets out 0 and L -inf (as does one whose scores
- * are all -inf).  Scores, maxima, sums and outputs are held in fp32; e^(s_p -
+ * are all -inf).  A row with a score of NaN is NaN.  Scores, maxima, sums and outputs are held in fp32; e^(s_p -
  * M), M a maximum of the scores met so far or up to 8 powers of two below it,
  * is rounded to the cache's type for the product with v.  What is stored
  * at places that no token sees (unwritten slots of the last page, NaN and

@@ -870,8 +870,9 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 #pragma unroll 1
         for (int p = x; p < kRowsA; p += per) {
           const float2 u = stats[p], v = stats[kRowsA + p];
-          if (u.x != -INFINITY) sum += u.y * ex2((u.x - top) * c);
-          if (v.x != -INFINITY) sum += v.y * ex2((v.x - top) * c);
+          // (a part without a maximum has the sum 0, or NaN where all scores that it sees are NaN)
+          sum += u.x != -INFINITY ? u.y * ex2((u.x - top) * c) : u.y;
+          sum += v.x != -INFINITY ? v.y * ex2((v.x - top) * c) : v.y;
         }
         return top;
       };
@@ -879,13 +880,15 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       const float big = row_of(row, sum_l);
       const uint32_t slot = head[kHOut];
       const bool direct = slot == 0xFFFFFFFFu, empty = sum_l == 0.f;
+      const bool lost = sum_l != sum_l;  // some score is NaN: so is the row, whichever part saw it
       // what this lane's two halves weigh in the row
-      const float inv = empty ? 0.f : direct ? 1.f / sum_l : 1.f, m0 = stats[lane_row].x, m1 = stats[kRowsA + lane_row].x;
-      const float g0 = m0 == -INFINITY ? 0.f : ex2((m0 - big) * c) * inv, g1 = m1 == -INFINITY ? 0.f : ex2((m1 - big) * c) * inv;
+      const float inv = empty ? 0.f : direct || lost ? 1.f / sum_l : 1.f, m0 = stats[lane_row].x, m1 = stats[kRowsA + lane_row].x;
+      const float g0 = m0 == -INFINITY && !lost ? 0.f : ex2((m0 - big) * c) * inv;
+      const float g1 = m1 == -INFINITY && !lost ? 0.f : ex2((m1 - big) * c) * inv;
       const int tok0 = (int)head[kHTok0], kvh = (int)head[kHHead];
       if (row < rows && half == 0 && copy == 0) {
         const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
-        if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : big * c, sum_l);
+        if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : lost ? sum_l : big * c, sum_l);
         else if (a.lse != nullptr)
           a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + __log2f(sum_l)) * 0.6931471805599453f;
       }

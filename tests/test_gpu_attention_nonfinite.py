@@ -88,6 +88,34 @@ def test_every_place_bad(lib):
     check(lib, c)
 
 
+def test_scores_that_are_not_finite_stay_in_their_rows(lib):
+    c = make(41, [3000, 40], [6, 3], 16, 2, 128, 128, "bf16")
+    want, l0, _ = run(lib, c)
+    c["q"][2, 5, 7] = float("nan")
+    c["q"][7, 9, 1] = float("inf")
+    out, L, st = run(lib, c)
+    assert st == 0 and out[2, 5].isnan().all() and out[7, 9].isnan().all()
+    out[2, 5], out[7, 9] = want[2, 5], want[7, 9]
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("ctx", [0, 1, 128, 143, 1000, 20_000])
+@pytest.mark.parametrize("hq,hk,dim,lists", [(4, 1, 128, 0), (64, 4, 64, 0), (64, 1, 128, 0), (8, 2, 64, 2)])
+def test_a_key_that_is_nan_reaches_the_rows_that_see_it(lib, ctx, hq, hk, dim, lists):
+    """The first and the last place in turn: in short contexts and at a tile's begin the only place that a part of a row sees."""
+    for place in (0, ctx):
+        c = make(44 + ctx, [ctx, 50], [1, 2], hq, hk, dim, 128, "bf16")
+        if lists:
+            c["pages"] = np.tile(np.array([0, ctx // 128, -1], dtype=np.int32), (3, lists, 1))
+        want, l0, _ = run(lib, c)
+        c["cache"][0, int(c["table"][0, place // 128]), place % 128, 0, 3] = float("nan")
+        out, L, st = run(lib, c)
+        g = hq // hk
+        assert st == 0 and out[0, :g].isnan().all() and L[0, :g].isnan().all()
+        out[0, :g], L[0, :g] = want[0, :g], l0[0, :g]
+        assert torch.equal(out, want) and torch.equal(L, l0)
+
+
 def test_an_infinity_far_below_the_largest_weight(lib):
     """Seen with a weight that fp32 cannot hold, in a stretch of its own."""
     c = make(42, [40_000], [2], 4, 1, 64, 128, "bf16")
