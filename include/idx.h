@@ -531,8 +531,9 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  * (scale finite; negative and zero ones too).
  * A token that sees nothing gets out 0 and L -inf (as does one whose scores
  * are all -inf).  A row with a score of NaN is NaN.  Scores, maxima, sums and outputs are held in fp32; e^(s_p -
- * M), M a maximum of the scores met so far or up to 8 powers of two below it,
- * is rounded to the cache's type for the product with v.  What is stored
+ * M), M a maximum of the scores met so far or up to 8 powers of two (fp16: 4)
+ * below it, is rounded to the cache's type for the product with v; in fp16 in
+ * steps of no less than 2^-31.  Scores are meant to stay below 2^24.  What is stored
  * at places that no token sees (unwritten slots of the last page, NaN and
  * infinities among them) has no effect, and what a drafted token has stored
  * reaches only the tokens that see it.

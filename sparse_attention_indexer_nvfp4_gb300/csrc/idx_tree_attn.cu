@@ -91,7 +91,6 @@ constexpr int kRecWords = 32;
 constexpr int kSlotWords = (kChunk + 1) * kRecWords;  // a header, then the tiles
 constexpr int kGroup = 16;          // places of a record's group
 constexpr int kMaxListTokens = 32;  // tokens of a block with page lists (bits of a mask)
-constexpr float kRescale = 8.f;     // powers of two that a weight may exceed 1 before O is rescaled
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kScratchRow = 20;     // floats: 16 columns, and 4 that keep rows on different banks
 
@@ -274,12 +273,15 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// kRescale: powers of two that a score may exceed the reference maximum before O
+// is rescaled; kLift: powers of two that all weights are larger by.
 template <typename T>
 struct Num;
 template <>
 struct Num<__nv_bfloat16> {
   static constexpr bool kBf16 = true;
   static constexpr CUtensorMapDataType kMap = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  static constexpr float kLift = 0.f, kRescale = 8.f;
   // two values rounded to nearest: the weights of the product with v
   static __device__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -292,6 +294,11 @@ template <>
 struct Num<__half> {
   static constexpr bool kBf16 = false;
   static constexpr CUtensorMapDataType kMap = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  // Weights (and their sum) are 2^7 larger, which an output's quotient drops
+  // again: the smallest that fp16 keeps is then 2^-32 of a row's largest.  With
+  // 2^-25 a long tail below one key was lost in O while the sum counted it.  4
+  // powers until a rescale leave 5 below fp16's largest number.
+  static constexpr float kLift = 7.f, kRescale = 4.f;
   static __device__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -463,7 +470,7 @@ __device__ __forceinline__ bool soft_tile(uint32_t half_s, uint32_t half_o, cons
   const float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 
   float scale = 1.f;
-  if (big > m && (m == -INFINITY || (big - m) * c > kRescale)) {
+  if (big > m && (m == -INFINITY || (big - m) * c > Num<T>::kRescale)) {
     scale = m == -INFINITY ? 1.f : ex2((m - big) * c);  // with no score so far O and l are zero
     m = big;
   }
@@ -484,7 +491,7 @@ __device__ __forceinline__ bool soft_tile(uint32_t half_s, uint32_t half_o, cons
       tmem_st8(half_o + (uint32_t)k + 8, o + 8);
     }
   }
-  const float mc = m == -INFINITY ? 0.f : m * c;
+  const float mc = m == -INFINITY ? 0.f : fmaf(m, c, -Num<T>::kLift);
   const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
   float2 sum[2] = {};
 #pragma unroll
@@ -888,9 +895,9 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       const int tok0 = (int)head[kHTok0], kvh = (int)head[kHHead];
       if (row < rows && half == 0 && copy == 0) {
         const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
-        if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : lost ? sum_l : big * c, sum_l);
+        if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : lost ? sum_l : fmaf(big, c, -Num<T>::kLift), sum_l);
         else if (a.lse != nullptr)
-          a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (big * c + __log2f(sum_l)) * 0.6931471805599453f;
+          a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (fmaf(big, c, -Num<T>::kLift) + __log2f(sum_l)) * 0.6931471805599453f;
       }
       const bool sum_ok = sum_l > 0.f && sum_l < INFINITY;  // else its scores are not finite, or it sees nothing
       uint32_t pos[D / 64] = {}, neg[D / 64] = {};  // marks of the row's columns of this half
