@@ -552,7 +552,9 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  *                 (IDX_ST_LEN_CLAMPED), nor those of a block id outside
  *                 [0, num_blocks) (IDX_ST_BLOCK_OOR)
  *   seq_lens      [num_reqs] int32 tokens per request, this step's included
- *   cu_tokens     [num_reqs + 1] int32, non-decreasing, from 0 to num_tokens
+ *   cu_tokens     [num_reqs + 1] int32, non-decreasing, from 0 to at most
+ *                 num_tokens; rows past the last request's (a padded batch)
+ *                 get out 0 and L -inf
  *   tree_mask     [num_tokens] uint64 or NULL
  *   pages         [num_tokens, page_lists, pages_per_list] int32 or NULL: the
  *                 logical pages of each token and list, as idx_decode_step

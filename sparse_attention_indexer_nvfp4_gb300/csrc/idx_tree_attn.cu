@@ -644,6 +644,19 @@ __device__ __forceinline__ bool take_out(uint4* v, int place, uint32_t (&pos)[2]
   return any;
 }
 
+// Rows of a padded batch, past the last request: a warp of each CTA that is done
+// long before the others clears its share.
+template <typename T, int D>
+__device__ __noinline__ void clear_rest(const TreeArgs& a) {
+  const int lane = (int)lane_id();
+  const int64_t all = (int64_t)a.num_tokens * a.q_heads;
+  for (int64_t x = (int64_t)Plan(a).tok0(a.num_reqs) * a.q_heads + blockIdx.x; x < all; x += gridDim.x) {
+    const int64_t t = x / a.q_heads, h = x - t * a.q_heads;
+    if (lane < D / 8) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.o_ts + h * a.o_hs + 8 * lane) = make_uint4(0, 0, 0, 0);
+    if (lane == 0 && a.lse != nullptr) a.lse[x] = -INFINITY;
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreadsA, 1)
     k_tree_attention(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -1089,6 +1102,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         cut[kCRows] = rows;
       }
       if (bad_block) report(a.status, IDX_ST_BLOCK_OOR);
+      __syncwarp();
+      clear_rest<T, D>(a);
     } else if (warp == kKeyTma || warp == kValueTma) {
       const bool keys = warp == kKeyTma;
       const CUtensorMap* map = keys ? &kmap : &vmap;

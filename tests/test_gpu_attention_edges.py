@@ -1,4 +1,4 @@
-"""idx_tree_attention: weights far below the largest.
+"""idx_tree_attention: weights far below the largest, padded batches.
 
 Tolerances are those of the main tests; where weights below fp16's smallest
 normal number carry the result, each adds half of their step, 2^-32 of the
@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_tree_attention import compare, make, reference, run
+from test_gpu_tree_attention import check, compare, lists_of, make, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,46 @@ def test_a_largest_score_far_above_the_others(lib, ctx, hq, hk, dim, sign, top, 
     best = c["cache"][1, b, o].double().repeat_interleave(hq // hk, 0)
     assert ((out.double() - best).abs() <= torch.finfo(c["dt"]).eps * (1 + 2.0**-8) * best.abs()).all()
     assert ((L.double() - raw * c["scale"]).abs() <= 2.0**-21 * (raw * c["scale"]).abs()).all()
+
+
+@pytest.mark.parametrize("lists", [0, 2])
+@pytest.mark.parametrize("pad", [1, 7, 300])
+def test_rows_past_the_last_request_are_empty(lib, pad, lists):
+    c = make(30 + pad, [300, 0, 90], [5, 0, 3], 16, 2, 128, 16, "bf16")
+    extra = torch.randn(pad, 16, 128, device="cuda").bfloat16()
+    c["q"] = torch.cat([c["q"], extra])
+    c["mask"] = np.concatenate([c["mask"], np.full(pad, 2**64 - 1, dtype=np.uint64)])
+    if lists:
+        c["pages"] = lists_of(c, np.random.default_rng(pad), lists, 16, 16)
+    out, L, st = run(lib, c)  # out and L hold 9 before
+    assert st == 0
+    compare(c, out, L, reference(c))
+    assert not out[8:].any() and L[8:].isneginf().all()
+    # rows of a wider tensor: what lies between them stays
+    wide = torch.full((8 + pad, 20, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+    again, _, _ = run(lib, c, out=wide[:, 2:18])
+    assert torch.equal(again, out) and wide[:, :2].eq(7).all() and wide[:, 18:].eq(7).all()
+
+
+def test_a_padded_batch_of_slots_feeds_the_attention(lib):
+    """idx_build_slots with room for more tokens than there are, then the attention over its lengths."""
+    reqs, page, cap, hq, hk, dim = 4, 16, 40, 8, 2, 64
+    d = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ctx, new = [37, 0, 64, 5], [3, 6, 0, 8]
+    width, blocks = 8, 30
+    e = lambda n, t=torch.int32: torch.full((n,), -77, dtype=t, device="cuda")
+    table = torch.full((reqs, width), -1, dtype=torch.int32, device="cuda")
+    cu, seq, pages, cur, pos, slots, mask = e(reqs + 1), e(reqs), e(reqs), e(1), e(cap), e(cap, torch.int64), e(cap, torch.int64)
+    parents = torch.full((cap,), -1, dtype=torch.int32, device="cuda")
+    lib.idx_build_slots(d(ctx), d(new), d([0] * reqs), table, torch.randperm(blocks, device="cuda").to(torch.int32), d([0]), blocks, page,
+                        cu, seq, pages, cur, pos, slots, parents=parents, tree_mask=mask)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    cache = torch.randn(2, blocks, page, hk, dim, device="cuda", generator=g).bfloat16()
+    q = torch.randn(cap, hq, dim, device="cuda", generator=g).bfloat16()
+    np_ = lambda t: t.cpu().numpy()
+    c = dict(q=q, cache=cache, table=np_(table), seq=np_(seq), cu=np_(cu), mask=np_(mask).view(np.uint64), dt=torch.bfloat16, pages=None,
+             scale=dim**-0.5)
+    assert c["cu"].tolist() == [0, 3, 9, 9, 17]
+    out = check(lib, c)
+    assert not out[17:].any()
