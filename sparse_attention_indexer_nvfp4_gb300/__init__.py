@@ -326,6 +326,8 @@ class _Torch:
         self.i32, self.i64, self.f32, self.f64 = torch.int32, torch.int64, torch.float32, torch.float64
         self.words = (torch.int64, torch.uint64)
         self.codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        self.many = torch.cuda.device_count() > 1
+        self.device = torch.cuda.current_device
         # the current stream's handle without a Stream object (3 us less a call)
         self.raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
@@ -345,24 +347,34 @@ def _stream_on(stream, t) -> int | None:
 
 
 def _are(dtype, shape, *tensors) -> bool:
-    """Whether every given tensor (None left out) has the type and the sizes and is contiguous."""
+    """Whether every given tensor (None left out) is on a GPU, has the type and the sizes and is contiguous."""
     for t in tensors:
-        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        if t is not None and (not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
             return False
     return True
+
+
+def _here(*tensors) -> bool:
+    """Whether all are on the current device.  Asked only where there are several: it costs as much as the other checks."""
+    dev = _T.device()
+    return all(t is None or t.get_device() == dev for t in tensors)
 
 
 # The checks below run as one expression a call; only where it fails does
 # _explain go through the tensors again to name the one that is wrong.
 def _explain(name: str, dense=(), **tensors) -> None:
-    """Raise for the first tensor that is not what is needed: each is (tensor, types, sizes with None for any); those
-    named in `dense` must be contiguous, the others in their last dimension."""
+    """Raise for the first tensor that is not what is needed: each is (tensor, types or None, sizes with None for any, or
+    None: not empty); those named in `dense` must be contiguous, the others in their last dimension.  The device comes last."""
     for arg, (t, dtypes, shape) in tensors.items():
         if t is None:
             continue
         dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-        if t.dtype not in dtypes:
+        if dtypes != (None,) and t.dtype not in dtypes:
             raise ValueError(f"{name}: {arg} has type {t.dtype}, {' or '.join(map(str, dtypes))} is needed")
+        if shape is None:
+            if t.numel() == 0 and dtypes != (None,):
+                raise ValueError(f"{name}: {arg} has no element")
+            continue
         if t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):
             need = tuple("any" if w is None else w for w in shape)
             raise ValueError(f"{name}: {arg} has shape {tuple(t.shape)}, {need} is needed")
@@ -371,13 +383,16 @@ def _explain(name: str, dense=(), **tensors) -> None:
                 raise ValueError(f"{name}: {arg} must be contiguous")
         elif t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"{name}: the last dimension of {arg} must be contiguous")
+    for arg, (t, *_) in tensors.items():
+        if t is not None and not (t.is_cuda and _here(t)):
+            raise ValueError(f"{name}: {arg} is on {t.device}, the current CUDA device is needed")
     raise ValueError(f"{name}: a tensor has the wrong type, shape or strides")
 
 
 def _rows_ok(dtype, shape, *tensors) -> bool:
-    """Type and sizes, and the last dimension contiguous (the others may have any strides)."""
+    """On a GPU, type and sizes, and the last dimension contiguous (the others may have any strides)."""
     for t in tensors:
-        if t is not None and (t.dtype is not dtype or t.shape != shape or (t.stride(-1) != 1 and shape[-1] > 1)):
+        if t is not None and (not t.is_cuda or t.dtype is not dtype or t.shape != shape or (t.stride(-1) != 1 and shape[-1] > 1)):
             return False
     return True
 
@@ -393,16 +408,20 @@ def idx_build_slots(ctx_lens, new_lens, owned_pages, block_table, free_blocks, f
     reqs, width, tokens, free = per_req[0], block_table.shape[-1], per_token[0], free_blocks.shape[0]
     if not (_are(i32, (reqs,), ctx_lens, new_lens, owned_pages, seq_lens, pages_out) and _are(i32, (reqs + 1,), cu_tokens)
             and _are(i32, (1,), free_cursor, cursor_out) and _are(i32, (free,), free_blocks)
-            and _are(i32, (tokens,), positions, parents) and slots.shape == per_token and slots.dtype in T.words
+            and _are(i32, (tokens,), positions, parents) and slots.is_cuda and slots.shape == per_token and slots.dtype in T.words
             and slots.is_contiguous() and _rows_ok(i32, (reqs, width), block_table)
-            and (tree_mask is None or (tree_mask.shape == per_token and tree_mask.dtype in T.words and tree_mask.is_contiguous()))):
+            and (tree_mask is None or (tree_mask.is_cuda and tree_mask.shape == per_token and tree_mask.dtype in T.words
+                                       and tree_mask.is_contiguous()))
+            and (status is None or (status.is_cuda and status.dtype is i32 and status.numel() > 0))
+            and (not T.many or _here(ctx_lens, new_lens, owned_pages, block_table, free_blocks, free_cursor, cu_tokens, seq_lens, pages_out,
+                                     cursor_out, positions, slots, parents, tree_mask, status))):
         r, t, one = (reqs,), (tokens,), (1,)
         _explain(fn, ("ctx_lens", "new_lens", "owned_pages", "free_blocks", "cu_tokens", "seq_lens", "pages_out", "positions", "slots",
                       "parents", "tree_mask"), ctx_lens=(ctx_lens, i32, r), new_lens=(new_lens, i32, r),
                  owned_pages=(owned_pages, i32, r), block_table=(block_table, i32, (reqs, None)), free_blocks=(free_blocks, i32, (None,)),
                  free_cursor=(free_cursor, i32, one), cu_tokens=(cu_tokens, i32, (reqs + 1,)), seq_lens=(seq_lens, i32, r),
                  pages_out=(pages_out, i32, r), cursor_out=(cursor_out, i32, one), positions=(positions, i32, t),
-                 slots=(slots, T.words, t), parents=(parents, i32, t), tree_mask=(tree_mask, T.words, t))
+                 slots=(slots, T.words, t), parents=(parents, i32, t), tree_mask=(tree_mask, T.words, t), status=(status, i32, None))
     rc = lib.idx_build_slots(
         ctx_lens.data_ptr(), new_lens.data_ptr(), owned_pages.data_ptr(), reqs, block_table.data_ptr(), _row_stride(block_table),
         width, free_blocks.data_ptr(), free, free_cursor.data_ptr(), num_blocks, page_tokens, None if parents is None else parents.data_ptr(), tokens,
@@ -442,12 +461,15 @@ def idx_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slots
     hq = 0 if q is None else q.shape[1]
     nb, page, hk = (0, 1, 0) if k is None else (k_cache.shape[0], k_cache.shape[1], k.shape[1])
     qshape, kshape, cshape = (tokens, hq, dim), (tokens, hk, dim), (nb, page, hk, dim)
-    if not (_rows_ok(kind, qshape, q, q_out) and _rows_ok(kind, kshape, k, v) and _rows_ok(kind, cshape, k_cache, v_cache) and _are(T.i32, (tokens,), positions)
-            and _are(T.f64, inv_freq.shape[:1], inv_freq)
-            and (slots is None or (slots.dtype in T.words and slots.shape == positions.shape and slots.is_contiguous()))):
+    if not (_rows_ok(kind, qshape, q, q_out) and _rows_ok(kind, kshape, k, v) and _rows_ok(kind, cshape, k_cache, v_cache)
+            and _are(T.i32, (tokens,), positions) and _are(T.f64, inv_freq.shape[:1], inv_freq)
+            and (slots is None or (slots.is_cuda and slots.dtype in T.words and slots.shape == positions.shape and slots.is_contiguous()))
+            and (status is None or (status.is_cuda and status.dtype is T.i32 and status.numel() > 0))
+            and (not T.many or _here(q, q_out, k, v, k_cache, v_cache, positions, inv_freq, slots, status))):
         _explain(fn, ("positions", "inv_freq", "slots"), q=(q, kind, qshape), q_out=(q_out, kind, qshape), k=(k, kind, kshape),
                  v=(v, kind, kshape), k_cache=(k_cache, kind, (None, None, hk, dim)), v_cache=(v_cache, kind, cshape),
-                 positions=(positions, T.i32, (tokens,)), inv_freq=(inv_freq, T.f64, (None,)), slots=(slots, T.words, (tokens,)))
+                 positions=(positions, T.i32, (tokens,)), inv_freq=(inv_freq, T.f64, (None,)), slots=(slots, T.words, (tokens,)),
+                 status=(status, T.i32, None))
     cs = (0, 0, 0, 0) if k is None else k_cache.stride()
     if v_cache is not None and v_cache.stride() != cs:
         raise ValueError(f"{fn}: k_cache and v_cache must have the same strides")
@@ -486,13 +508,19 @@ def idx_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, ou
     if not (_rows_ok(kind, shape, q, out) and cshape[3] == dim and _rows_ok(kind, cshape, k_cache, v_cache)
             and _rows_ok(T.i32, (reqs, width), block_table) and _are(T.i32, (reqs,), seq_lens)
             and _are(T.i32, (reqs + 1,), cu_tokens) and _are(T.f32, (tokens, hq), lse)
-            and (tree_mask is None or (tree_mask.dtype in T.words and tree_mask.shape == (tokens,) and tree_mask.is_contiguous()))
-            and (pages is None or (pages.dtype is T.i32 and pages.is_contiguous() and pages.numel() == tokens * lists * per))):
+            and (tree_mask is None or (tree_mask.is_cuda and tree_mask.dtype in T.words and tree_mask.shape == (tokens,)
+                                       and tree_mask.is_contiguous()))
+            and (pages is None or (pages.is_cuda and pages.dtype is T.i32 and pages.is_contiguous()
+                                   and pages.numel() == tokens * lists * per))
+            and (status is None or (status.is_cuda and status.dtype is T.i32 and status.numel() > 0))
+            and (workspace is None or workspace.is_cuda)
+            and (not T.many or _here(q, k_cache, v_cache, block_table, seq_lens, cu_tokens, out, tree_mask, pages, lse, workspace, status))):
         _explain(fn, ("seq_lens", "cu_tokens", "tree_mask", "lse", "pages"), q=(q, kind, shape), out=(out, kind, shape),
                  k_cache=(k_cache, kind, (nb, page, hk, dim)), v_cache=(v_cache, kind, (nb, page, hk, dim)),
                  block_table=(block_table, T.i32, (reqs, None)), seq_lens=(seq_lens, T.i32, (reqs,)),
                  cu_tokens=(cu_tokens, T.i32, (reqs + 1,)), tree_mask=(tree_mask, T.words, (tokens,)), lse=(lse, T.f32, (tokens, hq)),
-                 pages=(pages, T.i32, (tokens, lists, per)))
+                 pages=(pages if pages is None or pages.dim() < 4 else pages.flatten(0, -3), T.i32, (tokens, lists, per)),
+                 workspace=(workspace, None, None), status=(status, T.i32, None))
     cs = k_cache.stride()
     if v_cache.stride() != cs:
         raise ValueError(f"{fn}: k_cache and v_cache must have the same strides")
@@ -516,11 +544,15 @@ def idx_verify_drafts(target, draft, tokens, cu_tokens, accept_u, sample_u, out_
     reqs, max_out = out_shape = out_tokens.shape
     if not (_rows_ok(f32, rows, target, draft) and _are(i32, (total,), tokens, parents)
             and _are(i32, (reqs + 1,), cu_tokens) and _are(f32, (total,), accept_u) and _are(f32, (reqs,), sample_u)
-            and _are(i32, out_shape, out_tokens, out_nodes) and _are(i32, (reqs,), num_accepted)):
+            and _are(i32, out_shape, out_tokens, out_nodes) and _are(i32, (reqs,), num_accepted)
+            and (status is None or (status.is_cuda and status.dtype is i32 and status.numel() > 0))
+            and (not T.many or _here(target, draft, tokens, parents, cu_tokens, accept_u, sample_u, out_tokens, out_nodes, num_accepted,
+                                     status))):
         _explain(fn, ("tokens", "parents", "cu_tokens", "accept_u", "sample_u", "out_tokens", "out_nodes", "num_accepted"),
                  target=(target, f32, rows), draft=(draft, f32, rows), tokens=(tokens, i32, (total,)), parents=(parents, i32, (total,)),
                  cu_tokens=(cu_tokens, i32, (reqs + 1,)), accept_u=(accept_u, f32, (total,)), sample_u=(sample_u, f32, (reqs,)),
-                 out_tokens=(out_tokens, i32, out_shape), out_nodes=(out_nodes, i32, out_shape), num_accepted=(num_accepted, i32, (reqs,)))
+                 out_tokens=(out_tokens, i32, out_shape), out_nodes=(out_nodes, i32, out_shape), num_accepted=(num_accepted, i32, (reqs,)),
+                 status=(status, i32, None))
     rc = lib.idx_verify_drafts(
         target.data_ptr(), _row_stride(target), None if draft is None else draft.data_ptr(), 0 if draft is None else _row_stride(draft), vocab, tokens.data_ptr(),
         None if parents is None else parents.data_ptr(), cu_tokens.data_ptr(), reqs, total, accept_u.data_ptr(), sample_u.data_ptr(), out_tokens.data_ptr(),
