@@ -1,4 +1,4 @@
-"""idx_tree_attention: weights far below the largest, padded batches.
+"""idx_tree_attention: weights far below the largest, padded batches, many requests.
 
 Tolerances are those of the main tests; where weights below fp16's smallest
 normal number carry the result, each adds half of their step, 2^-32 of the
@@ -116,3 +116,21 @@ def test_a_padded_batch_of_slots_feeds_the_attention(lib):
     assert c["cu"].tolist() == [0, 3, 9, 9, 17]
     out = check(lib, c)
     assert not out[17:].any()
+
+
+@pytest.mark.parametrize("reqs", [417, 1300])
+@pytest.mark.parametrize("lists", [0, 2])
+def test_many_requests(lib, reqs, lists):
+    """More requests than a CTA has threads, some without tokens, some of several blocks of rows."""
+    rng = np.random.default_rng(reqs)
+    ctx = rng.integers(0, 60, reqs)
+    new = rng.choice([0, 0, 1, 1, 2, 3, 17], reqs)
+    new[rng.integers(0, reqs, 5)] = 40
+    ctx[rng.integers(0, reqs, 5)] = 900
+    c = make(reqs, ctx.tolist(), new.tolist(), 16, 2, 64, 16, "bf16")
+    if lists:
+        c["pages"] = lists_of(c, rng, lists, 16, 16)
+    check(lib, c)
+    first = [0] * 500  # runs without a token before the first and after the last
+    c = make(reqs + 1, first + [70, 3] + first, first + [3, 0] + first, 16, 2, 64, 16, "fp16")
+    check(lib, c)
