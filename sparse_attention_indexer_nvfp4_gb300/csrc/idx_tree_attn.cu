@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const uint32_t sbase = smem_u32(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint64_t* const all_bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
   MiscA* misc = reinterpret_cast<MiscA*>(smem + S::kOffMisc);
   uint32_t* recs = reinterpret_cast<uint32_t*>(smem + S::kOffRec);
   volatile int* abort_flag = &misc->abort_flag;
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     misc->issued[0] = misc->issued[1] = 0;
     misc->careful = misc->bad[0] = misc->bad[1] = 0;
     for (int s = 0; s < kRowsA / 32; ++s) misc->odd[s] = 0;
-    init_bars(bars);
+    init_bars(all_bars);
   }
   if (tid == 32) {  // a cold descriptor costs a copy a microsecond
     asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
@@ -744,227 +744,14 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     __syncthreads();
   }
 
-  // The softmax warps' part of a run.  A careful run is code of its own, so that
-  // the usual one has none of it in its loop.
-  auto softmax_role = [&](auto how) {
+  // A run over the stretch: once, or a second time where some value was not
+  // finite (see take_out), with barriers of its own, which no arrival of the
+  // first run can reach.  Code of its own as well: with both runs in one loop the
+  // warps' way to their barriers was longer, 168 us for 160 on 64 tokens over
+  // 65,536 places.
+  auto run = [&](auto how) {
     constexpr bool kCareful = decltype(how)::value;
-    const int lane_row = tid & (kRowsA - 1), half = warp >> 2;
-    const uint32_t tmem_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t half_o = tmem_row + kColO + (uint32_t)(half * D);
-    float* scratch = reinterpret_cast<float*>(smem + S::kOffScratch);
-    float2* stats = reinterpret_cast<float2*>(smem + S::kOffStats);
-    const bool negate = a.scale < 0.f;
-    // scores in powers of two; a scale of 0 becomes one that still hides masked places
-    const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
-    float m = -INFINITY, l = 0.f;
-    RowState st{};
-    int meets = 0;
-    int row = 0, copy = 0, fold = 1, col0 = 0, rows = 0;
-    bool warp_live = true, met = false;
-    // All eight warps meet, those that gave up among them (see below); the wait
-    // ends for all or for none, so that no warp misses a later barrier.  False:
-    // one gave up.
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kMerge]);
-      const bool all = mbar_wait(&bars[kMerge], (uint32_t)meets & 1u, nullptr);
-      ++meets;
-      return __all_sync(0xFFFFFFFFu, all) && !*reinterpret_cast<volatile int*>(&misc->soft_dead);
-    };
-    uint32_t* place_marks = reinterpret_cast<uint32_t*>(scratch);  // [place][+ columns, - columns]
-    uint32_t* row_marks = place_marks + kTile * S::kMarkWords;
-    if (kCareful)
-      for (int k = tid; k < kRowsA * S::kMarkWords; k += kSoftWarps * 32) row_marks[k] = 0;
-    Walk w(recs, bars, abort_flag, a.status, a.polls);
-    for (int i = 0; w.next(); ++i) {
-      const uint32_t s_par = (uint32_t)(i >> 1) & 1u;
-      const volatile uint32_t *rec = w.rec, *head = w.head;
-      const uint32_t flags = rec[kRFlags];
-      const bool first = (flags & kFlagFirst) != 0;
-      if (first) {
-        rows = (int)head[kHTokens] * a.group;
-        fold = 1 << (int)head[kHFold];
-        row = lane_row & (kRowsA / fold - 1), copy = lane_row / (kRowsA / fold);
-        col0 = half * kHalf + copy * (kHalf / fold);
-        warp_live = (row & ~31) < rows;
-        m = -INFINITY, l = 0.f;
-        st.token = min(token_of(a, row), (int)head[kHTokens] - 1);  // rows past the block's compute on the last token's mask
-        st.ctx = (int)head[kHCtx], st.len = (int)head[kHLen];
-        const int n = (int)head[kHNew];
-        st.chain_end = st.ctx + (int)head[kHNode0] + st.token + 1;
-        st.tree = tree ? a.mask[(int)head[kHTok0] + st.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
-      }
-      bool ok = timed_wait_flag(&bars[kSFull + (i & 1)], s_par, abort_flag, a.status, a.polls);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      tc_fence_after();
-      const uint32_t half_s = tmem_row + kColS + (uint32_t)((i & 1) * kTile + half * kHalf);
-      uint64_t* pv_prev = &bars[kPvDone + ((i + 1) & 1)];
-      const uint32_t pv_par = (uint32_t)((i - 1) >> 1) & 1u;
-      if (warp_live) {  // a warp without a live row leaves what lies there: its rows are not read
-        if (fold == 4)
-          ok = soft_tile<T, D, 4>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
-                                  a.status, a.polls);
-        else if (fold == 2)
-          ok = soft_tile<T, D, 2>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
-                                  a.status, a.polls);
-        else
-          ok = soft_tile<T, D, 1>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
-                                  a.status, a.polls);
-      }
-      if (!ok) break;
-      if (((flags >> kKindShift) & 3) == kGeneral && half < D / 64) {
-        // values at places that do not exist may be anything: zeros in their stead
-        const int pos = (int)rec[kRPos + lane_row / kGroup];
-        if (pos >= 0 && pos + lane_row % kGroup >= st.len) {
-          const int stage = i % Ring<D>::kValues;
-          ok = timed_wait_flag(&bars[kVFullA + stage], (uint32_t)(i / Ring<D>::kValues) & 1u, abort_flag, a.status, a.polls);
-          if (ok) {
-            uint4* vrow = reinterpret_cast<uint4*>(smem + S::kOffV + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) vrow[e] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      }
-      if constexpr (kCareful) {
-        const int stage = i % Ring<D>::kValues;
-        ok = timed_wait_flag(&bars[kVFullA + stage], (uint32_t)(i / Ring<D>::kValues) & 1u, abort_flag, a.status, a.polls);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        if (half < D / 64) {
-          uint32_t pos[2], neg[2];
-          uint4* v = reinterpret_cast<uint4*>(smem + S::kOffV + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
-          if (take_out<T>(v, lane_row, pos, neg)) misc->bad[i & 1] = 1;
-          uint32_t* mark = place_marks + lane_row * S::kMarkWords + 2 * half;
-          mark[0] = pos[0], mark[1] = pos[1], mark[D / 32] = neg[0], mark[D / 32 + 1] = neg[1];
-          fence_proxy_async_smem();
-        }
-        if (!meet()) {
-          met = true;
-          break;
-        }
-        if (*reinterpret_cast<volatile int*>(&misc->bad[i & 1]) && row < rows) {
-          // the marks of this thread's places that the row sees
-          const int kind = (flags >> kKindShift) & 3;
-          for (int p = col0; p < col0 + kHalf / fold; ++p) {
-            bool seen = kind == kFull || (kind == kRowMask && ((rec[kRMask] >> st.token) & 1u));
-            if (kind == kGeneral)
-              seen = (group_bits((int)rec[kRPos + p / kGroup], rec[kRMask + p / kGroup], st, tree, lists) >> (p % kGroup)) & 1u;
-            for (int k = 0; seen && k < S::kMarkWords; ++k) {
-              const uint32_t x = place_marks[p * S::kMarkWords + k];
-              if (x) atomicOr(&row_marks[row * S::kMarkWords + k], x);
-            }
-          }
-        }
-        if (tid == 0) misc->bad[(i + 1) & 1] = 0;
-        if (!meet()) {
-          met = true;
-          break;
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kPFull + (i & 1)]);
-      if (!(flags & kFlagLast)) {
-        w.done();
-        continue;
-      }
-
-      // the segment's rows
-      ok = timed_wait_flag(&bars[kPvDone + (i & 1)], s_par, abort_flag, a.status, a.polls);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      tc_fence_after();
-      stats[tid] = make_float2(m, l);
-      if (!meet()) {
-        met = true;
-        break;
-      }
-      // the row's parts: two halves of `fold` copies
-      const int per = kRowsA / fold;
-      auto row_of = [&](int x, float& sum) {  // the row's largest maximum, and its sum
-        float top = -INFINITY;
-        sum = 0.f;
-#pragma unroll 1
-        for (int p = x; p < kRowsA; p += per) top = fmaxf(top, fmaxf(stats[p].x, stats[kRowsA + p].x));
-#pragma unroll 1
-        for (int p = x; p < kRowsA; p += per) {
-          const float2 u = stats[p], v = stats[kRowsA + p];
-          // (a part without a maximum has the sum 0, or NaN where all scores that it sees are NaN)
-          sum += u.x != -INFINITY ? u.y * ex2((u.x - top) * c) : u.y;
-          sum += v.x != -INFINITY ? v.y * ex2((v.x - top) * c) : v.y;
-        }
-        return top;
-      };
-      float sum_l;
-      const float big = row_of(row, sum_l);
-      const uint32_t slot = head[kHOut];
-      const bool direct = slot == 0xFFFFFFFFu, empty = sum_l == 0.f;
-      const bool lost = sum_l != sum_l;  // some score is NaN: so is the row, whichever part saw it
-      // what this lane's two halves weigh in the row
-      const float inv = empty ? 0.f : direct || lost ? 1.f / sum_l : 1.f, m0 = stats[lane_row].x, m1 = stats[kRowsA + lane_row].x;
-      const float g0 = m0 == -INFINITY && !lost ? 0.f : ex2((m0 - big) * c) * inv;
-      const float g1 = m1 == -INFINITY && !lost ? 0.f : ex2((m1 - big) * c) * inv;
-      const int tok0 = (int)head[kHTok0], kvh = (int)head[kHHead];
-      if (row < rows && half == 0 && copy == 0) {
-        const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
-        if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(empty ? -INFINITY : lost ? sum_l : fmaf(big, c, -Num<T>::kLift), sum_l);
-        else if (a.lse != nullptr)
-          a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (fmaf(big, c, -Num<T>::kLift) + __log2f(sum_l)) * 0.6931471805599453f;
-      }
-      const bool sum_ok = sum_l > 0.f && sum_l < INFINITY;  // else its scores are not finite, or it sees nothing
-      uint32_t pos[D / 64] = {}, neg[D / 64] = {};  // marks of the row's columns of this half
-      if constexpr (kCareful) {
-        if (row < rows && copy == 0 && sum_ok) {
-#pragma unroll
-          for (int k = 0; k < D / 64; ++k) {
-            pos[k] = row_marks[row * S::kMarkWords + half * (D / 64) + k];
-            neg[k] = row_marks[row * S::kMarkWords + D / 32 + half * (D / 64) + k];
-          }
-        }
-        soft_sync();  // the scratch is free
-      }
-      bool odd;
-      if (fold == 4) odd = write_rows<T, D, 4>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
-      else if (fold == 2) odd = write_rows<T, D, 2>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
-      else odd = write_rows<T, D, 1>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
-      if constexpr (kCareful) {
-        soft_sync();  // the rows are written
-        const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
-        T* to = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs + half * (D / 2);
-        float* part = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row) * D + half * (D / 2);
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          for (uint32_t left = pos[k] | neg[k]; left; left &= left - 1u) {
-            const int e = __ffs((int)left) - 1;
-            const bool up = (pos[k] >> e) & 1u, down = (neg[k] >> e) & 1u;
-            const float x = up && down ? NAN : up ? INFINITY : -INFINITY;
-            if (direct) to[32 * k + e] = (T)x;
-            else part[32 * k + e] = x;
-          }
-        for (int k = tid; k < kRowsA * S::kMarkWords; k += kSoftWarps * 32) row_marks[k] = 0;
-      } else if (soft_any(odd)) {  // rare
-        if (row < rows && sum_ok && ((*reinterpret_cast<volatile uint32_t*>(&misc->odd[row >> 5]) >> (row & 31)) & 1u)) misc->careful = 1;
-        soft_sync();
-        if (tid < kRowsA / 32) misc->odd[tid] = 0;
-        soft_sync();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kOEmpty]);
-      w.done();
-    }
-    if (!w.ended && !met && lane == 0) {
-      // gave up: say so, then take this warp's place at the barrier that the others may wait at
-      *reinterpret_cast<volatile int*>(&misc->soft_dead) = 1;
-      mbar_arrive(&bars[kMerge]);
-    }
-  };
-
-  // once, or a second time where some value was not finite (see take_out)
-  bool careful = false;
-#pragma unroll 1
-  for (;;) {
+    uint64_t* const bars = all_bars + (kCareful ? kBarSet : 0);
     if (warp == kPlanWarp) {
       const bool some = w0 < w1;
       int r = some ? misc->begin[0] : 0, n = some ? misc->begin[1] : 0, t0 = some ? misc->begin[2] : 0, s = some ? misc->begin[3] : 0;
@@ -1103,7 +890,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       }
       if (bad_block) report(a.status, IDX_ST_BLOCK_OOR);
       __syncwarp();
-      clear_rest<T, D>(a);
+      if constexpr (!kCareful) clear_rest<T, D>(a);
     } else if (warp == kKeyTma || warp == kValueTma) {
       const bool keys = warp == kKeyTma;
       const CUtensorMap* map = keys ? &kmap : &vmap;
@@ -1255,30 +1042,246 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         mbar_wait(&bars[kDrainA], 0, nullptr);
       }
     } else if (warp < kSoftWarps) {
-      if (careful) softmax_role(std::true_type{});
-      else softmax_role(std::false_type{});
+      const int lane_row = tid & (kRowsA - 1), half = warp >> 2;
+      const uint32_t tmem_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t half_o = tmem_row + kColO + (uint32_t)(half * D);
+      float* scratch = reinterpret_cast<float*>(smem + S::kOffScratch);
+      float2* stats = reinterpret_cast<float2*>(smem + S::kOffStats);
+      const bool negate = a.scale < 0.f;
+      // scores in powers of two; a scale of 0 becomes one that still hides masked places
+      const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+      float m = -INFINITY, l = 0.f;
+      RowState st{};
+      int meets = 0;
+      int row = 0, copy = 0, fold = 1, col0 = 0, rows = 0;
+      bool warp_live = true, met = false;
+      // All eight warps meet, those that gave up among them (see below); the wait
+      // ends for all or for none, so that no warp misses a later barrier.  False:
+      // one gave up.
+      auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kMerge]);
+        const bool all = mbar_wait(&bars[kMerge], (uint32_t)meets & 1u, nullptr);
+        ++meets;
+        return __all_sync(0xFFFFFFFFu, all) && !*reinterpret_cast<volatile int*>(&misc->soft_dead);
+      };
+      uint32_t* place_marks = reinterpret_cast<uint32_t*>(scratch);  // [place][+ columns, - columns]
+      uint32_t* row_marks = place_marks + kTile * S::kMarkWords;
+      if (kCareful)
+        for (int k = tid; k < kRowsA * S::kMarkWords; k += kSoftWarps * 32) row_marks[k] = 0;
+      Walk w(recs, bars, abort_flag, a.status, a.polls);
+      for (int i = 0; w.next(); ++i) {
+        const uint32_t s_par = (uint32_t)(i >> 1) & 1u;
+        const volatile uint32_t *rec = w.rec, *head = w.head;
+        const uint32_t flags = rec[kRFlags];
+        const bool first = (flags & kFlagFirst) != 0;
+        if (first) {
+          rows = (int)head[kHTokens] * a.group;
+          fold = 1 << (int)head[kHFold];
+          row = lane_row & (kRowsA / fold - 1), copy = lane_row / (kRowsA / fold);
+          col0 = half * kHalf + copy * (kHalf / fold);
+          warp_live = (row & ~31) < rows;
+          m = -INFINITY, l = 0.f;
+          st.token = min(token_of(a, row), (int)head[kHTokens] - 1);  // rows past the block's compute on the last token's mask
+          st.ctx = (int)head[kHCtx], st.len = (int)head[kHLen];
+          const int n = (int)head[kHNew];
+          st.chain_end = st.ctx + (int)head[kHNode0] + st.token + 1;
+          st.tree = tree ? a.mask[(int)head[kHTok0] + st.token] & (n >= 64 ? ~0ull : (1ull << n) - 1ull) : 0ull;
+        }
+        bool ok = timed_wait_flag(&bars[kSFull + (i & 1)], s_par, abort_flag, a.status, a.polls);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
+        const uint32_t half_s = tmem_row + kColS + (uint32_t)((i & 1) * kTile + half * kHalf);
+        uint64_t* pv_prev = &bars[kPvDone + ((i + 1) & 1)];
+        const uint32_t pv_par = (uint32_t)((i - 1) >> 1) & 1u;
+        if (warp_live) {  // a warp without a live row leaves what lies there: its rows are not read
+          if (fold == 4)
+            ok = soft_tile<T, D, 4>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
+                                    a.status, a.polls);
+          else if (fold == 2)
+            ok = soft_tile<T, D, 2>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
+                                    a.status, a.polls);
+          else
+            ok = soft_tile<T, D, 1>(half_s, half_o, rec, st, tree, lists, c, negate, col0, copy, first, m, l, pv_prev, pv_par, abort_flag,
+                                    a.status, a.polls);
+        }
+        if (!ok) break;
+        if (((flags >> kKindShift) & 3) == kGeneral && half < D / 64) {
+          // values at places that do not exist may be anything: zeros in their stead
+          const int pos = (int)rec[kRPos + lane_row / kGroup];
+          if (pos >= 0 && pos + lane_row % kGroup >= st.len) {
+            const int stage = i % Ring<D>::kValues;
+            ok = timed_wait_flag(&bars[kVFullA + stage], (uint32_t)(i / Ring<D>::kValues) & 1u, abort_flag, a.status, a.polls);
+            if (ok) {
+              uint4* vrow = reinterpret_cast<uint4*>(smem + S::kOffV + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) vrow[e] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        }
+        if constexpr (kCareful) {
+          const int stage = i % Ring<D>::kValues;
+          ok = timed_wait_flag(&bars[kVFullA + stage], (uint32_t)(i / Ring<D>::kValues) & 1u, abort_flag, a.status, a.polls);
+          if (!__all_sync(0xFFFFFFFFu, ok)) break;
+          if (half < D / 64) {
+            uint32_t pos[2], neg[2];
+            uint4* v = reinterpret_cast<uint4*>(smem + S::kOffV + stage * S::kKv + half * (kTile * 128) + lane_row * 128);
+            if (take_out<T>(v, lane_row, pos, neg)) misc->bad[i & 1] = 1;
+            uint32_t* mark = place_marks + lane_row * S::kMarkWords + 2 * half;
+            mark[0] = pos[0], mark[1] = pos[1], mark[D / 32] = neg[0], mark[D / 32 + 1] = neg[1];
+            fence_proxy_async_smem();
+          }
+          if (!meet()) {
+            met = true;
+            break;
+          }
+          if (*reinterpret_cast<volatile int*>(&misc->bad[i & 1]) && row < rows) {
+            // the marks of this thread's places that the row sees
+            const int kind = (flags >> kKindShift) & 3;
+            for (int p = col0; p < col0 + kHalf / fold; ++p) {
+              bool seen = kind == kFull || (kind == kRowMask && ((rec[kRMask] >> st.token) & 1u));
+              if (kind == kGeneral)
+                seen = (group_bits((int)rec[kRPos + p / kGroup], rec[kRMask + p / kGroup], st, tree, lists) >> (p % kGroup)) & 1u;
+              for (int k = 0; seen && k < S::kMarkWords; ++k) {
+                const uint32_t x = place_marks[p * S::kMarkWords + k];
+                if (x) atomicOr(&row_marks[row * S::kMarkWords + k], x);
+              }
+            }
+          }
+          if (tid == 0) misc->bad[(i + 1) & 1] = 0;
+          if (!meet()) {
+            met = true;
+            break;
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kPFull + (i & 1)]);
+        if (!(flags & kFlagLast)) {
+          w.done();
+          continue;
+        }
+
+        // the segment's rows
+        ok = timed_wait_flag(&bars[kPvDone + (i & 1)], s_par, abort_flag, a.status, a.polls);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
+        stats[tid] = make_float2(m, l);
+        if (!meet()) {
+          met = true;
+          break;
+        }
+        // the row's parts: two halves of `fold` copies
+        const int per = kRowsA / fold;
+        auto row_of = [&](int x, float& sum) {  // the row's largest maximum, and its sum
+          float top = -INFINITY;
+          sum = 0.f;
+#pragma unroll 1
+          for (int p = x; p < kRowsA; p += per) top = fmaxf(top, fmaxf(stats[p].x, stats[kRowsA + p].x));
+#pragma unroll 1
+          for (int p = x; p < kRowsA; p += per) {
+            const float2 u = stats[p], v = stats[kRowsA + p];
+            // (a part without a maximum has the sum 0, or NaN where all scores that it sees are NaN)
+            sum += u.x != -INFINITY ? u.y * ex2((u.x - top) * c) : u.y;
+            sum += v.x != -INFINITY ? v.y * ex2((v.x - top) * c) : v.y;
+          }
+          return top;
+        };
+        float sum_l;
+        const float big = row_of(row, sum_l);
+        const uint32_t slot = head[kHOut];
+        const bool direct = slot == 0xFFFFFFFFu, empty = sum_l == 0.f;
+        const bool lost = sum_l != sum_l;  // some score is NaN: so is the row, whichever part saw it
+        // what this lane's two halves weigh in the row
+        const float inv = empty ? 0.f : direct || lost ? 1.f / sum_l : 1.f, m0 = stats[lane_row].x, m1 = stats[kRowsA + lane_row].x;
+        const float g0 = m0 == -INFINITY && !lost ? 0.f : ex2((m0 - big) * c) * inv;
+        const float g1 = m1 == -INFINITY && !lost ? 0.f : ex2((m1 - big) * c) * inv;
+        const int tok0 = (int)head[kHTok0], kvh = (int)head[kHHead];
+        if (row < rows && half == 0 && copy == 0) {
+          const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
+          const float ref = empty ? -INFINITY : lost ? sum_l : fmaf(big, c, -Num<T>::kLift);
+          if (!direct) reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kRowsA + row] = make_float2(ref, sum_l);
+          else if (a.lse != nullptr)
+            a.lse[(int64_t)t * a.q_heads + h] = empty ? -INFINITY : (ref + __log2f(sum_l)) * 0.6931471805599453f;
+        }
+        const bool sum_ok = sum_l > 0.f && sum_l < INFINITY;  // else its scores are not finite, or it sees nothing
+        uint32_t pos[D / 64] = {}, neg[D / 64] = {};  // marks of the row's columns of this half
+        if constexpr (kCareful) {
+          if (row < rows && copy == 0 && sum_ok) {
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+              pos[k] = row_marks[row * S::kMarkWords + half * (D / 64) + k];
+              neg[k] = row_marks[row * S::kMarkWords + D / 32 + half * (D / 64) + k];
+            }
+          }
+          soft_sync();  // the scratch is free
+        }
+        bool odd;
+        if (fold == 4) odd = write_rows<T, D, 4>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
+        else if (fold == 2) odd = write_rows<T, D, 2>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
+        else odd = write_rows<T, D, 1>(a, tmem_row + kColO, scratch, misc->odd, half, g0, g1, rows, tok0, kvh, slot);
+        if constexpr (kCareful) {
+          soft_sync();  // the rows are written
+          const int tk = token_of(a, row), t = tok0 + tk, h = kvh * a.group + row - tk * a.group;
+          T* to = static_cast<T*>(a.out) + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs + half * (D / 2);
+          float* part = a.part_o + ((int64_t)(direct ? 0 : slot) * kRowsA + row) * D + half * (D / 2);
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k)
+            for (uint32_t left = pos[k] | neg[k]; left; left &= left - 1u) {
+              const int e = __ffs((int)left) - 1;
+              const bool up = (pos[k] >> e) & 1u, down = (neg[k] >> e) & 1u;
+              const float x = up && down ? NAN : up ? INFINITY : -INFINITY;
+              if (direct) to[32 * k + e] = (T)x;
+              else part[32 * k + e] = x;
+            }
+          for (int k = tid; k < kRowsA * S::kMarkWords; k += kSoftWarps * 32) row_marks[k] = 0;
+        } else if (soft_any(odd)) {  // rare
+          if (row < rows && sum_ok && ((*reinterpret_cast<volatile uint32_t*>(&misc->odd[row >> 5]) >> (row & 31)) & 1u)) misc->careful = 1;
+          soft_sync();
+          if (tid < kRowsA / 32) misc->odd[tid] = 0;
+          soft_sync();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kOEmpty]);
+        w.done();
+      }
+      if (!w.ended && !met && lane == 0) {
+        // gave up: say so, then take this warp's place at the barrier that the others may wait at
+        *reinterpret_cast<volatile int*>(&misc->soft_dead) = 1;
+        mbar_arrive(&bars[kMerge]);
+      }
     }
 
+    if constexpr (!kCareful) {
+      if (tid == 0 && blockIdx.x == 0) *reinterpret_cast<unsigned long long*>(a.cuts + 8 * kMaxCtas) = W;
+      // lengths that the table does not hold
+      if (blockIdx.x == 0)
+        for (int r = tid; r < a.num_reqs; r += kThreadsA)
+          if (plan.ntok(r) > 0 && plan.len(plan.seq(r)) < plan.seq(r)) report(a.status, IDX_ST_LEN_CLAMPED);
+    }
     __syncwarp();
     __syncthreads();  // all copies have landed, all products are done
-    if (careful || *abort_flag || !*reinterpret_cast<volatile int*>(&misc->careful)) break;
+  };
+  run(std::false_type{});
+  bool careful = false;
+  if (!*abort_flag && *reinterpret_cast<volatile int*>(&misc->careful)) {
     careful = true;
-    bars += kBarSet;  // barriers of its own: no arrival of the first run can reach them
     if (tid == 0) {
       misc->issued[0] = misc->issued[1] = 0;
-      init_bars(bars);
+      init_bars(all_bars + kBarSet);
     }
     __syncthreads();
+    run(std::true_type{});
   }
 
-  if (tid == 0 && blockIdx.x == 0) *reinterpret_cast<unsigned long long*>(a.cuts + 8 * kMaxCtas) = W;
-  // lengths that the table does not hold
-  if (blockIdx.x == 0)
-    for (int r = tid; r < a.num_reqs; r += kThreadsA)
-      if (plan.ntok(r) > 0 && plan.len(plan.seq(r)) < plan.seq(r)) report(a.status, IDX_ST_LEN_CLAMPED);
   if (*abort_flag) {
     if (tid < 2) {
       // never leave with a copy in flight: the last ones of each ring
+      uint64_t* const bars = all_bars + (careful ? kBarSet : 0);
       const int stages = tid == 0 ? Ring<D>::kKeys : Ring<D>::kValues;
       for (int i = max(0, misc->issued[tid] - stages); i < misc->issued[tid]; ++i)
         mbar_wait(&bars[(tid == 0 ? kKFullA : kVFullA) + i % stages], (uint32_t)(i / stages) & 1u, nullptr);
