@@ -424,7 +424,9 @@ int idx_fp8_mma_probe(int32_t iters, float* check, double* flops, int32_t* statu
  *     first_r = *free_cursor + sum_{s < r} take_s
  *     block_table[r][owned_r + i] = free_blocks[first_r + i], i < take_r,
  *                                   or -1 from num_free on (IDX_ST_NO_BLOCKS)
- *     cu_tokens[r] = min(sum_{s < r} new_s, num_tokens)   (IDX_ST_LEN_CLAMPED)
+ *     cu_tokens[r] = min(sum_{s < r} new_s, num_tokens)   (IDX_ST_LEN_CLAMPED:
+ *                    seq_lens then count tokens that got no slot, so the step
+ *                    is to be made again with room for all its tokens)
  *     seq_lens[r]  = ctx_r + new_r
  *     pages_out[r] = max(owned_r, need_r), less the blocks that were missing
  *     *cursor_out  = min(*free_cursor + sum take, num_free)
@@ -491,10 +493,10 @@ int idx_rope_frequencies(int32_t rotary_dim, double base, int32_t kind, double f
  * rotary_dim / 2 of the head, or 2i and 2i + 1 with IDX_ROPE_INTERLEAVED.
  * Elements from rotary_dim on pass unchanged.  The angle is reduced as a
  * 64-bit fraction of a turn: at positions up to 2^31 - 1 it is off by at most
- * 2^-33 turns (and fp32's rounding of the fraction).  Rotated queries go to q_out; rotated keys and unchanged values
- * go to cache slot slots[t] (NULL: slot t); a negative slot is skipped, one
- * past the cache is skipped with IDX_ST_BLOCK_OOR.  Two tokens of one call
- * must not share a slot.
+ * 2^-33 turns (and fp32's rounding of the fraction).  Rotated queries go to
+ * q_out; rotated keys and unchanged values go to cache slot slots[t] (NULL:
+ * slot t); a negative slot is skipped, one past the cache is skipped with
+ * IDX_ST_BLOCK_OOR.  Two tokens of one call must not share a slot.
  *
  *   q, q_out      [num_tokens, q_heads, head_dim] with the given strides in
  *                 elements; the head's elements contiguous; q_out may be q
@@ -530,13 +532,14 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  *     s_p = scale (q . k_p),  out = sum_p e^(s_p - L) v_p,  L = ln sum_p e^s_p
  * (scale finite; negative and zero ones too).
  * A token that sees nothing gets out 0 and L -inf (as does one whose scores
- * are all -inf).  A row with a score of NaN is NaN.  Scores, maxima, sums and outputs are held in fp32; e^(s_p -
- * M), M a maximum of the scores met so far or up to 8 powers of two (fp16: 4)
- * below it, is rounded to the cache's type for the product with v; in fp16 in
- * steps of no less than 2^-31.  Scores are meant to stay below 2^24.  What is stored
- * at places that no token sees (unwritten slots of the last page, NaN and
- * infinities among them) has no effect, and what a drafted token has stored
- * reaches only the tokens that see it.
+ * are all -inf).  A row with a score of NaN is NaN.  Scores, maxima, sums and
+ * outputs are held in fp32; e^(s_p - M), M a maximum of the scores met so far
+ * or up to 8 powers of two (fp16: 4) below it, is rounded to the cache's type
+ * for the product with v; in fp16 in steps of no less than 2^-31.  Scores are
+ * meant to stay below 2^24.  What is stored at places that no token sees
+ * (unwritten slots of the last page, NaN and infinities among them) has no
+ * effect, and what a drafted token has stored reaches only the tokens that see
+ * it.
  *
  *   q, out        [num_tokens, q_heads, head_dim] with the given strides in
  *                 elements (multiples of 8), 16-byte aligned
@@ -565,6 +568,7 @@ int idx_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
  *                 multiple of page_lists, pages_per_list 1..64, and no more
  *                 than 2^31 - 1 entries in all.
  *   lse           [num_tokens, q_heads] float32 or NULL: L
+ *                 (out and lse must not overlap the inputs)
  *   workspace     >= idx_tree_attention_workspace_bytes(...) bytes, 256-byte
  *                 aligned, no initialisation needed
  */
@@ -598,9 +602,11 @@ int idx_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_str
  * residual is p without the refused tokens.  A residual without mass falls
  * back to p; p without mass gives token vocab - 1.
  * Tests of children are made in 64-bit floating point; masses and cumulative
- * sums are good to about 2^-45 of the mass and do not depend on anything but
- * the inputs and the sizes of the call.  Entries are probabilities: a negative or
- * NaN entry counts as 0, and a row's sum must stay below 8.
+ * sums are off by at most about 2^-45 of the sum of the row p and 2^-60 for
+ * each entry and refused child (2^-42 in all for 200,000 entries and one), and
+ * do not depend on anything but the inputs and the sizes of the call.  Entries
+ * are probabilities: a negative or NaN entry counts as 0, and a row's sum must
+ * stay below 8.
  *
  *   target, draft [num_tokens, vocab] float32, row strides in elements;
  *                 draft may be NULL

@@ -7,10 +7,11 @@
 // are its own (tokens in slices of equal length, taken blocks interleaved).
 // The walk is repeated in every CTA because it is short (a chunk of 1,024
 // requests is three 4 KB loads from L2 and one scan) while a second launch
-// that waits for the first costs more than the whole call: what bounds the
-// call is latency, not the 12 to 24 bytes a token that it writes: 4.6 us for 512
-// tokens of 64 trees, 12.7 us for a million tokens of 1,021 requests, whose 13
-// MB HBM would take in 2.0.
+// that waits for the first costs more than a small call: 4.5 us for 512 tokens
+// of 64 trees, all latency.  A million tokens of 1,021 requests take 12.7 us,
+// where HBM would take 2.0 for their 13 MB: there the instructions set the pace
+// (61% of the issue slots): the scan in 64 bits in each of 608 CTAs, a search for
+// each four tokens, a division by the page size a token.
 #include "idx_common.cuh"
 #include "idx_internal.h"
 

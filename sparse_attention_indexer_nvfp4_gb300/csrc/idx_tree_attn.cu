@@ -47,11 +47,14 @@
 // requests of up to 61 tokens, but 58.6 for 55.7 on 64 tokens over 16,384
 // places).  Measured with 64 query and 4 KV heads of 128 in bf16:
 //     64 requests, 8 tokens each over 1,024 to 16,384 places   213 us, 5.9 TB/s
-//     one request, 8 tokens over 500,000 places                169 us, 6.1 TB/s
-//     64 requests, one token each over 8,192 places            178 us, 6.0 TB/s
-//     one request, 64 tokens over 65,536 places                161 us, 855 TFLOP/s
-//     64 requests, 8 tokens each, 16 of their pages a list     131 us
-//     one request, one token over 1,000 places                 16.1 us
+//     one request, 8 tokens over 500,000 places                168 us, 6.1 TB/s
+//     64 requests, one token each over 8,192 places            177 us, 6.1 TB/s
+//     one request, 64 tokens over 65,536 places                160 us, 859 TFLOP/s
+//     one request, 2,048 tokens (a chain) after 16,384        1351 us, 865 TFLOP/s
+//     64 requests, 8 tokens each, 16 of their pages a list     132 us
+//     one request, one token over 1,000 places                 16.3 us
+// With heads of 64 a tile has half the bytes and takes nearly as long: 156 us
+// (3.5 TB/s) for the first, 137 us (3.9) for the third.
 // What the last spends: launches of the kernel and the join (~5 us), the
 // setup up to the first copy (~8 us), then a tile's latency from copy to row.
 #include <cuda_bf16.h>
@@ -282,7 +285,11 @@ struct Num<__nv_bfloat16> {
   static constexpr bool kBf16 = true;
   static constexpr CUtensorMapDataType kMap = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   static constexpr float kLift = 0.f, kRescale = 8.f;
-  // two values rounded to nearest: the weights of the product with v
+  // Two values rounded to nearest: outputs, and the weights of the product with
+  // v, whose two operands the tensor core wants in one 16-bit type.  That is the
+  // one rounding before the output's: against 64 bits outputs are off by 0.0023
+  // (bf16) and 0.00029 (fp16) of their size, with weights in fp32 by 0.0017 and
+  // 0.00021.
   static __device__ uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -34,8 +34,8 @@
 // of 8 over 200,003 entries: 28.8 us with clusters of 8 CTAs of 256 threads (of
 // 16, 4 and 2 CTAs: 42.7, 33.5 and 48.9; of 512 and 128 threads: 43 and 40; with
 // each pass' entries asked into L2 at its start: 33.4); 48 trees of 24 over
-// 128,000: 32.0 us (clusters of 16: 36.6; asked into L2: 33.0); a chain of 4 over
-// 32,000: 8.6 us.
+// 128,000: 32.6 us, up to 39 as the inputs go (clusters of 16: 36.6; asked into
+// L2: 33.0); a chain of 4 over 32,000: 8.6 us.
 #include "idx_common.cuh"
 #include "idx_internal.h"
 
