@@ -21,8 +21,9 @@
  *     so idx_dequant_nvfp4_pages, idx_score_pages, idx_topk16_select,
  *     idx_decode_step, idx_mtp_score_fp8, idx_prefill_index_step,
  *     idx_mxfp8_quantize, idx_build_slots, idx_rope_append,
- *     idx_tree_attention and idx_verify_drafts can sit inside CUDA-graph
- *     capture.
+ *     idx_tree_attention, idx_verify_drafts, idx_norm_rope_append,
+ *     idx_index_append, idx_logit_probs, idx_settle_drafts, idx_fork_pages
+ *     and idx_release_pages can sit inside CUDA-graph capture.
  *   - Return value: IDX_OK (0) when the work was enqueued (or there was
  *     nothing to do), else a negative IDX_E_* code; on an error nothing is
  *     launched.  Argument checks are on the host and never touch the GPU.
@@ -63,6 +64,7 @@ extern "C" {
 #define IDX_ST_TIMEOUT 8     /* an internal pipeline wait gave up; that CTA's outputs are incomplete */
 #define IDX_ST_NO_BLOCKS 16  /* the free list ran out: block ids and slots of -1 */
 #define IDX_ST_BAD_TREE 32   /* a parent outside [-1, own index), or a drafted token past 64 in a tree */
+#define IDX_ST_BAD_FORK 64   /* a fork whose child is a parent or another fork's child, or out of range: not made */
 
 /* Fixed geometry. */
 #define IDX_PAGE_TOKENS 128
@@ -397,10 +399,16 @@ int idx_fp8_mma_probe(int32_t iters, float* check, double* flops, int32_t* statu
  * One step of decoding with drafted tokens, around the indexer:
  *   idx_build_slots     where the step's tokens go: block tables, slots,
  *                       positions and tree masks from the requests' lengths;
- *   idx_rope_append     rotary positions of q and k; k and v into the cache;
+ *   idx_rope_append     rotary positions of q and k; k and v into the cache
+ *                       (idx_norm_rope_append: after a norm of each head);
+ *   idx_index_append    the indexer's queries, and its keys into the pages;
  *   (idx_decode_step    the pages that each drafted token looks at;)
  *   idx_tree_attention  attention of the drafted tokens over the cache;
- *   idx_verify_drafts   which drafted tokens stand, and the token after them.
+ *   idx_logit_probs     the probabilities of the tokens after them;
+ *   idx_verify_drafts   which drafted tokens stand, and the token after them;
+ *   idx_settle_drafts   the rows of those that stand moved together.
+ * Between steps, idx_fork_pages and idx_release_pages share a request's pages
+ * with new requests and give pages back.
  *
  * Tokens of all requests are packed: request r's are cu_tokens[r] ..
  * cu_tokens[r+1]-1.  Token i of a request is stored at place seq_len - n + i
@@ -633,6 +641,224 @@ int idx_verify_drafts(const float* target, int64_t target_stride, const float* d
                       int32_t num_reqs, int32_t num_tokens, const float* accept_u, const float* sample_u,
                       int32_t* out_tokens, int32_t* out_nodes, int32_t max_out, int32_t* num_accepted,
                       int32_t* status, void* stream);
+
+/*
+ * idx_rope_append after a norm of each head.  With weights w, for each row x of
+ * a head:
+ *     n = (offset + w) x / sqrt(mean x^2 + eps)
+ * and n's pairs turn as in idx_rope_append; elements from rotary_dim on are
+ * those of n.  Values are not normed.  Computed in 32 bits (the squares' sum
+ * must stay below 3e38: a row of larger elements becomes 0, one with an
+ * infinity or NaN is not finite), rounded once.
+ *
+ *   q_weight, k_weight   [head_dim] of the type of all tensors, or NULL: that
+ *                 side is turned only
+ *   eps           >= 0;  offset  added to the weights (0, or 1 where weights
+ *                 are stored less 1)
+ * Other arguments as in idx_rope_append (q_out may be q, with its strides).
+ */
+int idx_norm_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                         int64_t qo_token_stride, int64_t qo_head_stride, int32_t q_heads, const void* k,
+                         int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                         int64_t v_head_stride, int32_t kv_heads, int32_t num_tokens, int32_t head_dim,
+                         int32_t rotary_dim, const void* q_weight, const void* k_weight, float eps, float offset,
+                         const int32_t* positions, const double* inv_freq, float mscale, const int64_t* slots,
+                         void* k_cache, void* v_cache, int64_t num_blocks, int32_t page_tokens, int64_t c_block_stride,
+                         int64_t c_token_stride, int64_t c_head_stride, int32_t dtype, int32_t flags, int32_t* status,
+                         void* stream);
+
+/*
+ * The indexer's inputs: queries and keys of 128 elements normed and turned as
+ * in idx_norm_rope_append (y), then quantised.  For a query's row, with a =
+ * max |y|,
+ *     q_out = e4m3_rn(448 y / a),  q_scale = scale * a / 448 * head_weights
+ * and for a key's row, over each 16 consecutive elements, with a = max |y|,
+ *     s = e4m3_rn_satfinite(a / 6),  code = e2m1_rn_satfinite(y / s)
+ * (codes 0 where s is 0), written to the NVFP4 page of its slot.  Codes and key
+ * scales are those of 64-bit arithmetic (rounded to nearest, halves to even;
+ * angles as in idx_rope_append); q_scale is fp32.  A query's row that holds an
+ * infinity or NaN (or whose squares' sum passes 3e38) gets codes 0x7F and a NaN
+ * scale, a key's gets NaN scales and codes 0, so its scores are NaN and rank
+ * last.  A query's row whose largest magnitude (before the norm) is below
+ * 2^-100 gets codes 0.
+ *
+ *   q             [num_tokens, heads, 128], the head's elements contiguous, or
+ *                 NULL with heads 0 (up to 128)
+ *   k             [num_tokens, 128], or NULL (with index_k)
+ *   q_weight, k_weight   [128] of the type of q and k, or NULL: no norm there
+ *   rotary_dim    0..128, a multiple of 16 (of 8 with IDX_ROPE_INTERLEAVED)
+ *   head_weights  [num_tokens, heads] float32 contiguous, or NULL: 1
+ *   cu_tokens     [num_reqs + 1] int32, or NULL: q_out is [num_tokens, heads,
+ *                 128] and q_scale [num_tokens, heads], as
+ *                 idx_prefill_index_step and idx_mtp_score_fp8 take them.
+ *                 With it, q_out is [num_reqs, req_slots, heads, 128] and
+ *                 q_scale [num_reqs, req_slots, heads], as idx_decode_step
+ *                 takes them: a request's n tokens go to its last n slots, the
+ *                 others stay as they are; of more than req_slots tokens only
+ *                 the last have a slot (IDX_ST_BAD_OUTPUT).  Tokens outside
+ *                 every request have none.
+ *   slots         [num_tokens] int64 cache slot of each key, or NULL: slot t;
+ *                 a negative one is skipped, one past the pages is skipped
+ *                 with IDX_ST_BLOCK_OOR
+ *   index_k       [num_blocks, page_tokens, 72] uint8 pages, page_tokens 128
+ *                 (as in idx_dequant_nvfp4_pages) or 256 (IDX_PAGE_256)
+ *   dtype         of q, k and the weights;  flags  0 or IDX_ROPE_INTERLEAVED
+ * q_out and index_k 16-byte aligned.
+ */
+int idx_index_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t heads, const void* k,
+                     int64_t k_token_stride, int32_t num_tokens, int32_t rotary_dim, const void* q_weight,
+                     const void* k_weight, float eps, float offset, const int32_t* positions, const double* inv_freq,
+                     float mscale, const float* head_weights, float scale, const int32_t* cu_tokens, int32_t num_reqs,
+                     int32_t req_slots, uint8_t* q_out, float* q_scale, const int64_t* slots, uint8_t* index_k,
+                     int64_t num_blocks, int32_t page_tokens, int32_t dtype, int32_t flags, int32_t* status,
+                     void* stream);
+
+/*
+ * Probabilities from logits.  Row t is that of node i = t - cu_tokens[r] of
+ * request r; for entry v, with c the times that the request has token v
+ * already and each step rounded to fp32 in this order,
+ *     x = logit
+ *     seen (c > 0, or v in the prompt):  x <- x / repetition where x > 0, else
+ *                                        x * repetition
+ *     c > 0:  x <- x - (frequency * c + presence)
+ *     x <- x + bias, for each of the request's biases of v in their order
+ *     x <- -inf where the mask has no bit (whatever the logit is)
+ *     p = e^(x / T - L),  L = ln sum e^(x / T)
+ * With T = 0 (or below 2^-60, or NaN) p is 1 at the lowest v of the largest x
+ * and 0 elsewhere, and L is that x.  A row with nothing left gets p 0 and L
+ * -inf; one with a NaN or +inf that is not masked is NaN.  x, sums and p are
+ * fp32.
+ * c is the count in `counts` plus, with tokens, that of v among the drafted
+ * tokens of the row's path: nodes j >= 1 of tree_mask[t] (tree_mask NULL: 1 <=
+ * j <= i).  Node 0's token is taken to be counted already, as idx_settle_drafts
+ * does it.
+ *
+ *   logits        [num_tokens, vocab] of dtype, row stride in elements
+ *   vocab         up to IDX_PROBS_MAX_VOCAB
+ *   temperature, repetition, presence, frequency   [num_reqs] float32, each
+ *                 may be NULL: 1, 1, 0, 0 (with no penalty at all counts and
+ *                 tokens are not read)
+ *   counts        [num_reqs, vocab] int32, row stride in elements, or NULL: the
+ *                 count in the low 31 bits, the highest bit set for a token of
+ *                 the prompt
+ *   tokens        [num_tokens] int32 or NULL;  tree_mask [num_tokens] uint64 or
+ *                 NULL (with tokens); a path counts up to IDX_VERIFY_MAX_NODES
+ *                 tokens (IDX_ST_BAD_TREE), those outside [0, vocab) not
+ *   bias_cu       [num_reqs + 1] int32 or NULL: request r's biases are
+ *                 bias_tokens and bias_values (int32, float32, num_bias in
+ *                 all) bias_cu[r] .. bias_cu[r+1]-1
+ *   allowed       [num_tokens, ceil(vocab / 32)] int32, row stride in elements,
+ *                 or NULL: bit v % 32 of word v / 32
+ *   probs         [num_tokens, vocab] float32; may be logits (in fp32, with its
+ *                 stride).  Rows outside every request (a padded batch) get 0
+ *   lse           [num_tokens] float32 or NULL: L
+ */
+#define IDX_PROBS_MAX_VOCAB 393216
+int idx_logit_probs(const void* logits, int64_t logits_stride, int32_t dtype, int32_t vocab, int32_t num_tokens,
+                    const int32_t* cu_tokens, int32_t num_reqs, const float* temperature, const float* repetition,
+                    const float* presence, const float* frequency, const int32_t* counts, int64_t counts_stride,
+                    const int32_t* tokens, const uint64_t* tree_mask, const int32_t* bias_cu,
+                    const int32_t* bias_tokens, const float* bias_values, int32_t num_bias, const int32_t* allowed,
+                    int64_t allowed_stride, float* probs, int64_t probs_stride, float* lse, int32_t* status,
+                    void* stream);
+
+/*
+ * A cache whose rows the calls below move: `planes` (layers, keys and values)
+ * of the same blocks, a token's row in a plane `row_bytes` contiguous bytes.
+ * Strides are in bytes.  The codes and the scales of NVFP4 index-K pages are
+ * two caches: 64 bytes a token from the page's begin on, and 8 from byte 64 *
+ * page_tokens on.  Host memory, read during the call.
+ */
+#define IDX_MAX_CACHES 8
+typedef struct {
+  void* base;
+  int64_t plane_stride, block_stride, token_stride;
+  int32_t planes, row_bytes;
+} idx_cache;
+
+/*
+ * After idx_verify_drafts: the rows of the nodes that stand move together in
+ * every cache, from slots[cu_tokens[r] + out_nodes[r][i]] to
+ * slots[cu_tokens[r] + 1 + i] for i < num_accepted[r], so that the next step's
+ * context has no gaps, and
+ *     ctx_out[r] = ctx_lens[r] + 1 + num_accepted[r]   (a request without
+ *                  tokens in this step: ctx_lens[r])
+ *     counts[r][x] += 1 for the tokens x that stand and the one drawn after
+ *                  them (out_tokens[r][0 .. num_accepted[r]]), with counts
+ * num_accepted is taken as at most the request's tokens, or max_out, less one.
+ * A node outside [i + 1, tokens of the request) is not moved
+ * (IDX_ST_BAD_TREE), nor a row whose place has no slot, or one past the caches
+ * (IDX_ST_BLOCK_OOR).  Rows of other places stay as they are.
+ *
+ *   caches        num_caches of num_blocks blocks of page_tokens tokens
+ *   slots, cu_tokens, num_tokens   as idx_build_slots gives them
+ *   out_tokens, out_nodes [num_reqs, max_out], num_accepted   as
+ *                 idx_verify_drafts gives them (out_tokens: with counts)
+ *   ctx_lens, ctx_out   [num_reqs] int32; ctx_out may be ctx_lens
+ *   counts        [num_reqs, vocab] int32, row stride in elements, or NULL
+ */
+int idx_settle_drafts(const idx_cache* caches, int32_t num_caches, int64_t num_blocks, int32_t page_tokens,
+                      const int64_t* slots, const int32_t* cu_tokens, int32_t num_reqs, int32_t num_tokens,
+                      const int32_t* out_tokens, const int32_t* out_nodes, int32_t max_out,
+                      const int32_t* num_accepted, const int32_t* ctx_lens, int32_t* ctx_out, int32_t* counts,
+                      int64_t counts_stride, int32_t vocab, int32_t* status, void* stream);
+
+/*
+ * Requests forked: child c = children[f] gets the context of p = parents[f].
+ * With len = min(ctx_lens[p], owned_pages[p] * page_tokens)
+ * (IDX_ST_LEN_CLAMPED), full = floor(len / page_tokens), rest = len %
+ * page_tokens:
+ *     block_table[c][i] = block_table[p][i], refs[that block] += 1, i < full
+ *     rest > 0:  block_table[c][full] = the next free block, the first rest
+ *                tokens of the parent's page `full` copied to it in every cache
+ *     ctx_lens[c] = len,  owned_pages[c] = full + (rest > 0)
+ *     *cursor_out = min(*free_cursor + forks with rest > 0, num_free)
+ * Free blocks are taken in the forks' order; a fork for which there is none is
+ * not made (IDX_ST_NO_BLOCKS): its child gets length and pages 0.  A fork whose
+ * child is a parent in the same call, or the child of another fork, or that has
+ * a request outside [0, num_reqs), is not made and changes nothing
+ * (IDX_ST_BAD_FORK).  What a child owned before is not released.  Table
+ * entries outside [0, num_blocks) are passed on, not counted, and not copied
+ * from (IDX_ST_BLOCK_OOR).
+ *
+ *   parents, children   [num_forks] int32, up to IDX_MAX_FORKS
+ *   ctx_lens, owned_pages   [num_reqs] int32, in and out
+ *   block_table   [num_reqs, bt_stride] int32, in and out
+ *   refs          [num_blocks] int32, in and out: holders of each block beyond
+ *                 the first, >= 0 (0 for blocks fresh from the free list)
+ *   free_blocks, free_cursor, cursor_out   as in idx_build_slots
+ */
+#define IDX_MAX_FORKS 4096
+int idx_fork_pages(const idx_cache* caches, int32_t num_caches, int64_t num_blocks, int32_t page_tokens,
+                   const int32_t* parents, const int32_t* children, int32_t num_forks, int32_t* ctx_lens,
+                   int32_t* owned_pages, int32_t num_reqs, int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                   int32_t* refs, const int32_t* free_blocks, int32_t num_free, const int32_t* free_cursor,
+                   int32_t* cursor_out, int32_t* status, void* stream);
+
+/*
+ * Pages given back: request r keeps pages_out[r] = min(owned_pages[r],
+ * ceil(keep_lens[r] / page_tokens)) pages (negative lengths count as 0); of
+ * each page after those one holder is taken off.  A block whose last holder
+ * went (once, whatever the number of releases) goes back to the free list, its
+ * refs 0: with m such blocks,
+ *     *cursor_out = *free_cursor - m
+ *     free_blocks[*cursor_out + i] = the i-th lowest of their ids
+ * (the list's entries before the cursor are those taken from it; with more
+ * blocks than entries the lowest are dropped: IDX_ST_BAD_OUTPUT).  Table
+ * entries from pages_out[r] on mean nothing afterwards.  Entries of -1 are
+ * skipped, others outside [0, num_blocks) too (IDX_ST_BLOCK_OOR).
+ *
+ *   keep_lens, owned_pages, pages_out   [num_reqs] int32 (a finished request
+ *                 keeps 0); pages_out is another array than owned_pages
+ *   block_table   [num_reqs, bt_stride] int32;  refs [num_blocks] int32, in and
+ *                 out, as in idx_fork_pages
+ *   free_blocks   [num_free] int32, in and out; free_cursor and cursor_out at
+ *                 different addresses
+ */
+int idx_release_pages(const int32_t* keep_lens, const int32_t* owned_pages, int32_t num_reqs,
+                      const int32_t* block_table, int64_t bt_stride, int32_t max_blocks, int32_t* refs,
+                      int64_t num_blocks, int32_t* free_blocks, int32_t num_free, const int32_t* free_cursor,
+                      int32_t* cursor_out, int32_t* pages_out, int32_t page_tokens, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

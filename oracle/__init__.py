@@ -21,6 +21,9 @@ Modules:
 * ``step`` - a decoding step's calls around the indexer: block tables and slots,
   rotary positions, attention of a tree of drafted tokens over pages, and the
   verification of drafts, each from its formula in 64 bits.
+* ``serve`` - what stands between those calls: norms with the rotation, the
+  indexer's queries and keys, probabilities from logits, and the moving,
+  sharing and giving back of cached rows and pages.
 
 Pins (checked by ``tests/test_oracle_*.py`` against the pages, closed forms
 and brute force, never against the CUDA path) are listed in each function's

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "IdxError",
@@ -48,6 +49,16 @@ __all__ = [
     "idx_tree_attention",
     "idx_verify_drafts",
     "VERIFY_MAX_NODES",
+    "idx_norm_rope_append",
+    "idx_index_append",
+    "idx_logit_probs",
+    "PROBS_MAX_VOCAB",
+    "index_caches",
+    "idx_settle_drafts",
+    "idx_fork_pages",
+    "idx_release_pages",
+    "MAX_CACHES",
+    "MAX_FORKS",
     "SYMBOLS",
     "ST_BLOCK_OOR",
     "ST_LEN_CLAMPED",
@@ -55,6 +66,7 @@ __all__ = [
     "ST_TIMEOUT",
     "ST_NO_BLOCKS",
     "ST_BAD_TREE",
+    "ST_BAD_FORK",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -67,6 +79,7 @@ ST_BAD_OUTPUT = 4
 ST_TIMEOUT = 8
 ST_NO_BLOCKS = 16
 ST_BAD_TREE = 32
+ST_BAD_FORK = 64
 NOALLOC_SCRATCH_BYTES = 4 << 20  # scratch inside the library used by idx_topk16_select_noalloc
 DEFAULT_WAIT_POLLS = 100_000  # pipeline-wait budget of the tensor-core kernels (about 2 s)
 
@@ -109,6 +122,18 @@ SYMBOLS = {
                                           _sz, _p, _p]),
     "idx_verify_drafts": (ctypes.c_int, [_p, _i64, _p, _i64, _i32, _p, _p, _p, _i32, _i32, _p, _p, _p, _p, _i32, _p, _p,
                                          _p]),
+    "idx_norm_rope_append": (ctypes.c_int, [_p, _i64, _i64, _p, _i64, _i64, _i32, _p, _i64, _i64, _p, _i64, _i64, _i32, _i32,
+                                            _i32, _i32, _p, _p, _f32, _f32, _p, _p, _f32, _p, _p, _p, _i64, _i32, _i64, _i64,
+                                            _i64, _i32, _i32, _p, _p]),
+    "idx_index_append": (ctypes.c_int, [_p, _i64, _i64, _i32, _p, _i64, _i32, _i32, _p, _p, _f32, _f32, _p, _p, _f32, _p, _f32,
+                                        _p, _i32, _i32, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _p, _p]),
+    "idx_logit_probs": (ctypes.c_int, [_p, _i64, _i32, _i32, _i32, _p, _i32, _p, _p, _p, _p, _p, _i64, _p, _p, _p, _p, _p, _i32,
+                                       _p, _i64, _p, _i64, _p, _p, _p]),
+    "idx_settle_drafts": (ctypes.c_int, [_p, _i32, _i64, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p, _p, _p, _i64, _i32, _p,
+                                         _p]),
+    "idx_fork_pages": (ctypes.c_int, [_p, _i32, _i64, _i32, _p, _p, _i32, _p, _p, _i32, _p, _i64, _i32, _p, _p, _i32, _p, _p, _p,
+                                      _p]),
+    "idx_release_pages": (ctypes.c_int, [_p, _p, _i32, _p, _i64, _i32, _p, _i64, _p, _i32, _p, _p, _p, _i32, _p, _p]),
 }
 
 
@@ -323,7 +348,7 @@ class _Torch:
     def __init__(self):
         import torch
 
-        self.i32, self.i64, self.f32, self.f64 = torch.int32, torch.int64, torch.float32, torch.float64
+        self.i32, self.i64, self.f32, self.f64, self.u8 = torch.int32, torch.int64, torch.float32, torch.float64, torch.uint8
         self.words = (torch.int64, torch.uint64)
         self.codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
         self.many = torch.cuda.device_count() > 1
@@ -557,4 +582,256 @@ def idx_verify_drafts(target, draft, tokens, cu_tokens, accept_u, sample_u, out_
         target.data_ptr(), _row_stride(target), None if draft is None else draft.data_ptr(), 0 if draft is None else _row_stride(draft), vocab, tokens.data_ptr(),
         None if parents is None else parents.data_ptr(), cu_tokens.data_ptr(), reqs, total, accept_u.data_ptr(), sample_u.data_ptr(), out_tokens.data_ptr(),
         out_nodes.data_ptr(), max_out, num_accepted.data_ptr(), None if status is None else status.data_ptr(), _stream_on(stream, target))
+    return rc if rc >= 0 else _check(fn, rc)
+
+
+# ---------------------------------------------------------------------------
+# Between those calls: norms, the indexer's inputs, probabilities, caches
+# ---------------------------------------------------------------------------
+
+PROBS_MAX_VOCAB = 393216  # entries of a row of idx_logit_probs
+MAX_CACHES = 8  # caches of one call of idx_settle_drafts and idx_fork_pages
+MAX_FORKS = 4096  # forks of one call
+
+
+def _at(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _status_ok(T, status) -> bool:
+    return status is None or (status.is_cuda and status.dtype is T.i32 and status.numel() > 0)
+
+
+def _words_ok(T, shape, t) -> bool:
+    return t is None or (t.is_cuda and t.dtype in T.words and t.shape == shape and t.is_contiguous())
+
+
+def idx_norm_rope_append(q, k, v, q_weight, k_weight, eps: float, positions, inv_freq, q_out, k_cache, v_cache, slots=None,
+                         mscale: float = 1.0, offset: float = 0.0, interleaved: bool = False, status=None, stream=None) -> int:
+    """idx_rope_append after a norm of each head with q_weight, k_weight [D] (None: that side is turned only)."""
+    lib, T, fn = load_library(), _torch(), "idx_norm_rope_append"
+    some = q if q is not None else k
+    if some is None or (v is not None and k is None):
+        raise ValueError(f"{fn}: q, or k (with or without v), is needed")
+    if (q is None) != (q_out is None) or (k is None) != (k_cache is None) or (v is None) != (v_cache is None):
+        raise ValueError(f"{fn}: q and q_out, k and k_cache, v and v_cache go together")
+    kind = some.dtype
+    code = T.codes.get(kind)
+    if code is None:
+        raise ValueError(f"{fn}: bfloat16, float16 or float32 is needed, got {kind}")
+    tokens, dim = some.shape[0], some.shape[-1]
+    hq = 0 if q is None else q.shape[1]
+    nb, page, hk = (0, 1, 0) if k is None else (k_cache.shape[0], k_cache.shape[1], k.shape[1])
+    qshape, kshape, cshape, one = (tokens, hq, dim), (tokens, hk, dim), (nb, page, hk, dim), (tokens,)
+    if not (_rows_ok(kind, qshape, q, q_out) and _rows_ok(kind, kshape, k, v) and _rows_ok(kind, cshape, k_cache, v_cache)
+            and _are(kind, (dim,), q_weight, k_weight) and _are(T.i32, one, positions) and _are(T.f64, inv_freq.shape[:1], inv_freq)
+            and _words_ok(T, one, slots) and _status_ok(T, status)
+            and (not T.many or _here(q, q_out, k, v, k_cache, v_cache, q_weight, k_weight, positions, inv_freq, slots, status))):
+        _explain(fn, ("positions", "inv_freq", "slots", "q_weight", "k_weight"), q=(q, kind, qshape), q_out=(q_out, kind, qshape),
+                 k=(k, kind, kshape), v=(v, kind, kshape), k_cache=(k_cache, kind, (None, None, hk, dim)), v_cache=(v_cache, kind, cshape),
+                 q_weight=(q_weight, kind, (dim,)), k_weight=(k_weight, kind, (dim,)), positions=(positions, T.i32, one),
+                 inv_freq=(inv_freq, T.f64, (None,)), slots=(slots, T.words, one), status=(status, T.i32, None))
+    none = (0, 0, 0, 0)
+    cs = none if k is None else k_cache.stride()
+    if v_cache is not None and v_cache.stride() != cs:
+        raise ValueError(f"{fn}: k_cache and v_cache must have the same strides")
+    qs, os_ = (none, none) if q is None else (q.stride(), q_out.stride())
+    ks = none if k is None else k.stride()
+    vs = none if v is None else v.stride()
+    rc = lib.idx_norm_rope_append(
+        _at(q), qs[0], qs[1], _at(q_out), os_[0], os_[1], hq, _at(k), ks[0], ks[1], _at(v), vs[0], vs[1], hk, tokens, dim, 2 * inv_freq.shape[0],
+        _at(q_weight), _at(k_weight), eps, offset, positions.data_ptr(), inv_freq.data_ptr(), mscale, _at(slots), _at(k_cache), _at(v_cache), nb, page,
+        cs[0], cs[1], cs[2], code, _ROPE_INTERLEAVED if interleaved else 0, _at(status), _stream_on(stream, some))
+    return rc if rc >= 0 else _check(fn, rc)
+
+
+def idx_index_append(q, k, q_weight, k_weight, eps: float, positions, inv_freq, q_out, q_scale, index_k, slots=None, cu_tokens=None,
+                     head_weights=None, scale: float = 1.0, mscale: float = 1.0, offset: float = 0.0, interleaved: bool = False, status=None,
+                     stream=None) -> int:
+    """The indexer's inputs: q [T,H,128] -> q_out E4M3 bytes and q_scale f32, [T,H,128] and [T,H], or with cu_tokens [R+1] i32
+    [R,S,H,128] and [R,S,H] (a request's tokens in its last slots); k [T,128] -> index_k [nb,P,72] u8 pages at slots [T] i64
+    (None: slot t).  q, q_out and q_scale, or k and index_k may be None; weights [128] (None: no norm); head_weights [T,H] f32."""
+    lib, T, fn = load_library(), _torch(), "idx_index_append"
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError(f"{fn}: q or k is needed")
+    if (q is None) != (q_out is None) or (q is None) != (q_scale is None) or (k is None) != (index_k is None):
+        raise ValueError(f"{fn}: q, q_out and q_scale, k and index_k go together")
+    kind = some.dtype
+    code = T.codes.get(kind)
+    if code is None:
+        raise ValueError(f"{fn}: bfloat16, float16 or float32 is needed, got {kind}")
+    tokens, u8 = some.shape[0], T.u8
+    heads = reqs = per = 0
+    one, wide = (tokens,), (128,)
+    if q is not None:
+        heads = q.shape[1]
+        out = (tokens, heads)
+        if cu_tokens is not None:
+            reqs, per = cu_tokens.shape[0] - 1, q_out.shape[1]
+            out = (reqs, per, heads)
+    nb, page = (0, 128) if k is None else index_k.shape[:2]
+    if not ((q is None or (_rows_ok(kind, (tokens, heads, 128), q) and _are(u8, out + wide, q_out) and _are(T.f32, out, q_scale)))
+            and (k is None or (_rows_ok(kind, (tokens, 128), k) and _are(u8, (nb, page, 72), index_k)))
+            and _are(kind, wide, q_weight, k_weight) and _are(T.i32, one, positions) and _are(T.f64, inv_freq.shape[:1], inv_freq)
+            and _words_ok(T, one, slots) and _are(T.f32, (tokens, heads), head_weights)
+            and (cu_tokens is None or _are(T.i32, cu_tokens.shape[:1], cu_tokens)) and _status_ok(T, status)
+            and (not T.many or _here(q, k, q_out, q_scale, index_k, q_weight, k_weight, positions, inv_freq, slots, cu_tokens, head_weights, status))):
+        _explain(fn, ("q_out", "q_scale", "index_k", "q_weight", "k_weight", "positions", "inv_freq", "slots", "head_weights", "cu_tokens"),
+                 q=(q, kind, (tokens, heads, 128)), k=(k, kind, (tokens, 128)), q_out=(q_out, u8, out + wide if heads else None),
+                 q_scale=(q_scale, T.f32, out if heads else None), index_k=(index_k, u8, (None, None, 72)), q_weight=(q_weight, kind, wide),
+                 k_weight=(k_weight, kind, wide), positions=(positions, T.i32, one), inv_freq=(inv_freq, T.f64, (None,)),
+                 slots=(slots, T.words, one), cu_tokens=(cu_tokens, T.i32, (None,)), head_weights=(head_weights, T.f32, (tokens, heads)),
+                 status=(status, T.i32, None))
+    qs = (0, 0) if q is None else q.stride()
+    rc = lib.idx_index_append(
+        _at(q), qs[0], qs[1], heads, _at(k), 0 if k is None else k.stride(0), tokens, 2 * inv_freq.shape[0], _at(q_weight), _at(k_weight), eps, offset,
+        positions.data_ptr(), inv_freq.data_ptr(), mscale, _at(head_weights), scale, None if q is None else _at(cu_tokens), reqs, per, _at(q_out),
+        _at(q_scale), _at(slots), _at(index_k), nb, page, code, _ROPE_INTERLEAVED if interleaved else 0, _at(status), _stream_on(stream, some))
+    return rc if rc >= 0 else _check(fn, rc)
+
+
+def idx_logit_probs(logits, probs, cu_tokens, temperature=None, repetition=None, presence=None, frequency=None, counts=None, tokens=None,
+                    tree_mask=None, bias_cu=None, bias_tokens=None, bias_values=None, allowed=None, lse=None, status=None, stream=None) -> int:
+    """logits [T,V] -> probs [T,V] f32 (+ lse [T] f32); temperature, repetition, presence, frequency [R] f32; counts [R,V] i32 (highest
+    bit: in the prompt); tokens [T] i32 and tree_mask [T] i64 (None: a chain) of the drafts; biases bias_cu [R+1] i32, bias_tokens i32,
+    bias_values f32; allowed [T,ceil(V/32)] i32 bits."""
+    lib, T, fn = load_library(), _torch(), "idx_logit_probs"
+    i32, f32, kind = T.i32, T.f32, logits.dtype
+    code = T.codes.get(kind)
+    if code is None:
+        raise ValueError(f"{fn}: bfloat16, float16 or float32 is needed, got {kind}")
+    if (bias_cu is None) != (bias_tokens is None) or (bias_cu is None) != (bias_values is None):
+        raise ValueError(f"{fn}: bias_cu, bias_tokens and bias_values go together")
+    if tree_mask is not None and tokens is None:
+        raise ValueError(f"{fn}: tree_mask goes with tokens")
+    total, vocab = shape = logits.shape
+    reqs = cu_tokens.shape[0] - 1
+    one, per_req, words = (total,), (reqs,), (total, (vocab + 31) // 32)
+    biases = 0 if bias_tokens is None else bias_tokens.shape[0]
+    if not (_rows_ok(kind, shape, logits) and _rows_ok(f32, shape, probs) and _are(i32, (reqs + 1,), cu_tokens, bias_cu)
+            and _are(f32, per_req, temperature, repetition, presence, frequency) and _rows_ok(i32, (reqs, vocab), counts)
+            and _are(i32, one, tokens) and _words_ok(T, one, tree_mask) and _are(i32, (biases,), bias_tokens) and _are(f32, (biases,), bias_values)
+            and _rows_ok(i32, words, allowed) and _are(f32, one, lse) and _status_ok(T, status)
+            and (not T.many or _here(logits, probs, cu_tokens, temperature, repetition, presence, frequency, counts, tokens, tree_mask, bias_cu,
+                                     bias_tokens, bias_values, allowed, lse, status))):
+        _explain(fn, ("cu_tokens", "temperature", "repetition", "presence", "frequency", "tokens", "tree_mask", "bias_cu", "bias_tokens",
+                      "bias_values", "lse"), logits=(logits, kind, shape), probs=(probs, f32, shape), cu_tokens=(cu_tokens, i32, (None,)),
+                 temperature=(temperature, f32, per_req), repetition=(repetition, f32, per_req), presence=(presence, f32, per_req),
+                 frequency=(frequency, f32, per_req), counts=(counts, i32, (reqs, vocab)), tokens=(tokens, i32, one),
+                 tree_mask=(tree_mask, T.words, one), bias_cu=(bias_cu, i32, (reqs + 1,)), bias_tokens=(bias_tokens, i32, (biases,)),
+                 bias_values=(bias_values, f32, (biases,)), allowed=(allowed, i32, words), lse=(lse, f32, one), status=(status, i32, None))
+    rc = lib.idx_logit_probs(
+        logits.data_ptr(), _row_stride(logits), code, vocab, total, cu_tokens.data_ptr(), reqs, _at(temperature), _at(repetition), _at(presence),
+        _at(frequency), _at(counts), 0 if counts is None else _row_stride(counts), _at(tokens), _at(tree_mask), _at(bias_cu), _at(bias_tokens),
+        _at(bias_values), biases, _at(allowed), 0 if allowed is None else _row_stride(allowed), probs.data_ptr(), _row_stride(probs), _at(lse),
+        _at(status), _stream_on(stream, logits))
+    return rc if rc >= 0 else _check(fn, rc)
+
+
+def index_caches(index_k):
+    """The two caches that NVFP4 index-K pages [nb,P,72] u8 are to idx_settle_drafts and idx_fork_pages: codes and scales."""
+    blocks, page, width = index_k.shape
+    if width != 72 or not index_k.is_contiguous():
+        raise ValueError("index_caches: contiguous pages [num_blocks, page_tokens, 72] are needed")
+    flat = index_k.view(1, blocks, page * 72)
+    return flat[:, :, : page * 64].unflatten(2, (page, 64)), flat[:, :, page * 64 :].unflatten(2, (page, 8))
+
+
+def _pack_caches(fn: str, T, caches):
+    """idx_cache entries of tensors [planes, blocks, page_tokens, row...] (the row contiguous), and the blocks and page they share."""
+    blocks, page = caches[0].shape[1:3] if caches and caches[0].dim() > 3 else (0, 1)
+    fields = []
+    for c in caches:
+        shape, strides, size = c.shape, c.stride(), c.element_size()
+        row, fine = 1, len(shape) > 3 and shape[1] == blocks and shape[2] == page and c.is_cuda and (not T.many or _here(c))
+        for n, s in zip(shape[:2:-1], strides[:2:-1]):
+            fine = fine and (n == 1 or s == row)
+            row *= n
+        if not fine:
+            if len(shape) < 4 or shape[1] != blocks or shape[2] != page:
+                raise ValueError(f"{fn}: a cache has shape {tuple(shape)}, (any, {blocks}, {page}, any...) is needed")
+            if not (c.is_cuda and (not T.many or _here(c))):
+                raise ValueError(f"{fn}: a cache is on {c.device}, the current CUDA device is needed")
+            raise ValueError(f"{fn}: a token's row of a cache must be contiguous")
+        fields += (c.data_ptr(), strides[0] * size, strides[1] * size, strides[2] * size, shape[0], row * size)
+    return struct.pack("Pqqqii" * len(caches), *fields), blocks, page
+
+
+def idx_settle_drafts(caches, slots, cu_tokens, out_tokens, out_nodes, num_accepted, ctx_lens, ctx_out, counts=None, status=None,
+                      stream=None) -> int:
+    """After idx_verify_drafts: rows of the nodes that stand moved together in caches (tensors [planes,nb,P,row...]; index_caches gives
+    those of index-K pages), ctx_out [R] i32 from ctx_lens (may be the same), counts [R,V] i32 with the step's tokens."""
+    lib, T, fn = load_library(), _torch(), "idx_settle_drafts"
+    i32 = T.i32
+    reqs, max_out = out_shape = out_nodes.shape
+    per_req, tokens = (reqs,), slots.shape[0]
+    vocab = 0 if counts is None else counts.shape[-1]
+    if not (_words_ok(T, (tokens,), slots) and _are(i32, (reqs + 1,), cu_tokens) and _are(i32, out_shape, out_tokens, out_nodes)
+            and _are(i32, per_req, num_accepted, ctx_lens, ctx_out) and (reqs == 0 or _rows_ok(i32, (reqs, vocab), counts)) and _status_ok(T, status)
+            and (not T.many or _here(slots, cu_tokens, out_tokens, out_nodes, num_accepted, ctx_lens, ctx_out, counts, status))):
+        _explain(fn, ("slots", "cu_tokens", "out_tokens", "out_nodes", "num_accepted", "ctx_lens", "ctx_out"), slots=(slots, T.words, (tokens,)),
+                 cu_tokens=(cu_tokens, i32, (reqs + 1,)), out_tokens=(out_tokens, i32, out_shape), out_nodes=(out_nodes, i32, out_shape),
+                 num_accepted=(num_accepted, i32, per_req), ctx_lens=(ctx_lens, i32, per_req), ctx_out=(ctx_out, i32, per_req),
+                 counts=(counts, i32, (reqs, vocab)), status=(status, i32, None))
+    packed, blocks, page = _pack_caches(fn, T, caches)
+    rc = lib.idx_settle_drafts(
+        packed, len(caches), blocks, page, slots.data_ptr(), cu_tokens.data_ptr(), reqs, tokens, out_tokens.data_ptr(), out_nodes.data_ptr(), max_out,
+        num_accepted.data_ptr(), ctx_lens.data_ptr(), ctx_out.data_ptr(), _at(counts), 0 if counts is None else _row_stride(counts), vocab, _at(status),
+        _stream_on(stream, out_nodes))
+    return rc if rc >= 0 else _check(fn, rc)
+
+
+def idx_fork_pages(caches, parents, children, ctx_lens, owned_pages, block_table, refs, free_blocks, free_cursor, cursor_out, page_tokens=None,
+                   status=None, stream=None) -> int:
+    """Requests children [F] i32 forked off parents [F] i32: ctx_lens and owned_pages [R] i32 and block_table [R,maxb] i32 in place, full
+    pages shared (refs [nb] i32), the last one copied in caches (as in idx_settle_drafts; page_tokens where there are none)."""
+    lib, T, fn = load_library(), _torch(), "idx_fork_pages"
+    i32 = T.i32
+    forks, free = parents.shape[0], free_blocks.shape[0]
+    reqs, width = block_table.shape
+    some, per_req, nb = (forks,), (reqs,), refs.shape[0]
+    if not (_are(i32, some, parents, children) and _are(i32, per_req, ctx_lens, owned_pages) and _rows_ok(i32, (reqs, width), block_table)
+            and _are(i32, (nb,), refs) and _are(i32, (free,), free_blocks) and _are(i32, (1,), free_cursor, cursor_out) and _status_ok(T, status)
+            and (not T.many or _here(parents, children, ctx_lens, owned_pages, block_table, refs, free_blocks, free_cursor, cursor_out, status))):
+        _explain(fn, ("parents", "children", "ctx_lens", "owned_pages", "refs", "free_blocks", "free_cursor", "cursor_out"),
+                 parents=(parents, i32, some), children=(children, i32, some), ctx_lens=(ctx_lens, i32, per_req),
+                 owned_pages=(owned_pages, i32, per_req), block_table=(block_table, i32, (reqs, None)), refs=(refs, i32, (None,)),
+                 free_blocks=(free_blocks, i32, (None,)), free_cursor=(free_cursor, i32, (1,)), cursor_out=(cursor_out, i32, (1,)),
+                 status=(status, i32, None))
+    packed, blocks, page = _pack_caches(fn, T, caches)
+    if caches and blocks != nb:
+        raise ValueError(f"{fn}: refs has {nb} entries, the caches have {blocks} blocks")
+    if caches and page_tokens is not None and page_tokens != page:
+        raise ValueError(f"{fn}: page_tokens is {page_tokens}, the caches have pages of {page}")
+    if not caches:
+        if page_tokens is None:
+            raise ValueError(f"{fn}: page_tokens is needed where there are no caches")
+        page = page_tokens
+    rc = lib.idx_fork_pages(
+        packed, len(caches), nb, page, parents.data_ptr(), children.data_ptr(), forks, ctx_lens.data_ptr(), owned_pages.data_ptr(), reqs,
+        block_table.data_ptr(), _row_stride(block_table), width, refs.data_ptr(), free_blocks.data_ptr(), free, free_cursor.data_ptr(),
+        cursor_out.data_ptr(), _at(status), _stream_on(stream, parents))
+    return rc if rc >= 0 else _check(fn, rc)
+
+
+def idx_release_pages(keep_lens, owned_pages, block_table, refs, free_blocks, free_cursor, cursor_out, pages_out, page_tokens: int, status=None,
+                      stream=None) -> int:
+    """Pages past keep_lens [R] i32 given back: refs [nb] i32 less one each, the blocks that nobody holds into free_blocks before the
+    cursor by ascending id; cursor_out, and pages_out [R] i32, the pages that are left."""
+    lib, T, fn = load_library(), _torch(), "idx_release_pages"
+    i32 = T.i32
+    reqs, width = block_table.shape
+    per_req, nb, free = (reqs,), refs.shape[0], free_blocks.shape[0]
+    if not (_are(i32, per_req, keep_lens, owned_pages, pages_out) and _rows_ok(i32, (reqs, width), block_table) and _are(i32, (nb,), refs)
+            and _are(i32, (free,), free_blocks) and _are(i32, (1,), free_cursor, cursor_out) and _status_ok(T, status)
+            and (not T.many or _here(keep_lens, owned_pages, pages_out, block_table, refs, free_blocks, free_cursor, cursor_out, status))):
+        _explain(fn, ("keep_lens", "owned_pages", "pages_out", "refs", "free_blocks", "free_cursor", "cursor_out"),
+                 keep_lens=(keep_lens, i32, per_req), owned_pages=(owned_pages, i32, per_req), pages_out=(pages_out, i32, per_req),
+                 block_table=(block_table, i32, (reqs, None)), refs=(refs, i32, (None,)), free_blocks=(free_blocks, i32, (None,)),
+                 free_cursor=(free_cursor, i32, (1,)), cursor_out=(cursor_out, i32, (1,)), status=(status, i32, None))
+    rc = lib.idx_release_pages(
+        keep_lens.data_ptr(), owned_pages.data_ptr(), reqs, block_table.data_ptr(), _row_stride(block_table), width, refs.data_ptr(), nb,
+        free_blocks.data_ptr(), free, free_cursor.data_ptr(), cursor_out.data_ptr(), pages_out.data_ptr(), page_tokens, _at(status),
+        _stream_on(stream, refs))
     return rc if rc >= 0 else _check(fn, rc)

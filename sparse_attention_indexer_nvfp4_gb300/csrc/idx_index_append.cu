@@ -1,0 +1,465 @@
+// The indexer's inputs from a projection's rows: E4M3 queries with one scale a
+// head, NVFP4 keys written into the index-K pages.
+//
+// A row x of 128 elements is normed (r = 1 / sqrt(mean x^2 + eps)) and turned
+// as in idx_norm_rope_append, y = r u with u = x cw + x_p sw.  A query's codes
+// are those of 448 u / max|u|: r cancels, and only the scale has it.  A key's
+// blocks of 16 take s = e4m3(max|y| / 6) ("vllm ... gather_nvfp4_index_k": no
+// global scale) and codes e2m1(y / s).
+//
+// The codes are those of 64-bit arithmetic.  In units of 2^-24 of M = |x cw| +
+// |x_p sw|, u comes in fp32 with an error of at most 7: 2 from the angle's
+// rounding, 2 from sincospif, 3 from products and sum.  The largest element's
+// own, at most sqrt 2 as large relative to it (a pair's M is at most that many
+// times its larger element), and the scaling add 13: 20 M for 448 u / max|u|.
+// A norm's r is off by 8, a key's y / s by 19 M in all.  M is at most 2 (|u| +
+// |x_p sw|), so each element is converted at both ends of kSlack (kSlackKey)
+// times that sum around it; where the two codes differ (2% of the rows) the
+// element is formed again in 64 bits, sines and cosines by their Taylor series,
+// and compared with the middle between the codes.  A key whose codes or scales
+// may differ is formed again as a whole.
+//
+// Bound by HBM and, with many heads, by the instructions of a row.  A warp
+// takes a token (with few tokens a part of its heads), 16 lanes a row, 8
+// elements a lane; cosines, sines and weights are folded into a lane's factors
+// once a token.  A key's scale byte belongs to two lanes.
+#include "idx_internal.h"
+#include "idx_rope.cuh"
+
+namespace idx {
+namespace {
+
+constexpr int kThreadsI = 256;
+constexpr int kBatchI = 2;  // rows in flight a lane
+constexpr int kLanesI = 16;  // of a row
+constexpr float kSlack = 2.5e-6f, kSlackKey = 4e-6f;
+
+struct IndexArgs {
+  const void *q, *k;
+  int64_t q_ts, q_hs, k_ts;
+  int32_t heads, num_tokens, rotary_dim;
+  const void *q_w, *k_w;
+  float eps, offset, mscale, scale;
+  const int32_t* positions;
+  const double* inv_freq;
+  uint8_t* q_out;
+  float* q_scale;
+  const float* head_weights;
+  const int32_t* cu;
+  int32_t num_reqs, req_slots;
+  const int64_t* slots;
+  uint8_t* index_k;
+  int64_t num_slots;
+  int32_t page;
+  int32_t* status;
+};
+
+// Two fp32 values to E2M1, to nearest even, at most 6 in magnitude; `lo` in bits 0-3.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight elements of a row as words.
+template <typename T>
+struct Eight {
+  static constexpr int kN = 2 * (int)sizeof(T);
+  uint32_t w[kN];
+};
+template <typename T, bool kWide>
+__device__ __forceinline__ Eight<T> load8(const T* p) {
+  Eight<T> x;
+  if (kWide) {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::kN / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      x.w[4 * i] = v.x, x.w[4 * i + 1] = v.y, x.w[4 * i + 2] = v.z, x.w[4 * i + 3] = v.w;
+    }
+  } else if (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::kN; ++i) x.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::kN; ++i)
+      x.w[i] = (uint32_t) reinterpret_cast<const uint16_t*>(p)[2 * i] | (uint32_t) reinterpret_cast<const uint16_t*>(p)[2 * i + 1] << 16;
+  }
+  return x;
+}
+
+// cos and sin of 2 pi phase / 2^64: the phase less its nearest quarter turn, then the Taylor series (|y| <= pi / 4: the
+// terms left out are below 2^-52).
+__device__ __forceinline__ double2 turn_of_64(unsigned long long phase) {
+  const unsigned long long quarter = (phase + (1ull << 61)) >> 62;
+  const double y = (double)(long long)(phase - (quarter << 62)) * 3.4061215800865545e-19, z = y * y;  // 2 pi / 2^64
+  double s = 1.0 / 355687428096000.0, c = 1.0 / 20922789888000.0;                              // 1 / 17!, 1 / 16!
+  s = fma(s, z, -1.0 / 1307674368000.0), c = fma(c, z, -1.0 / 87178291200.0);
+  s = fma(s, z, 1.0 / 6227020800.0), c = fma(c, z, 1.0 / 479001600.0);
+  s = fma(s, z, -1.0 / 39916800.0), c = fma(c, z, -1.0 / 3628800.0);
+  s = fma(s, z, 1.0 / 362880.0), c = fma(c, z, 1.0 / 40320.0);
+  s = fma(s, z, -1.0 / 5040.0), c = fma(c, z, -1.0 / 720.0);
+  s = fma(s, z, 1.0 / 120.0), c = fma(c, z, 1.0 / 24.0);
+  s = fma(s, z, -1.0 / 6.0), c = fma(c, z, -0.5);
+  s = fma(s, z * y, y), c = fma(c, z, 1.0);
+  const double2 swapped = quarter & 1ull ? make_double2(-s, c) : make_double2(c, s);
+  return quarter & 2ull ? make_double2(-swapped.x, -swapped.y) : swapped;
+}
+
+// A row as its elements are formed in 64 bits.
+template <typename T>
+struct Row64 {
+  const T* x;
+  const float* w;
+  const unsigned long long* steps;
+  int position, rd;
+  float mscale;
+  template <bool kInter>
+  __device__ __forceinline__ double u(int e) const {
+    const double n = (double)to_f(x[e]) * (double)w[e];
+    if (e >= rd) return n;
+    const int half = rd / 2, pair = kInter ? e / 2 : e < half ? e : e - half;
+    const int mate = kInter ? e ^ 1 : e < half ? e + half : e - half;
+    const bool second = kInter ? e & 1 : e >= half;
+    const double2 cs = turn_of_64(steps[pair] * (unsigned long long)(long long)position);
+    const double o = (double)to_f(x[mate]) * (double)w[mate];
+    return (double)mscale * (second ? fma(n, cs.x, o * cs.y) : fma(n, cs.x, -(o * cs.y)));
+  }
+};
+
+__device__ __forceinline__ double shfl_xor_64(double x, int o) {
+  return __hiloint2double(__shfl_xor_sync(0xFFFFFFFFu, __double2hiint(x), o), __shfl_xor_sync(0xFFFFFFFFu, __double2loint(x), o));
+}
+
+// A query's codes where some lie near a border: the elements of `near` (bits, from `at` on) again; those of `tops` may be
+// the row's largest.  All lanes together.
+template <typename T, bool kInter>
+__device__ __noinline__ uint2 codes_64(const Row64<T> row, int at, uint32_t near, uint32_t tops, uint2 codes) {
+  double top = 0.0;
+  for (uint32_t m = tops; m != 0; m &= m - 1) top = fmax(top, fabs(row.template u<kInter>(at + __ffs(m) - 1)));
+#pragma unroll
+  for (int o = 1; o < kLanesI; o <<= 1) top = fmax(top, shfl_xor_64(top, o));
+  for (; near != 0; near &= near - 1) {
+    const int e = __ffs(near) - 1;
+    const double u = row.template u<kInter>(at + e), v = 448.0 * fabs(u);
+    // from a code at or below the value, up while the middle to the next one is (halves to even)
+    uint32_t code = f32x2_to_e4m3x2(__double2float_rz(v / top) * (1.f - kSlack), 0.f) & 0x7Fu;
+    if (code > 0) --code;
+    for (; code < 0x7Eu; ++code) {
+      const double edge = 0.5 * ((double)e4m3_to_f32(code) + (double)e4m3_to_f32(code + 1)) * top;
+      if (!(v > edge || (v == edge && (code & 1u)))) break;
+    }
+    code |= u < 0.0 ? 0x80u : 0u;
+    uint32_t& word = e < 4 ? codes.x : codes.y;
+    word = (word & ~(0xFFu << (8 * (e & 3)))) | code << (8 * (e & 3));
+  }
+  return codes;
+}
+
+// A key's lane again: scale (in y) and codes (in x) of its 8 elements.  All lanes together.
+template <typename T, bool kInter>
+__device__ __noinline__ uint2 key_64(const Row64<T> row, int at, bool normed, float eps) {
+  double u[8], ss = 0.0, top = 0.0;
+  for (int e = 0; e < 8; ++e) {
+    const double x = (double)to_f(row.x[at + e]);
+    ss = fma(x, x, ss), u[e] = row.template u<kInter>(at + e), top = fmax(top, fabs(u[e]));
+  }
+#pragma unroll
+  for (int o = 1; o < kLanesI; o <<= 1) ss += shfl_xor_64(ss, o);
+  top = fmax(top, shfl_xor_64(top, 1));
+  const double r = normed ? 1.0 / sqrt(ss * (1.0 / kHeadDim) + (double)eps) : 1.0;
+  const double six = top * r / 6.0;
+  uint32_t scale = f32x2_to_e4m3x2(__double2float_rz(six) * (1.f - kSlackKey), 0.f) & 0x7Fu;
+  if (scale > 0) --scale;
+  for (; scale < 0x7Eu; ++scale) {
+    const double edge = 0.5 * ((double)e4m3_to_f32(scale) + (double)e4m3_to_f32(scale + 1));
+    if (!(six > edge || (six == edge && (scale & 1u)))) break;
+  }
+  uint32_t codes = 0;
+  const double s = (double)e4m3_to_f32(scale);
+  for (int e = 0; e < 8 && scale != 0; ++e) {
+    const double z = fabs(u[e]) * r / s;
+    // borders between the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6, halves to the even code
+    const uint32_t code = (z > 0.25) + (z >= 0.75) + (z > 1.25) + (z >= 1.75) + (z > 2.5) + (z >= 3.5) + (z > 5.0);
+    codes |= (code | (u[e] < 0.0 ? 8u : 0u)) << (4 * e);
+  }
+  return make_uint2(codes, scale);
+}
+
+// The request of token t: greatest r with cu[r] <= t, all lanes together.
+__device__ __forceinline__ int request_of(const int32_t* cu, int num_reqs, int t, int lane) {
+  int lo = 0, hi = num_reqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + step * lane;
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < hi && cu[min(at, num_reqs)] <= t);
+    lo += step * max(0, __popc(below) - 1);
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+template <typename T, bool kInter, bool kWide>
+__global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_constant__ IndexArgs a, int parts, int key_part) {
+  pdl_enter();
+  constexpr int kN = Eight<T>::kN;
+  __shared__ float angles[kThreadsI / 32][2][kHeadDim / 2];
+  __shared__ unsigned long long steps[kHeadDim / 2];
+  __shared__ float weights[2][kHeadDim];  // offset + w of queries and keys, 1 without
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rd = a.rotary_dim, half = rd / 2;
+  const int sub = lane / kLanesI, piece = lane % kLanesI, at = piece * 8;
+  for (int i = threadIdx.x; i < half; i += kThreadsI) steps[i] = step_of(a.inv_freq[i]);
+  for (int i = threadIdx.x; i < kHeadDim; i += kThreadsI) {
+    weights[0][i] = a.q_w != nullptr ? a.offset + to_f(static_cast<const T*>(a.q_w)[i]) : 1.f;
+    weights[1][i] = a.k_w != nullptr ? a.offset + to_f(static_cast<const T*>(a.k_w)[i]) : 1.f;
+  }
+  __syncthreads();
+  float(*mine)[kHeadDim / 2] = angles[warp];
+  // a pair's other half lies a whole number of pieces away (rotary_dim a multiple of 16, or of 8 with neighbours paired)
+  const bool turns = at < rd, upper = !kInter && at >= half;
+  const int hop = turns && !kInter ? (upper ? -half / 8 : half / 8) : 0, partner = lane + hop;
+  const int angle = kInter ? at / 2 : upper ? at - half : at, mate = at + 8 * hop;
+  const int rows = (a.heads + 1) / 2;
+  const int all = parts + (key_part ? 1 : 0);
+  const int64_t tasks = (int64_t)a.num_tokens * all;
+  for (int64_t task = (int64_t)blockIdx.x * (kThreadsI / 32) + warp; task < tasks; task += (int64_t)gridDim.x * (kThreadsI / 32)) {
+    const int t = (int)(task / all), part = (int)(task - (int64_t)t * all);
+    const int position = a.positions[t];
+    __syncwarp();  // the angles of the task before are used up
+    for (int i = lane; i < half; i += 32) {
+      const float2 w = turn_of(position, steps[i], a.mscale);
+      mine[0][i] = w.x, mine[1][i] = w.y;
+    }
+    __syncwarp();
+    float2 c[4], s[4];
+    auto factors = [&](const float* w) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w0 = w[at + 2 * e], w1 = w[at + 2 * e + 1];
+        if (turns && kInter) {
+          const float x = mine[0][angle + e], y = mine[1][angle + e];
+          c[e] = make_float2(x * w0, x * w1), s[e] = make_float2(-y * w1, y * w0);
+        } else if (turns) {
+          const float y0 = mine[1][angle + 2 * e] * w[mate + 2 * e], y1 = mine[1][angle + 2 * e + 1] * w[mate + 2 * e + 1];
+          c[e] = make_float2(mine[0][angle + 2 * e] * w0, mine[0][angle + 2 * e + 1] * w1);
+          s[e] = upper ? make_float2(y0, y1) : make_float2(-y0, -y1);
+        } else {
+          c[e] = make_float2(w0, w1), s[e] = make_float2(0.f, 0.f);
+        }
+      }
+    };
+    // u of this lane's elements and what their errors go by, and the sum of squares of the row
+    auto turn = [&](const Eight<T>& x, float2 (&u)[4], float2 (&mag)[4]) {
+      Eight<T> y;
+      if (!kInter) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) y.w[e] = __shfl_sync(0xFFFFFFFFu, x.w[e], partner);
+      }
+      float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 one = Words<T>::get(x.w, e), two = kInter ? make_float2(one.y, one.x) : Words<T>::get(y.w, e);
+        const float2 part = mul2(two, s[e]);
+        u[e] = fma2(one, c[e], part);
+        mag[e] = make_float2(fabsf(u[e].x) + fabsf(part.x), fabsf(u[e].y) + fabsf(part.y));
+        ss = fma2(one, one, ss);
+      }
+      return ss.x + ss.y;
+    };
+    auto largest = [&](const float2 (&u)[4]) {
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(u[e].x), fabsf(u[e].y)));
+      return m;
+    };
+
+    if (a.heads > 0 && part < parts) {
+      factors(weights[0]);
+      int64_t out = (int64_t)t * a.heads;  // the token's first row
+      bool stored = true;
+      if (a.cu != nullptr) {
+        const int r = request_of(a.cu, a.num_reqs, t, lane);
+        const int begin = a.cu[r], end = a.cu[r + 1], slot = a.req_slots - end + t;
+        stored = t >= begin && t < end && slot >= 0;
+        if (t >= begin && t < end && slot < 0 && lane == 0 && part == 0) report(a.status, IDX_ST_BAD_OUTPUT);
+        out = ((int64_t)r * a.req_slots + slot) * a.heads;
+      }
+      const int r0 = rows * part / parts, r1 = rows * (part + 1) / parts;
+      const T* src = static_cast<const T*>(a.q) + (int64_t)t * a.q_ts + at;
+      if (stored) {
+        for (int g = r0; g < r1; g += kBatchI) {
+          Eight<T> x[kBatchI];
+#pragma unroll
+          for (int b = 0; b < kBatchI; ++b) {
+            const int h = 2 * (g + b) + sub;
+            if (g + b < r1 && h < a.heads) x[b] = load8<T, kWide>(src + h * a.q_hs);
+            else x[b] = Eight<T>{};
+          }
+          float2 u[kBatchI][4], mag[kBatchI][4];
+          float ss[kBatchI], top[kBatchI];
+#pragma unroll
+          for (int b = 0; b < kBatchI; ++b) ss[b] = turn(x[b], u[b], mag[b]), top[b] = largest(u[b]);
+#pragma unroll
+          for (int o = 1; o < kLanesI; o <<= 1) {
+#pragma unroll
+            for (int b = 0; b < kBatchI; ++b) {
+              ss[b] += __shfl_xor_sync(0xFFFFFFFFu, ss[b], o);
+              top[b] = fmaxf(top[b], __shfl_xor_sync(0xFFFFFFFFu, top[b], o));
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBatchI; ++b) {
+            const int h = 2 * (g + b) + sub;
+            const bool live = g + b < r1 && h < a.heads, bad = !(ss[b] <= 3.4e38f);
+            const float inv = top[b] > 7.9e-31f ? 448.f / top[b] : 0.f, slack = inv * kSlack;
+            // both ends of where the values may lie
+            uint32_t low[2], high[2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = mul2(u[b][e], make_float2(inv, inv));
+              const float2 l = fma2(mag[b][e], make_float2(-slack, -slack), v), t = fma2(mag[b][e], make_float2(slack, slack), v);
+              const uint32_t lc = f32x2_to_e4m3x2(l.x, l.y), tc = f32x2_to_e4m3x2(t.x, t.y);
+              low[e / 2] = e % 2 ? low[e / 2] | lc << 16 : lc, high[e / 2] = e % 2 ? high[e / 2] | tc << 16 : tc;
+            }
+            uint2 codes = make_uint2(low[0], low[1]);
+            const bool open = live && !bad && inv != 0.f && ((low[0] ^ high[0]) | (low[1] ^ high[1])) != 0;
+            if (__any_sync(0xFFFFFFFFu, open)) {
+              uint32_t near = 0, tops = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float m = e % 2 ? u[b][e / 2].y : u[b][e / 2].x;
+                if (open && ((low[e / 4] ^ high[e / 4]) >> (8 * (e % 4)) & 0xFFu)) near |= 1u << e;
+                if (live && !bad && fabsf(m) >= top[b] * (1.f - 4.f * kSlack)) tops |= 1u << e;
+              }
+              const Row64<T> row{static_cast<const T*>(a.q) + (int64_t)t * a.q_ts + min(h, a.heads - 1) * a.q_hs, weights[0], steps, position, rd, a.mscale};
+              codes = codes_64<T, kInter>(row, at, near, tops, codes);
+            }
+            if (!live) continue;
+            if (bad) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (inv == 0.f && !bad) codes = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(a.q_out + (out + h) * kHeadDim + at) = codes;
+            if (piece == 0) {
+              const float r = a.q_w != nullptr ? rsqrtf(fmaf(ss[b], 1.f / kHeadDim, a.eps)) : 1.f;
+              float f = top[b] * r * (1.f / 448.f) * a.scale;
+              if (a.head_weights != nullptr) f *= a.head_weights[(int64_t)t * a.heads + h];
+              a.q_scale[out + h] = bad ? __int_as_float(0x7FC00000) : f;
+            }
+          }
+        }
+      }
+    }
+    if (a.k != nullptr && part == all - 1) {
+      const int64_t slot = a.slots != nullptr ? a.slots[t] : t;
+      if (slot >= a.num_slots && lane == 0) report(a.status, IDX_ST_BLOCK_OOR);
+      if (slot >= 0 && slot < a.num_slots) {
+        factors(weights[1]);
+        const T* src = static_cast<const T*>(a.k) + (int64_t)t * a.k_ts;
+        float2 u[4], mag[4];
+        float ss = turn(load8<T, kWide>(src + at), u, mag);  // the same row in both halves
+#pragma unroll
+        for (int o = 1; o < kLanesI; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        float top = largest(u), most = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(mag[e].x, mag[e].y));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        const float r = a.k_w != nullptr ? rsqrtf(fmaf(ss, 1.f / kHeadDim, a.eps)) : 1.f;
+        const bool bad = !(ss <= 3.4e38f);
+        const float six = top * r * (1.f / 6.f), off = most * r * (kSlackKey / 6.f);
+        const uint32_t both = f32x2_to_e4m3x2(six - off, six + off);
+        uint32_t scale = both & 0xFFu, codes = 0;
+        const float sv = e4m3_to_f32(scale), inv = scale == 0x7Fu || scale == 0u ? 0.f : r / sv;
+        bool open = (both & 0xFFu) != both >> 8;
+        if (inv != 0.f) {
+          uint32_t high = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = mul2(u[e], make_float2(inv, inv)), d = mul2(mag[e], make_float2(inv * kSlackKey, inv * kSlackKey));
+            codes |= f32x2_to_e2m1x2(v.x - d.x, v.y - d.y) << (8 * e), high |= f32x2_to_e2m1x2(v.x + d.x, v.y + d.y) << (8 * e);
+          }
+          open |= codes != high;
+        }
+        if (__any_sync(0xFFFFFFFFu, open && !bad)) {
+          const uint2 again = key_64<T, kInter>(Row64<T>{src, weights[1], steps, position, rd, a.mscale}, at, a.k_w != nullptr, a.eps);
+          codes = again.x, scale = again.y;
+        }
+        if (bad) codes = 0, scale = 0x7Fu;
+        if (sub == 0) {
+          const int64_t block = slot / a.page;
+          const int place = (int)(slot - block * a.page);
+          uint8_t* page = a.index_k + block * (a.page * 72);
+          *reinterpret_cast<uint32_t*>(page + place * 64 + piece * 4) = codes;
+          if (piece % 2 == 0) page[a.page * 64 + place * 8 + piece / 2] = (uint8_t)scale;
+        }
+      }
+    }
+  }
+}
+
+template <typename T>
+void launch_index(const IndexArgs& a, bool inter, bool wide, cudaStream_t s) {
+  const int sms = max(device_sms(), 1), rows = (a.heads + 1) / 2;
+  const int64_t room = (int64_t)sms * 32;
+  const int most = max(1, (rows + kBatchI - 1) / kBatchI);
+  const int parts = a.heads == 0 ? 0 : (int)min((int64_t)most, max((int64_t)1, (room + a.num_tokens - 1) / a.num_tokens));
+  // the key is a task of its own while there is room: its row waits for no other
+  const int key_part = a.k != nullptr && (parts == 0 || (int64_t)a.num_tokens * (parts + 1) <= room);
+  const int64_t ctas = ((int64_t)a.num_tokens * (parts + key_part) + kThreadsI / 32 - 1) / (kThreadsI / 32);
+  const dim3 grid((unsigned)min(ctas, (int64_t)sms * 8)), block(kThreadsI);
+  if (inter) {
+    if (wide) launch_pdl(k_index_append<T, true, true>, grid, block, 0, s, a, parts, key_part);
+    else launch_pdl(k_index_append<T, true, false>, grid, block, 0, s, a, parts, key_part);
+  } else {
+    if (wide) launch_pdl(k_index_append<T, false, true>, grid, block, 0, s, a, parts, key_part);
+    else launch_pdl(k_index_append<T, false, false>, grid, block, 0, s, a, parts, key_part);
+  }
+}
+
+}  // namespace
+}  // namespace idx
+
+extern "C" int idx_index_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, int32_t heads, const void* k, int64_t k_token_stride,
+                                int32_t num_tokens, int32_t rotary_dim, const void* q_weight, const void* k_weight, float eps, float offset,
+                                const int32_t* positions, const double* inv_freq, float mscale, const float* head_weights, float scale,
+                                const int32_t* cu_tokens, int32_t num_reqs, int32_t req_slots, uint8_t* q_out, float* q_scale,
+                                const int64_t* slots, uint8_t* index_k, int64_t num_blocks, int32_t page_tokens, int32_t dtype, int32_t flags,
+                                int32_t* status, void* stream) {
+  using namespace idx;
+  const bool inter = (flags & IDX_ROPE_INTERLEAVED) != 0;
+  if (num_tokens < 0 || heads < 0 || rotary_dim < 0 || rotary_dim > kHeadDim || rotary_dim % (inter ? 8 : 16) != 0 || num_blocks < 0 ||
+      (page_tokens != 128 && page_tokens != 256) || (flags & ~IDX_ROPE_INTERLEAVED) != 0 || dtype < IDX_BF16 || dtype > IDX_F32 || !(eps >= 0.f) ||
+      q_token_stride < 0 || q_head_stride < 0 || k_token_stride < 0 || num_reqs < 0 || (cu_tokens != nullptr && req_slots < 1))
+    return IDX_E_BAD_SHAPE;
+  if (heads > kMtpMaxHeads || num_reqs > 65535) return IDX_E_TOO_LARGE;
+  if (num_tokens == 0 || (heads == 0 && k == nullptr)) return IDX_OK;
+  if (heads > 0 && (!q || !q_out || !q_scale)) return IDX_E_NULL_PTR;
+  if ((k == nullptr) != (index_k == nullptr) || !positions || (rotary_dim > 0 && !inv_freq)) return IDX_E_NULL_PTR;
+  const int size = dtype == IDX_F32 ? 4 : 2;
+  for (const void* p : {q, k, q_weight, k_weight})
+    if (!aligned(p, size)) return IDX_E_MISALIGNED;
+  for (const void* p : {(const void*)positions, (const void*)head_weights, (const void*)cu_tokens, (const void*)q_scale, (const void*)status})
+    if (!aligned(p, 4)) return IDX_E_MISALIGNED;
+  if (!aligned(inv_freq, 8) || !aligned(slots, 8) || !aligned(q_out, 16) || !aligned(index_k, 16)) return IDX_E_MISALIGNED;
+  int rc;
+  if ((rc = check_device()) != IDX_OK) return rc;
+  IndexArgs a{};
+  a.heads = cu_tokens != nullptr && num_reqs == 0 ? 0 : heads;  // no request, no slot for a query
+  if (a.heads == 0 && k == nullptr) return IDX_OK;
+  a.num_tokens = num_tokens, a.rotary_dim = rotary_dim, a.eps = eps, a.offset = offset, a.mscale = mscale, a.scale = scale;
+  a.positions = positions, a.inv_freq = inv_freq, a.status = status;
+  bool wide = true;
+  auto fit = [&](const void* p, int64_t stride) { wide = wide && aligned(p, 16) && stride * size % 16 == 0; };
+  if (a.heads > 0) {
+    a.q = q, a.q_ts = q_token_stride, a.q_hs = q_head_stride, a.q_w = q_weight, a.q_out = q_out, a.q_scale = q_scale;
+    a.head_weights = head_weights, a.cu = cu_tokens, a.num_reqs = num_reqs, a.req_slots = req_slots;
+    fit(q, q_token_stride), fit(q, q_head_stride);
+  }
+  if (k != nullptr) {
+    a.k = k, a.k_ts = k_token_stride, a.k_w = k_weight, a.slots = slots, a.index_k = index_k, a.page = page_tokens;
+    a.num_slots = num_blocks * page_tokens;
+    fit(k, k_token_stride);
+  }
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == IDX_BF16) launch_index<__nv_bfloat16>(a, inter, wide, s);
+  else if (dtype == IDX_F16) launch_index<__half>(a, inter, wide, s);
+  else launch_index<float>(a, inter, wide, s);
+  return launch_result();
+}
