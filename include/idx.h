@@ -742,7 +742,7 @@ int idx_index_append(const void* q, int64_t q_token_stride, int64_t q_head_strid
  *                 count in the low 31 bits, the highest bit set for a token of
  *                 the prompt
  *   tokens        [num_tokens] int32 or NULL;  tree_mask [num_tokens] uint64 or
- *                 NULL (with tokens); a path counts up to IDX_VERIFY_MAX_NODES
+ *                 NULL (with tokens); a chain counts up to IDX_VERIFY_MAX_NODES
  *                 tokens (IDX_ST_BAD_TREE), those outside [0, vocab) not
  *   bias_cu       [num_reqs + 1] int32 or NULL: request r's biases are
  *                 bias_tokens and bias_values (int32, float32, num_bias in
@@ -753,7 +753,7 @@ int idx_index_append(const void* q, int64_t q_token_stride, int64_t q_head_strid
  *                 stride).  Rows outside every request (a padded batch) get 0
  *   lse           [num_tokens] float32 or NULL: L
  */
-#define IDX_PROBS_MAX_VOCAB 393216
+#define IDX_PROBS_MAX_VOCAB 262144
 int idx_logit_probs(const void* logits, int64_t logits_stride, int32_t dtype, int32_t vocab, int32_t num_tokens,
                     const int32_t* cu_tokens, int32_t num_reqs, const float* temperature, const float* repetition,
                     const float* presence, const float* frequency, const int32_t* counts, int64_t counts_stride,

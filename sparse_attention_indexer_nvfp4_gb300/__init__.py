@@ -589,7 +589,7 @@ def idx_verify_drafts(target, draft, tokens, cu_tokens, accept_u, sample_u, out_
 # Between those calls: norms, the indexer's inputs, probabilities, caches
 # ---------------------------------------------------------------------------
 
-PROBS_MAX_VOCAB = 393216  # entries of a row of idx_logit_probs
+PROBS_MAX_VOCAB = 262144  # entries of a row of idx_logit_probs
 MAX_CACHES = 8  # caches of one call of idx_settle_drafts and idx_fork_pages
 MAX_FORKS = 4096  # forks of one call
 

@@ -10,22 +10,30 @@
 // as the formula is written.
 //
 // Bound by HBM: a row is read once and written once.  A cluster of CTAs takes a
-// row, each a stretch of the vocabulary, whose x stay in shared memory as fp32
-// between the pass that finds maximum and sum (a running maximum and a sum
-// rescaled when it grows, a thread) and the one that writes; the CTAs exchange
-// both through distributed shared memory.  A cluster takes rows that follow one
-// another, so a request's bits are formed from its counts once for its rows.
+// row, each a stretch of the vocabulary, which stays in shared memory as it was
+// read (masked and changed entries as -inf) between the pass that finds maximum
+// and sum (a running maximum and a sum rescaled when it grows, a thread) and the
+// one that writes; the CTAs exchange both through distributed shared memory.  The
+// next row is copied into a second buffer meanwhile (where two CTAs an SM have
+// room for one: 16-bit logits).  A cluster takes rows that follow one another, so a request's bits are formed from its counts once for its rows, and
+// there are no more clusters than run at once.
 #include "idx_internal.h"
 #include "idx_rope.cuh"
 
 namespace idx {
 namespace {
 
-constexpr int kThreadsP = 512;
+constexpr int kThreadsP = 256;
 constexpr int kWarpsP = kThreadsP / 32;
 constexpr int kClusterP = 8;
 constexpr int kPathP = IDX_VERIFY_MAX_NODES;
-constexpr int kFixP = 8;  // words of bits a warp looks at together
+constexpr int kTreeP = 64;    // bits of a tree's mask
+constexpr int kMaskP = IDX_PROBS_MAX_VOCAB / kClusterP / 32 / kThreadsP;  // words of bits a thread
+constexpr int kCountP = 8;    // counts in flight a thread
+constexpr int kFixP = 4;      // changed entries a thread takes at a time
+constexpr int kListP = kFixP * kThreadsP;
+constexpr size_t kRoomP = 104 * 1024;  // dynamic shared memory of each of two CTAs an SM (which has 228 KB)
+constexpr int kBiased = 0x8000;  // an entry of the list that has a bias
 constexpr float kNegInf = -INFINITY;
 
 struct ProbArgs {
@@ -48,6 +56,8 @@ struct ProbArgs {
   float* lse;
   int32_t* status;
   int32_t slice;  // entries of a CTA, a multiple of 32
+  int32_t buffers;  // rows in shared memory: the next one comes while one is worked on, or after it
+  uint32_t polls;
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -66,6 +76,14 @@ __device__ __forceinline__ void sync_cluster() {
 __device__ __forceinline__ void put_cluster(void* p, uint32_t rank, unsigned long long v) {
   asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u64 [a], %2;\n\t}" ::"r"(smem_u32(p)), "r"(rank), "l"(v)
                : "memory");
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -87,41 +105,194 @@ struct Mass {
     raise(x, k);
     s += ex2((x - base()) * k);
   }
-  __device__ __forceinline__ void join(float om, float os, float k) {
-    const float top = fmaxf(m, om), b = top == kNegInf ? 0.f : top;
-    s = s * ex2((m - b) * k) + os * ex2((om - b) * k);
-    m = top;
+};
+
+// Four entries of a row in shared memory from element e on.
+__device__ __forceinline__ float4 four_of(const float* xs, int e) { return make_float4(xs[e], xs[e + 1], xs[e + 2], xs[e + 3]); }
+template <typename T>
+__device__ __forceinline__ float4 four_of(const T* xs, int e) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(xs) + (e >> 1);
+  uint32_t y[2] = {w[0], w[1]};
+  if (e & 1) y[0] = __funnelshift_r(y[0], y[1], 16), y[1] = __funnelshift_r(y[1], w[2], 16);
+  const float2 a = Words<T>::get(y, 0), b = Words<T>::get(y, 1);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// What depends on the type of a row's words: -inf, the larger of two words' entries, masked entries.
+template <typename T>
+struct Packed;
+template <>
+struct Packed<__nv_bfloat16> {
+  static constexpr uint32_t kNeg = 0xFF80FF80u;
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 c = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&c);
   }
 };
+template <>
+struct Packed<__half> {
+  static constexpr uint32_t kNeg = 0xFC00FC00u;
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    const __half2 c = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&c);
+  }
+};
+template <>
+struct Packed<float> {
+  static constexpr uint32_t kNeg = 0xFF800000u;
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }
+};
+// Bytes of the sign bits of x's bytes, as the selector's nibbles (8 + byte) say.
+__device__ __forceinline__ uint32_t signs_of(uint32_t x, uint32_t selector) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(x), "r"(selector));
+  return r;
+}
+// Entries whose bit is set become -inf.
+template <typename T>
+__device__ __forceinline__ void take_out(uint32_t (&w)[4], uint32_t bits) {
+  // bit i to the sign of byte i
+  const uint32_t low = (bits & 15u) * 0x10204080u, high = (bits >> 4 & 15u) * 0x10204080u;
+  const uint32_t m[4] = {signs_of(low, sizeof(T) == 2 ? 0x9988u : 0x8888u), signs_of(low, sizeof(T) == 2 ? 0xBBAAu : 0x9999u),
+                         signs_of(sizeof(T) == 2 ? high : low, sizeof(T) == 2 ? 0x9988u : 0xAAAAu),
+                         signs_of(sizeof(T) == 2 ? high : low, sizeof(T) == 2 ? 0xBBAAu : 0xBBBBu)};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = (w[e] & ~m[e]) | (Packed<T>::kNeg & m[e]);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_constant__ ProbArgs a) {
   pdl_enter();
   constexpr int kV = 16 / (int)sizeof(T);
-  constexpr int kUnroll = 4;
-  extern __shared__ __align__(16) float xs[];  // slice + 16 entries, then three rows of bits
-  const int words = a.slice / 32;
-  uint32_t* seen = reinterpret_cast<uint32_t*>(xs + a.slice + 16);  // tokens with counts
-  uint32_t* listed = seen + words;                                  // tokens on the path or in the biases
-  uint32_t* skip = listed + words;                                  // entries that the main pass leaves out
-  __shared__ int path[kPathP];
-  __shared__ float2 warp_mass[kWarpsP];
-  __shared__ unsigned long long cta_mass[2][kClusterP];
+  // buffers of slice + 16 entries, then two rows of bits, a word before and behind each
+  extern __shared__ __align__(16) unsigned char store[];
+  const int stretch = a.slice + 16;
+  uint32_t* special = reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(store) + (size_t)a.buffers * stretch) + 1;  // entries that the request's counts or biases change
+  uint32_t* skip = special + a.slice / 32 + 2;  // entries that the main pass leaves out, those around the stretch among them
+  __shared__ uint64_t full[2];
+  __shared__ int tokens[kPathP + 1];   // of the request: node j's at j
+  __shared__ uint64_t masks[kTreeP];   // of its nodes
+  __shared__ int path_of_tree[kTreeP];
+  __shared__ uint16_t list[kListP];  // the special entries; kBiased: some bias is theirs
+  __shared__ int warp_count[kWarpsP];
+  __shared__ unsigned long long parts[2][kClusterP * kWarpsP];  // maximum and sum of each warp of the cluster
   __shared__ unsigned long long cta_first[2][kClusterP];
   __shared__ int first_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cta_rank(), cs = (int)cta_count();
-  const int cluster = blockIdx.x / cs, clusters = gridDim.x / cs;
-  const int lo = min(a.vocab, rank * a.slice), hi = min(a.vocab, lo + a.slice), n_here = hi - lo;
+  const int lo = min(a.vocab, rank * a.slice), n_here = min(a.vocab, lo + a.slice) - lo, here = (n_here + 31) / 32;
+  const int clusters = gridDim.x / cs, cluster = blockIdx.x / cs;
   const int t_lo = (int)((int64_t)a.num_tokens * cluster / clusters), t_hi = (int)((int64_t)a.num_tokens * (cluster + 1) / clusters);
-  int r_at = -1, parity = 0;
+  const T* logits = static_cast<const T*>(a.logits);
+  const T* logits_end = logits + (int64_t)(a.num_tokens - 1) * a.l_stride + a.vocab;
+  const bool any = a.counts != nullptr || a.bias_cu != nullptr;
   bool bad_tree = false;
+
+  auto row_of = [&](int t) { return logits + (int64_t)t * a.l_stride + lo; };
+  auto shift_of = [&](const T* row) { return (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) % kV); };
+  auto vectors_of = [&](int shift) { return n_here > 0 ? (n_here + shift + kV - 1) / kV : 0; };
+  auto buffer_of = [&](int t) { return a.buffers == 2 ? (t - t_lo) & 1 : 0; };
+  // Thread 0 asks for a row, as whole vectors at their aligned addresses, whatever else is in them; the tensor's first and last
+  // vectors may not be whole and are left out.
+  auto ask = [&](int t) {
+    const T* row = row_of(t);
+    const int shift = shift_of(row), vectors = vectors_of(shift);
+    const int first = vectors > 0 && row - shift < logits ? 1 : 0, last = vectors > 0 && row - shift + vectors * kV > logits_end ? vectors - 1 : vectors;
+    uint64_t* bar = &full[buffer_of(t)];
+    const uint32_t bytes = (uint32_t)max(0, last - first) * 16u;
+    mbar_arrive_expect_tx(bar, bytes);
+    if (bytes > 0) bulk_g2s(reinterpret_cast<T*>(store) + (size_t)buffer_of(t) * stretch + first * kV, row - shift + first * kV, bytes, bar);
+  };
+  const uint32_t behind = n_here % 32 != 0 ? ~0u << (n_here % 32) : 0u;  // bits past the stretch in its last word
+  auto mask_row = [&](int t) { return reinterpret_cast<const uint32_t*>(a.allowed) + (int64_t)t * a.a_stride + lo / 32; };
+  if (tid == 0) {
+    skip[-1] = skip[here] = ~0u;
+    mbar_init(&full[0], 1), mbar_init(&full[1], 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    if (t_lo < t_hi) ask(t_lo);
+  }
   sync_cluster();  // every CTA of the cluster runs: its shared memory may be written
 
+  // the request that the rows are of, and counts and biases of this thread's special entries
+  int r = 0, begin = 0, end = 0, changed = 0, mine_at = 0, b0 = 0, b1 = 0;
+  float heat = 1.f, repetition = 1.f, presence = 0.f, frequency = 0.f;
+  const int32_t* counts = nullptr;
+  const int* path = a.mask != nullptr ? path_of_tree : tokens + 1;  // the drafted tokens on the node's path
+  int fix_c[kFixP];
+  float fix_b[kFixP], fix[kFixP];
+  uint32_t mask_words[kMaskP], fix_mask[kFixP];
+  bool timed_out = false;
+  bool known = false, rounds = false, ready = false;  // of the request; more special entries than the list holds; bits and path of the row are there
+  int parity = 0, n_path = 0;
+
+  // special entries of ranks from `first` on into the list (its biased ones by `flags`, or all)
+  auto fill = [&](int first, const uint32_t* flags) {
+    int at = mine_at - first;
+    for (int w = tid; w < here; w += kThreadsP) {
+      const uint32_t biased = flags != nullptr ? flags[w] : ~0u;
+      for (uint32_t bits = special[w]; bits != 0; bits &= bits - 1, ++at) {
+        const int e = __ffs(bits) - 1;
+        if (at >= 0 && at < kListP) list[at] = (uint16_t)((32 * w + e) | (biased >> e & 1u ? kBiased : 0));
+      }
+    }
+  };
+  // counts and biases of this thread's entries of the list
+  auto look_up = [&](int first) {
+#pragma unroll
+    for (int u = 0; u < kFixP; ++u) {
+      const int at = tid + u * kThreadsP;
+      fix_c[u] = 0, fix_b[u] = 0.f;
+      if (first + at >= changed) continue;
+      const int i = list[at] & ~kBiased;
+      if (counts != nullptr) fix_c[u] = counts[i];
+      if (list[at] & kBiased) {
+        int found = 0;
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b)
+          if (a.bias_tokens[b] == lo + i) fix_b[u] = found++ == 0 ? a.bias_values[b] : __int_as_float(0x7FC00000);
+      }
+    }
+  };
+  // an entry as it becomes
+  auto changed_value = [&](int i, float y, int c, bool biased, float bias) {
+    int times = c & 0x7FFFFFFF;
+    for (int j = 0; j < n_path; ++j) times += path[j] == lo + i;
+    if (c < 0 || times > 0) y = y > 0.f ? __fdiv_rn(y, repetition) : __fmul_rn(y, repetition);
+    if (times > 0) y = __fsub_rn(y, __fadd_rn(__fmul_rn(frequency, (float)times), presence));
+    if (biased) {
+      if (bias == bias) {
+        y = __fadd_rn(y, bias);
+      } else {  // several
+        for (int b = b0; b < b1; ++b)
+          if (a.bias_tokens[b] == lo + i) y = __fadd_rn(y, a.bias_values[b]);
+      }
+    }
+    return y;
+  };
+
   for (int t = t_lo; t < t_hi; ++t) {
-    // the row's request
-    int r = 0;
-    {
+    float* out = a.probs + (int64_t)t * a.p_stride + lo;
+    const T* row = row_of(t);
+    const int shift = shift_of(row), vectors = vectors_of(shift);
+    T* xs = reinterpret_cast<T*>(store) + (size_t)buffer_of(t) * stretch;
+    const bool next = t + 1 < t_hi;
+    // (the row before, which was in the other buffer, is used up)
+    if (next && a.buffers == 2 && tid == 0) ask(t + 1);
+    auto arrived = [&] {
+      const uint32_t phase = (uint32_t)(a.buffers == 2 ? (t - t_lo) >> 1 : t - t_lo) & 1u;
+      uint64_t* bar = &full[buffer_of(t)];
+      if (!mbar_try_wait_nosuspend(bar, phase) && !mbar_wait(bar, phase, nullptr, timed_out ? 0u : a.polls)) timed_out = true;
+    };
+    // with one buffer, the next row is asked for when all are done with this one
+    auto used_up = [&] {
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (next && a.buffers == 1 && tid == 0) ask(t + 1);
+    };
+    if (!known || t < begin || t >= end) {
+      // the row's request
+      r = 0;
       int top = a.num_reqs;
       while (top - r > 1) {
         const int step = (top - r + 31) / 32, at = r + step * lane;
@@ -129,194 +300,339 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
         r += step * max(0, __popc(below) - 1);
         top = min(top, r + step);
       }
+      begin = a.num_reqs > 0 ? max(a.cu[r], 0) : 0, end = a.num_reqs > 0 ? min(a.cu[r + 1], a.num_tokens) : 0;
+      known = t >= begin && t < end, ready = false;
+      if (!known) {  // a padded batch
+        for (int i = tid; i < n_here; i += kThreadsP) out[i] = 0.f;
+        if (rank == 0 && tid == 0 && a.lse != nullptr) a.lse[t] = kNegInf;
+        arrived();
+        used_up();
+        continue;
+      }
+      heat = a.temperature != nullptr ? a.temperature[r] : 1.f;
+      repetition = a.repetition != nullptr ? a.repetition[r] : 1.f;
+      presence = a.presence != nullptr ? a.presence[r] : 0.f, frequency = a.frequency != nullptr ? a.frequency[r] : 0.f;
+      if (a.tokens != nullptr) {
+        for (int j = tid; j < min(end - begin, kPathP + 1); j += kThreadsP) tokens[j] = a.tokens[begin + j];
+        if (a.mask != nullptr && tid < min(end - begin, kTreeP)) masks[tid] = a.mask[begin + tid];
+      }
+      changed = 0;
+      if (any) {
+        counts = a.counts != nullptr ? a.counts + (int64_t)r * a.c_stride + lo : nullptr;
+        if (a.bias_cu != nullptr) b0 = max(0, a.bias_cu[r]), b1 = min(a.num_bias, a.bias_cu[r + 1]);
+        for (int w = tid; w < here; w += kThreadsP) special[w] = 0, skip[w] = 0;
+        __syncthreads();
+        if (counts != nullptr) {
+          // Fours at aligned addresses, kCountP of them in flight a thread; eight lanes' make a word of bits, which lies across two.
+          const int off = (int)(reinterpret_cast<uintptr_t>(counts) >> 2 & 3), quads = (n_here + off + 3) / 4;
+          for (int q0 = tid; q0 - lane < quads; q0 += kThreadsP * kCountP) {
+            int4 c[kCountP];
+#pragma unroll
+            for (int u = 0; u < kCountP; ++u) {
+              const int q = q0 + u * kThreadsP, i = 4 * q - off;
+              c[u] = make_int4(0, 0, 0, 0);
+              if (i >= 0 && i + 4 <= n_here) {
+                c[u] = *reinterpret_cast<const int4*>(counts + i);
+              } else if (q < quads) {
+                if (i >= 0) c[u].x = counts[i];
+                if (i + 1 >= 0 && i + 1 < n_here) c[u].y = counts[i + 1];
+                if (i + 2 >= 0 && i + 2 < n_here) c[u].z = counts[i + 2];
+                if (i + 3 < n_here) c[u].w = counts[i + 3];
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < kCountP; ++u) {
+              uint32_t bits = ((c[u].x != 0) | (c[u].y != 0) << 1 | (c[u].z != 0) << 2 | (c[u].w != 0) << 3) << (4 * (lane & 7));
+#pragma unroll
+              for (int o = 1; o < 8; o <<= 1) bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, o);
+              if ((lane & 7) == 0 && bits != 0) {
+                const int i = 4 * (q0 + u * kThreadsP) - off, w = i >> 5, sh = i & 31;  // (w -1: no bit is its)
+                if (bits << sh) atomicOr(&special[w], bits << sh);
+                if (sh != 0 && bits >> (32 - sh)) atomicOr(&special[w + 1], bits >> (32 - sh));
+              }
+            }
+          }
+        }
+        __syncthreads();
+        if (b1 > b0) {
+          for (int b = b0 + tid; b < b1; b += kThreadsP) {
+            const int i = a.bias_tokens[b] - lo;
+            if (i >= 0 && i < n_here) atomicOr(&special[i >> 5], 1u << (i & 31)), atomicOr(&skip[i >> 5], 1u << (i & 31));
+          }
+          __syncthreads();
+        }
+        mine_at = 0;
+        for (int w = tid; w < here; w += kThreadsP) mine_at += __popc(special[w]);
+        int incl = mine_at;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (lane == 31) warp_count[warp] = incl;
+        __syncthreads();
+        int before = 0;
+#pragma unroll
+        for (int w = 0; w < kWarpsP; ++w) {
+          const int c = warp_count[w];
+          before += w < warp ? c : 0, changed += c;
+        }
+        mine_at = before + incl - mine_at;
+        rounds = changed > kListP;
+        if (changed > 0) fill(0, skip);
+        __syncthreads();
+        if (changed > 0 && !rounds) look_up(0);
+      }
     }
-    const int begin = a.num_reqs > 0 ? max(a.cu[r], 0) : 0, end = a.num_reqs > 0 ? min(a.cu[r + 1], a.num_tokens) : 0;
-    float* out = a.probs + (int64_t)t * a.p_stride + lo;
-    if (t < begin || t >= end) {  // a padded batch
-      for (int i = tid; i < n_here; i += kThreadsP) out[i] = 0.f;
-      if (rank == 0 && tid == 0 && a.lse != nullptr) a.lse[t] = kNegInf;
-      continue;
-    }
-    const float heat = a.temperature != nullptr ? a.temperature[r] : 1.f;
     const bool greedy = !(heat > 8.7e-19f);  // 2^-60
     const float k = greedy ? 1.44269504f : 1.44269504f / heat;
-    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.l_stride + lo;
-    const int32_t* counts = a.counts != nullptr ? a.counts + (int64_t)r * a.c_stride + lo : nullptr;
-    const uint32_t* allowed = a.allowed != nullptr ? reinterpret_cast<const uint32_t*>(a.allowed) + (int64_t)t * a.a_stride + lo / 32 : nullptr;
 
-    // which entries are changed
-    const bool any = counts != nullptr || a.tokens != nullptr || a.bias_cu != nullptr, some = any || allowed != nullptr;
-    const int here = (n_here + 31) / 32;
-    if (counts != nullptr && r != r_at) {
-      for (int w = warp; w < here; w += kWarpsP) {
-        const int i = 32 * w + lane;
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, i < n_here && counts[i] != 0);
-        if (lane == 0) seen[w] = bits;
+    // The path of row t among its request's tokens; then its bits.
+    auto put_path = [&](int t) {
+      if (a.tokens == nullptr) return;
+      const int node = t - begin;
+      if (a.mask != nullptr) {
+        uint64_t m = node < kTreeP ? masks[node] & ~1ull : 0ull;
+        if (end - begin < kTreeP) m &= (1ull << (end - begin)) - 1ull;
+        n_path = __popcll(m);
+        if (tid < kTreeP && (m >> tid & 1)) path_of_tree[__popcll(m & ((1ull << tid) - 1ull))] = tokens[tid];
+      } else {
+        bad_tree |= node > kPathP;
+        n_path = min(node, kPathP);
       }
-    }
-    r_at = r;
-    int n_path = 0, b0 = 0, b1 = 0;
-    if (any) {
-      for (int w = tid; w < here; w += kThreadsP) listed[w] = 0;
-      if (a.tokens != nullptr) {
-        const int node = t - begin;
-        if (a.mask != nullptr) {
-          uint64_t m = a.mask[t] & ~1ull;
-          if (end - begin < 64) m &= (1ull << (end - begin)) - 1ull;
-          n_path = __popcll(m);
-          if (tid < 64 && (m >> tid & 1)) path[__popcll(m & ((1ull << tid) - 1ull))] = a.tokens[begin + tid];
-        } else {
-          n_path = min(node, kPathP);
-          bad_tree |= node > kPathP;
-          for (int j = tid; j < n_path; j += kThreadsP) path[j] = a.tokens[begin + 1 + j];
-        }
-      }
-      if (a.bias_cu != nullptr) b0 = max(0, a.bias_cu[r]), b1 = min(a.num_bias, a.bias_cu[r + 1]);
-      __syncthreads();
+    };
+    auto mark_path = [&] {
       for (int j = tid; j < n_path; j += kThreadsP) {
         const int v = path[j];
-        if (v >= lo && v < hi) atomicOr(&listed[(v - lo) >> 5], 1u << ((v - lo) & 31));
+        if (v >= lo && v < lo + n_here) atomicOr(&skip[(v - lo) >> 5], 1u << ((v - lo) & 31));
       }
-      for (int b = b0 + tid; b < b1; b += kThreadsP) {
-        const int v = a.bias_tokens[b];
-        if (v >= lo && v < hi) atomicOr(&listed[(v - lo) >> 5], 1u << ((v - lo) & 31));
+    };
+    // bits of this thread's words of row t's mask, and of its special entries (asked for before they are needed)
+    auto ask_mask = [&](int t) {
+#pragma unroll
+      for (int u = 0; u < kMaskP; ++u) {
+        mask_words[u] = ~0u;
+        if (a.allowed != nullptr && tid + u * kThreadsP < here) mask_words[u] = mask_row(t)[tid + u * kThreadsP];
       }
+#pragma unroll
+      for (int u = 0; u < kFixP; ++u) {
+        fix_mask[u] = ~0u;
+        if (a.allowed != nullptr && !rounds && tid + u * kThreadsP < changed) fix_mask[u] = mask_row(t)[(list[tid + u * kThreadsP] & ~kBiased) >> 5];
+      }
+    };
+    auto put_skip = [&] {
+#pragma unroll
+      for (int u = 0; u < kMaskP; ++u) {
+        const int w = tid + u * kThreadsP;
+        if (w < here) skip[w] = (any ? special[w] : 0u) | ~mask_words[u] | (w == here - 1 ? behind : 0u);
+      }
+    };
+    if (!ready) {
+      ask_mask(t);
+      put_skip();
+      put_path(t);
       __syncthreads();
+      mark_path();
     }
-    if (some) {
-      for (int w = tid; w < here; w += kThreadsP) {
-        uint32_t bits = 0;
-        if (any) bits = listed[w] | (counts != nullptr ? seen[w] : 0u);
-        if (allowed != nullptr) bits |= ~allowed[w];
-        skip[w] = bits;
-      }
-      __syncthreads();
-    }
+    const uint32_t* mask = a.allowed != nullptr ? mask_row(t) : nullptr;
+    const bool slow = rounds || n_path > kThreadsP;  // more special entries, or tokens of a path, than one for each thread
+    const bool same = next && t + 1 < end && !slow && n_path < kThreadsP;  // the next row is the request's too
 
-    // the row into shared memory, as vectors at their aligned addresses
-    const int shift = (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) % kV);
-    const int vectors = n_here > 0 ? (n_here + shift + kV - 1) / kV : 0;
-    Mass mass;
-    for (int j0 = tid; j0 < vectors; j0 += kThreadsP * kUnroll) {
-      uint4 raw[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int j = j0 + u * kThreadsP, i = j * kV - shift;
-        if (j < vectors && i >= 0 && i + kV <= n_here) raw[u] = ld_stream_u4(row + i);
+    // The row is there.  This thread's special entries as they are, and a token of the path that is none and comes first there.
+    arrived();
+    if (vectors > 0 && (row - shift < logits || row - shift + vectors * kV > logits_end)) {  // the tensor's first or last vector
+      if (tid < 2) {
+        const int j = tid == 0 ? 0 : vectors - 1, i = j * kV - shift;
+        if (row + i < logits || row + i + kV > logits_end)
+          for (int e = 0; e < kV; ++e)
+            if (i + e >= 0 && i + e < n_here) xs[j * kV + e] = row[i + e];
       }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int j = j0 + u * kThreadsP, i = j * kV - shift;
-        if (j >= vectors) continue;
-        float x[kV];
-        uint32_t bits = 0;
-        if (i >= 0 && i + kV <= n_here) {
-          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-          for (int e = 0; e < kV / 2; ++e) {
-            const float2 p = Words<T>::get(w, e);
-            x[2 * e] = p.x, x[2 * e + 1] = p.y;
-          }
-          if (some) bits = __funnelshift_r(skip[i >> 5], (i & 31) + kV > 32 ? skip[(i >> 5) + 1] : 0u, i & 31);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kV; ++e) {
-            const bool in = i + e >= 0 && i + e < n_here;
-            x[e] = in ? to_f(row[i + e]) : 0.f;
-            if (!in || (some && (skip[(i + e) >> 5] >> ((i + e) & 31) & 1u))) bits |= 1u << e;
-          }
-        }
-        if (some || bits) {
-#pragma unroll
-          for (int e = 0; e < kV; ++e) x[e] = bits >> e & 1u ? kNegInf : x[e];
-        }
-        float top = x[0];
-#pragma unroll
-        for (int e = 1; e < kV; ++e) top = fmaxf(top, x[e]);
-        mass.raise(top, k);
-        const float b = mass.base();
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int e = 0; e < kV; e += 2) s0 += ex2((x[e] - b) * k), s1 += ex2((x[e + 1] - b) * k);
-        mass.s += s0 + s1;
-#pragma unroll
-        for (int e = 0; e < kV; e += 4) *reinterpret_cast<float4*>(xs + j * kV + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-      }
-    }
-    if (any) {
-      // the changed entries: a warp looks at kFixP words of bits, a lane has a bit of each
-      const float rep = a.repetition != nullptr ? a.repetition[r] : 1.f, pres = a.presence != nullptr ? a.presence[r] : 0.f,
-                  freq = a.frequency != nullptr ? a.frequency[r] : 0.f;
       __syncthreads();
-      for (int w0 = warp * kFixP; w0 < here; w0 += kWarpsP * kFixP) {
-        float x[kFixP];
-        int c[kFixP];
-        uint32_t on = 0;
+    }
+    auto stray = [&](int j) {  // entry of the path's token j where it is in this stretch and not special; -1
+      const int v = path[j], i = v - lo;
+      return v >= lo && i < n_here && (!any || !(special[i >> 5] >> (i & 31) & 1u)) ? i : -1;
+    };
+    auto comes_first = [&](int j, int i) {
+      bool again = false;
+      for (int l = 0; l < j; ++l) again |= path[l] == lo + i;
+      return !again;
+    };
+    uint32_t on = 0, extra_mask = ~0u;
+    int extra = tid < n_path ? stray(tid) : -1;
+    float extra_y = 0.f;
+    if (!rounds) {
 #pragma unroll
-        for (int u = 0; u < kFixP; ++u) {
-          const int w = w0 + u, i = 32 * w + lane;
-          if (w >= here) continue;
-          uint32_t bits = listed[w] | (counts != nullptr ? seen[w] : 0u);
-          if (allowed != nullptr && bits != 0) bits &= allowed[w];
-          if (bits >> lane & 1u) {
-            on |= 1u << u;
-            x[u] = to_f(row[i]);
-            c[u] = counts != nullptr ? counts[i] : 0;
-          }
-        }
+      for (int u = 0; u < kFixP; ++u)
+        if (tid + u * kThreadsP < changed) fix[u] = to_f(xs[(list[tid + u * kThreadsP] & ~kBiased) + shift]);
+    }
+    if (extra >= 0) {
+      if (mask != nullptr) extra_mask = mask[extra >> 5];
+      extra_y = to_f(xs[extra + shift]);
+    }
+    __syncthreads();
+    // those that are left
+    auto resolve = [&](int first) {
+      on = 0;
 #pragma unroll
-        for (int u = 0; u < kFixP; ++u) {
-          if (!(on >> u & 1u)) continue;
-          const int w = w0 + u, i = 32 * w + lane;
-          const bool in_list = listed[w] >> lane & 1u, prompt = c[u] < 0;
-          int times = c[u] & 0x7FFFFFFF;
-          if (in_list)
-            for (int j = 0; j < n_path; ++j) times += path[j] == lo + i;
-          float y = x[u];
-          if (prompt || times > 0) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-          if (times > 0) y = __fsub_rn(y, __fadd_rn(__fmul_rn(freq, (float)times), pres));
-          if (in_list)
-            for (int b = b0; b < b1; ++b)
-              if (a.bias_tokens[b] == lo + i) y = __fadd_rn(y, a.bias_values[b]);
-          xs[i + shift] = y;
-          mass.add(y, k);
+      for (int u = 0; u < kFixP; ++u)
+        if (first + tid + u * kThreadsP < changed && (fix_mask[u] >> (list[tid + u * kThreadsP] & 31) & 1u)) on |= 1u << u;
+    };
+    // with rounds, from the tensor
+    auto fetch = [&](int first) {
+#pragma unroll
+      for (int u = 0; u < kFixP; ++u) {
+        const int at = tid + u * kThreadsP;
+        if (first + at >= changed) continue;
+        const int i = list[at] & ~kBiased;
+        fix_mask[u] = mask != nullptr ? mask[i >> 5] : ~0u, fix[u] = to_f(row[i]);
+      }
+    };
+
+    // the row: entries that are left out become -inf, then maximum and sum of the others
+    Mass mass;
+    uint32_t top2 = Packed<T>::kNeg;
+#pragma unroll 2
+    for (int j = tid; j < vectors; j += kThreadsP) {
+      const int i = j * kV - shift, at = i >> 5;  // rounded down: -1 in the first vector
+      uint4* here4 = reinterpret_cast<uint4*>(xs + j * kV);
+      const uint4 v = *here4;
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      take_out<T>(w, __funnelshift_r(skip[at], skip[at + 1], i & 31));
+      *here4 = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top2 = Packed<T>::larger(top2, w[e]);
+    }
+    if (sizeof(T) == 2) {
+      const float2 two = Words<T>::get(&top2, 0);
+      mass.raise(fmaxf(two.x, two.y), k);
+    } else {
+      mass.raise(__uint_as_float(top2), k);
+    }
+    {
+      const float b = mass.base();
+      const float2 nb = make_float2(-b, -b), kk = make_float2(k, k);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 2
+      for (int j = tid; j < vectors; j += kThreadsP) {
+        const uint4 v = *reinterpret_cast<const uint4*>(xs + j * kV);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < kV / 2; ++e) {
+          const float2 y = mul2(add2(Words<T>::get(w, e), nb), kk);
+          sum = add2(sum, make_float2(ex2(y.x), ex2(y.y)));
         }
       }
+      mass.s = sum.x + sum.y;
     }
+    // the changed entries
+    for (int first = 0; first < changed; first += kListP) {
+      if (rounds) {
+        __syncthreads();
+        fill(first, nullptr);
+        __syncthreads();
+        look_up(first), fetch(first);
+      }
+      resolve(first);
+#pragma unroll
+      for (int u = 0; u < kFixP; ++u)
+        if (on >> u & 1u) {
+          const int e = list[tid + u * kThreadsP];
+          fix[u] = changed_value(e & ~kBiased, fix[u], fix_c[u], (e & kBiased) && b1 > b0, fix_b[u]);
+          mass.add(fix[u], k);
+        }
+    }
+    if (extra >= 0 && (!(extra_mask >> (extra & 31) & 1u) || !comes_first(tid, extra))) extra = -1;
+    if (extra >= 0) extra_y = changed_value(extra, extra_y, 0, false, 0.f), mass.add(extra_y, k);
+    // (of a long chain a thread has more; their values are formed again for each use)
+    auto each_later = [&](auto&& body) {
+      for (int j = tid + kThreadsP; j < n_path; j += kThreadsP) {
+        const int i = stray(j);
+        if (i >= 0 && (mask == nullptr || (mask[i >> 5] >> (i & 31) & 1u)) && comes_first(j, i)) body(i, changed_value(i, to_f(row[i]), 0, false, 0.f));
+      }
+    };
+    each_later([&](int, float y) { mass.add(y, k); });
 
     // maximum and sum over the cluster
+    auto join = [&] {
+      float top = mass.m;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mass.join(__shfl_xor_sync(0xFFFFFFFFu, mass.m, o), __shfl_xor_sync(0xFFFFFFFFu, mass.s, o), k);
-    if (lane == 0) warp_mass[warp] = make_float2(mass.m, mass.s);
-    __syncthreads();
+      for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const float b = top == kNegInf ? 0.f : top;
+      mass.s *= ex2((mass.m - b) * k), mass.m = top;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) mass.s += __shfl_xor_sync(0xFFFFFFFFu, mass.s, o);
+    };
+    join();
     parity ^= 1;
-    if (warp == 0) {
-      const float2 w = lane < kWarpsP ? warp_mass[lane] : make_float2(kNegInf, 0.f);
-      mass.m = w.x, mass.s = w.y;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) mass.join(__shfl_xor_sync(0xFFFFFFFFu, mass.m, o), __shfl_xor_sync(0xFFFFFFFFu, mass.s, o), k);
-      if (lane < cs)
-        put_cluster(&cta_mass[parity][rank], (uint32_t)lane,
-                    (unsigned long long)__float_as_uint(mass.m) << 32 | (unsigned long long)__float_as_uint(mass.s));
-    }
+    if (lane < cs)
+      put_cluster(&parts[parity][rank * kWarpsP + warp], (uint32_t)lane,
+                  (unsigned long long)__float_as_uint(mass.m) << 32 | (unsigned long long)__float_as_uint(mass.s));
     if (tid == 0) first_s = 0x7FFFFFFF;
+    ready = same;
+    if (same) ask_mask(t + 1);
     __syncwarp();
     sync_cluster();
-    Mass all;
-    for (int c = 0; c < cs; ++c) {
-      const unsigned long long v = cta_mass[parity][c];
-      all.join(__uint_as_float((uint32_t)(v >> 32)), __uint_as_float((uint32_t)v), k);
+    if (same) put_skip(), put_path(t + 1);
+    // each warp puts the cluster's parts together by itself
+    float part_m[kClusterP * kWarpsP / 32], part_s[kClusterP * kWarpsP / 32];
+    mass.m = kNegInf;
+#pragma unroll
+    for (int q = 0; q < kClusterP * kWarpsP / 32; ++q) {
+      const unsigned long long v = lane + 32 * q < cs * kWarpsP ? parts[parity][lane + 32 * q] : (unsigned long long)__float_as_uint(kNegInf) << 32;
+      part_m[q] = __uint_as_float((uint32_t)(v >> 32)), part_s[q] = __uint_as_float((uint32_t)v);
+      mass.m = fmaxf(mass.m, part_m[q]);
     }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mass.m = fmaxf(mass.m, __shfl_xor_sync(0xFFFFFFFFu, mass.m, o));
+    mass.s = 0.f;
+#pragma unroll
+    for (int q = 0; q < kClusterP * kWarpsP / 32; ++q) mass.s += part_s[q] * ex2((part_m[q] - mass.base()) * k);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mass.s += __shfl_xor_sync(0xFFFFFFFFu, mass.s, o);
+    const Mass all = mass;
     const bool none = all.m == kNegInf && all.s == 0.f, broken = !(all.s <= 3.4e38f);
-    float value = 0.f;
-    if (greedy && !none && !broken) {
+    const float inv = none ? 0.f : 1.f / all.s, b = all.base();
+    const float2 nb = make_float2(-b, -b), kk = make_float2(k, k), ii = make_float2(inv, inv);
+    auto chance = [&](float2 x) {
+      const float2 y = mul2(add2(x, nb), kk);
+      return mul2(make_float2(ex2(y.x), ex2(y.y)), ii);
+    };
+    // body(entry, value) for each of this thread's changed entries; all threads together
+    auto each_changed = [&](auto&& body) {
+      for (int first = 0; first < changed; first += kListP) {
+        if (rounds) {
+          __syncthreads();
+          fill(first, nullptr);
+          __syncthreads();
+          look_up(first), fetch(first), resolve(first);
+        }
+#pragma unroll
+        for (int u = 0; u < kFixP; ++u)
+          if (on >> u & 1u) {
+            const int e = list[tid + u * kThreadsP];
+            body(e & ~kBiased, rounds ? changed_value(e & ~kBiased, fix[u], fix_c[u], b1 > b0, fix_b[u]) : fix[u]);
+          }
+      }
+      if (extra >= 0) body(extra, extra_y);
+      each_later(body);
+    };
+    float value = none ? kNegInf : broken ? __int_as_float(0x7FC00000) : all.m / heat + logf(all.s);
+    const bool one = greedy && !none && !broken;
+    int chosen = -1;
+    if (one) {
       // the lowest entry of the largest
       int first = 0x7FFFFFFF;
-      for (int i = tid; i < n_here; i += kThreadsP)
-        if (xs[i + shift] == all.m) {
-          first = i;
-          break;
+      for (int j = tid; j < vectors && first == 0x7FFFFFFF; j += kThreadsP) {
+        const uint4 v = *reinterpret_cast<const uint4*>(xs + j * kV);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = kV / 2 - 1; e >= 0; --e) {
+          const float2 x = Words<T>::get(w, e);
+          first = x.x == all.m ? j * kV - shift + 2 * e : x.y == all.m ? j * kV - shift + 2 * e + 1 : first;
         }
+      }
+      each_changed([&](int i, float y) { first = y == all.m ? min(first, i) : first; });
       first = __reduce_min_sync(0xFFFFFFFFu, first);
       if (lane == 0 && first != 0x7FFFFFFF) atomicMin(&first_s, first);
       __syncthreads();
@@ -326,45 +642,88 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       sync_cluster();
       unsigned long long at = ~0ull;
       for (int c = 0; c < cs; ++c) at = min(at, cta_first[parity][c]);
-      for (int i = tid; i < n_here; i += kThreadsP) out[i] = (unsigned long long)(lo + i) == at ? 1.f : 0.f;
+      chosen = at < ~0ull && at >= (unsigned long long)lo && at < (unsigned long long)(lo + n_here) ? (int)(at - lo) : -1;
       value = all.m;
+    }
+    // fours at the output's aligned addresses
+    const int head = min(n_here, (int)(-(reinterpret_cast<uintptr_t>(out) >> 2) & 3)), fours = (n_here - head) / 4, tail = head + 4 * fours;
+    const int edge = tid < 4 ? tid : tail + tid - 4;
+    const bool at_edge = (tid < 4 && tid < head) || (tid >= 4 && tid < 8 && edge < n_here);
+    if (one) {
+      for (int f = tid; f < fours; f += kThreadsP) *reinterpret_cast<float4*>(out + head + 4 * f) = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (at_edge) out[edge] = 0.f;
+    } else if (slow) {
+      // changed entries are left as they are (probs may be logits) until each is formed again
+      for (int i = tid; i < n_here; i += kThreadsP)
+        if (!(skip[i >> 5] >> (i & 31) & 1u) || !(mask == nullptr || (mask[i >> 5] >> (i & 31) & 1u)))
+          out[i] = chance(make_float2(to_f(xs[i + shift]), 0.f)).x;
+      each_changed([&](int i, float y) { out[i] = chance(make_float2(y, 0.f)).x; });
     } else {
-      const float inv = none ? 0.f : 1.f / all.s, b = all.base();
 #pragma unroll 4
-      for (int i = tid; i < n_here; i += kThreadsP) out[i] = ex2((xs[i + shift] - b) * k) * inv;
-      value = none ? kNegInf : broken ? __int_as_float(0x7FC00000) : all.m / heat + logf(all.s);
+      for (int f = tid; f < fours; f += kThreadsP) {
+        const int i = head + 4 * f;
+        const float4 x = four_of(xs, i + shift);
+        const float2 p = chance(make_float2(x.x, x.y)), q = chance(make_float2(x.z, x.w));
+        *reinterpret_cast<float4*>(out + i) = make_float4(p.x, p.y, q.x, q.y);
+      }
+      if (at_edge) out[edge] = chance(make_float2(to_f(xs[edge + shift]), 0.f)).x;
     }
     if (rank == 0 && tid == 0 && a.lse != nullptr) a.lse[t] = value;
-    __syncthreads();  // the entries are used up
+    used_up();
+    if (one) {
+      if (tid == 0 && chosen >= 0) out[chosen] = 1.f;
+    } else if (!slow) {
+      each_changed([&](int i, float y) { out[i] = chance(make_float2(y, 0.f)).x; });
+    }
+    if (same) mark_path();
+  }
+  if (timed_out) {
+    report(a.status, IDX_ST_TIMEOUT);
+    // no copy may come after the CTA is gone
+    if (tid == 0)
+      for (int t = max(t_lo, t_hi - a.buffers); t < t_hi; ++t)
+        mbar_wait(&full[buffer_of(t)], (uint32_t)(a.buffers == 2 ? (t - t_lo) >> 1 : t - t_lo) & 1u, nullptr);
   }
   if (bad_tree && tid == 0) report(a.status, IDX_ST_BAD_TREE);
 }
 
 template <typename T>
-void launch_probs(ProbArgs a, cudaStream_t s) {
+int launch_probs(ProbArgs a, cudaStream_t s) {
   const int sms = max(device_sms(), 1);
   // CTAs a row: stretches of at most 8,192 entries, shorter ones where a few rows leave SMs without any
   int cs = 1;
   auto slice_of = [&](int c) { return ((a.vocab + c - 1) / c + 31) / 32 * 32; };
   while (cs < kClusterP && (slice_of(cs) > 8192 || ((int64_t)a.num_tokens * cs < 2 * sms && slice_of(cs) > 2048))) cs *= 2;
   a.slice = slice_of(cs);
-  const size_t smem = (size_t)(a.slice + 16) * 4 + (size_t)a.slice / 32 * 12;
-  const int per_sm = max(1, min(4, (int)(220 * 1024 / (smem + 8192))));
-  const int clusters = (int)min((int64_t)a.num_tokens, max((int64_t)1, (int64_t)sms * per_sm / cs));
+  // two rows in shared memory where two CTAs an SM keep room for them
+  const size_t row = ((size_t)a.slice + 16) * sizeof(T), bits = ((size_t)a.slice / 32 + 2) * 8;
+  a.buffers = 2 * row + bits <= kRoomP ? 2 : 1;
+  a.polls = wait_polls();
+  const size_t smem = a.buffers * row + bits;
   cudaFuncSetAttribute(k_logit_probs<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * cs));
   cfg.blockDim = dim3(kThreadsP);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cs, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // as many clusters as run at once, and no more than rows
+  int clusters = a.num_tokens;
+  if ((int64_t)a.num_tokens * cs > sms) {
+    cfg.gridDim = dim3((unsigned)(cs * sms));
+    int most = 0;
+    if (cudaOccupancyMaxActiveClusters(&most, k_logit_probs<T>, &cfg) != cudaSuccess || most < 1) return IDX_E_CUDA;
+    clusters = min(clusters, most);
+  }
+  cfg.gridDim = dim3((unsigned)(clusters * cs));
   cfg.numAttrs = 2;
   cudaLaunchKernelEx(&cfg, k_logit_probs<T>, a);
+  return launch_result();
 }
 
 }  // namespace
@@ -402,8 +761,7 @@ extern "C" int idx_logit_probs(const void* logits, int64_t logits_stride, int32_
   if (num_bias > 0) a.bias_cu = bias_cu, a.bias_tokens = bias_tokens, a.bias_values = bias_values, a.num_bias = num_bias;
   a.allowed = allowed, a.a_stride = allowed_stride, a.lse = lse, a.status = status;
   cudaStream_t s = (cudaStream_t)stream;
-  if (dtype == IDX_BF16) launch_probs<__nv_bfloat16>(a, s);
-  else if (dtype == IDX_F16) launch_probs<__half>(a, s);
-  else launch_probs<float>(a, s);
-  return launch_result();
+  if (dtype == IDX_BF16) return launch_probs<__nv_bfloat16>(a, s);
+  if (dtype == IDX_F16) return launch_probs<__half>(a, s);
+  return launch_probs<float>(a, s);
 }
