@@ -592,18 +592,7 @@ def idx_verify_drafts(target, draft, tokens, cu_tokens, accept_u, sample_u, out_
 PROBS_MAX_VOCAB = 262144  # entries of a row of idx_logit_probs
 MAX_CACHES = 8  # caches of one call of idx_settle_drafts and idx_fork_pages
 MAX_FORKS = 4096  # forks of one call
-
-
-def _at(t) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
-def _status_ok(T, status) -> bool:
-    return status is None or (status.is_cuda and status.dtype is T.i32 and status.numel() > 0)
-
-
-def _words_ok(T, shape, t) -> bool:
-    return t is None or (t.is_cuda and t.dtype in T.words and t.shape == shape and t.is_contiguous())
+_CACHE = "Pqqqii"  # idx_cache
 
 
 def idx_norm_rope_append(q, k, v, q_weight, k_weight, eps: float, positions, inv_freq, q_out, k_cache, v_cache, slots=None,
@@ -619,29 +608,46 @@ def idx_norm_rope_append(q, k, v, q_weight, k_weight, eps: float, positions, inv
     code = T.codes.get(kind)
     if code is None:
         raise ValueError(f"{fn}: bfloat16, float16 or float32 is needed, got {kind}")
-    tokens, dim = some.shape[0], some.shape[-1]
-    hq = 0 if q is None else q.shape[1]
-    nb, page, hk = (0, 1, 0) if k is None else (k_cache.shape[0], k_cache.shape[1], k.shape[1])
-    qshape, kshape, cshape, one = (tokens, hq, dim), (tokens, hk, dim), (nb, page, hk, dim), (tokens,)
-    if not (_rows_ok(kind, qshape, q, q_out) and _rows_ok(kind, kshape, k, v) and _rows_ok(kind, cshape, k_cache, v_cache)
-            and _are(kind, (dim,), q_weight, k_weight) and _are(T.i32, one, positions) and _are(T.f64, inv_freq.shape[:1], inv_freq)
-            and _words_ok(T, one, slots) and _status_ok(T, status)
+    tokens, _, dim = shape = some.shape
+    none = (0, 0, 1, 1)
+    qs = os_ = ks = vs = cs = none
+    hq = hk = nb = 0
+    page, one, per_dim = 1, (tokens,), (dim,)
+    qshape = kshape = cshape = shape
+    if q is not None:
+        qshape, qs, os_ = q.shape, q.stride(), q_out.stride()
+        hq = qshape[1]
+    if k is not None:
+        hk, ks, cs = k.shape[1], k.stride(), k_cache.stride()
+        nb, page = k_cache.shape[:2]
+        kshape, cshape = (tokens, hk, dim), (nb, page, hk, dim)
+        vs = none if v is None else v.stride()
+    # (the checks stand in one expression: a call each would cost as much as the launch)
+    if not (some.is_cuda and (q is None or (q_out.is_cuda and q_out.dtype is kind and q_out.shape == qshape))
+            and (k is None or (k.is_cuda and k.dtype is kind and k.shape == kshape and k_cache.is_cuda and k_cache.dtype is kind and k_cache.shape == cshape
+                               and (v is None or (v.is_cuda and v.dtype is kind and v.shape == kshape and v_cache.is_cuda and v_cache.dtype is kind
+                                                  and v_cache.shape == cshape))))
+            and ((qs[2] == 1 and os_[2] == 1 and ks[2] == 1 and vs[2] == 1 and cs[3] == 1) or dim == 1)
+            and (q_weight is None or (q_weight.is_cuda and q_weight.dtype is kind and q_weight.shape == per_dim and q_weight.is_contiguous()))
+            and (k_weight is None or (k_weight.is_cuda and k_weight.dtype is kind and k_weight.shape == per_dim and k_weight.is_contiguous()))
+            and positions.is_cuda and positions.dtype is T.i32 and positions.shape == one and positions.is_contiguous()
+            and inv_freq.is_cuda and inv_freq.dtype is T.f64 and inv_freq.dim() == 1 and inv_freq.is_contiguous()
+            and (slots is None or (slots.is_cuda and slots.dtype in T.words and slots.shape == one and slots.is_contiguous()))
+            and (status is None or (status.is_cuda and status.dtype is T.i32 and status.numel() > 0))
             and (not T.many or _here(q, q_out, k, v, k_cache, v_cache, q_weight, k_weight, positions, inv_freq, slots, status))):
         _explain(fn, ("positions", "inv_freq", "slots", "q_weight", "k_weight"), q=(q, kind, qshape), q_out=(q_out, kind, qshape),
                  k=(k, kind, kshape), v=(v, kind, kshape), k_cache=(k_cache, kind, (None, None, hk, dim)), v_cache=(v_cache, kind, cshape),
                  q_weight=(q_weight, kind, (dim,)), k_weight=(k_weight, kind, (dim,)), positions=(positions, T.i32, one),
                  inv_freq=(inv_freq, T.f64, (None,)), slots=(slots, T.words, one), status=(status, T.i32, None))
-    none = (0, 0, 0, 0)
-    cs = none if k is None else k_cache.stride()
     if v_cache is not None and v_cache.stride() != cs:
         raise ValueError(f"{fn}: k_cache and v_cache must have the same strides")
-    qs, os_ = (none, none) if q is None else (q.stride(), q_out.stride())
-    ks = none if k is None else k.stride()
-    vs = none if v is None else v.stride()
     rc = lib.idx_norm_rope_append(
-        _at(q), qs[0], qs[1], _at(q_out), os_[0], os_[1], hq, _at(k), ks[0], ks[1], _at(v), vs[0], vs[1], hk, tokens, dim, 2 * inv_freq.shape[0],
-        _at(q_weight), _at(k_weight), eps, offset, positions.data_ptr(), inv_freq.data_ptr(), mscale, _at(slots), _at(k_cache), _at(v_cache), nb, page,
-        cs[0], cs[1], cs[2], code, _ROPE_INTERLEAVED if interleaved else 0, _at(status), _stream_on(stream, some))
+        None if q is None else q.data_ptr(), qs[0], qs[1], None if q is None else q_out.data_ptr(), os_[0], os_[1], hq, None if k is None else k.data_ptr(),
+        ks[0], ks[1], None if v is None else v.data_ptr(), vs[0], vs[1], hk, tokens, dim, 2 * inv_freq.shape[0],
+        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps, offset, positions.data_ptr(),
+        inv_freq.data_ptr(), mscale, None if slots is None else slots.data_ptr(), None if k is None else k_cache.data_ptr(),
+        None if v is None else v_cache.data_ptr(), nb, page, cs[0], cs[1], cs[2], code, _ROPE_INTERLEAVED if interleaved else 0,
+        None if status is None else status.data_ptr(), _stream_on(stream, some))
     return rc if rc >= 0 else _check(fn, rc)
 
 
@@ -661,33 +667,46 @@ def idx_index_append(q, k, q_weight, k_weight, eps: float, positions, inv_freq, 
     code = T.codes.get(kind)
     if code is None:
         raise ValueError(f"{fn}: bfloat16, float16 or float32 is needed, got {kind}")
-    tokens, u8 = some.shape[0], T.u8
-    heads = reqs = per = 0
-    one, wide = (tokens,), (128,)
+    tokens, u8, f32, i32 = some.shape[0], T.u8, T.f32, T.i32
+    heads = reqs = per = nb = 0
+    page, one, wide, out = 128, (tokens,), (128,), ()
+    qs, ks = (0, 0, 1), (0, 1)
     if q is not None:
-        heads = q.shape[1]
-        out = (tokens, heads)
+        tokens, heads, _ = qshape = q.shape
+        qs, out = q.stride(), qshape[:2]
         if cu_tokens is not None:
             reqs, per = cu_tokens.shape[0] - 1, q_out.shape[1]
             out = (reqs, per, heads)
-    nb, page = (0, 128) if k is None else index_k.shape[:2]
-    if not ((q is None or (_rows_ok(kind, (tokens, heads, 128), q) and _are(u8, out + wide, q_out) and _are(T.f32, out, q_scale)))
-            and (k is None or (_rows_ok(kind, (tokens, 128), k) and _are(u8, (nb, page, 72), index_k)))
-            and _are(kind, wide, q_weight, k_weight) and _are(T.i32, one, positions) and _are(T.f64, inv_freq.shape[:1], inv_freq)
-            and _words_ok(T, one, slots) and _are(T.f32, (tokens, heads), head_weights)
-            and (cu_tokens is None or _are(T.i32, cu_tokens.shape[:1], cu_tokens)) and _status_ok(T, status)
+    if k is not None:
+        ks = k.stride()
+        nb, page, _ = index_k.shape
+    if not (some.is_cuda and (q is None or (qshape[2] == 128 and qs[2] == 1 and q_out.is_cuda and q_out.dtype is u8 and q_out.shape == (*out, 128)
+                                            and q_out.is_contiguous() and q_scale.is_cuda and q_scale.dtype is f32 and q_scale.shape == out
+                                            and q_scale.is_contiguous()))
+            and (k is None or (k.is_cuda and k.dtype is kind and k.shape == (tokens, 128) and ks[1] == 1 and index_k.is_cuda and index_k.dtype is u8
+                               and index_k.shape[2] == 72 and index_k.is_contiguous()))
+            and (q_weight is None or (q_weight.is_cuda and q_weight.dtype is kind and q_weight.shape == wide and q_weight.is_contiguous()))
+            and (k_weight is None or (k_weight.is_cuda and k_weight.dtype is kind and k_weight.shape == wide and k_weight.is_contiguous()))
+            and positions.is_cuda and positions.dtype is i32 and positions.shape == one and positions.is_contiguous()
+            and inv_freq.is_cuda and inv_freq.dtype is T.f64 and inv_freq.dim() == 1 and inv_freq.is_contiguous()
+            and (slots is None or (slots.is_cuda and slots.dtype in T.words and slots.shape == one and slots.is_contiguous()))
+            and (cu_tokens is None or (cu_tokens.is_cuda and cu_tokens.dtype is i32 and cu_tokens.dim() == 1 and cu_tokens.is_contiguous()))
+            and (head_weights is None or _are(f32, (tokens, heads), head_weights))
+            and (status is None or (status.is_cuda and status.dtype is i32 and status.numel() > 0))
             and (not T.many or _here(q, k, q_out, q_scale, index_k, q_weight, k_weight, positions, inv_freq, slots, cu_tokens, head_weights, status))):
         _explain(fn, ("q_out", "q_scale", "index_k", "q_weight", "k_weight", "positions", "inv_freq", "slots", "head_weights", "cu_tokens"),
-                 q=(q, kind, (tokens, heads, 128)), k=(k, kind, (tokens, 128)), q_out=(q_out, u8, out + wide if heads else None),
-                 q_scale=(q_scale, T.f32, out if heads else None), index_k=(index_k, u8, (None, None, 72)), q_weight=(q_weight, kind, wide),
+                 q=(q, kind, (tokens, heads, 128)), k=(k, kind, (tokens, 128)), q_out=(q_out, u8, (*out, 128)), q_scale=(q_scale, f32, tuple(out)),
+                 index_k=(index_k, u8, (None, None, 72)), q_weight=(q_weight, kind, wide),
                  k_weight=(k_weight, kind, wide), positions=(positions, T.i32, one), inv_freq=(inv_freq, T.f64, (None,)),
                  slots=(slots, T.words, one), cu_tokens=(cu_tokens, T.i32, (None,)), head_weights=(head_weights, T.f32, (tokens, heads)),
                  status=(status, T.i32, None))
-    qs = (0, 0) if q is None else q.stride()
     rc = lib.idx_index_append(
-        _at(q), qs[0], qs[1], heads, _at(k), 0 if k is None else k.stride(0), tokens, 2 * inv_freq.shape[0], _at(q_weight), _at(k_weight), eps, offset,
-        positions.data_ptr(), inv_freq.data_ptr(), mscale, _at(head_weights), scale, None if q is None else _at(cu_tokens), reqs, per, _at(q_out),
-        _at(q_scale), _at(slots), _at(index_k), nb, page, code, _ROPE_INTERLEAVED if interleaved else 0, _at(status), _stream_on(stream, some))
+        None if q is None else q.data_ptr(), qs[0], qs[1], heads, None if k is None else k.data_ptr(), ks[0], tokens, 2 * inv_freq.shape[0],
+        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps, offset, positions.data_ptr(),
+        inv_freq.data_ptr(), mscale, None if head_weights is None else head_weights.data_ptr(), scale,
+        None if q is None or cu_tokens is None else cu_tokens.data_ptr(), reqs, per, None if q is None else q_out.data_ptr(),
+        None if q is None else q_scale.data_ptr(), None if slots is None else slots.data_ptr(), None if k is None else index_k.data_ptr(), nb, page, code,
+        _ROPE_INTERLEAVED if interleaved else 0, None if status is None else status.data_ptr(), _stream_on(stream, some))
     return rc if rc >= 0 else _check(fn, rc)
 
 
@@ -709,10 +728,16 @@ def idx_logit_probs(logits, probs, cu_tokens, temperature=None, repetition=None,
     reqs = cu_tokens.shape[0] - 1
     one, per_req, words = (total,), (reqs,), (total, (vocab + 31) // 32)
     biases = 0 if bias_tokens is None else bias_tokens.shape[0]
-    if not (_rows_ok(kind, shape, logits) and _rows_ok(f32, shape, probs) and _are(i32, (reqs + 1,), cu_tokens, bias_cu)
-            and _are(f32, per_req, temperature, repetition, presence, frequency) and _rows_ok(i32, (reqs, vocab), counts)
-            and _are(i32, one, tokens) and _words_ok(T, one, tree_mask) and _are(i32, (biases,), bias_tokens) and _are(f32, (biases,), bias_values)
-            and _rows_ok(i32, words, allowed) and _are(f32, one, lse) and _status_ok(T, status)
+    per_cu, ls, ps = (reqs + 1,), logits.stride(), probs.stride()
+    if not (logits.is_cuda and probs.is_cuda and probs.dtype is f32 and probs.shape == shape and ((ls[1] == 1 and ps[1] == 1) or vocab == 1)
+            and cu_tokens.is_cuda and cu_tokens.dtype is i32 and cu_tokens.dim() == 1 and cu_tokens.is_contiguous()
+            and _are(f32, per_req, temperature, repetition, presence, frequency) and (counts is None or reqs == 0 or _rows_ok(i32, (reqs, vocab), counts))
+            and (tokens is None or (tokens.is_cuda and tokens.dtype is i32 and tokens.shape == one and tokens.is_contiguous()))
+            and (tree_mask is None or (tree_mask.is_cuda and tree_mask.dtype in T.words and tree_mask.shape == one and tree_mask.is_contiguous()))
+            and (bias_cu is None or (_are(i32, per_cu, bias_cu) and _are(i32, (biases,), bias_tokens) and _are(f32, (biases,), bias_values)))
+            and (allowed is None or _rows_ok(i32, words, allowed))
+            and (lse is None or (lse.is_cuda and lse.dtype is f32 and lse.shape == one and lse.is_contiguous()))
+            and (status is None or (status.is_cuda and status.dtype is i32 and status.numel() > 0))
             and (not T.many or _here(logits, probs, cu_tokens, temperature, repetition, presence, frequency, counts, tokens, tree_mask, bias_cu,
                                      bias_tokens, bias_values, allowed, lse, status))):
         _explain(fn, ("cu_tokens", "temperature", "repetition", "presence", "frequency", "tokens", "tree_mask", "bias_cu", "bias_tokens",
@@ -722,10 +747,14 @@ def idx_logit_probs(logits, probs, cu_tokens, temperature=None, repetition=None,
                  tree_mask=(tree_mask, T.words, one), bias_cu=(bias_cu, i32, (reqs + 1,)), bias_tokens=(bias_tokens, i32, (biases,)),
                  bias_values=(bias_values, f32, (biases,)), allowed=(allowed, i32, words), lse=(lse, f32, one), status=(status, i32, None))
     rc = lib.idx_logit_probs(
-        logits.data_ptr(), _row_stride(logits), code, vocab, total, cu_tokens.data_ptr(), reqs, _at(temperature), _at(repetition), _at(presence),
-        _at(frequency), _at(counts), 0 if counts is None else _row_stride(counts), _at(tokens), _at(tree_mask), _at(bias_cu), _at(bias_tokens),
-        _at(bias_values), biases, _at(allowed), 0 if allowed is None else _row_stride(allowed), probs.data_ptr(), _row_stride(probs), _at(lse),
-        _at(status), _stream_on(stream, logits))
+        logits.data_ptr(), ls[0] if total > 1 else vocab, code, vocab, total, cu_tokens.data_ptr(), reqs,
+        None if temperature is None else temperature.data_ptr(), None if repetition is None else repetition.data_ptr(),
+        None if presence is None else presence.data_ptr(), None if frequency is None else frequency.data_ptr(),
+        None if counts is None else counts.data_ptr(), 0 if counts is None else _row_stride(counts), None if tokens is None else tokens.data_ptr(),
+        None if tree_mask is None else tree_mask.data_ptr(), None if bias_cu is None else bias_cu.data_ptr(),
+        None if bias_cu is None else bias_tokens.data_ptr(), None if bias_cu is None else bias_values.data_ptr(), biases,
+        None if allowed is None else allowed.data_ptr(), 0 if allowed is None else _row_stride(allowed), probs.data_ptr(), ps[0] if total > 1 else vocab,
+        None if lse is None else lse.data_ptr(), None if status is None else status.data_ptr(), _stream_on(stream, logits))
     return rc if rc >= 0 else _check(fn, rc)
 
 
@@ -744,10 +773,13 @@ def _pack_caches(fn: str, T, caches):
     fields = []
     for c in caches:
         shape, strides, size = c.shape, c.stride(), c.element_size()
-        row, fine = 1, len(shape) > 3 and shape[1] == blocks and shape[2] == page and c.is_cuda and (not T.many or _here(c))
-        for n, s in zip(shape[:2:-1], strides[:2:-1]):
-            fine = fine and (n == 1 or s == row)
-            row *= n
+        row, fine, n = 1, len(shape) > 3 and shape[1] == blocks and shape[2] == page and c.is_cuda and (not T.many or _here(c)), len(shape) - 1
+        while n > 2:
+            m = shape[n]
+            if m != 1 and strides[n] != row:
+                fine = False
+            row *= m
+            n -= 1
         if not fine:
             if len(shape) < 4 or shape[1] != blocks or shape[2] != page:
                 raise ValueError(f"{fn}: a cache has shape {tuple(shape)}, (any, {blocks}, {page}, any...) is needed")
@@ -755,7 +787,7 @@ def _pack_caches(fn: str, T, caches):
                 raise ValueError(f"{fn}: a cache is on {c.device}, the current CUDA device is needed")
             raise ValueError(f"{fn}: a token's row of a cache must be contiguous")
         fields += (c.data_ptr(), strides[0] * size, strides[1] * size, strides[2] * size, shape[0], row * size)
-    return struct.pack("Pqqqii" * len(caches), *fields), blocks, page
+    return struct.pack(_CACHE * len(caches), *fields), blocks, page
 
 
 def idx_settle_drafts(caches, slots, cu_tokens, out_tokens, out_nodes, num_accepted, ctx_lens, ctx_out, counts=None, status=None,
@@ -767,8 +799,15 @@ def idx_settle_drafts(caches, slots, cu_tokens, out_tokens, out_nodes, num_accep
     reqs, max_out = out_shape = out_nodes.shape
     per_req, tokens = (reqs,), slots.shape[0]
     vocab = 0 if counts is None else counts.shape[-1]
-    if not (_words_ok(T, (tokens,), slots) and _are(i32, (reqs + 1,), cu_tokens) and _are(i32, out_shape, out_tokens, out_nodes)
-            and _are(i32, per_req, num_accepted, ctx_lens, ctx_out) and (reqs == 0 or _rows_ok(i32, (reqs, vocab), counts)) and _status_ok(T, status)
+    if not (slots.is_cuda and slots.dtype in T.words and slots.dim() == 1 and slots.is_contiguous()
+            and cu_tokens.is_cuda and cu_tokens.dtype is i32 and cu_tokens.shape == (reqs + 1,) and cu_tokens.is_contiguous()
+            and out_tokens.is_cuda and out_tokens.dtype is i32 and out_tokens.shape == out_shape and out_tokens.is_contiguous()
+            and out_nodes.is_cuda and out_nodes.dtype is i32 and out_nodes.is_contiguous()
+            and num_accepted.is_cuda and num_accepted.dtype is i32 and num_accepted.shape == per_req and num_accepted.is_contiguous()
+            and ctx_lens.is_cuda and ctx_lens.dtype is i32 and ctx_lens.shape == per_req and ctx_lens.is_contiguous()
+            and ctx_out.is_cuda and ctx_out.dtype is i32 and ctx_out.shape == per_req and ctx_out.is_contiguous()
+            and (counts is None or reqs == 0 or _rows_ok(i32, (reqs, vocab), counts))
+            and (status is None or (status.is_cuda and status.dtype is i32 and status.numel() > 0))
             and (not T.many or _here(slots, cu_tokens, out_tokens, out_nodes, num_accepted, ctx_lens, ctx_out, counts, status))):
         _explain(fn, ("slots", "cu_tokens", "out_tokens", "out_nodes", "num_accepted", "ctx_lens", "ctx_out"), slots=(slots, T.words, (tokens,)),
                  cu_tokens=(cu_tokens, i32, (reqs + 1,)), out_tokens=(out_tokens, i32, out_shape), out_nodes=(out_nodes, i32, out_shape),
@@ -777,8 +816,8 @@ def idx_settle_drafts(caches, slots, cu_tokens, out_tokens, out_nodes, num_accep
     packed, blocks, page = _pack_caches(fn, T, caches)
     rc = lib.idx_settle_drafts(
         packed, len(caches), blocks, page, slots.data_ptr(), cu_tokens.data_ptr(), reqs, tokens, out_tokens.data_ptr(), out_nodes.data_ptr(), max_out,
-        num_accepted.data_ptr(), ctx_lens.data_ptr(), ctx_out.data_ptr(), _at(counts), 0 if counts is None else _row_stride(counts), vocab, _at(status),
-        _stream_on(stream, out_nodes))
+        num_accepted.data_ptr(), ctx_lens.data_ptr(), ctx_out.data_ptr(), None if counts is None else counts.data_ptr(),
+        0 if counts is None else _row_stride(counts), vocab, None if status is None else status.data_ptr(), _stream_on(stream, out_nodes))
     return rc if rc >= 0 else _check(fn, rc)
 
 
@@ -792,7 +831,7 @@ def idx_fork_pages(caches, parents, children, ctx_lens, owned_pages, block_table
     reqs, width = block_table.shape
     some, per_req, nb = (forks,), (reqs,), refs.shape[0]
     if not (_are(i32, some, parents, children) and _are(i32, per_req, ctx_lens, owned_pages) and _rows_ok(i32, (reqs, width), block_table)
-            and _are(i32, (nb,), refs) and _are(i32, (free,), free_blocks) and _are(i32, (1,), free_cursor, cursor_out) and _status_ok(T, status)
+            and _are(i32, (nb,), refs) and _are(i32, (free,), free_blocks) and _are(i32, (1,), free_cursor, cursor_out) and (status is None or (status.is_cuda and status.dtype is i32 and status.numel() > 0))
             and (not T.many or _here(parents, children, ctx_lens, owned_pages, block_table, refs, free_blocks, free_cursor, cursor_out, status))):
         _explain(fn, ("parents", "children", "ctx_lens", "owned_pages", "refs", "free_blocks", "free_cursor", "cursor_out"),
                  parents=(parents, i32, some), children=(children, i32, some), ctx_lens=(ctx_lens, i32, per_req),
@@ -811,7 +850,7 @@ def idx_fork_pages(caches, parents, children, ctx_lens, owned_pages, block_table
     rc = lib.idx_fork_pages(
         packed, len(caches), nb, page, parents.data_ptr(), children.data_ptr(), forks, ctx_lens.data_ptr(), owned_pages.data_ptr(), reqs,
         block_table.data_ptr(), _row_stride(block_table), width, refs.data_ptr(), free_blocks.data_ptr(), free, free_cursor.data_ptr(),
-        cursor_out.data_ptr(), _at(status), _stream_on(stream, parents))
+        cursor_out.data_ptr(), None if status is None else status.data_ptr(), _stream_on(stream, parents))
     return rc if rc >= 0 else _check(fn, rc)
 
 
@@ -824,7 +863,7 @@ def idx_release_pages(keep_lens, owned_pages, block_table, refs, free_blocks, fr
     reqs, width = block_table.shape
     per_req, nb, free = (reqs,), refs.shape[0], free_blocks.shape[0]
     if not (_are(i32, per_req, keep_lens, owned_pages, pages_out) and _rows_ok(i32, (reqs, width), block_table) and _are(i32, (nb,), refs)
-            and _are(i32, (free,), free_blocks) and _are(i32, (1,), free_cursor, cursor_out) and _status_ok(T, status)
+            and _are(i32, (free,), free_blocks) and _are(i32, (1,), free_cursor, cursor_out) and (status is None or (status.is_cuda and status.dtype is i32 and status.numel() > 0))
             and (not T.many or _here(keep_lens, owned_pages, pages_out, block_table, refs, free_blocks, free_cursor, cursor_out, status))):
         _explain(fn, ("keep_lens", "owned_pages", "pages_out", "refs", "free_blocks", "free_cursor", "cursor_out"),
                  keep_lens=(keep_lens, i32, per_req), owned_pages=(owned_pages, i32, per_req), pages_out=(pages_out, i32, per_req),
@@ -832,6 +871,6 @@ def idx_release_pages(keep_lens, owned_pages, block_table, refs, free_blocks, fr
                  free_cursor=(free_cursor, i32, (1,)), cursor_out=(cursor_out, i32, (1,)), status=(status, i32, None))
     rc = lib.idx_release_pages(
         keep_lens.data_ptr(), owned_pages.data_ptr(), reqs, block_table.data_ptr(), _row_stride(block_table), width, refs.data_ptr(), nb,
-        free_blocks.data_ptr(), free, free_cursor.data_ptr(), cursor_out.data_ptr(), pages_out.data_ptr(), page_tokens, _at(status),
+        free_blocks.data_ptr(), free, free_cursor.data_ptr(), cursor_out.data_ptr(), pages_out.data_ptr(), page_tokens, None if status is None else status.data_ptr(),
         _stream_on(stream, refs))
     return rc if rc >= 0 else _check(fn, rc)

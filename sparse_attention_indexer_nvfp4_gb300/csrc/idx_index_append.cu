@@ -7,17 +7,17 @@
 // blocks of 16 take s = e4m3(max|y| / 6) ("vllm ... gather_nvfp4_index_k": no
 // global scale) and codes e2m1(y / s).
 //
-// The codes are those of 64-bit arithmetic.  In units of 2^-24 of M = |x cw| +
-// |x_p sw|, u comes in fp32 with an error of at most 7: 2 from the angle's
-// rounding, 2 from sincospif, 3 from products and sum.  The largest element's
-// own, at most sqrt 2 as large relative to it (a pair's M is at most that many
-// times its larger element), and the scaling add 13: 20 M for 448 u / max|u|.
-// A norm's r is off by 8, a key's y / s by 19 M in all.  M is at most 2 (|u| +
-// |x_p sw|), so each element is converted at both ends of kSlack (kSlackKey)
-// times that sum around it; where the two codes differ (2% of the rows) the
-// element is formed again in 64 bits, sines and cosines by their Taylor series,
-// and compared with the middle between the codes.  A key whose codes or scales
-// may differ is formed again as a whole.
+// The codes are those of 64-bit arithmetic.  Sines and cosines are formed to
+// 2^-44, once a token, by their Taylor series.  In units of 2^-24 of M = |x cw| +
+// |x_p sw|, u comes in fp32 with an error of at most 4: sines and their products
+// with weights 2, product and sum 2.  The largest element's own, at most sqrt 2
+// as large relative to it (a pair's M is at most that many times its larger
+// element), and the scaling add 11: 15 M for 448 u / max|u|.  A norm's r is off
+// by 9, a key's y / s by 16 M in all.  So each element is converted at both ends
+// of kSlack (kSlackKey) times M around it; where the two codes differ (0.5% of
+// the rows) the element is formed again in 64 bits and compared with the middle
+// between the codes.  A key whose codes or scales may differ is formed again as
+// a whole.
 //
 // Bound by HBM and, with many heads, by the instructions of a row.  A warp
 // takes a token (with few tokens a part of its heads), 16 lanes a row, 8
@@ -29,10 +29,11 @@
 namespace idx {
 namespace {
 
-constexpr int kThreadsI = 256;
+constexpr int kThreadsI = 128;
+constexpr int kCtasI = 5;    // of an SM
 constexpr int kBatchI = 2;  // rows in flight a lane
 constexpr int kLanesI = 16;  // of a row
-constexpr float kSlack = 2.5e-6f, kSlackKey = 4e-6f;
+constexpr float kSlack = 1e-6f, kSlackKey = 1.2e-6f;
 
 struct IndexArgs {
   const void *q, *k;
@@ -87,22 +88,48 @@ __device__ __forceinline__ Eight<T> load8(const T* p) {
   return x;
 }
 
-// cos and sin of 2 pi phase / 2^64: the phase less its nearest quarter turn, then the Taylor series (|y| <= pi / 4: the
-// terms left out are below 2^-52).
-__device__ __forceinline__ double2 turn_of_64(unsigned long long phase) {
+// A number as hi + lo, hi the nearest fp32 to it.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // |a| >= |b| or a = 0
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two times(Two a, Two b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  return two_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p))));
+}
+// c + a b, where |c| is larger than |a b|
+__device__ __forceinline__ Two plus_times(Two c, Two a, Two b) {
+  const Two p = times(a, b), s = two_sum(c.hi, p.hi);
+  return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(c.lo, p.lo)));
+}
+__host__ __device__ constexpr Two two_of(double x) { return Two{(float)x, (float)(x - (double)(float)x)}; }
+
+// cos and sin of 2 pi phase / 2^64, to about 2^-44: the phase less its nearest quarter turn, then the Taylor series in pairs
+// of fp32 numbers (its later terms in one), |y| <= pi / 4.  (64-bit floating point gives two results a clock and SM here; a
+// token's angles took 12 us of 8,191 tokens.)
+__device__ __forceinline__ void turn_of_two(unsigned long long phase, Two* cosine, Two* sine) {
   const unsigned long long quarter = (phase + (1ull << 61)) >> 62;
-  const double y = (double)(long long)(phase - (quarter << 62)) * 3.4061215800865545e-19, z = y * y;  // 2 pi / 2^64
-  double s = 1.0 / 355687428096000.0, c = 1.0 / 20922789888000.0;                              // 1 / 17!, 1 / 16!
-  s = fma(s, z, -1.0 / 1307674368000.0), c = fma(c, z, -1.0 / 87178291200.0);
-  s = fma(s, z, 1.0 / 6227020800.0), c = fma(c, z, 1.0 / 479001600.0);
-  s = fma(s, z, -1.0 / 39916800.0), c = fma(c, z, -1.0 / 3628800.0);
-  s = fma(s, z, 1.0 / 362880.0), c = fma(c, z, 1.0 / 40320.0);
-  s = fma(s, z, -1.0 / 5040.0), c = fma(c, z, -1.0 / 720.0);
-  s = fma(s, z, 1.0 / 120.0), c = fma(c, z, 1.0 / 24.0);
-  s = fma(s, z, -1.0 / 6.0), c = fma(c, z, -0.5);
-  s = fma(s, z * y, y), c = fma(c, z, 1.0);
-  const double2 swapped = quarter & 1ull ? make_double2(-s, c) : make_double2(c, s);
-  return quarter & 2ull ? make_double2(-swapped.x, -swapped.y) : swapped;
+  const long long rest = (long long)(phase - (quarter << 62));  // |rest| <= 2^61
+  const long long top = (rest + (1ll << 37)) >> 38;             // 24 bits, then the 38 below
+  constexpr Two kStep = two_of(6.283185307179586 / 67108864.0);  // 2 pi / 2^26: a unit of top
+  const Two y = times(Two{(float)(int)top, (float)(rest - (top << 38)) * 3.637978807091713e-12f}, kStep);  // 2^-38
+  const Two z = times(y, y);
+  constexpr Two s3 = two_of(-1.0 / 6.0), s5 = two_of(1.0 / 120.0), s7 = two_of(-1.0 / 5040.0);
+  constexpr Two c4 = two_of(1.0 / 24.0), c6 = two_of(-1.0 / 720.0), c8 = two_of(1.0 / 40320.0);
+  float s = fmaf(z.hi, (float)(1.0 / 6227020800.0), (float)(-1.0 / 39916800.0));
+  s = fmaf(z.hi, s, (float)(1.0 / 362880.0));
+  float c = fmaf(z.hi, (float)(-1.0 / 87178291200.0), (float)(1.0 / 479001600.0));
+  c = fmaf(z.hi, c, (float)(-1.0 / 3628800.0));
+  Two sp = plus_times(s7, z, Two{s, 0.f});
+  sp = plus_times(s3, z, plus_times(s5, z, sp));
+  Two cp = plus_times(c8, z, Two{c, 0.f});
+  cp = plus_times(Two{-0.5f, 0.f}, z, plus_times(c4, z, plus_times(c6, z, cp)));
+  const Two sn = plus_times(y, times(y, z), sp), cn = plus_times(Two{1.f, 0.f}, z, cp);
+  const Two a = quarter & 1ull ? Two{-sn.hi, -sn.lo} : cn, b = quarter & 1ull ? cn : sn;
+  *cosine = quarter & 2ull ? Two{-a.hi, -a.lo} : a, *sine = quarter & 2ull ? Two{-b.hi, -b.lo} : b;
 }
 
 // A row as its elements are formed in 64 bits.
@@ -110,9 +137,8 @@ template <typename T>
 struct Row64 {
   const T* x;
   const float* w;
-  const unsigned long long* steps;
-  int position, rd;
-  float mscale;
+  const float4* turns;  // of the token's pairs: cosines (hi, lo), then sines
+  int rd;
   template <bool kInter>
   __device__ __forceinline__ double u(int e) const {
     const double n = (double)to_f(x[e]) * (double)w[e];
@@ -120,39 +146,15 @@ struct Row64 {
     const int half = rd / 2, pair = kInter ? e / 2 : e < half ? e : e - half;
     const int mate = kInter ? e ^ 1 : e < half ? e + half : e - half;
     const bool second = kInter ? e & 1 : e >= half;
-    const double2 cs = turn_of_64(steps[pair] * (unsigned long long)(long long)position);
+    const float4 t = turns[pair];
+    const double2 cs = make_double2((double)t.x + (double)t.y, (double)t.z + (double)t.w);
     const double o = (double)to_f(x[mate]) * (double)w[mate];
-    return (double)mscale * (second ? fma(n, cs.x, o * cs.y) : fma(n, cs.x, -(o * cs.y)));
+    return second ? fma(n, cs.x, o * cs.y) : fma(n, cs.x, -(o * cs.y));
   }
 };
 
 __device__ __forceinline__ double shfl_xor_64(double x, int o) {
   return __hiloint2double(__shfl_xor_sync(0xFFFFFFFFu, __double2hiint(x), o), __shfl_xor_sync(0xFFFFFFFFu, __double2loint(x), o));
-}
-
-// A query's codes where some lie near a border: the elements of `near` (bits, from `at` on) again; those of `tops` may be
-// the row's largest.  All lanes together.
-template <typename T, bool kInter>
-__device__ __noinline__ uint2 codes_64(const Row64<T> row, int at, uint32_t near, uint32_t tops, uint2 codes) {
-  double top = 0.0;
-  for (uint32_t m = tops; m != 0; m &= m - 1) top = fmax(top, fabs(row.template u<kInter>(at + __ffs(m) - 1)));
-#pragma unroll
-  for (int o = 1; o < kLanesI; o <<= 1) top = fmax(top, shfl_xor_64(top, o));
-  for (; near != 0; near &= near - 1) {
-    const int e = __ffs(near) - 1;
-    const double u = row.template u<kInter>(at + e), v = 448.0 * fabs(u);
-    // from a code at or below the value, up while the middle to the next one is (halves to even)
-    uint32_t code = f32x2_to_e4m3x2(__double2float_rz(v / top) * (1.f - kSlack), 0.f) & 0x7Fu;
-    if (code > 0) --code;
-    for (; code < 0x7Eu; ++code) {
-      const double edge = 0.5 * ((double)e4m3_to_f32(code) + (double)e4m3_to_f32(code + 1)) * top;
-      if (!(v > edge || (v == edge && (code & 1u)))) break;
-    }
-    code |= u < 0.0 ? 0x80u : 0u;
-    uint32_t& word = e < 4 ? codes.x : codes.y;
-    word = (word & ~(0xFFu << (8 * (e & 3)))) | code << (8 * (e & 3));
-  }
-  return codes;
 }
 
 // A key's lane again: scale (in y) and codes (in x) of its 8 elements.  All lanes together.
@@ -185,6 +187,121 @@ __device__ __noinline__ uint2 key_64(const Row64<T> row, int at, bool normed, fl
   return make_uint2(codes, scale);
 }
 
+// What a lane knows of its piece of a row: factors, u = x c + x_p s, and where x_p is.
+struct Piece8 {
+  float2 c[4], s[4];
+};
+struct Place {
+  int at, angle, mate, partner;  // first element, pair and partner's first element; the lane that has it
+  bool turns, upper;
+};
+template <bool kInter>
+__device__ __forceinline__ Place place_of(int lane, int rd) {
+  Place p;
+  p.at = lane % kLanesI * 8;
+  // a pair's other half lies a whole number of pieces away (rotary_dim a multiple of 16, or of 8 with neighbours paired)
+  p.turns = p.at < rd, p.upper = !kInter && p.at >= rd / 2;
+  const int hop = p.turns && !kInter ? (p.upper ? -(rd / 16) : rd / 16) : 0;
+  p.partner = lane + hop, p.mate = p.at + 8 * hop, p.angle = kInter ? p.at / 2 : p.upper ? p.at - rd / 2 : p.at;
+  return p;
+}
+template <bool kInter>
+__device__ __forceinline__ Piece8 factors_of(const Place& p, const float* w, const float4* turns) {
+  Piece8 f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float w0 = w[p.at + 2 * e], w1 = w[p.at + 2 * e + 1];
+    if (p.turns && kInter) {
+      const float x = turns[p.angle + e].x, y = turns[p.angle + e].z;
+      f.c[e] = make_float2(x * w0, x * w1), f.s[e] = make_float2(-y * w1, y * w0);
+    } else if (p.turns) {
+      const float4 t0 = turns[p.angle + 2 * e], t1 = turns[p.angle + 2 * e + 1];
+      const float y0 = t0.z * w[p.mate + 2 * e], y1 = t1.z * w[p.mate + 2 * e + 1];
+      f.c[e] = make_float2(t0.x * w0, t1.x * w1);
+      f.s[e] = p.upper ? make_float2(y0, y1) : make_float2(-y0, -y1);
+    } else {
+      f.c[e] = make_float2(w0, w1), f.s[e] = make_float2(0.f, 0.f);
+    }
+  }
+  return f;
+}
+// u of a lane's elements and M, which their errors go by; returns the sum of squares of the elements.
+template <typename T, bool kInter>
+__device__ __forceinline__ float turn8(const Eight<T>& x, const Place& p, const Piece8& f, float2 (&u)[4], float2 (&mag)[4]) {
+  Eight<T> y;
+  if (!kInter) {
+#pragma unroll
+    for (int e = 0; e < Eight<T>::kN; ++e) y.w[e] = __shfl_sync(0xFFFFFFFFu, x.w[e], p.partner);
+  }
+  float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 one = Words<T>::get(x.w, e), two = kInter ? make_float2(one.y, one.x) : Words<T>::get(y.w, e);
+    const float2 part = mul2(two, f.s[e]);
+    u[e] = fma2(one, f.c[e], part);
+    const float2 own = fma2(part, make_float2(-1.f, -1.f), u[e]);  // x cw, but for a rounding of u
+    mag[e] = make_float2(fabsf(own.x) + fabsf(part.x), fabsf(own.y) + fabsf(part.y));
+    ss = fma2(one, one, ss);
+  }
+  return ss.x + ss.y;
+}
+__device__ __forceinline__ float largest8(const float2 (&u)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(u[e].x), fabsf(u[e].y)));
+  return m;
+}
+// Codes of both ends of where 448 u / top may lie: pairs of elements in 16 bits.
+__device__ __forceinline__ float inverse_of(float top) { return top > 7.9e-31f ? __fdividef(448.f, top) : 0.f; }
+__device__ __forceinline__ void both_ends(const float2 (&u)[4], const float2 (&mag)[4], float inv, uint32_t (&low)[4], uint32_t (&high)[4]) {
+  const float slack = inv * kSlack;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = mul2(u[e], make_float2(inv, inv));
+    const float2 l = fma2(mag[e], make_float2(-slack, -slack), v), t = fma2(mag[e], make_float2(slack, slack), v);
+    low[e] = f32x2_to_e4m3x2(l.x, l.y), high[e] = f32x2_to_e4m3x2(t.x, t.y);
+  }
+}
+
+// A query's row again, whose codes may not all be right: those that lie near a border in 64 bits.  Each half of the warp has
+// a row of its own; all lanes together.
+template <typename T, bool kInter, bool kWide>
+__device__ __noinline__ void again_64(const T* x, const float* w, const float4* turns, int rd, uint8_t* out, bool live) {
+  const Place p = place_of<kInter>(threadIdx.x & 31, rd);
+  float2 u[4], mag[4];
+  float ss = turn8<T, kInter>(load8<T, kWide>(x + p.at), p, factors_of<kInter>(p, w, turns), u, mag), most = largest8(u);
+#pragma unroll
+  for (int o = 1; o < kLanesI; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o), most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  uint32_t low[4], high[4], near = 0, tops = 0;
+  both_ends(u, mag, inverse_of(most), low, high);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if ((low[e / 2] ^ high[e / 2]) >> (8 * (e % 2)) & 0xFFu) near |= 1u << e;
+    if (fabsf(e % 2 ? u[e / 2].y : u[e / 2].x) >= most * (1.f - 4.f * kSlack)) tops |= 1u << e;
+  }
+  uint32_t codes[2] = {__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410)};
+  if (!(ss <= 3.4e38f) || !(most > 7.9e-31f)) live = false, near = tops = 0;  // (its codes stand)
+  const Row64<T> row{x, w, turns, rd};
+  double top = 0.0;
+  for (uint32_t m = tops; m != 0; m &= m - 1) top = fmax(top, fabs(row.template u<kInter>(p.at + __ffs(m) - 1)));
+#pragma unroll
+  for (int o = 1; o < kLanesI; o <<= 1) top = fmax(top, shfl_xor_64(top, o));
+  for (; near != 0; near &= near - 1) {
+    const int e = __ffs(near) - 1;
+    const double y = row.template u<kInter>(p.at + e), v = 448.0 * fabs(y);
+    // from a code at or below the value, up while the middle to the next one is (halves to even)
+    uint32_t code = f32x2_to_e4m3x2(__double2float_rz(v / top) * (1.f - kSlack), 0.f) & 0x7Fu;
+    if (code > 0) --code;
+    for (; code < 0x7Eu; ++code) {
+      const double edge = 0.5 * ((double)e4m3_to_f32(code) + (double)e4m3_to_f32(code + 1)) * top;
+      if (!(v > edge || (v == edge && (code & 1u)))) break;
+    }
+    code |= y < 0.0 ? 0x80u : 0u;
+    codes[e / 4] = (codes[e / 4] & ~(0xFFu << (8 * (e & 3)))) | code << (8 * (e & 3));
+  }
+  if (live) *reinterpret_cast<uint2*>(out + p.at) = make_uint2(codes[0], codes[1]);
+}
+
 // The request of token t: greatest r with cu[r] <= t, all lanes together.
 __device__ __forceinline__ int request_of(const int32_t* cu, int num_reqs, int t, int lane) {
   int lo = 0, hi = num_reqs;
@@ -198,26 +315,22 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int num_reqs, int t
 }
 
 template <typename T, bool kInter, bool kWide>
-__global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_constant__ IndexArgs a, int parts, int key_part) {
+__global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid_constant__ IndexArgs a, int parts, int key_part) {
   pdl_enter();
-  constexpr int kN = Eight<T>::kN;
-  __shared__ float angles[kThreadsI / 32][2][kHeadDim / 2];
+  __shared__ float4 turns_[kThreadsI / 32][kHeadDim / 2];  // cosines and sines of a warp's token, each in two numbers
   __shared__ unsigned long long steps[kHeadDim / 2];
   __shared__ float weights[2][kHeadDim];  // offset + w of queries and keys, 1 without
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rd = a.rotary_dim, half = rd / 2;
-  const int sub = lane / kLanesI, piece = lane % kLanesI, at = piece * 8;
+  const int rd = a.rotary_dim, half = rd / 2, sub = lane / kLanesI, piece = lane % kLanesI;
+  const Place p = place_of<kInter>(lane, rd);
+  const int at = p.at;
   for (int i = threadIdx.x; i < half; i += kThreadsI) steps[i] = step_of(a.inv_freq[i]);
   for (int i = threadIdx.x; i < kHeadDim; i += kThreadsI) {
     weights[0][i] = a.q_w != nullptr ? a.offset + to_f(static_cast<const T*>(a.q_w)[i]) : 1.f;
     weights[1][i] = a.k_w != nullptr ? a.offset + to_f(static_cast<const T*>(a.k_w)[i]) : 1.f;
   }
   __syncthreads();
-  float(*mine)[kHeadDim / 2] = angles[warp];
-  // a pair's other half lies a whole number of pieces away (rotary_dim a multiple of 16, or of 8 with neighbours paired)
-  const bool turns = at < rd, upper = !kInter && at >= half;
-  const int hop = turns && !kInter ? (upper ? -half / 8 : half / 8) : 0, partner = lane + hop;
-  const int angle = kInter ? at / 2 : upper ? at - half : at, mate = at + 8 * hop;
+  float4* mine = turns_[warp];
   const int rows = (a.heads + 1) / 2;
   const int all = parts + (key_part ? 1 : 0);
   const int64_t tasks = (int64_t)a.num_tokens * all;
@@ -226,54 +339,14 @@ __global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_cons
     const int position = a.positions[t];
     __syncwarp();  // the angles of the task before are used up
     for (int i = lane; i < half; i += 32) {
-      const float2 w = turn_of(position, steps[i], a.mscale);
-      mine[0][i] = w.x, mine[1][i] = w.y;
+      Two c, s;
+      turn_of_two(steps[i] * (unsigned long long)(long long)position, &c, &s);
+      c = times(c, Two{a.mscale, 0.f}), s = times(s, Two{a.mscale, 0.f});
+      mine[i] = make_float4(c.hi, c.lo, s.hi, s.lo);
     }
     __syncwarp();
-    float2 c[4], s[4];
-    auto factors = [&](const float* w) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float w0 = w[at + 2 * e], w1 = w[at + 2 * e + 1];
-        if (turns && kInter) {
-          const float x = mine[0][angle + e], y = mine[1][angle + e];
-          c[e] = make_float2(x * w0, x * w1), s[e] = make_float2(-y * w1, y * w0);
-        } else if (turns) {
-          const float y0 = mine[1][angle + 2 * e] * w[mate + 2 * e], y1 = mine[1][angle + 2 * e + 1] * w[mate + 2 * e + 1];
-          c[e] = make_float2(mine[0][angle + 2 * e] * w0, mine[0][angle + 2 * e + 1] * w1);
-          s[e] = upper ? make_float2(y0, y1) : make_float2(-y0, -y1);
-        } else {
-          c[e] = make_float2(w0, w1), s[e] = make_float2(0.f, 0.f);
-        }
-      }
-    };
-    // u of this lane's elements and what their errors go by, and the sum of squares of the row
-    auto turn = [&](const Eight<T>& x, float2 (&u)[4], float2 (&mag)[4]) {
-      Eight<T> y;
-      if (!kInter) {
-#pragma unroll
-        for (int e = 0; e < kN; ++e) y.w[e] = __shfl_sync(0xFFFFFFFFu, x.w[e], partner);
-      }
-      float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 one = Words<T>::get(x.w, e), two = kInter ? make_float2(one.y, one.x) : Words<T>::get(y.w, e);
-        const float2 part = mul2(two, s[e]);
-        u[e] = fma2(one, c[e], part);
-        mag[e] = make_float2(fabsf(u[e].x) + fabsf(part.x), fabsf(u[e].y) + fabsf(part.y));
-        ss = fma2(one, one, ss);
-      }
-      return ss.x + ss.y;
-    };
-    auto largest = [&](const float2 (&u)[4]) {
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(u[e].x), fabsf(u[e].y)));
-      return m;
-    };
-
     if (a.heads > 0 && part < parts) {
-      factors(weights[0]);
+      const Piece8 f = factors_of<kInter>(p, weights[0], mine);
       int64_t out = (int64_t)t * a.heads;  // the token's first row
       bool stored = true;
       if (a.cu != nullptr) {
@@ -284,20 +357,31 @@ __global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_cons
         out = ((int64_t)r * a.req_slots + slot) * a.heads;
       }
       const int r0 = rows * part / parts, r1 = rows * (part + 1) / parts;
-      const T* src = static_cast<const T*>(a.q) + (int64_t)t * a.q_ts + at;
+      const T* row0 = static_cast<const T*>(a.q) + (int64_t)t * a.q_ts;
       if (stored) {
+        uint64_t open = 0;  // steps whose codes lie near a border (at most 64 heads' worth: kMtpMaxHeads / 2)
+        Eight<T> ahead[kBatchI];
+        const T* src = row0 + (int64_t)(2 * r0 + sub) * a.q_hs + at;
+        uint8_t* dst = a.q_out + (out + 2 * r0 + sub) * kHeadDim + at;
+        const int64_t step = 2 * a.q_hs;
+        auto ask = [&](int g) {
+#pragma unroll
+          for (int b = 0; b < kBatchI; ++b) {
+            if (g + b < r1 && 2 * (g + b) + sub < a.heads) ahead[b] = load8<T, kWide>(src + b * step);
+            else ahead[b] = Eight<T>{};
+          }
+        };
+        ask(r0);
         for (int g = r0; g < r1; g += kBatchI) {
           Eight<T> x[kBatchI];
 #pragma unroll
-          for (int b = 0; b < kBatchI; ++b) {
-            const int h = 2 * (g + b) + sub;
-            if (g + b < r1 && h < a.heads) x[b] = load8<T, kWide>(src + h * a.q_hs);
-            else x[b] = Eight<T>{};
-          }
+          for (int b = 0; b < kBatchI; ++b) x[b] = ahead[b];
+          src += kBatchI * step;
+          if (g + kBatchI < r1) ask(g + kBatchI);
           float2 u[kBatchI][4], mag[kBatchI][4];
           float ss[kBatchI], top[kBatchI];
 #pragma unroll
-          for (int b = 0; b < kBatchI; ++b) ss[b] = turn(x[b], u[b], mag[b]), top[b] = largest(u[b]);
+          for (int b = 0; b < kBatchI; ++b) ss[b] = turn8<T, kInter>(x[b], p, f, u[b], mag[b]), top[b] = largest8(u[b]);
 #pragma unroll
           for (int o = 1; o < kLanesI; o <<= 1) {
 #pragma unroll
@@ -308,42 +392,35 @@ __global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_cons
           }
 #pragma unroll
           for (int b = 0; b < kBatchI; ++b) {
-            const int h = 2 * (g + b) + sub;
-            const bool live = g + b < r1 && h < a.heads, bad = !(ss[b] <= 3.4e38f);
-            const float inv = top[b] > 7.9e-31f ? 448.f / top[b] : 0.f, slack = inv * kSlack;
-            // both ends of where the values may lie
-            uint32_t low[2], high[2];
+            const float inv = inverse_of(top[b]);
+            uint32_t low[4], high[4];
+            both_ends(u[b], mag[b], inv, low, high);
+            const uint32_t differ = (low[0] ^ high[0]) | (low[1] ^ high[1]) | (low[2] ^ high[2]) | (low[3] ^ high[3]);
+            if (__any_sync(0xFFFFFFFFu, differ != 0)) open |= 1ull << (g + b - r0);
+            uint2 codes = make_uint2(__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410));
+            if (inv == 0.f) codes = make_uint2(0u, 0u);
+            if (!(ss[b] <= 3.4e38f)) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (g + b < r1 && 2 * (g + b) + sub < a.heads) *reinterpret_cast<uint2*>(dst + b * 2 * kHeadDim) = codes;
+          }
+          dst += kBatchI * 2 * kHeadDim;
+          // the scales: a lane each
+          if (piece < kBatchI) {
+            const int h = 2 * (g + piece) + sub;
+            float sq = ss[0], most = top[0];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 v = mul2(u[b][e], make_float2(inv, inv));
-              const float2 l = fma2(mag[b][e], make_float2(-slack, -slack), v), t = fma2(mag[b][e], make_float2(slack, slack), v);
-              const uint32_t lc = f32x2_to_e4m3x2(l.x, l.y), tc = f32x2_to_e4m3x2(t.x, t.y);
-              low[e / 2] = e % 2 ? low[e / 2] | lc << 16 : lc, high[e / 2] = e % 2 ? high[e / 2] | tc << 16 : tc;
-            }
-            uint2 codes = make_uint2(low[0], low[1]);
-            const bool open = live && !bad && inv != 0.f && ((low[0] ^ high[0]) | (low[1] ^ high[1])) != 0;
-            if (__any_sync(0xFFFFFFFFu, open)) {
-              uint32_t near = 0, tops = 0;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float m = e % 2 ? u[b][e / 2].y : u[b][e / 2].x;
-                if (open && ((low[e / 4] ^ high[e / 4]) >> (8 * (e % 4)) & 0xFFu)) near |= 1u << e;
-                if (live && !bad && fabsf(m) >= top[b] * (1.f - 4.f * kSlack)) tops |= 1u << e;
-              }
-              const Row64<T> row{static_cast<const T*>(a.q) + (int64_t)t * a.q_ts + min(h, a.heads - 1) * a.q_hs, weights[0], steps, position, rd, a.mscale};
-              codes = codes_64<T, kInter>(row, at, near, tops, codes);
-            }
-            if (!live) continue;
-            if (bad) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            if (inv == 0.f && !bad) codes = make_uint2(0u, 0u);
-            *reinterpret_cast<uint2*>(a.q_out + (out + h) * kHeadDim + at) = codes;
-            if (piece == 0) {
-              const float r = a.q_w != nullptr ? rsqrtf(fmaf(ss[b], 1.f / kHeadDim, a.eps)) : 1.f;
-              float f = top[b] * r * (1.f / 448.f) * a.scale;
-              if (a.head_weights != nullptr) f *= a.head_weights[(int64_t)t * a.heads + h];
-              a.q_scale[out + h] = bad ? __int_as_float(0x7FC00000) : f;
+            for (int b = 1; b < kBatchI; ++b)
+              if (piece == b) sq = ss[b], most = top[b];
+            if (g + piece < r1 && h < a.heads) {
+              const float r = a.q_w != nullptr ? rsqrtf(fmaf(sq, 1.f / kHeadDim, a.eps)) : 1.f;
+              float scale = most * r * (1.f / 448.f) * a.scale;
+              if (a.head_weights != nullptr) scale *= a.head_weights[(int64_t)t * a.heads + h];
+              a.q_scale[out + h] = sq <= 3.4e38f ? scale : __int_as_float(0x7FC00000);
             }
           }
+        }
+        for (; open != 0; open &= open - 1) {
+          const int h = 2 * (r0 + __ffsll(open) - 1) + sub;
+          again_64<T, kInter, kWide>(row0 + (int64_t)min(h, a.heads - 1) * a.q_hs, weights[0], mine, rd, a.q_out + (out + h) * kHeadDim, h < a.heads);
         }
       }
     }
@@ -351,13 +428,13 @@ __global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_cons
       const int64_t slot = a.slots != nullptr ? a.slots[t] : t;
       if (slot >= a.num_slots && lane == 0) report(a.status, IDX_ST_BLOCK_OOR);
       if (slot >= 0 && slot < a.num_slots) {
-        factors(weights[1]);
+        const Piece8 f = factors_of<kInter>(p, weights[1], mine);
         const T* src = static_cast<const T*>(a.k) + (int64_t)t * a.k_ts;
         float2 u[4], mag[4];
-        float ss = turn(load8<T, kWide>(src + at), u, mag);  // the same row in both halves
+        float ss = turn8<T, kInter>(load8<T, kWide>(src + at), p, f, u, mag);  // the same row in both halves
 #pragma unroll
         for (int o = 1; o < kLanesI; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        float top = largest(u), most = 0.f;
+        float top = largest8(u), most = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(mag[e].x, mag[e].y));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
@@ -378,7 +455,7 @@ __global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_cons
           open |= codes != high;
         }
         if (__any_sync(0xFFFFFFFFu, open && !bad)) {
-          const uint2 again = key_64<T, kInter>(Row64<T>{src, weights[1], steps, position, rd, a.mscale}, at, a.k_w != nullptr, a.eps);
+          const uint2 again = key_64<T, kInter>(Row64<T>{src, weights[1], mine, rd}, at, a.k_w != nullptr, a.eps);
           codes = again.x, scale = again.y;
         }
         if (bad) codes = 0, scale = 0x7Fu;
@@ -397,13 +474,16 @@ __global__ void __launch_bounds__(kThreadsI, 4) k_index_append(const __grid_cons
 template <typename T>
 void launch_index(const IndexArgs& a, bool inter, bool wide, cudaStream_t s) {
   const int sms = max(device_sms(), 1), rows = (a.heads + 1) / 2;
-  const int64_t room = (int64_t)sms * 32;
+  // Warps that run at once.  A token's heads in parts while there are not enough tokens, and where it evens out what a warp
+  // has to do: eight tasks each, of at least eight steps.
+  const int64_t room = (int64_t)sms * kCtasI * (kThreadsI / 32);
   const int most = max(1, (rows + kBatchI - 1) / kBatchI);
-  const int parts = a.heads == 0 ? 0 : (int)min((int64_t)most, max((int64_t)1, (room + a.num_tokens - 1) / a.num_tokens));
+  const int64_t want = (8 * room + a.num_tokens - 1) / a.num_tokens, fill = (room + a.num_tokens - 1) / a.num_tokens;
+  const int parts = a.heads == 0 ? 0 : (int)min((int64_t)most, max(fill, min(want, (int64_t)max(1, most / 8))));
   // the key is a task of its own while there is room: its row waits for no other
   const int key_part = a.k != nullptr && (parts == 0 || (int64_t)a.num_tokens * (parts + 1) <= room);
   const int64_t ctas = ((int64_t)a.num_tokens * (parts + key_part) + kThreadsI / 32 - 1) / (kThreadsI / 32);
-  const dim3 grid((unsigned)min(ctas, (int64_t)sms * 8)), block(kThreadsI);
+  const dim3 grid((unsigned)min(ctas, (int64_t)sms * kCtasI)), block(kThreadsI);
   if (inter) {
     if (wide) launch_pdl(k_index_append<T, true, true>, grid, block, 0, s, a, parts, key_part);
     else launch_pdl(k_index_append<T, true, false>, grid, block, 0, s, a, parts, key_part);

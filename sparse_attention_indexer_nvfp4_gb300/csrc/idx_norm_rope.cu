@@ -21,9 +21,10 @@
 namespace idx {
 namespace {
 
-constexpr int kThreadsN = 256;
+constexpr int kThreadsN = 128;
 constexpr int kMaxDimN = 512;
-constexpr int kBatchN = 4;  // rows in flight a lane
+constexpr int kBatchN = 2;  // rows in flight a lane
+constexpr int kCtasN = 6;   // of an SM
 
 struct NormArgs {
   const void* q;
@@ -55,13 +56,22 @@ __device__ __forceinline__ void norm_rows(const T* src, int64_t src_step, T* dst
                                           int partner, bool turns, const NormArgs& a, const Factors<V>& f) {
   constexpr int kN = (int)sizeof(T) * V / 4;
   using R = Row<kN>;
+  R ahead[kBatchN];
+  auto ask = [&](int g) {  // the batch from row g on; src and left are at it
+#pragma unroll
+    for (int u = 0; u < kBatchN; ++u) {
+      if (g + u < rows && left > u * per_warp) ahead[u] = *reinterpret_cast<const R*>(src + u * src_step);
+      else ahead[u] = R{};
+    }
+  };
+  ask(0);
   for (int g = 0; g < rows; g += kBatchN) {
     R x[kBatchN];
 #pragma unroll
-    for (int u = 0; u < kBatchN; ++u) {
-      if (g + u < rows && left > u * per_warp) x[u] = *reinterpret_cast<const R*>(src + u * src_step);
-      else x[u] = R{};
-    }
+    for (int u = 0; u < kBatchN; ++u) x[u] = ahead[u];
+    const int here = left;
+    src += kBatchN * src_step, left -= kBatchN * per_warp;
+    if (g + kBatchN < rows) ask(g + kBatchN);
     float r[kBatchN];
 #pragma unroll
     for (int u = 0; u < kBatchN; ++u) r[u] = 1.f;
@@ -99,9 +109,9 @@ __device__ __forceinline__ void norm_rows(const T* src, int64_t src_step, T* dst
       }
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) Words<T>::put(x[u].w, e, z[e], kNorm || turns);  // without a norm the other elements pass as they are
-      if (g + u < rows && left > u * per_warp) *reinterpret_cast<R*>(dst + u * dst_step) = x[u];
+      if (g + u < rows && here > u * per_warp) *reinterpret_cast<R*>(dst + u * dst_step) = x[u];
     }
-    src += kBatchN * src_step, dst += kBatchN * dst_step, left -= kBatchN * per_warp;
+    dst += kBatchN * dst_step;
   }
 }
 
@@ -122,7 +132,7 @@ __device__ __forceinline__ void copy_rows(const T* src, int64_t src_step, T* dst
 }
 
 template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreadsN, 3) k_norm_rows(const __grid_constant__ NormArgs a, int parts, int group) {
+__global__ void __launch_bounds__(kThreadsN, kCtasN) k_norm_rows(const __grid_constant__ NormArgs a, int parts, int group) {
   pdl_enter();
   __shared__ float angles[kThreadsN / 32][2][kMaxDimN / 2];
   __shared__ unsigned long long steps[kMaxDimN / 2];
@@ -259,9 +269,9 @@ void launch_rows(const NormArgs& a, bool inter, cudaStream_t s) {
   // parts of a token's heads while they keep a batch of rows and the SMs have room for their warps
   const int per_warp = 32 / group, rows = (a.q_heads + per_warp - 1) / per_warp;
   const int most = max(1, (rows + kBatchN - 1) / kBatchN);
-  const int parts = (int)min((int64_t)most, max((int64_t)1, ((int64_t)sms * 24 + a.num_tokens - 1) / a.num_tokens));
+  const int parts = (int)min((int64_t)most, max((int64_t)1, ((int64_t)sms * kCtasN * (kThreadsN / 32) + a.num_tokens - 1) / a.num_tokens));
   const int64_t ctas = ((int64_t)a.num_tokens * parts + kThreadsN / 32 - 1) / (kThreadsN / 32);
-  const unsigned grid = (unsigned)min(ctas, (int64_t)sms * 6);
+  const unsigned grid = (unsigned)min(ctas, (int64_t)sms * kCtasN);
   if (inter) launch_pdl(k_norm_rows<T, V, true>, dim3(grid), dim3(kThreadsN), 0, s, a, parts, group);
   else launch_pdl(k_norm_rows<T, V, false>, dim3(grid), dim3(kThreadsN), 0, s, a, parts, group);
 }
@@ -276,7 +286,7 @@ void launch_norm(const NormArgs& a, int v, bool inter, cudaStream_t s) {
     return;
   }
   const int64_t ctas = ((int64_t)a.num_tokens * (a.q_heads + a.kv_heads) + kThreadsN / 32 - 1) / (kThreadsN / 32);
-  const unsigned grid = (unsigned)min(ctas, (int64_t)max(device_sms(), 1) * 8);
+  const unsigned grid = (unsigned)min(ctas, (int64_t)max(device_sms(), 1) * 16);
   if (inter) launch_pdl(k_norm_any<T, true>, dim3(grid), dim3(kThreadsN), 0, s, a);
   else launch_pdl(k_norm_any<T, false>, dim3(grid), dim3(kThreadsN), 0, s, a);
 }

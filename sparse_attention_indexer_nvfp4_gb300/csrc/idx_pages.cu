@@ -28,11 +28,13 @@ namespace idx {
 namespace {
 
 constexpr int kThreadsC = 256;
-constexpr int kMoveS = 8;      // rows in flight a thread
+constexpr int kThreadsM = 128;  // of k_settle
+constexpr int kMoveS = 4;      // rows in flight a thread
 constexpr int kStageS = 64;    // nodes of a path looked up together
-constexpr int kUnrollF = 4;    // pieces in flight a thread
+constexpr int kPartsF = 16;    // CTAs a page of a plane, at most
 constexpr int kThreadsU = 1024;
-constexpr int kClusterU = 8;
+constexpr int kClusterU = 16;
+constexpr int kUnrollU = 16;   // words of refs in flight a warp
 
 struct Cache {
   char* base;
@@ -70,7 +72,7 @@ struct SettleArgs {
   int32_t* status;
 };
 
-__global__ void __launch_bounds__(kThreadsC) k_settle(const __grid_constant__ SettleArgs a, const __grid_constant__ Caches cs) {
+__global__ void __launch_bounds__(kThreadsM) k_settle(const __grid_constant__ SettleArgs a, const __grid_constant__ Caches cs) {
   pdl_enter();
   __shared__ int from_block[kStageS], from_tok[kStageS], to_block[kStageS], to_tok[kStageS];
   const int r = blockIdx.y, tid = threadIdx.x;
@@ -79,13 +81,13 @@ __global__ void __launch_bounds__(kThreadsC) k_settle(const __grid_constant__ Se
   if (blockIdx.x == 0) {
     if (tid == 0) a.ctx_out[r] = a.ctx[r] + (n > 0 ? 1 + stands : 0);
     if (a.counts != nullptr && n > 0)
-      for (int i = tid; i <= stands; i += kThreadsC) {
+      for (int i = tid; i <= stands; i += kThreadsM) {
         const int x = a.out_tokens[(int64_t)r * a.max_out + i];
         if (x >= 0 && x < a.vocab) atomicAdd(a.counts + (int64_t)r * a.counts_stride + x, 1);
       }
   }
   // this thread's piece of a row
-  int64_t at = (int64_t)blockIdx.x * kThreadsC + tid;
+  int64_t at = (int64_t)blockIdx.x * kThreadsM + tid;
   int c = 0;
   while (c < cs.num && at >= (int64_t)cs.c[c].planes * cs.c[c].pieces) at -= (int64_t)cs.c[c].planes * cs.c[c].pieces, ++c;
   const bool live = c < cs.num;
@@ -139,6 +141,7 @@ struct ForkArgs {
   const int32_t* cursor;
   int32_t* cursor_out;
   int32_t* status;
+  int32_t parts;
 };
 
 __global__ void __launch_bounds__(kThreadsC) k_fork(const __grid_constant__ ForkArgs a, const __grid_constant__ Caches cs) {
@@ -226,7 +229,8 @@ __global__ void __launch_bounds__(kThreadsC) k_fork(const __grid_constant__ Fork
     if (first && tid == 0) report(a.status, IDX_ST_BLOCK_OOR);
     return;
   }
-  for (int plane = blockIdx.x; plane < cs.planes; plane += gridDim.x) {
+  const int part = blockIdx.x % a.parts;
+  for (int plane = blockIdx.x / a.parts; plane < cs.planes; plane += gridDim.x / a.parts) {
     int ci = 0, pl = plane;
     while (pl >= cs.c[ci].planes) pl -= cs.c[ci].planes, ++ci;
     const Cache& k = cs.c[ci];
@@ -236,21 +240,11 @@ __global__ void __launch_bounds__(kThreadsC) k_fork(const __grid_constant__ Fork
       using P = decltype(one);
       const uint32_t pieces = (uint32_t)k.pieces, total = (uint32_t)rest * pieces;  // a page's rows of a plane stay below 4 GB
       const bool dense = k.token_stride == k.row_bytes;
-      for (uint32_t i = tid; i < total; i += kThreadsC * kUnrollF) {
-        P x[kUnrollF];
-        int64_t off[kUnrollF];
-#pragma unroll
-        for (int u = 0; u < kUnrollF; ++u) {
-          const uint32_t g = i + u * kThreadsC;
-          if (g < total) {
-            const uint32_t tok = dense ? 0 : g / pieces;
-            off[u] = tok * k.token_stride + (int64_t)(g - tok * pieces) * sizeof(P);
-            x[u] = *reinterpret_cast<const P*>(src + off[u]);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kUnrollF; ++u)
-          if (i + u * kThreadsC < total) *reinterpret_cast<P*>(dst + off[u]) = x[u];
+      // (one piece a thread and turn: two took 105 us for 64 forks over 48 layers, four 140)
+      for (int64_t i = part * kThreadsC + tid; i < total; i += a.parts * kThreadsC) {
+        const uint32_t tok = dense ? 0u : (uint32_t)i / pieces;
+        const int64_t off = tok * k.token_stride + (i - (int64_t)tok * pieces) * (int64_t)sizeof(P);
+        *reinterpret_cast<P*>(dst + off) = *reinterpret_cast<const P*>(src + off);
       }
     });
   }
@@ -292,16 +286,19 @@ __global__ void __launch_bounds__(kThreadsU) k_push(const __grid_constant__ Rele
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // stretches of whole 128s, one a warp of the cluster
-  const int64_t quads = (a.num_blocks + 127) / 128, w = (int64_t)rank * (kThreadsU / 32) + warp, warps = kClusterU * (kThreadsU / 32);
-  const int64_t lo = quads * w / warps * 128, hi = min(quads * (w + 1) / warps * 128, a.num_blocks);
+  // stretches of whole words of 32, one a warp of the cluster, kUnrollU words in flight
+  const int64_t all_words = (a.num_blocks + 31) / 32, w = (int64_t)rank * (kThreadsU / 32) + warp, warps = kClusterU * (kThreadsU / 32);
+  const int64_t lo = all_words * w / warps * 32, hi = min(all_words * (w + 1) / warps * 32, a.num_blocks);
+  auto load = [&](int64_t b, int (&v)[kUnrollU]) {
+#pragma unroll
+    for (int e = 0; e < kUnrollU; ++e) v[e] = b + 32 * e + lane < hi ? a.refs[b + 32 * e + lane] : 0;
+  };
   int mine = 0;
-  for (int64_t b = lo; b < hi; b += 128) {
-    int v[4];
+  for (int64_t b = lo; b < hi; b += 32 * kUnrollU) {
+    int v[kUnrollU];
+    load(b, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = b + 32 * e + lane < hi ? a.refs[b + 32 * e + lane] : 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) mine += v[e] < 0;
+    for (int e = 0; e < kUnrollU; ++e) mine += v[e] < 0;
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
@@ -332,12 +329,11 @@ __global__ void __launch_bounds__(kThreadsU) k_push(const __grid_constant__ Rele
     if (begin < 0) report(a.status, IDX_ST_BAD_OUTPUT);
   }
   at += begin;
-  for (int64_t b = lo; b < hi; b += 128) {
-    int v[4];
+  for (int64_t b = lo; b < hi; b += 32 * kUnrollU) {
+    int v[kUnrollU];
+    load(b, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = b + 32 * e + lane < hi ? a.refs[b + 32 * e + lane] : 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kUnrollU; ++e) {
       const uint32_t gone = __ballot_sync(0xFFFFFFFFu, v[e] < 0);
       const int64_t to = at + __popc(gone & ((1u << lane) - 1u));
       if (v[e] < 0) {
@@ -396,11 +392,11 @@ extern "C" int idx_settle_drafts(const idx_cache* caches, int32_t num_caches, in
                         (const void*)ctx_out, (const void*)counts, (const void*)status})
     if (!aligned(p, 4)) return IDX_E_MISALIGNED;
   if (!aligned(slots, 8)) return IDX_E_MISALIGNED;
-  const int64_t ctas = (cs.per_token + kThreadsC - 1) / kThreadsC;
+  const int64_t ctas = (cs.per_token + kThreadsM - 1) / kThreadsM;
   if (ctas > 0x7FFFFFFF) return IDX_E_TOO_LARGE;
   if ((rc = check_device()) != IDX_OK) return rc;
   const SettleArgs a{slots, cu_tokens, out_tokens, out_nodes, num_accepted, ctx_lens, num_reqs, num_tokens, max_out, ctx_out, counts, counts_stride, vocab, status};
-  launch_pdl(k_settle, dim3((unsigned)(ctas > 0 ? ctas : 1), (unsigned)num_reqs), dim3(kThreadsC), 0, (cudaStream_t)stream, a, cs);
+  launch_pdl(k_settle, dim3((unsigned)(ctas > 0 ? ctas : 1), (unsigned)num_reqs), dim3(kThreadsM), 0, (cudaStream_t)stream, a, cs);
   return launch_result();
 }
 
@@ -422,10 +418,13 @@ extern "C" int idx_fork_pages(const idx_cache* caches, int32_t num_caches, int64
                         (const void*)refs, (const void*)free_blocks, (const void*)free_cursor, (const void*)cursor_out, (const void*)status})
     if (!aligned(p, 4)) return IDX_E_MISALIGNED;
   if ((rc = check_device()) != IDX_OK) return rc;
+  // a page of a plane for several CTAs while that leaves SMs without any
+  const int sms = max(device_sms(), 1), planes = max(cs.planes, 1);
+  const int parts = (int)max((int64_t)1, min((int64_t)kPartsF, (int64_t)sms * 4 / ((int64_t)planes * num_forks)));
   const ForkArgs a{parents, children, num_forks, num_reqs, ctx_lens, owned_pages, block_table, bt_stride, max_blocks, refs, free_blocks, num_free,
-                   free_cursor, cursor_out, status};
+                   free_cursor, cursor_out, status, parts};
   const size_t smem = (size_t)((num_reqs + 31) / 32) * 8;
-  const int x = (int)min((int64_t)max(cs.planes, 1), max((int64_t)1, (int64_t)max(device_sms(), 1) * 64 / num_forks));
+  const int x = parts * (int)min((int64_t)planes, max((int64_t)1, (int64_t)sms * 64 / num_forks));
   launch_pdl(k_fork, dim3((unsigned)x, (unsigned)num_forks), dim3(kThreadsC), smem, (cudaStream_t)stream, a, cs);
   return launch_result();
 }
@@ -464,6 +463,7 @@ extern "C" int idx_release_pages(const int32_t* keep_lens, const int32_t* owned_
   attr[1].val.clusterDim.x = kClusterU, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  cudaFuncSetAttribute(k_push, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   cudaLaunchKernelEx(&cfg, k_push, a);
   return launch_result();
 }
