@@ -83,8 +83,9 @@ const char* idx_strerror(int code);
 int idx_have_qmul4(void);
 
 /*
- * Wait budget of the tensor-core kernels (the decode scorer, the
- * multi-token scorer and the tree attention).  Their warp roles hand pages to one another through
+ * Wait budget of the kernels that copy ahead of their work (the decode
+ * scorer, the multi-token scorer, the tree attention and idx_logit_probs, which
+ * waits for its rows).  The tensor-core kernels' warp roles hand pages to one another through
  * shared-memory barriers; every such wait gives up after `polls` suspended
  * polls of at most ~20 us each (spinning roles: polls * 1024 spins), records
  * IDX_ST_TIMEOUT in the status word, and the CTA winds down: it stops taking
@@ -817,7 +818,7 @@ int idx_settle_drafts(const idx_cache* caches, int32_t num_caches, int64_t num_b
  * not made (IDX_ST_NO_BLOCKS): its child gets length and pages 0.  A fork whose
  * child is a parent in the same call, or the child of another fork, or that has
  * a request outside [0, num_reqs), is not made and changes nothing
- * (IDX_ST_BAD_FORK).  What a child owned before is not released.  Table
+ * (IDX_ST_BAD_FORK); one with child -1 is none (a captured call's empty places).  What a child owned before is not released.  Table
  * entries outside [0, num_blocks) are passed on, not counted, and not copied
  * from (IDX_ST_BLOCK_OOR).
  *

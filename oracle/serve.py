@@ -147,6 +147,8 @@ def fork(caches, parents, children, ctx, owned, table, refs, free, cursor, page,
     old = (ctx.copy(), owned.copy(), table.copy())
     for f in range(len(parents)):
         p, c = parents[f], children[f]
+        if c == -1:
+            continue
         if not (0 <= p < reqs and 0 <= c < reqs) or c in parents or list(children).count(c) > 1:
             status |= 64
             continue

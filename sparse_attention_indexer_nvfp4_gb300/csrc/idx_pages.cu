@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kThreadsC) k_fork(const __grid_constant__ Fork
   // tokens of fork j; -1: it is not made
   auto length = [&](int j, int& report_bits) {
     const int c = a.children[j], p = a.parents[j];
+    if (c == -1) return -1;  // none
     if (c < 0 || c >= a.num_reqs || p < 0 || p >= a.num_reqs || (bad[c >> 5] >> (c & 31) & 1u)) {
       report_bits |= IDX_ST_BAD_FORK;
       return -1;
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kThreadsC) k_fork(const __grid_constant__ Fork
     if (tid == 0) *a.cursor_out = (int)min((int64_t)cursor + all, (int64_t)a.num_free);
     if (said) report(a.status, said);
   }
+  if (fork >= a.num_forks) return;
   int none = 0;
   const int len = length(fork, none);
   if (len < 0) return;
@@ -410,8 +412,7 @@ extern "C" int idx_fork_pages(const idx_cache* caches, int32_t num_caches, int64
   Caches cs{};
   int rc = take_caches(caches, num_caches, num_blocks, page_tokens, &cs);
   if (rc != IDX_OK) return rc;
-  if (num_forks == 0) return IDX_OK;
-  if (!parents || !children || !free_cursor || !cursor_out || (num_free > 0 && !free_blocks)) return IDX_E_NULL_PTR;
+  if ((num_forks > 0 && (!parents || !children)) || !free_cursor || !cursor_out || (num_free > 0 && !free_blocks)) return IDX_E_NULL_PTR;
   if (num_reqs > 0 && (!ctx_lens || !owned_pages || (max_blocks > 0 && !block_table) || (num_blocks > 0 && !refs))) return IDX_E_NULL_PTR;
   if (free_cursor == cursor_out) return IDX_E_BAD_SHAPE;
   for (const void* p : {(const void*)parents, (const void*)children, (const void*)ctx_lens, (const void*)owned_pages, (const void*)block_table,
@@ -420,12 +421,12 @@ extern "C" int idx_fork_pages(const idx_cache* caches, int32_t num_caches, int64
   if ((rc = check_device()) != IDX_OK) return rc;
   // a page of a plane for several CTAs while that leaves SMs without any
   const int sms = max(device_sms(), 1), planes = max(cs.planes, 1);
-  const int parts = (int)max((int64_t)1, min((int64_t)kPartsF, (int64_t)sms * 4 / ((int64_t)planes * num_forks)));
+  const int parts = (int)max((int64_t)1, min((int64_t)kPartsF, (int64_t)sms * 4 / ((int64_t)planes * max(num_forks, 1))));
   const ForkArgs a{parents, children, num_forks, num_reqs, ctx_lens, owned_pages, block_table, bt_stride, max_blocks, refs, free_blocks, num_free,
                    free_cursor, cursor_out, status, parts};
   const size_t smem = (size_t)((num_reqs + 31) / 32) * 8;
-  const int x = parts * (int)min((int64_t)planes, max((int64_t)1, (int64_t)sms * 64 / num_forks));
-  launch_pdl(k_fork, dim3((unsigned)x, (unsigned)num_forks), dim3(kThreadsC), smem, (cudaStream_t)stream, a, cs);
+  const int x = parts * (int)min((int64_t)planes, max((int64_t)1, (int64_t)sms * 64 / max(num_forks, 1)));
+  launch_pdl(k_fork, dim3((unsigned)x, (unsigned)max(num_forks, 1)), dim3(kThreadsC), smem, (cudaStream_t)stream, a, cs);
   return launch_result();
 }
 

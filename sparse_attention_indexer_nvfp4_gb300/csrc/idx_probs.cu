@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   uint32_t* skip = special + a.slice / 32 + 2;  // entries that the main pass leaves out, those around the stretch among them
   __shared__ uint64_t full[2];
   __shared__ int tokens[kPathP + 1];   // of the request: node j's at j
-  __shared__ uint64_t masks[kTreeP];   // of its nodes
+  __shared__ uint64_t masks[kTreeP];   // of its first nodes
   __shared__ int path_of_tree[kTreeP];
   __shared__ uint16_t list[kListP];  // the special entries; kBiased: some bias is theirs
   __shared__ int warp_count[kWarpsP];
@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   auto row_of = [&](int t) { return logits + (int64_t)t * a.l_stride + lo; };
   auto shift_of = [&](const T* row) { return (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) % kV); };
   auto vectors_of = [&](int shift) { return n_here > 0 ? (n_here + shift + kV - 1) / kV : 0; };
+  int asked = t_lo - 1;  // thread 0's last; after a wait that ran out it asks for none, so a buffer has one copy at most
   auto buffer_of = [&](int t) { return a.buffers == 2 ? (t - t_lo) & 1 : 0; };
   // Thread 0 asks for a row, as whole vectors at their aligned addresses, whatever else is in them; the tensor's first and last
   // vectors may not be whole and are left out.
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
     const int first = vectors > 0 && row - shift < logits ? 1 : 0, last = vectors > 0 && row - shift + vectors * kV > logits_end ? vectors - 1 : vectors;
     uint64_t* bar = &full[buffer_of(t)];
     const uint32_t bytes = (uint32_t)max(0, last - first) * 16u;
+    asked = t;
     mbar_arrive_expect_tx(bar, bytes);
     if (bytes > 0) bulk_g2s(reinterpret_cast<T*>(store) + (size_t)buffer_of(t) * stretch + first * kV, row - shift + first * kV, bytes, bar);
   };
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
     T* xs = reinterpret_cast<T*>(store) + (size_t)buffer_of(t) * stretch;
     const bool next = t + 1 < t_hi;
     // (the row before, which was in the other buffer, is used up)
-    if (next && a.buffers == 2 && tid == 0) ask(t + 1);
+    if (next && a.buffers == 2 && tid == 0 && !timed_out) ask(t + 1);
     auto arrived = [&] {
       const uint32_t phase = (uint32_t)(a.buffers == 2 ? (t - t_lo) >> 1 : t - t_lo) & 1u;
       uint64_t* bar = &full[buffer_of(t)];
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
     auto used_up = [&] {
       fence_proxy_async_smem();
       __syncthreads();
-      if (next && a.buffers == 1 && tid == 0) ask(t + 1);
+      if (next && a.buffers == 1 && tid == 0 && !timed_out) ask(t + 1);
     };
     if (!known || t < begin || t >= end) {
       // the row's request
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       if (a.tokens == nullptr) return;
       const int node = t - begin;
       if (a.mask != nullptr) {
-        uint64_t m = node < kTreeP ? masks[node] & ~1ull : 0ull;
+        uint64_t m = (node < kTreeP ? masks[node] : a.mask[begin + node]) & ~1ull;
         if (end - begin < kTreeP) m &= (1ull << (end - begin)) - 1ull;
         n_path = __popcll(m);
         if (tid < kTreeP && (m >> tid & 1)) path_of_tree[__popcll(m & ((1ull << tid) - 1ull))] = tokens[tid];
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
     report(a.status, IDX_ST_TIMEOUT);
     // no copy may come after the CTA is gone
     if (tid == 0)
-      for (int t = max(t_lo, t_hi - a.buffers); t < t_hi; ++t)
+      for (int t = max(t_lo, asked + 1 - a.buffers); t <= asked; ++t)
         mbar_wait(&full[buffer_of(t)], (uint32_t)(a.buffers == 2 ? (t - t_lo) >> 1 : t - t_lo) & 1u, nullptr);
   }
   if (bad_tree && tid == 0) report(a.status, IDX_ST_BAD_TREE);

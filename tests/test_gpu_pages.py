@@ -226,6 +226,13 @@ def test_forks_that_are_refused(lib):
         Pool([5, 6, 7], reqs=6).fork(lib, parents, children, status=lib.ST_BAD_FORK)
 
 
+def test_forks_that_are_none(lib):
+    """Empty places of a call, and a call of none: the cursor is passed on."""
+    Pool([5, 6, 7], reqs=6).fork(lib, [0, 7, 2], [3, -1, 5])
+    Pool([5, 6, 7], reqs=6).fork(lib, [0], [-1])
+    Pool([5, 6, 7], reqs=6).fork(lib, np.zeros(0, dtype=np.int32), np.zeros(0, dtype=np.int32))
+
+
 def test_fork_of_bad_tables(lib):
     p = Pool([9, 6])
     p.table[0, 1], p.table[1, 1] = -1, 10**6

@@ -152,6 +152,30 @@ def test_trees(lib):
     c.check(lib)
 
 
+def test_trees_of_more_nodes_than_a_mask_has_bits(lib):
+    """Nodes from 64 on have the mask that is given, over the first 64."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    masks = torch.randint(-(2**62), 2**62, (150,), device="cuda", generator=g)
+    masks[70:75] = 0
+    Case([0, 75, 150], 130, tree=masks).check(lib)
+
+
+def test_waits_that_run_out(lib):
+    """With a budget of 0 a row that is not there yet is given up; the call returns, and the next one is right."""
+    c = Case([0, 40, 80], 30_001, grammar=True)
+    want = c.run(lib).probs.clone()
+    before = lib.idx_set_wait_limit(0)
+    try:
+        c.run(lib)
+        torch.cuda.synchronize()
+    finally:
+        lib.idx_set_wait_limit(before)
+    assert c.status.item() in (0, lib.ST_TIMEOUT)
+    c.status.zero_()
+    assert torch.equal(c.run(lib).probs, want) and c.status.item() == 0
+
+
 def test_long_chains(lib):
     Case([0, 300], 1000).check(lib)
     c = Case([0, 1027], 64)

@@ -85,7 +85,7 @@ def test_fork_pages(lib):
     refuse(lib.load_library().idx_fork_pages, good, [(0, c, want) for c, want in BAD_CACHES] + [
         (6, -1, E_SHAPE), (6, 4097, E_LARGE), (9, -1, E_SHAPE), (9, 65536, E_LARGE), (11, 9, E_SHAPE), (12, -1, E_SHAPE), (15, -1, E_SHAPE),
         (17, A, E_SHAPE), (4, None, E_NULL), (5, None, E_NULL), (7, None, E_NULL), (8, None, E_NULL), (10, None, E_NULL), (13, None, E_NULL),
-        (14, None, E_NULL), (16, None, E_NULL), (17, None, E_NULL), (13, A + 2, E_MIS), (6, 0, 0)])
+        (14, None, E_NULL), (16, None, E_NULL), (17, None, E_NULL), (13, A + 2, E_MIS)])
 
 
 def test_release_pages(lib):
