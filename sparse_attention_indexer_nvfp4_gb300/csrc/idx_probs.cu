@@ -29,7 +29,7 @@ constexpr int kClusterP = 8;
 constexpr int kPathP = IDX_VERIFY_MAX_NODES;
 constexpr int kTreeP = 64;    // bits of a tree's mask
 constexpr int kMaskP = IDX_PROBS_MAX_VOCAB / kClusterP / 32 / kThreadsP;  // words of bits a thread
-constexpr int kCountP = 8;    // counts in flight a thread
+constexpr int kCountP = 10;   // fours of counts in flight a thread
 constexpr int kFixP = 4;      // changed entries a thread takes at a time
 constexpr int kListP = kFixP * kThreadsP;
 constexpr size_t kRoomP = 104 * 1024;  // dynamic shared memory of each of two CTAs an SM (which has 228 KB)
@@ -75,6 +75,10 @@ __device__ __forceinline__ void sync_cluster() {
 }
 __device__ __forceinline__ void put_cluster(void* p, uint32_t rank, unsigned long long v) {
   asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u64 [a], %2;\n\t}" ::"r"(smem_u32(p)), "r"(rank), "l"(v)
+               : "memory");
+}
+__device__ __forceinline__ void put_cluster_32(void* p, uint32_t rank, uint32_t v) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(smem_u32(p)), "r"(rank), "r"(v)
                : "memory");
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -176,8 +180,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   __shared__ uint16_t list[kListP];  // the special entries; kBiased: some bias is theirs
   __shared__ int warp_count[kWarpsP];
   __shared__ unsigned long long parts[2][kClusterP * kWarpsP];  // maximum and sum of each warp of the cluster
-  __shared__ unsigned long long cta_first[2][kClusterP];
-  __shared__ int first_s;
+  __shared__ int part_at[2][kClusterP * kWarpsP];  // the lowest entry of that maximum (rows of temperature 0)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cta_rank(), cs = (int)cta_count();
   const int lo = min(a.vocab, rank * a.slice), n_here = min(a.vocab, lo + a.slice) - lo, here = (n_here + 31) / 32;
@@ -241,18 +244,24 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   };
   // counts and biases of this thread's entries of the list
   auto look_up = [&](int first) {
+    int found = 0, i[kFixP];
+    bool biased = false;
 #pragma unroll
     for (int u = 0; u < kFixP; ++u) {
       const int at = tid + u * kThreadsP;
-      fix_c[u] = 0, fix_b[u] = 0.f;
+      fix_c[u] = 0, fix_b[u] = 0.f, i[u] = -1;
       if (first + at >= changed) continue;
-      const int i = list[at] & ~kBiased;
-      if (counts != nullptr) fix_c[u] = counts[i];
-      if (list[at] & kBiased) {
-        int found = 0;
+      const int e = list[at];
+      if (counts != nullptr) fix_c[u] = counts[e & ~kBiased];
+      if (e & kBiased) biased = true, i[u] = lo + (e & ~kBiased);
+    }
+    if (biased) {
 #pragma unroll 8
-        for (int b = b0; b < b1; ++b)
-          if (a.bias_tokens[b] == lo + i) fix_b[u] = found++ == 0 ? a.bias_values[b] : __int_as_float(0x7FC00000);
+      for (int b = b0; b < b1; ++b) {
+        const int v = a.bias_tokens[b];
+#pragma unroll
+        for (int u = 0; u < kFixP; ++u)
+          if (v == i[u]) fix_b[u] = (found >> u & 1) == 0 ? a.bias_values[b] : __int_as_float(0x7FC00000), found |= 1 << u;  // NaN: several
       }
     }
   };
@@ -324,6 +333,12 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
         if (a.bias_cu != nullptr) b0 = max(0, a.bias_cu[r]), b1 = min(a.num_bias, a.bias_cu[r + 1]);
         for (int w = tid; w < here; w += kThreadsP) special[w] = 0, skip[w] = 0;
         __syncthreads();
+        if (counts != nullptr && tid == 0 && end < t_hi && r + 1 < a.num_reqs && n_here > 0) {
+          // the next request's counts into L2 (whole 16 bytes inside them)
+          const uintptr_t from = (reinterpret_cast<uintptr_t>(counts + a.c_stride) + 15) & ~(uintptr_t)15;
+          const uintptr_t to = reinterpret_cast<uintptr_t>(counts + a.c_stride + n_here) & ~(uintptr_t)15;
+          if (to > from) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
+        }
         if (counts != nullptr) {
           // Fours at aligned addresses, kCountP of them in flight a thread; eight lanes' make a word of bits, which lies across two.
           const int off = (int)(reinterpret_cast<uintptr_t>(counts) >> 2 & 3), quads = (n_here + off + 3) / 4;
@@ -555,6 +570,25 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
     };
     each_later([&](int, float y) { mass.add(y, k); });
 
+    // body(entry, value) for each of this thread's changed entries; all threads together
+    auto each_changed = [&](auto&& body) {
+      for (int first = 0; first < changed; first += kListP) {
+        if (rounds) {
+          __syncthreads();
+          fill(first, nullptr);
+          __syncthreads();
+          look_up(first), fetch(first), resolve(first);
+        }
+#pragma unroll
+        for (int u = 0; u < kFixP; ++u)
+          if (on >> u & 1u) {
+            const int e = list[tid + u * kThreadsP];
+            body(e & ~kBiased, rounds ? changed_value(e & ~kBiased, fix[u], fix_c[u], b1 > b0, fix_b[u]) : fix[u]);
+          }
+      }
+      if (extra >= 0) body(extra, extra_y);
+      each_later(body);
+    };
     // maximum and sum over the cluster
     auto join = [&] {
       float top = mass.m;
@@ -565,12 +599,30 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) mass.s += __shfl_xor_sync(0xFFFFFFFFu, mass.s, o);
     };
+    const float top_here = mass.m;  // of this thread
     join();
     parity ^= 1;
+    if (greedy) {
+      int first = 0x7FFFFFFF;
+      if (top_here == mass.m && top_here > kNegInf) {  // a thread or few
+        for (int j = tid; j < vectors && first == 0x7FFFFFFF; j += kThreadsP) {
+          const uint4 v = *reinterpret_cast<const uint4*>(xs + j * kV);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = kV / 2 - 1; e >= 0; --e) {
+            const float2 x = Words<T>::get(w, e);
+            first = x.x == mass.m ? j * kV - shift + 2 * e : x.y == mass.m ? j * kV - shift + 2 * e + 1 : first;
+          }
+        }
+      }
+      __syncwarp();
+      each_changed([&](int i, float y) { first = y == mass.m ? min(first, i) : first; });
+      const int lowest = __reduce_min_sync(0xFFFFFFFFu, first);
+      if (lane < cs) put_cluster_32(&part_at[parity][rank * kWarpsP + warp], (uint32_t)lane, (uint32_t)(lowest == 0x7FFFFFFF ? lowest : lo + lowest));
+    }
     if (lane < cs)
       put_cluster(&parts[parity][rank * kWarpsP + warp], (uint32_t)lane,
                   (unsigned long long)__float_as_uint(mass.m) << 32 | (unsigned long long)__float_as_uint(mass.s));
-    if (tid == 0) first_s = 0x7FFFFFFF;
     ready = same;
     if (same) ask_mask(t + 1);
     __syncwarp();
@@ -600,51 +652,17 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       const float2 y = mul2(add2(x, nb), kk);
       return mul2(make_float2(ex2(y.x), ex2(y.y)), ii);
     };
-    // body(entry, value) for each of this thread's changed entries; all threads together
-    auto each_changed = [&](auto&& body) {
-      for (int first = 0; first < changed; first += kListP) {
-        if (rounds) {
-          __syncthreads();
-          fill(first, nullptr);
-          __syncthreads();
-          look_up(first), fetch(first), resolve(first);
-        }
-#pragma unroll
-        for (int u = 0; u < kFixP; ++u)
-          if (on >> u & 1u) {
-            const int e = list[tid + u * kThreadsP];
-            body(e & ~kBiased, rounds ? changed_value(e & ~kBiased, fix[u], fix_c[u], b1 > b0, fix_b[u]) : fix[u]);
-          }
-      }
-      if (extra >= 0) body(extra, extra_y);
-      each_later(body);
-    };
     float value = none ? kNegInf : broken ? __int_as_float(0x7FC00000) : all.m / heat + logf(all.s);
     const bool one = greedy && !none && !broken;
     int chosen = -1;
     if (one) {
       // the lowest entry of the largest
-      int first = 0x7FFFFFFF;
-      for (int j = tid; j < vectors && first == 0x7FFFFFFF; j += kThreadsP) {
-        const uint4 v = *reinterpret_cast<const uint4*>(xs + j * kV);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      int at = 0x7FFFFFFF;
 #pragma unroll
-        for (int e = kV / 2 - 1; e >= 0; --e) {
-          const float2 x = Words<T>::get(w, e);
-          first = x.x == all.m ? j * kV - shift + 2 * e : x.y == all.m ? j * kV - shift + 2 * e + 1 : first;
-        }
-      }
-      each_changed([&](int i, float y) { first = y == all.m ? min(first, i) : first; });
-      first = __reduce_min_sync(0xFFFFFFFFu, first);
-      if (lane == 0 && first != 0x7FFFFFFF) atomicMin(&first_s, first);
-      __syncthreads();
-      if (tid < cs)
-        put_cluster(&cta_first[parity][rank], (uint32_t)tid, first_s == 0x7FFFFFFF ? ~0ull : (unsigned long long)(lo + first_s));
-      __syncwarp();
-      sync_cluster();
-      unsigned long long at = ~0ull;
-      for (int c = 0; c < cs; ++c) at = min(at, cta_first[parity][c]);
-      chosen = at < ~0ull && at >= (unsigned long long)lo && at < (unsigned long long)(lo + n_here) ? (int)(at - lo) : -1;
+      for (int q = 0; q < kClusterP * kWarpsP / 32; ++q)
+        if (lane + 32 * q < cs * kWarpsP && part_m[q] == all.m) at = min(at, part_at[parity][lane + 32 * q]);
+      at = __reduce_min_sync(0xFFFFFFFFu, at);
+      chosen = at >= lo && at < lo + n_here ? at - lo : -1;
       value = all.m;
     }
     // fours at the output's aligned addresses
