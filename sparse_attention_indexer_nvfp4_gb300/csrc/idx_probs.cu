@@ -174,11 +174,14 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   uint32_t* special = reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(store) + (size_t)a.buffers * stretch) + 1;  // entries that the request's counts or biases change
   uint32_t* skip = special + a.slice / 32 + 2;  // entries that the main pass leaves out, those around the stretch among them
   __shared__ uint64_t full[2];
-  __shared__ int tokens[kPathP + 1];   // of the request: node j's at j
+  __shared__ int tokens[kThreadsP + 1];  // of the request's first nodes: node j's at j
+  __shared__ int bias_at[kThreadsP];     // its biases, where they are no more than this; with `placed`, bias_of as the list has them
+  __shared__ float bias_of[kThreadsP];
   __shared__ uint64_t masks[kTreeP];   // of its first nodes
   __shared__ int path_of_tree[kTreeP];
   __shared__ uint16_t list[kListP];  // the special entries; kBiased: some bias is theirs
-  __shared__ int warp_count[kWarpsP];
+  __shared__ uint32_t warp_count[kWarpsP];
+  __shared__ int warp_biases[kWarpsP];
   __shared__ unsigned long long parts[2][kClusterP * kWarpsP];  // maximum and sum of each warp of the cluster
   __shared__ int part_at[2][kClusterP * kWarpsP];  // the lowest entry of that maximum (rows of temperature 0)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -220,10 +223,11 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   sync_cluster();  // every CTA of the cluster runs: its shared memory may be written
 
   // the request that the rows are of, and counts and biases of this thread's special entries
-  int r = 0, begin = 0, end = 0, changed = 0, mine_at = 0, b0 = 0, b1 = 0;
+  int r = 0, begin = 0, end = 0, changed = 0, unbiased = 0, mine_at = 0, b0 = 0, b1 = 0;
+  bool placed = true;  // the list ends with the biased entries, in the biases' order; not where a token has several
   float heat = 1.f, repetition = 1.f, presence = 0.f, frequency = 0.f;
   const int32_t* counts = nullptr;
-  const int* path = a.mask != nullptr ? path_of_tree : tokens + 1;  // the drafted tokens on the node's path
+  const int* path = path_of_tree;  // the drafted tokens on the node's path
   int fix_c[kFixP];
   float fix_b[kFixP], fix[kFixP];
   uint32_t mask_words[kMaskP], fix_mask[kFixP];
@@ -231,37 +235,35 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   bool known = false, rounds = false, ready = false;  // of the request; more special entries than the list holds; bits and path of the row are there
   int parity = 0, n_path = 0;
 
-  // special entries of ranks from `first` on into the list (its biased ones by `flags`, or all)
+  // Special entries of ranks from `first` on into the list: those without a bias (`flags`: the others), or, for rounds, all.
   auto fill = [&](int first, const uint32_t* flags) {
     int at = mine_at - first;
-    for (int w = tid; w < here; w += kThreadsP) {
-      const uint32_t biased = flags != nullptr ? flags[w] : ~0u;
-      for (uint32_t bits = special[w]; bits != 0; bits &= bits - 1, ++at) {
-        const int e = __ffs(bits) - 1;
-        if (at >= 0 && at < kListP) list[at] = (uint16_t)((32 * w + e) | (biased >> e & 1u ? kBiased : 0));
-      }
-    }
+    for (int w = tid; w < here; w += kThreadsP)
+      for (uint32_t bits = special[w] & (flags != nullptr ? ~flags[w] : ~0u); bits != 0; bits &= bits - 1, ++at)
+        if (at >= 0 && at < kListP) list[at] = (uint16_t)((32 * w + __ffs(bits) - 1) | (flags != nullptr ? 0 : kBiased));
   };
-  // counts and biases of this thread's entries of the list
+  // counts and biases of this thread's entries of the list; a warp looks for a bias together
   auto look_up = [&](int first) {
-    int found = 0, i[kFixP];
-    bool biased = false;
+    const bool near = b1 - b0 <= kThreadsP;
+    const int* tokens_of = near ? bias_at : a.bias_tokens + b0;
+    const float* values = near ? bias_of : a.bias_values + b0;
 #pragma unroll
     for (int u = 0; u < kFixP; ++u) {
-      const int at = tid + u * kThreadsP;
-      fix_c[u] = 0, fix_b[u] = 0.f, i[u] = -1;
-      if (first + at >= changed) continue;
-      const int e = list[at];
-      if (counts != nullptr) fix_c[u] = counts[e & ~kBiased];
-      if (e & kBiased) biased = true, i[u] = lo + (e & ~kBiased);
-    }
-    if (biased) {
-#pragma unroll 8
-      for (int b = b0; b < b1; ++b) {
-        const int v = a.bias_tokens[b];
-#pragma unroll
-        for (int u = 0; u < kFixP; ++u)
-          if (v == i[u]) fix_b[u] = (found >> u & 1) == 0 ? a.bias_values[b] : __int_as_float(0x7FC00000), found |= 1 << u;  // NaN: several
+      const int at = tid + u * kThreadsP, e = first + at < changed ? list[at] : 0;
+      fix_c[u] = first + at < changed && counts != nullptr ? counts[e & ~kBiased] : 0, fix_b[u] = 0.f;
+      if (placed) {
+        if (e & kBiased) fix_b[u] = bias_of[at - unbiased];
+        continue;
+      }
+      for (uint32_t left = __ballot_sync(0xFFFFFFFFu, (e & kBiased) != 0 && b1 > b0); left != 0; left &= left - 1) {
+        const int of = __ffs(left) - 1, v = lo + (__shfl_sync(0xFFFFFFFFu, e, of) & ~kBiased);
+        int found = 0, where = 0;
+        for (int b = 0; b < b1 - b0; b += 32) {
+          const uint32_t hits = __ballot_sync(0xFFFFFFFFu, b + lane < b1 - b0 && tokens_of[b + lane] == v);
+          if (found == 0 && hits != 0) where = b + __ffs(hits) - 1;
+          found += __popc(hits);
+        }
+        if (lane == of && found > 0) fix_b[u] = found == 1 ? values[where] : __int_as_float(0x7FC00000);  // NaN: several
       }
     }
   };
@@ -324,7 +326,8 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       repetition = a.repetition != nullptr ? a.repetition[r] : 1.f;
       presence = a.presence != nullptr ? a.presence[r] : 0.f, frequency = a.frequency != nullptr ? a.frequency[r] : 0.f;
       if (a.tokens != nullptr) {
-        for (int j = tid; j < min(end - begin, kPathP + 1); j += kThreadsP) tokens[j] = a.tokens[begin + j];
+        for (int j = tid; j < min(end - begin, kThreadsP + 1); j += kThreadsP) tokens[j] = a.tokens[begin + j];
+        if (a.mask == nullptr) path = end - begin <= kThreadsP + 1 ? tokens + 1 : a.tokens + begin + 1;  // (a long chain's stay where they are)
         if (a.mask != nullptr && tid < min(end - begin, kTreeP)) masks[tid] = a.mask[begin + tid];
       }
       changed = 0;
@@ -371,32 +374,46 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
           }
         }
         __syncthreads();
-        if (b1 > b0) {
-          for (int b = b0 + tid; b < b1; b += kThreadsP) {
-            const int i = a.bias_tokens[b] - lo;
-            if (i >= 0 && i < n_here) atomicOr(&special[i >> 5], 1u << (i & 31)), atomicOr(&skip[i >> 5], 1u << (i & 31));
+        bool mine = false, twice = false;  // this thread's bias (the first kThreadsP) is in the stretch; a token has two
+        int mine_i = 0;
+        float mine_b = 0.f;
+        for (int b = b0 + tid; b < b1; b += kThreadsP) {
+          const int v = a.bias_tokens[b], i = v - lo;
+          const float y = a.bias_values[b];
+          if (b1 - b0 <= kThreadsP) bias_at[tid] = v, bias_of[tid] = y, mine_b = y;
+          if (v >= lo && i < n_here) {
+            atomicOr(&special[i >> 5], 1u << (i & 31));
+            twice |= (atomicOr(&skip[i >> 5], 1u << (i & 31)) >> (i & 31) & 1u) != 0;
+            mine = true, mine_i = i;
           }
-          __syncthreads();
         }
-        mine_at = 0;
-        for (int w = tid; w < here; w += kThreadsP) mine_at += __popc(special[w]);
-        int incl = mine_at;
+        placed = !__syncthreads_or(twice) && b1 - b0 <= kThreadsP;
+        // numbers of special entries: of those without a bias, and (above 16 bits) of all
+        uint32_t number = 0;
+        for (int w = tid; w < here; w += kThreadsP) number += (uint32_t)__popc(special[w] & ~skip[w]) + ((uint32_t)__popc(special[w]) << 16);
+        uint32_t incl = number;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
           if (lane >= o) incl += y;
         }
+        const uint32_t with_bias = __ballot_sync(0xFFFFFFFFu, mine);
         if (lane == 31) warp_count[warp] = incl;
+        if (lane == 0) warp_biases[warp] = __popc(with_bias);
         __syncthreads();
-        int before = 0;
+        uint32_t before = incl - number, all_of = 0;
+        int biases = 0, rank_b = __popc(with_bias & ((1u << lane) - 1u));
 #pragma unroll
         for (int w = 0; w < kWarpsP; ++w) {
-          const int c = warp_count[w];
-          before += w < warp ? c : 0, changed += c;
+          before += w < warp ? warp_count[w] : 0u, all_of += warp_count[w];
+          rank_b += w < warp ? warp_biases[w] : 0, biases += warp_biases[w];
         }
-        mine_at = before + incl - mine_at;
+        unbiased = (int)(all_of & 0xFFFFu), mine_at = (int)(before & 0xFFFFu), changed = unbiased + biases;
+        placed = placed && changed <= kListP;
+        if (!placed) changed = (int)(all_of >> 16), mine_at = (int)(before >> 16);
         rounds = changed > kListP;
-        if (changed > 0) fill(0, skip);
+        if (changed > 0) fill(0, placed ? skip : nullptr);
+        if (placed && mine) list[unbiased + rank_b] = (uint16_t)(mine_i | kBiased), bias_of[rank_b] = mine_b;
         __syncthreads();
         if (changed > 0 && !rounds) look_up(0);
       }
