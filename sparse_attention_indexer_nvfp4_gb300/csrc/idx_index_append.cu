@@ -19,7 +19,10 @@
 // between the codes.  A key whose codes or scales may differ is formed again as
 // a whole.
 //
-// Bound by HBM and, with many heads, by the instructions of a row.  A warp
+// Bound by the instructions and latencies of a row: 8,191 tokens of 64 heads take
+// 105 us, 0.29 of HBM (without the look for borders 75; with angles in 64-bit
+// floating point 127; 2, 3 and 4 CTAs of 256 threads an SM 115 to 117, 5 of 128
+// 105).  512 tokens of 4 heads take 9 us.  A warp
 // takes a token (with few tokens a part of its heads), 16 lanes a row, 8
 // elements a lane; cosines, sines and weights are folded into a lane's factors
 // once a token.  A key's scale byte belongs to two lanes.

@@ -9,14 +9,23 @@
 // second, short pass forms the changed ones one by one, rounded at each step
 // as the formula is written.
 //
-// Bound by HBM: a row is read once and written once.  A cluster of CTAs takes a
-// row, each a stretch of the vocabulary, which stays in shared memory as it was
-// read (masked and changed entries as -inf) between the pass that finds maximum
-// and sum (a running maximum and a sum rescaled when it grows, a thread) and the
-// one that writes; the CTAs exchange both through distributed shared memory.  The
-// next row is copied into a second buffer meanwhile (where two CTAs an SM have
-// room for one: 16-bit logits).  A cluster takes rows that follow one another, so a request's bits are formed from its counts once for its rows, and
-// there are no more clusters than run at once.
+// A cluster of CTAs takes a row, each a stretch of the vocabulary, which stays in
+// shared memory as it was read (entries that are left out as -inf) between the
+// pass that finds maximum and sum and the one that writes.  Every warp sends its
+// two numbers to all CTAs through distributed shared memory and puts the
+// cluster's together by itself.  The next row is copied into a second buffer
+// meanwhile, where two CTAs an SM have room for one (16-bit logits, up to 200,000
+// entries).  A cluster takes rows that follow one another, so a request's special
+// entries are found in its counts once for its rows, and there are no more
+// clusters than run at once.
+//
+// HBM bounds it, and the stages of a row: 512 rows of 200,003 bf16 logits with
+// counts, 16 biases a request and masks take 193 us where HBM would take 100 for
+// their 679 MB.  A row's stages follow one another (in cycles of a CTA: left out
+// and summed 3,300, changed entries 2,300, the exchange 5,000, written 4,000,
+// between them 2,500), and two CTAs an SM do not cover all of it.  512 threads a
+// CTA took 272 us, 3 CTAs of 256 with one buffer 219, 128 threads 257; entries
+// kept in fp32, one CTA an SM, 833.  One row of 32,000: 9.0 us, all latency.
 #include "idx_internal.h"
 #include "idx_rope.cuh"
 
@@ -29,9 +38,12 @@ constexpr int kClusterP = 8;
 constexpr int kPathP = IDX_VERIFY_MAX_NODES;
 constexpr int kTreeP = 64;    // bits of a tree's mask
 constexpr int kMaskP = IDX_PROBS_MAX_VOCAB / kClusterP / 32 / kThreadsP;  // words of bits a thread
-constexpr int kCountP = 10;   // fours of counts in flight a thread
+constexpr int kCountP = 16;   // words of counts in flight a warp
 constexpr int kFixP = 4;      // changed entries a thread takes at a time
 constexpr int kListP = kFixP * kThreadsP;
+constexpr int kBitsP = IDX_PROBS_MAX_VOCAB / kClusterP / 32;  // words of a stretch
+constexpr int kWordP = 4;      // words of special entries a warp takes at a time
+constexpr int kStretchP = 8192;  // entries of a CTA with counts, unless a row has 4 CTAs
 constexpr size_t kRoomP = 104 * 1024;  // dynamic shared memory of each of two CTAs an SM (which has 228 KB)
 constexpr int kBiased = 0x8000;  // an entry of the list that has a bias
 constexpr float kNegInf = -INFINITY;
@@ -174,12 +186,14 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   uint32_t* special = reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(store) + (size_t)a.buffers * stretch) + 1;  // entries that the request's counts or biases change
   uint32_t* skip = special + a.slice / 32 + 2;  // entries that the main pass leaves out, those around the stretch among them
   __shared__ uint64_t full[2];
-  __shared__ int tokens[kThreadsP + 1];  // of the request's first nodes: node j's at j
+  __shared__ int tokens[kTreeP];       // of the request's first nodes
   __shared__ int bias_at[kThreadsP];     // its biases, where they are no more than this; with `placed`, bias_of as the list has them
   __shared__ float bias_of[kThreadsP];
   __shared__ uint64_t masks[kTreeP];   // of its first nodes
   __shared__ int path_of_tree[kTreeP];
-  __shared__ uint16_t list[kListP];  // the special entries; kBiased: some bias is theirs
+  // The special entries (kBiased: some bias is theirs); where they are more than that, the bits of those that have a bias.
+  __shared__ uint32_t list_or_bits[kBitsP];
+  uint16_t* list = reinterpret_cast<uint16_t*>(list_or_bits);
   __shared__ uint32_t warp_count[kWarpsP];
   __shared__ int warp_biases[kWarpsP];
   __shared__ unsigned long long parts[2][kClusterP * kWarpsP];  // maximum and sum of each warp of the cluster
@@ -232,38 +246,42 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
   float fix_b[kFixP], fix[kFixP];
   uint32_t mask_words[kMaskP], fix_mask[kFixP];
   bool timed_out = false;
-  bool known = false, rounds = false, ready = false;  // of the request; more special entries than the list holds; bits and path of the row are there
+  bool known = false, many = false, ready = false;  // of the request; more special entries than the list holds; bits and path of the row are there
   int parity = 0, n_path = 0;
 
-  // Special entries of ranks from `first` on into the list: those without a bias (`flags`: the others), or, for rounds, all.
-  auto fill = [&](int first, const uint32_t* flags) {
-    int at = mine_at - first;
+  // The special entries into the list: those without a bias (`flags`: the others), or all.
+  auto fill = [&](const uint32_t* flags) {
+    int at = mine_at;
     for (int w = tid; w < here; w += kThreadsP)
       for (uint32_t bits = special[w] & (flags != nullptr ? ~flags[w] : ~0u); bits != 0; bits &= bits - 1, ++at)
-        if (at >= 0 && at < kListP) list[at] = (uint16_t)((32 * w + __ffs(bits) - 1) | (flags != nullptr ? 0 : kBiased));
+        list[at] = (uint16_t)((32 * w + __ffs(bits) - 1) | (flags != nullptr ? 0 : kBiased));
   };
-  // counts and biases of this thread's entries of the list; a warp looks for a bias together
-  auto look_up = [&](int first) {
+  // The bias of entry i of lane `of`, a warp together: NaN for several.
+  auto find_bias = [&](int i, int of) {
     const bool near = b1 - b0 <= kThreadsP;
     const int* tokens_of = near ? bias_at : a.bias_tokens + b0;
-    const float* values = near ? bias_of : a.bias_values + b0;
+    const int v = lo + __shfl_sync(0xFFFFFFFFu, i, of);
+    int found = 0, where = 0;
+    for (int b = 0; b < b1 - b0; b += 32) {
+      const uint32_t hits = __ballot_sync(0xFFFFFFFFu, b + lane < b1 - b0 && tokens_of[b + lane] == v);
+      if (found == 0 && hits != 0) where = b + __ffs(hits) - 1;
+      found += __popc(hits);
+    }
+    return found == 0 ? 0.f : found > 1 ? __int_as_float(0x7FC00000) : near ? bias_of[where] : a.bias_values[b0 + where];
+  };
+  // counts and biases of this thread's entries of the list
+  auto look_up = [&] {
 #pragma unroll
     for (int u = 0; u < kFixP; ++u) {
-      const int at = tid + u * kThreadsP, e = first + at < changed ? list[at] : 0;
-      fix_c[u] = first + at < changed && counts != nullptr ? counts[e & ~kBiased] : 0, fix_b[u] = 0.f;
+      const int at = tid + u * kThreadsP, e = at < changed ? list[at] : 0;
+      fix_c[u] = at < changed && counts != nullptr ? counts[e & ~kBiased] : 0, fix_b[u] = 0.f;
       if (placed) {
         if (e & kBiased) fix_b[u] = bias_of[at - unbiased];
         continue;
       }
       for (uint32_t left = __ballot_sync(0xFFFFFFFFu, (e & kBiased) != 0 && b1 > b0); left != 0; left &= left - 1) {
-        const int of = __ffs(left) - 1, v = lo + (__shfl_sync(0xFFFFFFFFu, e, of) & ~kBiased);
-        int found = 0, where = 0;
-        for (int b = 0; b < b1 - b0; b += 32) {
-          const uint32_t hits = __ballot_sync(0xFFFFFFFFu, b + lane < b1 - b0 && tokens_of[b + lane] == v);
-          if (found == 0 && hits != 0) where = b + __ffs(hits) - 1;
-          found += __popc(hits);
-        }
-        if (lane == of && found > 0) fix_b[u] = found == 1 ? values[where] : __int_as_float(0x7FC00000);  // NaN: several
+        const float bias = find_bias(e & ~kBiased, __ffs(left) - 1);
+        if (lane == __ffs(left) - 1) fix_b[u] = bias;
       }
     }
   };
@@ -326,51 +344,28 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       repetition = a.repetition != nullptr ? a.repetition[r] : 1.f;
       presence = a.presence != nullptr ? a.presence[r] : 0.f, frequency = a.frequency != nullptr ? a.frequency[r] : 0.f;
       if (a.tokens != nullptr) {
-        for (int j = tid; j < min(end - begin, kThreadsP + 1); j += kThreadsP) tokens[j] = a.tokens[begin + j];
-        if (a.mask == nullptr) path = end - begin <= kThreadsP + 1 ? tokens + 1 : a.tokens + begin + 1;  // (a long chain's stay where they are)
+        if (a.mask == nullptr) path = a.tokens + begin + 1;  // (a chain's stay where they are)
+        else if (tid < min(end - begin, kTreeP)) tokens[tid] = a.tokens[begin + tid];
         if (a.mask != nullptr && tid < min(end - begin, kTreeP)) masks[tid] = a.mask[begin + tid];
       }
       changed = 0;
       if (any) {
         counts = a.counts != nullptr ? a.counts + (int64_t)r * a.c_stride + lo : nullptr;
         if (a.bias_cu != nullptr) b0 = max(0, a.bias_cu[r]), b1 = min(a.num_bias, a.bias_cu[r + 1]);
-        for (int w = tid; w < here; w += kThreadsP) special[w] = 0, skip[w] = 0;
-        __syncthreads();
-        if (counts != nullptr && tid == 0 && end < t_hi && r + 1 < a.num_reqs && n_here > 0) {
-          // the next request's counts into L2 (whole 16 bytes inside them)
-          const uintptr_t from = (reinterpret_cast<uintptr_t>(counts + a.c_stride) + 15) & ~(uintptr_t)15;
-          const uintptr_t to = reinterpret_cast<uintptr_t>(counts + a.c_stride + n_here) & ~(uintptr_t)15;
-          if (to > from) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
-        }
-        if (counts != nullptr) {
-          // Fours at aligned addresses, kCountP of them in flight a thread; eight lanes' make a word of bits, which lies across two.
-          const int off = (int)(reinterpret_cast<uintptr_t>(counts) >> 2 & 3), quads = (n_here + off + 3) / 4;
-          for (int q0 = tid; q0 - lane < quads; q0 += kThreadsP * kCountP) {
-            int4 c[kCountP];
+        if (counts == nullptr)
+          for (int w = tid; w < here; w += kThreadsP) special[w] = 0, skip[w] = 0;
+        // words of bits from 32 counts each, kCountP of them in flight a warp (fours a thread, put together by shuffles, took twice the time)
+        for (int w0 = counts != nullptr ? warp : here; w0 < here; w0 += kWarpsP * kCountP) {
+          int c[kCountP];
 #pragma unroll
-            for (int u = 0; u < kCountP; ++u) {
-              const int q = q0 + u * kThreadsP, i = 4 * q - off;
-              c[u] = make_int4(0, 0, 0, 0);
-              if (i >= 0 && i + 4 <= n_here) {
-                c[u] = *reinterpret_cast<const int4*>(counts + i);
-              } else if (q < quads) {
-                if (i >= 0) c[u].x = counts[i];
-                if (i + 1 >= 0 && i + 1 < n_here) c[u].y = counts[i + 1];
-                if (i + 2 >= 0 && i + 2 < n_here) c[u].z = counts[i + 2];
-                if (i + 3 < n_here) c[u].w = counts[i + 3];
-              }
-            }
+          for (int u = 0; u < kCountP; ++u) {
+            const int i = 32 * (w0 + u * kWarpsP) + lane;
+            c[u] = i < n_here ? counts[i] : 0;
+          }
 #pragma unroll
-            for (int u = 0; u < kCountP; ++u) {
-              uint32_t bits = ((c[u].x != 0) | (c[u].y != 0) << 1 | (c[u].z != 0) << 2 | (c[u].w != 0) << 3) << (4 * (lane & 7));
-#pragma unroll
-              for (int o = 1; o < 8; o <<= 1) bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, o);
-              if ((lane & 7) == 0 && bits != 0) {
-                const int i = 4 * (q0 + u * kThreadsP) - off, w = i >> 5, sh = i & 31;  // (w -1: no bit is its)
-                if (bits << sh) atomicOr(&special[w], bits << sh);
-                if (sh != 0 && bits >> (32 - sh)) atomicOr(&special[w + 1], bits >> (32 - sh));
-              }
-            }
+          for (int u = 0; u < kCountP; ++u) {
+            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, c[u] != 0);
+            if (lane == 0 && w0 + u * kWarpsP < here) special[w0 + u * kWarpsP] = bits, skip[w0 + u * kWarpsP] = 0;
           }
         }
         __syncthreads();
@@ -411,12 +406,23 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
         unbiased = (int)(all_of & 0xFFFFu), mine_at = (int)(before & 0xFFFFu), changed = unbiased + biases;
         placed = placed && changed <= kListP;
         if (!placed) changed = (int)(all_of >> 16), mine_at = (int)(before >> 16);
-        rounds = changed > kListP;
-        if (changed > 0) fill(0, placed ? skip : nullptr);
+        many = changed > kListP;
+        if (many) {
+          for (int w = tid; w < here; w += kThreadsP) list_or_bits[w] = skip[w];
+          changed = 0;
+        } else if (changed > 0) {
+          fill(placed ? skip : nullptr);
+        }
         if (placed && mine) list[unbiased + rank_b] = (uint16_t)(mine_i | kBiased), bias_of[rank_b] = mine_b;
         __syncthreads();
-        if (changed > 0 && !rounds) look_up(0);
+        if (changed > 0) look_up();
       }
+    }
+    if (tid == 0 && counts != nullptr && t + 2 >= end && end < t_hi && r + 1 < a.num_reqs && n_here > 0) {
+      // soon the next request's: its counts into L2 (whole 16 bytes inside them)
+      const uintptr_t from = (reinterpret_cast<uintptr_t>(counts + a.c_stride) + 15) & ~(uintptr_t)15;
+      const uintptr_t to = reinterpret_cast<uintptr_t>(counts + a.c_stride + n_here) & ~(uintptr_t)15;
+      if (to > from) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
     }
     const bool greedy = !(heat > 8.7e-19f);  // 2^-60
     const float k = greedy ? 1.44269504f : 1.44269504f / heat;
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
 #pragma unroll
       for (int u = 0; u < kFixP; ++u) {
         fix_mask[u] = ~0u;
-        if (a.allowed != nullptr && !rounds && tid + u * kThreadsP < changed) fix_mask[u] = mask_row(t)[(list[tid + u * kThreadsP] & ~kBiased) >> 5];
+        if (a.allowed != nullptr && tid + u * kThreadsP < changed) fix_mask[u] = mask_row(t)[(list[tid + u * kThreadsP] & ~kBiased) >> 5];
       }
     };
     auto put_skip = [&] {
@@ -469,7 +475,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       mark_path();
     }
     const uint32_t* mask = a.allowed != nullptr ? mask_row(t) : nullptr;
-    const bool slow = rounds || n_path > kThreadsP;  // more special entries, or tokens of a path, than one for each thread
+    const bool slow = many || n_path > kThreadsP;  // more special entries, or tokens of a path, than one for each thread
     const bool same = next && t + 1 < end && !slow && n_path < kThreadsP;  // the next row is the request's too
 
     // The row is there.  This thread's special entries as they are, and a token of the path that is none and comes first there.
@@ -495,31 +501,40 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
     uint32_t on = 0, extra_mask = ~0u;
     int extra = tid < n_path ? stray(tid) : -1;
     float extra_y = 0.f;
-    if (!rounds) {
 #pragma unroll
-      for (int u = 0; u < kFixP; ++u)
-        if (tid + u * kThreadsP < changed) fix[u] = to_f(xs[(list[tid + u * kThreadsP] & ~kBiased) + shift]);
-    }
+    for (int u = 0; u < kFixP; ++u)
+      if (tid + u * kThreadsP < changed) fix[u] = to_f(xs[(list[tid + u * kThreadsP] & ~kBiased) + shift]);
     if (extra >= 0) {
       if (mask != nullptr) extra_mask = mask[extra >> 5];
       extra_y = to_f(xs[extra + shift]);
     }
     __syncthreads();
-    // those that are left
-    auto resolve = [&](int first) {
-      on = 0;
+    // Where they are many: body(entry, value) for each, a lane a bit of a word, from the tensor.
+    auto each_word = [&](auto&& body) {
+      for (int w0 = warp; w0 < here; w0 += kWarpsP * kWordP) {
+        float x[kWordP];
+        int c[kWordP];
+        uint32_t own = 0;
 #pragma unroll
-      for (int u = 0; u < kFixP; ++u)
-        if (first + tid + u * kThreadsP < changed && (fix_mask[u] >> (list[tid + u * kThreadsP] & 31) & 1u)) on |= 1u << u;
-    };
-    // with rounds, from the tensor
-    auto fetch = [&](int first) {
+        for (int u = 0; u < kWordP; ++u) {
+          const int w = w0 + u * kWarpsP, i = 32 * w + lane;
+          if (w >= here) continue;
+          const uint32_t bits = special[w] & (mask != nullptr ? mask[w] : ~0u);
+          x[u] = 0.f, c[u] = 0;
+          if (bits >> lane & 1u) own |= 1u << u, x[u] = to_f(row[i]), c[u] = counts != nullptr ? counts[i] : 0;
+        }
 #pragma unroll
-      for (int u = 0; u < kFixP; ++u) {
-        const int at = tid + u * kThreadsP;
-        if (first + at >= changed) continue;
-        const int i = list[at] & ~kBiased;
-        fix_mask[u] = mask != nullptr ? mask[i >> 5] : ~0u, fix[u] = to_f(row[i]);
+        for (int u = 0; u < kWordP; ++u) {
+          const int w = w0 + u * kWarpsP, i = 32 * w + lane;
+          if (w >= here) continue;
+          const bool mine = own >> u & 1u, biased = mine && (list_or_bits[w] >> lane & 1u);
+          float bias = 0.f;
+          for (uint32_t left = __ballot_sync(0xFFFFFFFFu, biased); left != 0; left &= left - 1) {
+            const float b = find_bias(i, __ffs(left) - 1);
+            if (lane == __ffs(left) - 1) bias = b;
+          }
+          if (mine) body(i, changed_value(i, x[u], c[u], biased, bias));
+        }
       }
     };
 
@@ -560,22 +575,15 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       mass.s = sum.x + sum.y;
     }
     // the changed entries
-    for (int first = 0; first < changed; first += kListP) {
-      if (rounds) {
-        __syncthreads();
-        fill(first, nullptr);
-        __syncthreads();
-        look_up(first), fetch(first);
-      }
-      resolve(first);
 #pragma unroll
-      for (int u = 0; u < kFixP; ++u)
-        if (on >> u & 1u) {
-          const int e = list[tid + u * kThreadsP];
-          fix[u] = changed_value(e & ~kBiased, fix[u], fix_c[u], (e & kBiased) && b1 > b0, fix_b[u]);
-          mass.add(fix[u], k);
-        }
+    for (int u = 0; u < kFixP; ++u) {
+      const int at = tid + u * kThreadsP;
+      if (at >= changed || !(fix_mask[u] >> (list[at] & 31) & 1u)) continue;
+      on |= 1u << u;
+      fix[u] = changed_value(list[at] & ~kBiased, fix[u], fix_c[u], (list[at] & kBiased) && b1 > b0, fix_b[u]);
+      mass.add(fix[u], k);
     }
+    if (many) each_word([&](int, float y) { mass.add(y, k); });
     if (extra >= 0 && (!(extra_mask >> (extra & 31) & 1u) || !comes_first(tid, extra))) extra = -1;
     if (extra >= 0) extra_y = changed_value(extra, extra_y, 0, false, 0.f), mass.add(extra_y, k);
     // (of a long chain a thread has more; their values are formed again for each use)
@@ -589,20 +597,10 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
 
     // body(entry, value) for each of this thread's changed entries; all threads together
     auto each_changed = [&](auto&& body) {
-      for (int first = 0; first < changed; first += kListP) {
-        if (rounds) {
-          __syncthreads();
-          fill(first, nullptr);
-          __syncthreads();
-          look_up(first), fetch(first), resolve(first);
-        }
 #pragma unroll
-        for (int u = 0; u < kFixP; ++u)
-          if (on >> u & 1u) {
-            const int e = list[tid + u * kThreadsP];
-            body(e & ~kBiased, rounds ? changed_value(e & ~kBiased, fix[u], fix_c[u], b1 > b0, fix_b[u]) : fix[u]);
-          }
-      }
+      for (int u = 0; u < kFixP; ++u)
+        if (on >> u & 1u) body(list[tid + u * kThreadsP] & ~kBiased, fix[u]);
+      if (many) each_word(body);
       if (extra >= 0) body(extra, extra_y);
       each_later(body);
     };
@@ -727,13 +725,16 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
 template <typename T>
 int launch_probs(ProbArgs a, cudaStream_t s) {
   const int sms = max(device_sms(), 1);
-  // CTAs a row: stretches of at most 8,192 entries, shorter ones where a few rows leave SMs without any
-  int cs = 1;
+  // CTAs a row: as few as hold two of its stretches in shared memory, two CTAs an SM (3,200 rows of 32,000 bf16: 2 a row, 152
+  // us, where 4 took 213); with counts 4 of them, between which some thousand tokens of a long prompt fit the lists (220 rows
+  // of 17,427: 29 us, where 1 took 152; 264 rows of 79,678: 57, where 8 took 71); and more where a few rows leave SMs without any
   auto slice_of = [&](int c) { return ((a.vocab + c - 1) / c + 31) / 32 * 32; };
-  while (cs < kClusterP && (slice_of(cs) > 8192 || ((int64_t)a.num_tokens * cs < 2 * sms && slice_of(cs) > 2048))) cs *= 2;
+  auto row_of = [&](int c) { return ((size_t)slice_of(c) + 16) * sizeof(T); };
+  auto bits_of = [&](int c) { return ((size_t)slice_of(c) / 32 + 2) * 8; };
+  int cs = 1;
+  while (cs < kClusterP && (2 * row_of(cs) + bits_of(cs) > kRoomP || (a.counts != nullptr && cs < 4 && slice_of(cs) > kStretchP) || ((int64_t)a.num_tokens * cs < 2 * sms && slice_of(cs) > 2048))) cs *= 2;
   a.slice = slice_of(cs);
-  // two rows in shared memory where two CTAs an SM keep room for them
-  const size_t row = ((size_t)a.slice + 16) * sizeof(T), bits = ((size_t)a.slice / 32 + 2) * 8;
+  const size_t row = row_of(cs), bits = bits_of(cs);
   a.buffers = 2 * row + bits <= kRoomP ? 2 : 1;
   a.polls = wait_polls();
   const size_t smem = a.buffers * row + bits;

@@ -126,6 +126,24 @@ def test_tokens_seen(lib, seen):
     Case([0, 4, 8], 3001, seen=seen, biases=2).check(lib)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_more_special_entries_than_a_list_holds(lib, dtype):
+    """Most tokens of a stretch seen, with and without biases, masks, a greedy row; and written in place.
+
+    Of 600 biases over these vocabularies some tokens have several, whose sums round more often than the tolerance's 5 times,
+    but at far less than the largest magnitude, which the sum of all biases is part of.
+    """
+    for cu, vocab in (([0, 2, 3, 7], 70_001), ([0, 30, 300], 9001)):
+        for biases in (0, 100, 600):
+            c = Case(cu, vocab, dtype, seen=0.7, biases=biases, grammar=biases != 100)
+            c.args["temperature"][1] = 0.0
+            c.check(lib)
+            if dtype == "fp32":
+                x = c.logits.clone()
+                lib.idx_logit_probs(x, x, c.cu, **c.args)
+                assert torch.equal(x, c.probs[:, :vocab])
+
+
 def test_only_one_penalty(lib):
     for name in ("repetition", "presence", "frequency"):
         c = Case([0, 3, 5], 501)
