@@ -648,9 +648,9 @@ int idx_verify_drafts(const float* target, int64_t target_stride, const float* d
  * a head:
  *     n = (offset + w) x / sqrt(mean x^2 + eps)
  * and n's pairs turn as in idx_rope_append; elements from rotary_dim on are
- * those of n.  Values are not normed.  Computed in 32 bits (the squares' sum
- * must stay below 3e38: a row of larger elements becomes 0, one with an
- * infinity or NaN is not finite), rounded once.
+ * those of n.  Values are not normed.  Computed in 32 bits, rounded once: a row
+ * whose squares' sum passes 3e38 becomes 0, one with an infinity or NaN is not
+ * finite, nor is one whose mean of squares and eps add up to 0.
  *
  *   q_weight, k_weight   [head_dim] of the type of all tensors, or NULL: that
  *                 side is turned only
@@ -680,8 +680,8 @@ int idx_norm_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
  * angles as in idx_rope_append); q_scale is fp32.  A query's row that holds an
  * infinity or NaN (or whose squares' sum passes 3e38) gets codes 0x7F and a NaN
  * scale, a key's gets NaN scales and codes 0, so its scores are NaN and rank
- * last.  A query's row whose largest magnitude (before the norm) is below
- * 2^-100 gets codes 0.
+ * last.  A query's row whose largest magnitude (turned, with the weights, before
+ * the norm) is below 2^-100 or above 2^126 gets codes 0.
  *
  *   q             [num_tokens, heads, 128], the head's elements contiguous, or
  *                 NULL with heads 0 (up to 128)
@@ -700,7 +700,7 @@ int idx_norm_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
  *                 every request have none.
  *   slots         [num_tokens] int64 cache slot of each key, or NULL: slot t;
  *                 a negative one is skipped, one past the pages is skipped
- *                 with IDX_ST_BLOCK_OOR
+ *                 with IDX_ST_BLOCK_OOR; two tokens must not share one
  *   index_k       [num_blocks, page_tokens, 72] uint8 pages, page_tokens 128
  *                 (as in idx_dequant_nvfp4_pages) or 256 (IDX_PAGE_256)
  *   dtype         of q, k and the weights;  flags  0 or IDX_ROPE_INTERLEAVED
@@ -818,7 +818,8 @@ int idx_settle_drafts(const idx_cache* caches, int32_t num_caches, int64_t num_b
  * not made (IDX_ST_NO_BLOCKS): its child gets length and pages 0.  A fork whose
  * child is a parent in the same call, or the child of another fork, or that has
  * a request outside [0, num_reqs), is not made and changes nothing
- * (IDX_ST_BAD_FORK); one with child -1 is none (a captured call's empty places).  What a child owned before is not released.  Table
+ * (IDX_ST_BAD_FORK); one with child -1 is none, whatever its parent (a captured
+ * call's empty places).  What a child owned before is not released.  Table
  * entries outside [0, num_blocks) are passed on, not counted, and not copied
  * from (IDX_ST_BLOCK_OOR).
  *
@@ -850,7 +851,7 @@ int idx_fork_pages(const idx_cache* caches, int32_t num_caches, int64_t num_bloc
  * skipped, others outside [0, num_blocks) too (IDX_ST_BLOCK_OOR).
  *
  *   keep_lens, owned_pages, pages_out   [num_reqs] int32 (a finished request
- *                 keeps 0); pages_out is another array than owned_pages
+ *                 keeps 0); pages_out is an array of its own
  *   block_table   [num_reqs, bt_stride] int32;  refs [num_blocks] int32, in and
  *                 out, as in idx_fork_pages
  *   free_blocks   [num_free] int32, in and out; free_cursor and cursor_out at

@@ -145,11 +145,12 @@ def fork(caches, parents, children, ctx, owned, table, refs, free, cursor, page,
     reqs, width = table.shape
     status, taken = 0, 0
     old = (ctx.copy(), owned.copy(), table.copy())
+    parents_of = [p for p, c in zip(parents, children) if c != -1]
     for f in range(len(parents)):
         p, c = parents[f], children[f]
         if c == -1:
             continue
-        if not (0 <= p < reqs and 0 <= c < reqs) or c in parents or list(children).count(c) > 1:
+        if not (0 <= p < reqs and 0 <= c < reqs) or c in parents_of or list(children).count(c) > 1:
             status |= 64
             continue
         own = min(max(old[1][p], 0), width)

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreadsC) k_fork(const __grid_constant__ Fork
   for (int j = tid; j < a.num_forks; j += kThreadsC) {
     const int c = a.children[j], p = a.parents[j];
     if (c >= 0 && c < a.num_reqs && (atomicOr(&child[c >> 5], 1u << (c & 31)) >> (c & 31) & 1u)) atomicOr(&bad[c >> 5], 1u << (c & 31));
-    if (p >= 0 && p < a.num_reqs) atomicOr(&bad[p >> 5], 1u << (p & 31));
+    if (c != -1 && p >= 0 && p < a.num_reqs) atomicOr(&bad[p >> 5], 1u << (p & 31));
   }
   __syncthreads();
   // tokens of fork j; -1: it is not made
@@ -444,7 +444,7 @@ extern "C" int idx_release_pages(const int32_t* keep_lens, const int32_t* owned_
   if (num_reqs > 65535 || num_blocks > 0x7FFFFFFF) return IDX_E_TOO_LARGE;
   if (!free_cursor || !cursor_out || (num_free > 0 && !free_blocks) || (num_blocks > 0 && !refs)) return IDX_E_NULL_PTR;
   if (num_reqs > 0 && (!keep_lens || !owned_pages || !pages_out || (max_blocks > 0 && !block_table))) return IDX_E_NULL_PTR;
-  if (free_cursor == cursor_out || (num_reqs > 0 && owned_pages == pages_out)) return IDX_E_BAD_SHAPE;
+  if (free_cursor == cursor_out || (num_reqs > 0 && (owned_pages == pages_out || keep_lens == pages_out))) return IDX_E_BAD_SHAPE;
   for (const void* p : {(const void*)keep_lens, (const void*)owned_pages, (const void*)block_table, (const void*)refs, (const void*)free_blocks,
                         (const void*)free_cursor, (const void*)cursor_out, (const void*)pages_out, (const void*)status})
     if (!aligned(p, 4)) return IDX_E_MISALIGNED;

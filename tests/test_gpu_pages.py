@@ -230,6 +230,9 @@ def test_forks_that_are_none(lib):
     """Empty places of a call, and a call of none: the cursor is passed on."""
     Pool([5, 6, 7], reqs=6).fork(lib, [0, 7, 2], [3, -1, 5])
     Pool([5, 6, 7], reqs=6).fork(lib, [0], [-1])
+    p = Pool([5, 6, 7], reqs=6)
+    p.fork(lib, [0, 4, -9], [4, -1, -1])  # whatever the parent there
+    assert p.owned[4] == p.owned[0] > 0
     Pool([5, 6, 7], reqs=6).fork(lib, np.zeros(0, dtype=np.int32), np.zeros(0, dtype=np.int32))
 
 

@@ -81,6 +81,12 @@ def test_settle():
     assert ctx[0] == 13 and list(counts[0]) == [0, 2, 1]
 
 
+def test_a_place_without_a_fork_names_no_parent():
+    ctx, owned, table = np.array([6, 0, 0]), np.array([2, 0, 0]), np.array([[3, 1], [-1, -1], [-1, -1]])
+    _, ctx, owned, table, refs, cursor, status = serve.fork([], [0, 1], [1, -1], ctx, owned, table, np.zeros(5, dtype=np.int32), np.array([0, 2, 4]), 0, 4, 5)
+    assert status == 0 and list(ctx) == [6, 6, 0] and list(owned) == [2, 2, 0] and list(table[1]) == [3, 0] and list(refs) == [0, 0, 0, 1, 0] and cursor == 1
+
+
 @pytest.mark.parametrize("seed", range(4))
 def test_forks_and_releases_balance(seed):
     """Random forks, then everything released: every block comes back once."""

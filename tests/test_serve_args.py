@@ -97,6 +97,11 @@ def test_release_pages(lib):
         (8, None, E_NULL), (10, None, E_NULL), (11, None, E_NULL), (12, None, E_NULL), (6, A + 2, E_MIS)])
 
 
+def test_release_pages_writes_no_input(lib):
+    good = [A, A + 64, 5, A, 10, 10, A, 30, A, 7, A, A + 4, A + 128, 16, None, None]
+    refuse(lib.load_library().idx_release_pages, good, [(12, A, E_SHAPE)])
+
+
 def calls(idx, device):
     """Each function with arguments that pass every check but, perhaps, that of the device."""
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)
