@@ -91,6 +91,32 @@ __device__ __forceinline__ Eight<T> load8(const T* p) {
   return x;
 }
 
+// The same as two fours, from p and q on.
+template <typename T, bool kWide>
+__device__ __forceinline__ Eight<T> load4x2(const T* p, const T* q) {
+  Eight<T> x;
+  constexpr int kN = Eight<T>::kN / 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const T* from = i == 0 ? p : q;
+    if (kWide && sizeof(T) == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(from);
+      x.w[kN * i] = v.x, x.w[kN * i + 1] = v.y, x.w[kN * i + kN - 2] = v.z, x.w[kN * i + kN - 1] = v.w;
+    } else if (kWide) {
+      const uint2 v = *reinterpret_cast<const uint2*>(from);
+      x.w[kN * i] = v.x, x.w[kN * i + 1] = v.y;
+    } else if (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) x.w[kN * i + e] = reinterpret_cast<const uint32_t*>(from)[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        x.w[kN * i + e] = (uint32_t) reinterpret_cast<const uint16_t*>(from)[2 * e] | (uint32_t) reinterpret_cast<const uint16_t*>(from)[2 * e + 1] << 16;
+    }
+  }
+  return x;
+}
+
 // A number as hi + lo, hi the nearest fp32 to it.
 struct Two {
   float hi, lo;
@@ -248,6 +274,53 @@ __device__ __forceinline__ float turn8(const Eight<T>& x, const Place& p, const 
   }
   return ss.x + ss.y;
 }
+// A query's lane has both elements of its pairs: fours of elements from a0 and from a1 on.
+struct Fours {
+  int a0, a1;
+  bool turns;
+};
+template <bool kInter>
+__device__ __forceinline__ Fours fours_of(int lane, int rd) {
+  const int piece = lane % kLanesI;
+  if (!kInter && 8 * piece < rd) return {4 * piece, rd / 2 + 4 * piece, true};
+  return {8 * piece, 8 * piece + 4, 8 * piece < rd};
+}
+template <bool kInter>
+__device__ __forceinline__ Piece8 factors_of(const Fours& p, const float* w, const float4* turns) {
+  Piece8 f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = (e < 2 ? p.a0 : p.a1) + 2 * (e & 1), mate = (e < 2 ? p.a1 : p.a0) + 2 * (e & 1);
+    const float w0 = w[i], w1 = w[i + 1];
+    if (p.turns && kInter) {
+      const float x = turns[i / 2].x, y = turns[i / 2].z;
+      f.c[e] = make_float2(x * w0, x * w1), f.s[e] = make_float2(-y * w1, y * w0);
+    } else if (p.turns) {
+      const float4 t0 = turns[p.a0 + 2 * (e & 1)], t1 = turns[p.a0 + 2 * (e & 1) + 1];
+      const float y0 = t0.z * w[mate], y1 = t1.z * w[mate + 1];
+      f.c[e] = make_float2(t0.x * w0, t1.x * w1);
+      f.s[e] = e < 2 ? make_float2(-y0, -y1) : make_float2(y0, y1);
+    } else {
+      f.c[e] = make_float2(w0, w1), f.s[e] = make_float2(0.f, 0.f);
+    }
+  }
+  return f;
+}
+template <typename T, bool kInter>
+__device__ __forceinline__ float turn4x2(const Eight<T>& x, const Piece8& f, float2 (&u)[4], float2 (&mag)[4]) {
+  float2 one[4], ss = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) one[e] = Words<T>::get(x.w, e);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 part = mul2(kInter ? make_float2(one[e].y, one[e].x) : one[e ^ 2], f.s[e]);
+    u[e] = fma2(one[e], f.c[e], part);
+    const float2 own = fma2(part, make_float2(-1.f, -1.f), u[e]);  // x cw, but for a rounding of u
+    mag[e] = make_float2(fabsf(own.x) + fabsf(part.x), fabsf(own.y) + fabsf(part.y));
+    ss = fma2(one[e], one[e], ss);
+  }
+  return ss.x + ss.y;
+}
 __device__ __forceinline__ float largest8(const float2 (&u)[4]) {
   float m = 0.f;
 #pragma unroll
@@ -285,18 +358,25 @@ __device__ __noinline__ void again_64(const T* x, const float* w, const float4* 
   uint32_t codes[2] = {__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410)};
   if (!(ss <= 3.4e38f) || !(most > 7.9e-31f)) live = false, near = tops = 0;  // (its codes stand)
   const Row64<T> row{x, w, turns, rd};
-  double top = 0.0;
-  for (uint32_t m = tops; m != 0; m &= m - 1) top = fmax(top, fabs(row.template u<kInter>(p.at + __ffs(m) - 1)));
+  long long most_64 = 0;  // the largest magnitude's bits
+  for (uint32_t m = tops; m != 0; m &= m - 1) {
+    const long long bits = __double_as_longlong(row.template u<kInter>(p.at + __ffs(m) - 1)) & 0x7FFFFFFFFFFFFFFFll;
+    most_64 = bits > most_64 ? bits : most_64;
+  }
 #pragma unroll
-  for (int o = 1; o < kLanesI; o <<= 1) top = fmax(top, shfl_xor_64(top, o));
+  for (int o = 1; o < kLanesI; o <<= 1) {
+    const long long bits = __double_as_longlong(shfl_xor_64(__longlong_as_double(most_64), o));
+    most_64 = bits > most_64 ? bits : most_64;
+  }
+  const double top = __longlong_as_double(most_64);
   for (; near != 0; near &= near - 1) {
     const int e = __ffs(near) - 1;
     const double y = row.template u<kInter>(p.at + e), v = 448.0 * fabs(y);
-    // from a code at or below the value, up while the middle to the next one is (halves to even)
-    uint32_t code = f32x2_to_e4m3x2(__double2float_rz(v / top) * (1.f - kSlack), 0.f) & 0x7Fu;
-    if (code > 0) --code;
+    // from the lower end's code up while the middle to the next one is (halves to even)
+    const uint32_t l = low[e / 2] >> (8 * (e % 2)) & 0xFFu, h = high[e / 2] >> (8 * (e % 2)) & 0xFFu;
+    uint32_t code = (l ^ h) & 0x80u ? 0u : min(l, h) & 0x7Fu;
     for (; code < 0x7Eu; ++code) {
-      const double edge = 0.5 * ((double)e4m3_to_f32(code) + (double)e4m3_to_f32(code + 1)) * top;
+      const double edge = (double)(0.5f * (e4m3_to_f32(code) + e4m3_to_f32(code + 1))) * top;
       if (!(v > edge || (v == edge && (code & 1u)))) break;
     }
     code |= y < 0.0 ? 0x80u : 0u;
@@ -318,7 +398,7 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int num_reqs, int t
 }
 
 template <typename T, bool kInter, bool kWide>
-__global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid_constant__ IndexArgs a, int parts, int key_part) {
+__global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid_constant__ IndexArgs a, int64_t warps) {
   pdl_enter();
   __shared__ float4 turns_[kThreadsI / 32][kHeadDim / 2];  // cosines and sines of a warp's token, each in two numbers
   __shared__ unsigned long long steps[kHeadDim / 2];
@@ -326,6 +406,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rd = a.rotary_dim, half = rd / 2, sub = lane / kLanesI, piece = lane % kLanesI;
   const Place p = place_of<kInter>(lane, rd);
+  const Fours fours = fours_of<kInter>(lane, rd);
   const int at = p.at;
   for (int i = threadIdx.x; i < half; i += kThreadsI) steps[i] = step_of(a.inv_freq[i]);
   for (int i = threadIdx.x; i < kHeadDim; i += kThreadsI) {
@@ -334,13 +415,15 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
   }
   __syncthreads();
   float4* mine = turns_[warp];
-  const int rows = (a.heads + 1) / 2;
-  const int all = parts + (key_part ? 1 : 0);
-  const int64_t tasks = (int64_t)a.num_tokens * all;
-  for (int64_t task = (int64_t)blockIdx.x * (kThreadsI / 32) + warp; task < tasks; task += (int64_t)gridDim.x * (kThreadsI / 32)) {
-    const int t = (int)(task / all), part = (int)(task - (int64_t)t * all);
+  // A token's units: batches of steps of two heads, then its key.  Every warp takes as many units, one after another.
+  const int rows = (a.heads + 1) / 2, batches = (rows + kBatchI - 1) / kBatchI, units = batches + (a.k != nullptr ? 1 : 0);
+  const int64_t all = (int64_t)a.num_tokens * units, number = (int64_t)blockIdx.x * (kThreadsI / 32) + warp;
+  const int64_t last = number < warps ? all * (number + 1) / warps : 0;
+  for (int64_t unit = number < warps ? all * number / warps : 0; unit < last;) {
+    const int t = (int)(unit / units), first = (int)(unit - (int64_t)t * units), past = (int)min((int64_t)units, first + (last - unit));
+    unit += past - first;
     const int position = a.positions[t];
-    __syncwarp();  // the angles of the task before are used up
+    __syncwarp();  // the angles of the token before are used up
     for (int i = lane; i < half; i += 32) {
       Two c, s;
       turn_of_two(steps[i] * (unsigned long long)(long long)position, &c, &s);
@@ -348,29 +431,30 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
       mine[i] = make_float4(c.hi, c.lo, s.hi, s.lo);
     }
     __syncwarp();
-    if (a.heads > 0 && part < parts) {
-      const Piece8 f = factors_of<kInter>(p, weights[0], mine);
+    if (first < batches) {
+      const Piece8 f = factors_of<kInter>(fours, weights[0], mine);
       int64_t out = (int64_t)t * a.heads;  // the token's first row
       bool stored = true;
       if (a.cu != nullptr) {
         const int r = request_of(a.cu, a.num_reqs, t, lane);
         const int begin = a.cu[r], end = a.cu[r + 1], slot = a.req_slots - end + t;
         stored = t >= begin && t < end && slot >= 0;
-        if (t >= begin && t < end && slot < 0 && lane == 0 && part == 0) report(a.status, IDX_ST_BAD_OUTPUT);
+        if (t >= begin && t < end && slot < 0 && lane == 0 && first == 0) report(a.status, IDX_ST_BAD_OUTPUT);
         out = ((int64_t)r * a.req_slots + slot) * a.heads;
       }
-      const int r0 = rows * part / parts, r1 = rows * (part + 1) / parts;
+      const int r0 = first * kBatchI, r1 = min(rows, past * kBatchI);
       const T* row0 = static_cast<const T*>(a.q) + (int64_t)t * a.q_ts;
       if (stored) {
         uint64_t open = 0;  // steps whose codes lie near a border (at most 64 heads' worth: kMtpMaxHeads / 2)
         Eight<T> ahead[kBatchI];
-        const T* src = row0 + (int64_t)(2 * r0 + sub) * a.q_hs + at;
-        uint8_t* dst = a.q_out + (out + 2 * r0 + sub) * kHeadDim + at;
+        const T* src = row0 + (int64_t)(2 * r0 + sub) * a.q_hs + fours.a0;
+        uint8_t* dst = a.q_out + (out + 2 * r0 + sub) * kHeadDim + fours.a0;
+        const int apart = fours.a1 - fours.a0;
         const int64_t step = 2 * a.q_hs;
         auto ask = [&](int g) {
 #pragma unroll
           for (int b = 0; b < kBatchI; ++b) {
-            if (g + b < r1 && 2 * (g + b) + sub < a.heads) ahead[b] = load8<T, kWide>(src + b * step);
+            if (g + b < r1 && 2 * (g + b) + sub < a.heads) ahead[b] = load4x2<T, kWide>(src + b * step, src + b * step + apart);
             else ahead[b] = Eight<T>{};
           }
         };
@@ -384,7 +468,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
           float2 u[kBatchI][4], mag[kBatchI][4];
           float ss[kBatchI], top[kBatchI];
 #pragma unroll
-          for (int b = 0; b < kBatchI; ++b) ss[b] = turn8<T, kInter>(x[b], p, f, u[b], mag[b]), top[b] = largest8(u[b]);
+          for (int b = 0; b < kBatchI; ++b) ss[b] = turn4x2<T, kInter>(x[b], f, u[b], mag[b]), top[b] = largest8(u[b]);
 #pragma unroll
           for (int o = 1; o < kLanesI; o <<= 1) {
 #pragma unroll
@@ -399,11 +483,14 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
             uint32_t low[4], high[4];
             both_ends(u[b], mag[b], inv, low, high);
             const uint32_t differ = (low[0] ^ high[0]) | (low[1] ^ high[1]) | (low[2] ^ high[2]) | (low[3] ^ high[3]);
-            if (__any_sync(0xFFFFFFFFu, differ != 0)) open |= 1ull << (g + b - r0);
+            if (differ != 0) open |= 1ull << (g + b - r0);
             uint2 codes = make_uint2(__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410));
             if (inv == 0.f) codes = make_uint2(0u, 0u);
             if (!(ss[b] <= 3.4e38f)) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            if (g + b < r1 && 2 * (g + b) + sub < a.heads) *reinterpret_cast<uint2*>(dst + b * 2 * kHeadDim) = codes;
+            if (g + b < r1 && 2 * (g + b) + sub < a.heads) {
+              *reinterpret_cast<uint32_t*>(dst + b * 2 * kHeadDim) = codes.x;
+              *reinterpret_cast<uint32_t*>(dst + b * 2 * kHeadDim + apart) = codes.y;
+            }
           }
           dst += kBatchI * 2 * kHeadDim;
           // the scales: a lane each
@@ -421,13 +508,16 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
             }
           }
         }
+        // (a vote for each step took 11 us)
+        open = __reduce_or_sync(0xFFFFFFFFu, (uint32_t)open) | (uint64_t)__reduce_or_sync(0xFFFFFFFFu, (uint32_t)(open >> 32)) << 32;
+        if (open != 0) __syncwarp();  // the codes are stored, by other lanes than those that store them now
         for (; open != 0; open &= open - 1) {
           const int h = 2 * (r0 + __ffsll(open) - 1) + sub;
           again_64<T, kInter, kWide>(row0 + (int64_t)min(h, a.heads - 1) * a.q_hs, weights[0], mine, rd, a.q_out + (out + h) * kHeadDim, h < a.heads);
         }
       }
     }
-    if (a.k != nullptr && part == all - 1) {
+    if (a.k != nullptr && past == units) {
       const int64_t slot = a.slots != nullptr ? a.slots[t] : t;
       if (slot >= a.num_slots && lane == 0) report(a.status, IDX_ST_BLOCK_OOR);
       if (slot >= 0 && slot < a.num_slots) {
@@ -476,23 +566,17 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
 
 template <typename T>
 void launch_index(const IndexArgs& a, bool inter, bool wide, cudaStream_t s) {
-  const int sms = max(device_sms(), 1), rows = (a.heads + 1) / 2;
-  // Warps that run at once.  A token's heads in parts while there are not enough tokens, and where it evens out what a warp
-  // has to do: eight tasks each, of at least eight steps.
-  const int64_t room = (int64_t)sms * kCtasI * (kThreadsI / 32);
-  const int most = max(1, (rows + kBatchI - 1) / kBatchI);
-  const int64_t want = (8 * room + a.num_tokens - 1) / a.num_tokens, fill = (room + a.num_tokens - 1) / a.num_tokens;
-  const int parts = a.heads == 0 ? 0 : (int)min((int64_t)most, max(fill, min(want, (int64_t)max(1, most / 8))));
-  // the key is a task of its own while there is room: its row waits for no other
-  const int key_part = a.k != nullptr && (parts == 0 || (int64_t)a.num_tokens * (parts + 1) <= room);
-  const int64_t ctas = ((int64_t)a.num_tokens * (parts + key_part) + kThreadsI / 32 - 1) / (kThreadsI / 32);
-  const dim3 grid((unsigned)min(ctas, (int64_t)sms * kCtasI)), block(kThreadsI);
+  const int rows = (a.heads + 1) / 2;
+  const int64_t all = (int64_t)a.num_tokens * ((rows + kBatchI - 1) / kBatchI + (a.k != nullptr ? 1 : 0));
+  // a unit a warp, or an equal number of them a warp of those that run at once
+  const int64_t warps = min(all, (int64_t)max(device_sms(), 1) * kCtasI * (kThreadsI / 32));
+  const dim3 grid((unsigned)((warps + kThreadsI / 32 - 1) / (kThreadsI / 32))), block(kThreadsI);
   if (inter) {
-    if (wide) launch_pdl(k_index_append<T, true, true>, grid, block, 0, s, a, parts, key_part);
-    else launch_pdl(k_index_append<T, true, false>, grid, block, 0, s, a, parts, key_part);
+    if (wide) launch_pdl(k_index_append<T, true, true>, grid, block, 0, s, a, warps);
+    else launch_pdl(k_index_append<T, true, false>, grid, block, 0, s, a, warps);
   } else {
-    if (wide) launch_pdl(k_index_append<T, false, true>, grid, block, 0, s, a, parts, key_part);
-    else launch_pdl(k_index_append<T, false, false>, grid, block, 0, s, a, parts, key_part);
+    if (wide) launch_pdl(k_index_append<T, false, true>, grid, block, 0, s, a, warps);
+    else launch_pdl(k_index_append<T, false, false>, grid, block, 0, s, a, warps);
   }
 }
 
