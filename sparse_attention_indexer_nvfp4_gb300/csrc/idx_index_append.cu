@@ -19,13 +19,16 @@
 // between the codes.  A key whose codes or scales may differ is formed again as
 // a whole.
 //
-// Bound by the instructions and latencies of a row: 8,191 tokens of 64 heads take
-// 105 us, 0.29 of HBM (without the look for borders 75; with angles in 64-bit
-// floating point 127; 2, 3 and 4 CTAs of 256 threads an SM 115 to 117, 5 of 128
-// 105).  512 tokens of 4 heads take 9 us.  A warp
-// takes a token (with few tokens a part of its heads), 16 lanes a row, 8
-// elements a lane; cosines, sines and weights are folded into a lane's factors
-// once a token.  A key's scale byte belongs to two lanes.
+// Bound by the instructions of a row (about 220 a warp for two heads): 8,191
+// tokens of 64 heads take 91 us, 0.34 of HBM; without forming the elements near a
+// border again about 8 less, with angles in 64-bit floating point 20 more; 4 and 6
+// CTAs of 128 threads an SM 94 and 96.  512 tokens of 4 heads take 8 us.  A query's
+// row is 16 lanes', both elements of a pair in one (passed between lanes they took
+// as long, and more registers); cosines, sines and weights are folded into a
+// lane's factors once a token; a lane forms the scale of one row in 16.  Every warp
+// takes as many batches of heads as the others, whichever tokens they are of (whole
+// parts of tokens left SMs idle: 105).  A key's row keeps 8 elements in a row a
+// lane: two lanes have a block.
 #include "idx_internal.h"
 #include "idx_rope.cuh"
 
@@ -449,12 +452,13 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
         Eight<T> ahead[kBatchI];
         const T* src = row0 + (int64_t)(2 * r0 + sub) * a.q_hs + fours.a0;
         uint8_t* dst = a.q_out + (out + 2 * r0 + sub) * kHeadDim + fours.a0;
-        const int apart = fours.a1 - fours.a0;
+        const int apart = fours.a1 - fours.a0, mine_to = min(r1, (a.heads - sub + 1) / 2);  // this half's steps
+        float kept_sq = 0.f, kept_top = 0.f;  // of the step that this lane forms the scale of
         const int64_t step = 2 * a.q_hs;
         auto ask = [&](int g) {
 #pragma unroll
           for (int b = 0; b < kBatchI; ++b) {
-            if (g + b < r1 && 2 * (g + b) + sub < a.heads) ahead[b] = load4x2<T, kWide>(src + b * step, src + b * step + apart);
+            if (g + b < mine_to) ahead[b] = load4x2<T, kWide>(src + b * step, src + b * step + apart);
             else ahead[b] = Eight<T>{};
           }
         };
@@ -485,26 +489,23 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
             const uint32_t differ = (low[0] ^ high[0]) | (low[1] ^ high[1]) | (low[2] ^ high[2]) | (low[3] ^ high[3]);
             if (differ != 0) open |= 1ull << (g + b - r0);
             uint2 codes = make_uint2(__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410));
-            if (inv == 0.f) codes = make_uint2(0u, 0u);
-            if (!(ss[b] <= 3.4e38f)) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            if (g + b < r1 && 2 * (g + b) + sub < a.heads) {
+            if (inv == 0.f || !(ss[b] <= 3.4e38f)) codes = ss[b] <= 3.4e38f ? make_uint2(0u, 0u) : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (g + b < mine_to) {
               *reinterpret_cast<uint32_t*>(dst + b * 2 * kHeadDim) = codes.x;
               *reinterpret_cast<uint32_t*>(dst + b * 2 * kHeadDim + apart) = codes.y;
             }
+            if (piece == ((g + b - r0) & (kLanesI - 1))) kept_sq = ss[b], kept_top = top[b];
           }
           dst += kBatchI * 2 * kHeadDim;
-          // the scales: a lane each
-          if (piece < kBatchI) {
-            const int h = 2 * (g + piece) + sub;
-            float sq = ss[0], most = top[0];
-#pragma unroll
-            for (int b = 1; b < kBatchI; ++b)
-              if (piece == b) sq = ss[b], most = top[b];
-            if (g + piece < r1 && h < a.heads) {
-              const float r = a.q_w != nullptr ? rsqrtf(fmaf(sq, 1.f / kHeadDim, a.eps)) : 1.f;
-              float scale = most * r * (1.f / 448.f) * a.scale;
+          const int done = g + kBatchI - r0;
+          if (done % kLanesI == 0 || g + kBatchI >= r1) {
+            // the scales of the last steps, a lane each
+            const int step_of_lane = r0 + (done - 1) / kLanesI * kLanesI + piece, h = 2 * step_of_lane + sub;
+            if (step_of_lane < mine_to) {
+              const float r = a.q_w != nullptr ? rsqrtf(fmaf(kept_sq, 1.f / kHeadDim, a.eps)) : 1.f;
+              float scale = kept_top * r * (1.f / 448.f) * a.scale;
               if (a.head_weights != nullptr) scale *= a.head_weights[(int64_t)t * a.heads + h];
-              a.q_scale[out + h] = sq <= 3.4e38f ? scale : __int_as_float(0x7FC00000);
+              a.q_scale[out + h] = kept_sq <= 3.4e38f ? scale : __int_as_float(0x7FC00000);
             }
           }
         }

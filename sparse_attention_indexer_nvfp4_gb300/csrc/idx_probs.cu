@@ -285,10 +285,8 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       }
     }
   };
-  // an entry as it becomes
-  auto changed_value = [&](int i, float y, int c, bool biased, float bias) {
-    int times = c & 0x7FFFFFFF;
-    for (int j = 0; j < n_path; ++j) times += path[j] == lo + i;
+  // an entry as it becomes, which the request has `times` times
+  auto value_of = [&](int i, float y, int c, int times, bool biased, float bias) {
     if (c < 0 || times > 0) y = y > 0.f ? __fdiv_rn(y, repetition) : __fmul_rn(y, repetition);
     if (times > 0) y = __fsub_rn(y, __fadd_rn(__fmul_rn(frequency, (float)times), presence));
     if (biased) {
@@ -300,6 +298,11 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       }
     }
     return y;
+  };
+  auto changed_value = [&](int i, float y, int c, bool biased, float bias) {
+    int times = c & 0x7FFFFFFF;
+    for (int j = 0; j < n_path; ++j) times += path[j] == lo + i;
+    return value_of(i, y, c, times, biased, bias);
   };
 
   for (int t = t_lo; t < t_hi; ++t) {
@@ -574,14 +577,31 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       }
       mass.s = sum.x + sum.y;
     }
-    // the changed entries
+    // the changed entries, all of a thread's together
+    {
+      int times[kFixP], entry[kFixP];
+      float top = kNegInf;
 #pragma unroll
-    for (int u = 0; u < kFixP; ++u) {
-      const int at = tid + u * kThreadsP;
-      if (at >= changed || !(fix_mask[u] >> (list[at] & 31) & 1u)) continue;
-      on |= 1u << u;
-      fix[u] = changed_value(list[at] & ~kBiased, fix[u], fix_c[u], (list[at] & kBiased) && b1 > b0, fix_b[u]);
-      mass.add(fix[u], k);
+      for (int u = 0; u < kFixP; ++u) {
+        const int at = tid + u * kThreadsP;
+        entry[u] = at < changed ? list[at] : 0, times[u] = fix_c[u] & 0x7FFFFFFF;
+        if (at < changed && (fix_mask[u] >> (entry[u] & 31) & 1u)) on |= 1u << u;
+      }
+      for (int j = 0; j < n_path; ++j) {
+        const int i = path[j] - lo;
+#pragma unroll
+        for (int u = 0; u < kFixP; ++u) times[u] += i == (entry[u] & ~kBiased);
+      }
+#pragma unroll
+      for (int u = 0; u < kFixP; ++u) {
+        if (!(on >> u & 1u)) continue;
+        fix[u] = value_of(entry[u] & ~kBiased, fix[u], fix_c[u], times[u], (entry[u] & kBiased) && b1 > b0, fix_b[u]);
+        top = fmaxf(top, fix[u]);
+      }
+      mass.raise(top, k);
+#pragma unroll
+      for (int u = 0; u < kFixP; ++u)
+        if (on >> u & 1u) mass.s += ex2((fix[u] - mass.base()) * k);
     }
     if (many) each_word([&](int, float y) { mass.add(y, k); });
     if (extra >= 0 && (!(extra_mask >> (extra & 31) & 1u) || !comes_first(tid, extra))) extra = -1;
