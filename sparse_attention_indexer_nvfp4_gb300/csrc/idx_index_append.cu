@@ -15,20 +15,21 @@
 // element), and the scaling add 11: 15 M for 448 u / max|u|.  A norm's r is off
 // by 9, a key's y / s by 16 M in all.  So each element is converted at both ends
 // of kSlack (kSlackKey) times M around it; where the two codes differ (0.5% of
-// the rows) the element is formed again in 64 bits and compared with the middle
-// between the codes.  A key whose codes or scales may differ is formed again as
-// a whole.
+// the rows) the element is formed again as a pair of fp32 numbers (exact products,
+// 2^-44) and compared with the middle between the codes.  A key whose codes or
+// scales may differ is formed again as a whole, in 64 bits.
 //
 // Bound by the instructions of a row (about 220 a warp for two heads): 8,191
-// tokens of 64 heads take 91 us, 0.34 of HBM; without forming the elements near a
-// border again about 8 less, with angles in 64-bit floating point 20 more; 4 and 6
-// CTAs of 128 threads an SM 94 and 96.  512 tokens of 4 heads take 8 us.  A query's
-// row is 16 lanes', both elements of a pair in one (passed between lanes they took
-// as long, and more registers); cosines, sines and weights are folded into a
-// lane's factors once a token; a lane forms the scale of one row in 16.  Every warp
-// takes as many batches of heads as the others, whichever tokens they are of (whole
-// parts of tokens left SMs idle: 105).  A key's row keeps 8 elements in a row a
-// lane: two lanes have a block.
+// tokens of 64 heads take 89 us, 0.35 of HBM; without the look for borders 68,
+// with 64-bit floating point for the elements near one 91, for the angles about
+// 20 more; 4 and 6 CTAs of 128 threads an SM 91 and 95.  512 tokens of 4 heads take
+// 8 us.  A query's row is 16 lanes', both elements of a pair in one (passed between
+// lanes they took as long); cosines, sines and weights are folded into a lane's
+// factors once a token; a lane forms the scale of one row in 16.  Every warp takes
+// as many batches of heads as the others, whichever tokens they are of (whole parts
+// of tokens left SMs idle: 105).  Rows near a border put off to the end of a CTA and
+// shared among its warps took 97.  A key's row keeps 8 elements in a row a lane: two
+// lanes have a block.
 #include "idx_internal.h"
 #include "idx_rope.cuh"
 
@@ -132,6 +133,15 @@ __device__ __forceinline__ Two times(Two a, Two b) {
   const float p = __fmul_rn(a.hi, b.hi);
   return two_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p))));
 }
+__device__ __forceinline__ Two plus(Two a, Two b) {  // of any magnitudes, to 2^-46 of the larger one
+  const float s = __fadd_rn(a.hi, b.hi), from_b = __fsub_rn(s, a.hi);
+  const float lo = __fadd_rn(__fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, from_b)), __fsub_rn(b.hi, from_b)), __fadd_rn(a.lo, b.lo));
+  const float t = __fadd_rn(s, lo), from_lo = __fsub_rn(t, s);
+  return {t, __fadd_rn(__fsub_rn(s, __fsub_rn(t, from_lo)), __fsub_rn(lo, from_lo))};
+}
+__device__ __forceinline__ Two negative(Two a) { return {-a.hi, -a.lo}; }
+__device__ __forceinline__ Two magnitude(Two a) { return a.hi < 0.f || (a.hi == 0.f && a.lo < 0.f) ? negative(a) : a; }
+__device__ __forceinline__ bool above(Two a, Two b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 // c + a b, where |c| is larger than |a b|
 __device__ __forceinline__ Two plus_times(Two c, Two a, Two b) {
   const Two p = times(a, b), s = two_sum(c.hi, p.hi);
@@ -184,6 +194,19 @@ struct Row64 {
     return second ? fma(n, cs.x, o * cs.y) : fma(n, cs.x, -(o * cs.y));
   }
 };
+
+// The same as pairs of fp32 numbers: products of elements and weights exactly, turned ones to 2^-44.
+template <typename T, bool kInter>
+__device__ __forceinline__ Two element_of(const T* x, const float* w, const float4* turns, int rd, int e) {
+  const Two n = times(Two{to_f(x[e]), 0.f}, Two{w[e], 0.f});
+  if (e >= rd) return n;
+  const int half = rd / 2, pair = kInter ? e / 2 : e < half ? e : e - half;
+  const int mate = kInter ? e ^ 1 : e < half ? e + half : e - half;
+  const bool second = kInter ? e & 1 : e >= half;
+  const float4 t = turns[pair];
+  const Two o = times(times(Two{to_f(x[mate]), 0.f}, Two{w[mate], 0.f}), Two{t.z, t.w});
+  return plus(times(n, Two{t.x, t.y}), second ? o : negative(o));
+}
 
 __device__ __forceinline__ double shfl_xor_64(double x, int o) {
   return __hiloint2double(__shfl_xor_sync(0xFFFFFFFFu, __double2hiint(x), o), __shfl_xor_sync(0xFFFFFFFFu, __double2loint(x), o));
@@ -342,10 +365,11 @@ __device__ __forceinline__ void both_ends(const float2 (&u)[4], const float2 (&m
   }
 }
 
-// A query's row again, whose codes may not all be right: those that lie near a border in 64 bits.  Each half of the warp has
+// A query's row again, whose codes may not all be right: those that lie near a border in pairs of fp32 numbers
+// (in 64-bit floating point, which is slow here, it took 15 us of 8,191 tokens).  Each half of the warp has
 // a row of its own; all lanes together.
 template <typename T, bool kInter, bool kWide>
-__device__ __noinline__ void again_64(const T* x, const float* w, const float4* turns, int rd, uint8_t* out, bool live) {
+__device__ __noinline__ void again(const T* x, const float* w, const float4* turns, int rd, uint8_t* out, bool live) {
   const Place p = place_of<kInter>(threadIdx.x & 31, rd);
   float2 u[4], mag[4];
   float ss = turn8<T, kInter>(load8<T, kWide>(x + p.at), p, factors_of<kInter>(p, w, turns), u, mag), most = largest8(u);
@@ -360,29 +384,27 @@ __device__ __noinline__ void again_64(const T* x, const float* w, const float4* 
   }
   uint32_t codes[2] = {__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410)};
   if (!(ss <= 3.4e38f) || !(most > 7.9e-31f)) live = false, near = tops = 0;  // (its codes stand)
-  const Row64<T> row{x, w, turns, rd};
-  long long most_64 = 0;  // the largest magnitude's bits
+  Two top{0.f, 0.f};  // the largest magnitude
   for (uint32_t m = tops; m != 0; m &= m - 1) {
-    const long long bits = __double_as_longlong(row.template u<kInter>(p.at + __ffs(m) - 1)) & 0x7FFFFFFFFFFFFFFFll;
-    most_64 = bits > most_64 ? bits : most_64;
+    const Two y = magnitude(element_of<T, kInter>(x, w, turns, rd, p.at + __ffs(m) - 1));
+    if (above(y, top)) top = y;
   }
 #pragma unroll
   for (int o = 1; o < kLanesI; o <<= 1) {
-    const long long bits = __double_as_longlong(shfl_xor_64(__longlong_as_double(most_64), o));
-    most_64 = bits > most_64 ? bits : most_64;
+    const Two y{__shfl_xor_sync(0xFFFFFFFFu, top.hi, o), __shfl_xor_sync(0xFFFFFFFFu, top.lo, o)};
+    if (above(y, top)) top = y;
   }
-  const double top = __longlong_as_double(most_64);
   for (; near != 0; near &= near - 1) {
     const int e = __ffs(near) - 1;
-    const double y = row.template u<kInter>(p.at + e), v = 448.0 * fabs(y);
+    const Two y = element_of<T, kInter>(x, w, turns, rd, p.at + e), v = times(Two{448.f, 0.f}, magnitude(y));
     // from the lower end's code up while the middle to the next one is (halves to even)
     const uint32_t l = low[e / 2] >> (8 * (e % 2)) & 0xFFu, h = high[e / 2] >> (8 * (e % 2)) & 0xFFu;
     uint32_t code = (l ^ h) & 0x80u ? 0u : min(l, h) & 0x7Fu;
     for (; code < 0x7Eu; ++code) {
-      const double edge = (double)(0.5f * (e4m3_to_f32(code) + e4m3_to_f32(code + 1))) * top;
-      if (!(v > edge || (v == edge && (code & 1u)))) break;
+      const Two edge = times(Two{0.5f * (e4m3_to_f32(code) + e4m3_to_f32(code + 1)), 0.f}, top);
+      if (!(above(v, edge) || (!above(edge, v) && (code & 1u)))) break;
     }
-    code |= y < 0.0 ? 0x80u : 0u;
+    code |= above(Two{0.f, 0.f}, y) ? 0x80u : 0u;
     codes[e / 4] = (codes[e / 4] & ~(0xFFu << (8 * (e & 3)))) | code << (8 * (e & 3));
   }
   if (live) *reinterpret_cast<uint2*>(out + p.at) = make_uint2(codes[0], codes[1]);
@@ -514,7 +536,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
         if (open != 0) __syncwarp();  // the codes are stored, by other lanes than those that store them now
         for (; open != 0; open &= open - 1) {
           const int h = 2 * (r0 + __ffsll(open) - 1) + sub;
-          again_64<T, kInter, kWide>(row0 + (int64_t)min(h, a.heads - 1) * a.q_hs, weights[0], mine, rd, a.q_out + (out + h) * kHeadDim, h < a.heads);
+          again<T, kInter, kWide>(row0 + (int64_t)min(h, a.heads - 1) * a.q_hs, weights[0], mine, rd, a.q_out + (out + h) * kHeadDim, h < a.heads);
         }
       }
     }
