@@ -383,7 +383,7 @@ __device__ __noinline__ void again(const T* x, const float* w, const float4* tur
     if (fabsf(e % 2 ? u[e / 2].y : u[e / 2].x) >= most * (1.f - 4.f * kSlack)) tops |= 1u << e;
   }
   uint32_t codes[2] = {__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410)};
-  if (!(ss <= 3.4e38f) || !(most > 7.9e-31f)) live = false, near = tops = 0;  // (its codes stand)
+  if (!(ss <= 3.4e38f) || inverse_of(most) == 0.f) live = false, near = tops = 0;  // (its codes stand)
   Two top{0.f, 0.f};  // the largest magnitude
   for (uint32_t m = tops; m != 0; m &= m - 1) {
     const Two y = magnitude(element_of<T, kInter>(x, w, turns, rd, p.at + __ffs(m) - 1));
@@ -394,14 +394,15 @@ __device__ __noinline__ void again(const T* x, const float* w, const float4* tur
     const Two y{__shfl_xor_sync(0xFFFFFFFFu, top.hi, o), __shfl_xor_sync(0xFFFFFFFFu, top.lo, o)};
     if (above(y, top)) top = y;
   }
+  const float unit = top.hi > 1.f ? 0x1p-9f : 1.f;  // (448 times the largest may pass fp32's range)
   for (; near != 0; near &= near - 1) {
     const int e = __ffs(near) - 1;
-    const Two y = element_of<T, kInter>(x, w, turns, rd, p.at + e), v = times(Two{448.f, 0.f}, magnitude(y));
+    const Two y = element_of<T, kInter>(x, w, turns, rd, p.at + e), v = times(Two{448.f * unit, 0.f}, magnitude(y));
     // from the lower end's code up while the middle to the next one is (halves to even)
     const uint32_t l = low[e / 2] >> (8 * (e % 2)) & 0xFFu, h = high[e / 2] >> (8 * (e % 2)) & 0xFFu;
     uint32_t code = (l ^ h) & 0x80u ? 0u : min(l, h) & 0x7Fu;
     for (; code < 0x7Eu; ++code) {
-      const Two edge = times(Two{0.5f * (e4m3_to_f32(code) + e4m3_to_f32(code + 1)), 0.f}, top);
+      const Two edge = times(Two{0.5f * unit * (e4m3_to_f32(code) + e4m3_to_f32(code + 1)), 0.f}, top);
       if (!(above(v, edge) || (!above(edge, v) && (code & 1u)))) break;
     }
     code |= above(Two{0.f, 0.f}, y) ? 0x80u : 0u;

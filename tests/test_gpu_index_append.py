@@ -106,6 +106,16 @@ def test_types_and_parts(lib, dtype, inter, rd):
     Case(lib, 77, 5, rd=rd, inter=inter, dtype=dtype, weigh=(False, False), mscale=1.25).check()
 
 
+@pytest.mark.parametrize("power", [119, 40, -40, -90])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_queries_near_the_ends_of_the_range(lib, dtype, power):
+    """Weights that make rows large or small: enough rows that some have elements near a border between codes."""
+    for inter in (False, True):
+        c = Case(lib, 1500, 8, inter=inter, dtype=dtype, keys=False, seed=power)
+        c.qw = (c.qw.double() * 2.0**power).to(c.qw.dtype)
+        c.check()
+
+
 @pytest.mark.parametrize("tokens,heads", [(1, 4), (1, 1), (513, 4), (300, 64), (19, 128), (40, 3), (0, 4), (9, 0)])
 def test_sizes(lib, tokens, heads):
     Case(lib, tokens, heads, hw=heads > 0).check()
