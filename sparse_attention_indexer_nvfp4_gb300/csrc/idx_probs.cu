@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
         if (a.mask == nullptr) path = a.tokens + begin + 1;  // (a chain's stay where they are)
         else if (tid < min(end - begin, kTreeP)) tokens[tid] = a.tokens[begin + tid];
         if (a.mask != nullptr && tid < min(end - begin, kTreeP)) masks[tid] = a.mask[begin + tid];
+        if (a.mask != nullptr) __syncthreads();  // put_path reads other threads' masks
       }
       changed = 0;
       if (any) {
