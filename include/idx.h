@@ -792,7 +792,8 @@ typedef struct {
  * (IDX_ST_BLOCK_OOR).  Rows of other places stay as they are.
  *
  *   caches        num_caches of num_blocks blocks of page_tokens tokens
- *   slots, cu_tokens, num_tokens   as idx_build_slots gives them
+ *   slots, cu_tokens, num_tokens   as idx_build_slots gives them; without caches
+ *                 nothing moves, slots are not read and may be NULL
  *   out_tokens, out_nodes [num_reqs, max_out], num_accepted   as
  *                 idx_verify_drafts gives them (out_tokens: with counts)
  *   ctx_lens, ctx_out   [num_reqs] int32; ctx_out may be ctx_lens

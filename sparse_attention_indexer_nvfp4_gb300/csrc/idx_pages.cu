@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreadsM) k_settle(const __grid_constant__ Se
       int64_t from = -1, to = -1;
       if (node < i + 1 || node >= n) {
         if (blockIdx.x == 0) report(a.status, IDX_ST_BAD_TREE);
-      } else if (node != i + 1) {
+      } else if (node != i + 1 && cs.num > 0) {  // (without caches no row has a place, and slots may be NULL)
         from = a.slots[t0 + node], to = a.slots[t0 + 1 + i];
         if ((from >= places || to >= places) && blockIdx.x == 0) report(a.status, IDX_ST_BLOCK_OOR);
         if (from < 0 || to < 0 || from >= places || to >= places) from = -1;
