@@ -96,6 +96,18 @@ __device__ __forceinline__ void norm_rows(const T* src, int64_t src_step, T* dst
 #pragma unroll
       for (int u = 0; u < kBatchN; ++u) r[u] = rsqrtf(fmaf(r[u], a.inv_dim, a.eps));
     }
+    float least = r[0];
+#pragma unroll
+    for (int u = 1; u < kBatchN; ++u) least = fminf(least, r[u]);
+    if (kNorm && __any_sync(0xFFFFFFFFu, least == 0.f)) {
+      // a squares' sum passed fp32's range, and the row's turn may: 0 for each of its elements, NaN for an infinity (a test
+      // of each row took 201 us where this takes what none takes)
+#pragma unroll
+      for (int u = 0; u < kBatchN; ++u) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) Words<T>::put(x[u].w, e, mul2(Words<T>::get(x[u].w, e), make_float2(0.f, 0.f)), r[u] == 0.f);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kBatchN; ++u) {
       R y;
@@ -252,6 +264,8 @@ __global__ void __launch_bounds__(kThreadsN) k_norm_any(const __grid_constant__ 
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     const float r = w != nullptr ? rsqrtf(fmaf(ss, a.inv_dim, a.eps)) : 1.f;
+    if (r == 0.f)  // (as in norm_rows)
+      for (int e = lane; e < dim; e += 32) row[e] = __fmul_rn(to_f(src[e]), 0.f);
     __syncwarp();
     const int position = a.positions[t];
     for (int p = lane; p < half; p += 32) {
