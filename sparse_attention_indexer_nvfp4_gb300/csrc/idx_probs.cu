@@ -26,6 +26,9 @@
 // 5,000, written 4,000, between them 2,500), and two CTAs an SM do not cover all of it.  512 threads a
 // CTA took 272 us, 3 CTAs of 256 with one buffer 219, 128 threads 257; entries
 // kept in fp32, one CTA an SM, 833.  One row of 32,000: 9.1 us, all latency.
+#include <algorithm>
+#include <atomic>
+
 #include "idx_internal.h"
 #include "idx_rope.cuh"
 
@@ -45,6 +48,8 @@ constexpr int kBitsP = IDX_PROBS_MAX_VOCAB / kClusterP / 32;  // words of a stre
 constexpr int kWordP = 4;      // words of special entries a warp takes at a time
 constexpr int kStretchP = 8192;  // entries of a CTA with counts, unless a row has 4 CTAs
 constexpr size_t kRoomP = 104 * 1024;  // dynamic shared memory of each of two CTAs an SM (which has 228 KB)
+// The most that a call takes: that, or one fp32 buffer of the longest stretch with its bits.
+constexpr size_t kMostP = std::max(kRoomP, (IDX_PROBS_MAX_VOCAB / kClusterP + 16) * sizeof(float) + (kBitsP + 2) * 8);
 constexpr int kBiased = 0x8000;  // an entry of the list that has a bias
 constexpr float kNegInf = -INFINITY;
 
@@ -759,7 +764,15 @@ int launch_probs(ProbArgs a, cudaStream_t s) {
   a.buffers = 2 * row + bits <= kRoomP ? 2 : 1;
   a.polls = wait_polls();
   const size_t smem = a.buffers * row + bits;
-  cudaFuncSetAttribute(k_logit_probs<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit belongs to the kernel, not to a call: it is set once a device to what the largest call takes.  (Set by each call
+  // to its own size, one host thread lowered it between another's and its launch.)
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return IDX_E_CUDA;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(k_logit_probs<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostP) != cudaSuccess) return IDX_E_CUDA;
+    ready[dev].store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreadsP);
   cfg.dynamicSmemBytes = smem;
