@@ -726,9 +726,9 @@ int idx_index_append(const void* q, int64_t q_token_stride, int64_t q_head_strid
  *     x <- -inf where the mask has no bit (whatever the logit is)
  *     p = e^(x / T - L),  L = ln sum e^(x / T)
  * With T = 0 (or below 2^-60, or NaN) p is 1 at the lowest v of the largest x
- * and 0 elsewhere, and L is that x.  A row with nothing left gets p 0 and L
- * -inf; one with a NaN or +inf that is not masked is NaN.  x, sums and p are
- * fp32.
+ * and 0 elsewhere, and L is that x.  With T infinite all entries above -inf get
+ * the same p.  A row with nothing left gets p 0 and L -inf; one with a NaN or
+ * +inf that is not masked is NaN.  x, x less the largest x, sums and p are fp32.
  * c is the count in `counts` plus, with tokens, that of v among the drafted
  * tokens of the row's path: nodes j >= 1 of tree_mask[t] (tree_mask NULL: 1 <=
  * j <= i).  Node 0's token is taken to be counted already, as idx_settle_drafts

@@ -108,7 +108,7 @@ def logit_probs(logits, cu, temperature=None, repetition=None, presence=None, fr
             if not heat > 2.0**-60:
                 p[t, np.argmax(x)], lse[t] = 1.0, x.max()
                 continue
-            x = x / heat
+            x[x > -np.inf] /= heat  # (an infinite T leaves out what is left out)
             e = np.exp(x - x.max())
             p[t], lse[t] = e / e.sum(), np.log(e.sum()) + x.max()
     return p, lse

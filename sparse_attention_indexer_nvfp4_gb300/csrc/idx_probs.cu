@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(kThreadsP, 2) k_logit_probs(const __grid_const
       if (to > from) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
     }
     const bool greedy = !(heat > 8.7e-19f);  // 2^-60
-    const float k = greedy ? 1.44269504f : 1.44269504f / heat;
+    // (not 0 where T is infinite: an entry at -inf, left out ones among them, times 0 would be NaN)
+    const float k = greedy ? 1.44269504f : fmaxf(1.44269504f / heat, 0x1p-149f);
 
     // The path of row t among its request's tokens; then its bits.
     auto put_path = [&](int t) {
