@@ -9,11 +9,12 @@
 //
 // The codes are those of 64-bit arithmetic.  Sines and cosines are formed to
 // 2^-44, once a token, by their Taylor series.  In units of 2^-24 of M = |x cw| +
-// |x_p sw|, u comes in fp32 with an error of at most 4: sines and their products
-// with weights 2, product and sum 2.  The largest element's own, at most sqrt 2
-// as large relative to it (a pair's M is at most that many times its larger
-// element), and the scaling add 11: 15 M for 448 u / max|u|.  A norm's r is off
-// by 9, a key's y / s by 16 M in all.  So each element is converted at both ends
+// |x_p sw|, u comes in fp32 with an error of at most 5: weights (their sum with the
+// offset), sines and the products of the two 3, product and sum 2.  The largest
+// element's own is at most 5 sqrt 2 (a pair's M is at most sqrt 2 times its larger
+// element), the scaling adds 5 and the ends' rounding 1: 18.1 M for 448 u / max|u|.
+// A norm's r is off by 9, a key's y / s by 18 M in all (kSlack is 18.4, kSlackKey
+// 20.1 units).  So each element is converted at both ends
 // of kSlack (kSlackKey) times M around it; where the two codes differ (0.5% of
 // the rows) the element is formed again as a pair of fp32 numbers (exact products,
 // 2^-44) and compared with the middle between the codes.  A key whose codes or
@@ -40,7 +41,7 @@ constexpr int kThreadsI = 128;
 constexpr int kCtasI = 5;    // of an SM
 constexpr int kBatchI = 2;  // rows in flight a lane
 constexpr int kLanesI = 16;  // of a row
-constexpr float kSlack = 1e-6f, kSlackKey = 1.2e-6f;
+constexpr float kSlack = 1.1e-6f, kSlackKey = 1.2e-6f;
 
 struct IndexArgs {
   const void *q, *k;
@@ -129,6 +130,10 @@ __device__ __forceinline__ Two two_sum(float a, float b) {  // |a| >= |b| or a =
   const float s = __fadd_rn(a, b);
   return {s, __fsub_rn(b, __fsub_rn(s, a))};
 }
+__device__ __forceinline__ Two exact_sum(float a, float b) {  // of any magnitudes
+  const float s = __fadd_rn(a, b), from_b = __fsub_rn(s, a), lo = __fadd_rn(__fsub_rn(a, __fsub_rn(s, from_b)), __fsub_rn(b, from_b));
+  return {s, lo == lo ? lo : 0.f};  // (of an infinity nothing is left out)
+}
 __device__ __forceinline__ Two times(Two a, Two b) {
   const float p = __fmul_rn(a.hi, b.hi);
   return two_sum(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p))));
@@ -174,6 +179,9 @@ __device__ __forceinline__ void turn_of_two(unsigned long long phase, Two* cosin
   *cosine = quarter & 2ull ? Two{-a.hi, -a.lo} : a, *sine = quarter & 2ull ? Two{-b.hi, -b.lo} : b;
 }
 
+// A weight, with the offset, as the CTA keeps it.
+__device__ __forceinline__ Two weight_of(const float* w, int e) { return {w[e], w[kHeadDim + e]}; }
+
 // A row as its elements are formed in 64 bits.
 template <typename T>
 struct Row64 {
@@ -181,30 +189,31 @@ struct Row64 {
   const float* w;
   const float4* turns;  // of the token's pairs: cosines (hi, lo), then sines
   int rd;
+  __device__ __forceinline__ double weight(int e) const { return (double)w[e] + (double)w[kHeadDim + e]; }
   template <bool kInter>
   __device__ __forceinline__ double u(int e) const {
-    const double n = (double)to_f(x[e]) * (double)w[e];
+    const double n = (double)to_f(x[e]) * weight(e);
     if (e >= rd) return n;
     const int half = rd / 2, pair = kInter ? e / 2 : e < half ? e : e - half;
     const int mate = kInter ? e ^ 1 : e < half ? e + half : e - half;
     const bool second = kInter ? e & 1 : e >= half;
     const float4 t = turns[pair];
     const double2 cs = make_double2((double)t.x + (double)t.y, (double)t.z + (double)t.w);
-    const double o = (double)to_f(x[mate]) * (double)w[mate];
+    const double o = (double)to_f(x[mate]) * weight(mate);
     return second ? fma(n, cs.x, o * cs.y) : fma(n, cs.x, -(o * cs.y));
   }
 };
 
-// The same as pairs of fp32 numbers: products of elements and weights exactly, turned ones to 2^-44.
+// The same as pairs of fp32 numbers: products of elements and weights to 2^-46, turned ones to 2^-44.
 template <typename T, bool kInter>
 __device__ __forceinline__ Two element_of(const T* x, const float* w, const float4* turns, int rd, int e) {
-  const Two n = times(Two{to_f(x[e]), 0.f}, Two{w[e], 0.f});
+  const Two n = times(Two{to_f(x[e]), 0.f}, weight_of(w, e));
   if (e >= rd) return n;
   const int half = rd / 2, pair = kInter ? e / 2 : e < half ? e : e - half;
   const int mate = kInter ? e ^ 1 : e < half ? e + half : e - half;
   const bool second = kInter ? e & 1 : e >= half;
   const float4 t = turns[pair];
-  const Two o = times(times(Two{to_f(x[mate]), 0.f}, Two{w[mate], 0.f}), Two{t.z, t.w});
+  const Two o = times(times(Two{to_f(x[mate]), 0.f}, weight_of(w, mate)), Two{t.z, t.w});
   return plus(times(n, Two{t.x, t.y}), second ? o : negative(o));
 }
 
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
   pdl_enter();
   __shared__ float4 turns_[kThreadsI / 32][kHeadDim / 2];  // cosines and sines of a warp's token, each in two numbers
   __shared__ unsigned long long steps[kHeadDim / 2];
-  __shared__ float weights[2][kHeadDim];  // offset + w of queries and keys, 1 without
+  __shared__ float weights[2][2 * kHeadDim];  // offset + w of queries and keys, 1 without, then what its rounding left out
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rd = a.rotary_dim, half = rd / 2, sub = lane / kLanesI, piece = lane % kLanesI;
   const Place p = place_of<kInter>(lane, rd);
@@ -436,8 +445,9 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
   const int at = p.at;
   for (int i = threadIdx.x; i < half; i += kThreadsI) steps[i] = step_of(a.inv_freq[i]);
   for (int i = threadIdx.x; i < kHeadDim; i += kThreadsI) {
-    weights[0][i] = a.q_w != nullptr ? a.offset + to_f(static_cast<const T*>(a.q_w)[i]) : 1.f;
-    weights[1][i] = a.k_w != nullptr ? a.offset + to_f(static_cast<const T*>(a.k_w)[i]) : 1.f;
+    const Two q = a.q_w != nullptr ? exact_sum(a.offset, to_f(static_cast<const T*>(a.q_w)[i])) : Two{1.f, 0.f};
+    const Two k = a.k_w != nullptr ? exact_sum(a.offset, to_f(static_cast<const T*>(a.k_w)[i])) : Two{1.f, 0.f};
+    weights[0][i] = q.hi, weights[0][kHeadDim + i] = q.lo, weights[1][i] = k.hi, weights[1][kHeadDim + i] = k.lo;
   }
   __syncthreads();
   float4* mine = turns_[warp];
