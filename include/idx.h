@@ -680,8 +680,10 @@ int idx_norm_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_s
  * angles as in idx_rope_append); q_scale is fp32.  A query's row that holds an
  * infinity or NaN (or whose squares' sum passes 3e38) gets codes 0x7F and a NaN
  * scale, a key's gets NaN scales and codes 0, so its scores are NaN and rank
- * last.  A query's row whose largest magnitude (turned, with the weights, before
- * the norm) is below 2^-100 or above 2^126 gets codes 0.
+ * last; so does a row of zeros with weights and eps 0 (a query's codes are 0).  A
+ * query's row whose largest magnitude (turned, with the weights, before the norm)
+ * is below 2^-100 or above 2^126 gets codes 0.  With an eps below 2^-96 queries
+ * take a second launch, for rows whose squares fp32 does not hold.
  *
  *   q             [num_tokens, heads, 128], the head's elements contiguous, or
  *                 NULL with heads 0 (up to 128)

@@ -9,12 +9,13 @@
 //
 // The codes are those of 64-bit arithmetic.  Sines and cosines are formed to
 // 2^-44, once a token, by their Taylor series.  In units of 2^-24 of M = |x cw| +
-// |x_p sw|, u comes in fp32 with an error of at most 5: weights (their sum with the
-// offset), sines and the products of the two 3, product and sum 2.  The largest
-// element's own is at most 5 sqrt 2 (a pair's M is at most sqrt 2 times its larger
-// element), the scaling adds 5 and the ends' rounding 1: 18.1 M for 448 u / max|u|.
-// A norm's r is off by 9, a key's y / s by 18 M in all (kSlack is 18.4, kSlackKey
-// 20.1 units).  So each element is converted at both ends
+// |x_p sw|, u comes in fp32 with an error of at most 4, the sines' 1, their products
+// with weights 1, and 1 each of |x_p sw| and of |u| for product and sum; or of 5
+// where the sum of weight and offset is rounded.  M of the pair of the largest element
+// is at most sqrt 2 times that, so its own error is at most 3 sqrt 2 + 1 (4 sqrt 2 +
+// 1); the scaling adds 5, the ends' rounding 1: 15.3 M for 448 u / max|u| (17.7;
+// kSlack is 15.6, kSlackSums 17.9 units).  A norm's r is off by 9, a key's y / s by 18
+// M in all (kSlackKey 20.1).  So each element is converted at both ends
 // of kSlack (kSlackKey) times M around it; where the two codes differ (0.5% of
 // the rows) the element is formed again as a pair of fp32 numbers (exact products,
 // 2^-44) and compared with the middle between the codes.  A key whose codes or
@@ -41,7 +42,8 @@ constexpr int kThreadsI = 128;
 constexpr int kCtasI = 5;    // of an SM
 constexpr int kBatchI = 2;  // rows in flight a lane
 constexpr int kLanesI = 16;  // of a row
-constexpr float kSlack = 1.1e-6f, kSlackKey = 1.2e-6f;
+constexpr float kSlack = 9.3e-7f, kSlackSums = 1.07e-6f, kSlackKey = 1.2e-6f;
+constexpr float kSmallI = 0x1p-96f;  // a mean of squares with eps below it is formed again: fp32 holds the squares with fewer bits, or none
 
 struct IndexArgs {
   const void *q, *k;
@@ -234,6 +236,7 @@ __device__ __noinline__ uint2 key_64(const Row64<T> row, int at, bool normed, fl
   top = fmax(top, shfl_xor_64(top, 1));
   const double r = normed ? 1.0 / sqrt(ss * (1.0 / kHeadDim) + (double)eps) : 1.0;
   const double six = top * r / 6.0;
+  if (!(six >= 0.0)) return make_uint2(0u, 0x7Fu);  // (zeros without eps)
   uint32_t scale = f32x2_to_e4m3x2(__double2float_rz(six) * (1.f - kSlackKey), 0.f) & 0x7Fu;
   if (scale > 0) --scale;
   for (; scale < 0x7Eu; ++scale) {
@@ -364,8 +367,8 @@ __device__ __forceinline__ float largest8(const float2 (&u)[4]) {
 }
 // Codes of both ends of where 448 u / top may lie: pairs of elements in 16 bits.
 __device__ __forceinline__ float inverse_of(float top) { return top > 7.9e-31f ? __fdividef(448.f, top) : 0.f; }
-__device__ __forceinline__ void both_ends(const float2 (&u)[4], const float2 (&mag)[4], float inv, uint32_t (&low)[4], uint32_t (&high)[4]) {
-  const float slack = inv * kSlack;
+__device__ __forceinline__ void both_ends(const float2 (&u)[4], const float2 (&mag)[4], float inv, float slack, uint32_t (&low)[4], uint32_t (&high)[4]) {
+  slack *= inv;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 v = mul2(u[e], make_float2(inv, inv));
@@ -385,11 +388,11 @@ __device__ __noinline__ void again(const T* x, const float* w, const float4* tur
 #pragma unroll
   for (int o = 1; o < kLanesI; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o), most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
   uint32_t low[4], high[4], near = 0, tops = 0;
-  both_ends(u, mag, inverse_of(most), low, high);
+  both_ends(u, mag, inverse_of(most), kSlackSums, low, high);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     if ((low[e / 2] ^ high[e / 2]) >> (8 * (e % 2)) & 0xFFu) near |= 1u << e;
-    if (fabsf(e % 2 ? u[e / 2].y : u[e / 2].x) >= most * (1.f - 4.f * kSlack)) tops |= 1u << e;
+    if (fabsf(e % 2 ? u[e / 2].y : u[e / 2].x) >= most * (1.f - 4.f * kSlackSums)) tops |= 1u << e;
   }
   uint32_t codes[2] = {__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410)};
   if (!(ss <= 3.4e38f) || inverse_of(most) == 0.f) live = false, near = tops = 0;  // (its codes stand)
@@ -420,6 +423,28 @@ __device__ __noinline__ void again(const T* x, const float* w, const float4* tur
   if (live) *reinterpret_cast<uint2*>(out + p.at) = make_uint2(codes[0], codes[1]);
 }
 
+// The largest magnitude of a row after its norm, where the mean of its squares, with eps, is small: from the squares of 2^100
+// times the elements, which are below 2^56 then.  -1 for other rows.  Each half of the warp has a row of its own.
+template <typename T, bool kInter, bool kWide>
+__device__ __forceinline__ float small_top(const T* x, const float* w, const float4* turns, int rd, float eps) {
+  const Place p = place_of<kInter>(threadIdx.x & 31, rd);
+  float2 u[4], mag[4];
+  const Eight<T> row = load8<T, kWide>(x + p.at);
+  float ss = turn8<T, kInter>(row, p, factors_of<kInter>(p, w, turns), u, mag), most = largest8(u), scaled = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 y = mul2(Words<T>::get(row.w, e), make_float2(0x1p100f, 0x1p100f));
+    scaled = fmaf(y.x, y.x, fmaf(y.y, y.y, scaled));
+  }
+#pragma unroll
+  for (int o = 1; o < kLanesI; o <<= 1) {
+    ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o), scaled += __shfl_xor_sync(0xFFFFFFFFu, scaled, o);
+    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  }
+  const bool small = fmaf(ss, 1.f / kHeadDim, eps) < kSmallI;
+  return small ? most * 0x1p100f * rsqrtf(fmaf(scaled, 1.f / kHeadDim, eps * 0x1p100f * 0x1p100f)) : -1.f;
+}
+
 // The request of token t: greatest r with cu[r] <= t, all lanes together.
 __device__ __forceinline__ int request_of(const int32_t* cu, int num_reqs, int t, int lane) {
   int lo = 0, hi = num_reqs;
@@ -430,6 +455,63 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int num_reqs, int t
     hi = min(hi, lo + step);
   }
   return lo;
+}
+
+// Frequencies and weights of a CTA; whether a sum of a query's weight and the offset is rounded.
+template <typename T>
+__device__ __forceinline__ bool prepare(const IndexArgs& a, unsigned long long* steps, float (*weights)[2 * kHeadDim]) {
+  for (int i = threadIdx.x; i < a.rotary_dim / 2; i += kThreadsI) steps[i] = step_of(a.inv_freq[i]);
+  bool rounded = false;
+  for (int i = threadIdx.x; i < kHeadDim; i += kThreadsI) {
+    const Two q = a.q_w != nullptr ? exact_sum(a.offset, to_f(static_cast<const T*>(a.q_w)[i])) : Two{1.f, 0.f};
+    const Two k = a.k_w != nullptr ? exact_sum(a.offset, to_f(static_cast<const T*>(a.k_w)[i])) : Two{1.f, 0.f};
+    weights[0][i] = q.hi, weights[0][kHeadDim + i] = q.lo, weights[1][i] = k.hi, weights[1][kHeadDim + i] = k.lo;
+    rounded |= q.lo != 0.f;
+  }
+  return rounded;
+}
+
+// Cosines and sines of a token's pairs, a warp together.
+__device__ __forceinline__ void turn_token(const IndexArgs& a, int position, const unsigned long long* steps, float4* turns) {
+  for (int i = threadIdx.x & 31; i < a.rotary_dim / 2; i += 32) {
+    Two c, s;
+    turn_of_two(steps[i] * (unsigned long long)(long long)position, &c, &s);
+    c = times(c, Two{a.mscale, 0.f}), s = times(s, Two{a.mscale, 0.f});
+    turns[i] = make_float4(c.hi, c.lo, s.hi, s.lo);
+  }
+}
+
+// The scales of queries whose mean of squares, with eps, is below kSmallI, again: launched after k_index_append where eps is
+// below it.  (In that kernel, whose registers are all taken, it cost 3 to 5 us of 8,191 tokens of 64 heads that need none of it.)
+template <typename T, bool kInter, bool kWide>
+__global__ void __launch_bounds__(kThreadsI) k_index_small(const __grid_constant__ IndexArgs a) {
+  pdl_enter();
+  __shared__ float4 turns_[kThreadsI / 32][kHeadDim / 2];
+  __shared__ unsigned long long steps[kHeadDim / 2];
+  __shared__ float weights[2][2 * kHeadDim];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  prepare<T>(a, steps, weights);
+  __syncthreads();
+  float4* mine = turns_[warp];
+  for (int64_t t = (int64_t)blockIdx.x * (kThreadsI / 32) + warp; t < a.num_tokens; t += (int64_t)gridDim.x * (kThreadsI / 32)) {
+    int64_t out = t * a.heads;
+    if (a.cu != nullptr) {
+      const int r = request_of(a.cu, a.num_reqs, (int)t, lane);
+      const int begin = a.cu[r], end = a.cu[r + 1], slot = a.req_slots - end + (int)t;
+      if (t < begin || t >= end || slot < 0) continue;
+      out = ((int64_t)r * a.req_slots + slot) * a.heads;
+    }
+    __syncwarp();
+    turn_token(a, a.positions[t], steps, mine);
+    __syncwarp();
+    for (int h0 = 0; h0 < a.heads; h0 += 2) {
+      const int h = h0 + lane / kLanesI;
+      const T* row = static_cast<const T*>(a.q) + t * a.q_ts + (int64_t)min(h, a.heads - 1) * a.q_hs;
+      const float top = small_top<T, kInter, kWide>(row, weights[0], mine, a.rotary_dim, a.eps);
+      if (lane % kLanesI == 0 && h < a.heads && top >= 0.f)
+        a.q_scale[out + h] = top * (1.f / 448.f) * a.scale * (a.head_weights != nullptr ? a.head_weights[t * a.heads + h] : 1.f);
+    }
+  }
 }
 
 template <typename T, bool kInter, bool kWide>
@@ -443,13 +525,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
   const Place p = place_of<kInter>(lane, rd);
   const Fours fours = fours_of<kInter>(lane, rd);
   const int at = p.at;
-  for (int i = threadIdx.x; i < half; i += kThreadsI) steps[i] = step_of(a.inv_freq[i]);
-  for (int i = threadIdx.x; i < kHeadDim; i += kThreadsI) {
-    const Two q = a.q_w != nullptr ? exact_sum(a.offset, to_f(static_cast<const T*>(a.q_w)[i])) : Two{1.f, 0.f};
-    const Two k = a.k_w != nullptr ? exact_sum(a.offset, to_f(static_cast<const T*>(a.k_w)[i])) : Two{1.f, 0.f};
-    weights[0][i] = q.hi, weights[0][kHeadDim + i] = q.lo, weights[1][i] = k.hi, weights[1][kHeadDim + i] = k.lo;
-  }
-  __syncthreads();
+  const float slack = __syncthreads_or(prepare<T>(a, steps, weights)) ? kSlackSums : kSlack;
   float4* mine = turns_[warp];
   // A token's units: batches of steps of two heads, then its key.  Every warp takes as many units, one after another.
   const int rows = (a.heads + 1) / 2, batches = (rows + kBatchI - 1) / kBatchI, units = batches + (a.k != nullptr ? 1 : 0);
@@ -460,12 +536,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
     unit += past - first;
     const int position = a.positions[t];
     __syncwarp();  // the angles of the token before are used up
-    for (int i = lane; i < half; i += 32) {
-      Two c, s;
-      turn_of_two(steps[i] * (unsigned long long)(long long)position, &c, &s);
-      c = times(c, Two{a.mscale, 0.f}), s = times(s, Two{a.mscale, 0.f});
-      mine[i] = make_float4(c.hi, c.lo, s.hi, s.lo);
-    }
+    turn_token(a, position, steps, mine);
     __syncwarp();
     if (first < batches) {
       const Piece8 f = factors_of<kInter>(fours, weights[0], mine);
@@ -518,7 +589,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
           for (int b = 0; b < kBatchI; ++b) {
             const float inv = inverse_of(top[b]);
             uint32_t low[4], high[4];
-            both_ends(u[b], mag[b], inv, low, high);
+            both_ends(u[b], mag[b], inv, slack, low, high);
             const uint32_t differ = (low[0] ^ high[0]) | (low[1] ^ high[1]) | (low[2] ^ high[2]) | (low[3] ^ high[3]);
             if (differ != 0) open |= 1ull << (g + b - r0);
             uint2 codes = make_uint2(__byte_perm(low[0], low[1], 0x5410), __byte_perm(low[2], low[3], 0x5410));
@@ -565,13 +636,13 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
 #pragma unroll
         for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(mag[e].x, mag[e].y));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-        const float r = a.k_w != nullptr ? rsqrtf(fmaf(ss, 1.f / kHeadDim, a.eps)) : 1.f;
+        const float mean = fmaf(ss, 1.f / kHeadDim, a.eps), r = a.k_w != nullptr ? rsqrtf(mean) : 1.f;
         const bool bad = !(ss <= 3.4e38f);
         const float six = top * r * (1.f / 6.f), off = most * r * (kSlackKey / 6.f);
         const uint32_t both = f32x2_to_e4m3x2(six - off, six + off);
         uint32_t scale = both & 0xFFu, codes = 0;
         const float sv = e4m3_to_f32(scale), inv = scale == 0x7Fu || scale == 0u ? 0.f : r / sv;
-        bool open = (both & 0xFFu) != both >> 8;
+        bool open = (both & 0xFFu) != both >> 8 || (a.k_w != nullptr && mean < kSmallI);
         if (inv != 0.f) {
           uint32_t high = 0;
 #pragma unroll
@@ -598,20 +669,22 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
   }
 }
 
-template <typename T>
-void launch_index(const IndexArgs& a, bool inter, bool wide, cudaStream_t s) {
-  const int rows = (a.heads + 1) / 2;
+template <typename T, bool kInter, bool kWide>
+void launch_index(const IndexArgs& a, cudaStream_t s) {
+  const int rows = (a.heads + 1) / 2, sms = max(device_sms(), 1);
   const int64_t all = (int64_t)a.num_tokens * ((rows + kBatchI - 1) / kBatchI + (a.k != nullptr ? 1 : 0));
   // a unit a warp, or an equal number of them a warp of those that run at once
-  const int64_t warps = min(all, (int64_t)max(device_sms(), 1) * kCtasI * (kThreadsI / 32));
-  const dim3 grid((unsigned)((warps + kThreadsI / 32 - 1) / (kThreadsI / 32))), block(kThreadsI);
-  if (inter) {
-    if (wide) launch_pdl(k_index_append<T, true, true>, grid, block, 0, s, a, warps);
-    else launch_pdl(k_index_append<T, true, false>, grid, block, 0, s, a, warps);
-  } else {
-    if (wide) launch_pdl(k_index_append<T, false, true>, grid, block, 0, s, a, warps);
-    else launch_pdl(k_index_append<T, false, false>, grid, block, 0, s, a, warps);
+  const int64_t warps = min(all, (int64_t)sms * kCtasI * (kThreadsI / 32));
+  launch_pdl(k_index_append<T, kInter, kWide>, dim3((unsigned)((warps + kThreadsI / 32 - 1) / (kThreadsI / 32))), dim3(kThreadsI), 0, s, a, warps);
+  if (a.heads > 0 && a.q_w != nullptr && a.eps < kSmallI) {
+    const unsigned grid = (unsigned)min(((int64_t)a.num_tokens + kThreadsI / 32 - 1) / (kThreadsI / 32), (int64_t)sms * kCtasI);
+    launch_pdl(k_index_small<T, kInter, kWide>, dim3(grid), dim3(kThreadsI), 0, s, a);
   }
+}
+template <typename T>
+void launch_index(const IndexArgs& a, bool inter, bool wide, cudaStream_t s) {
+  if (inter) wide ? launch_index<T, true, true>(a, s) : launch_index<T, true, false>(a, s);
+  else wide ? launch_index<T, false, true>(a, s) : launch_index<T, false, false>(a, s);
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-"""idx_index_append against the definition in 64 bits where fp32 falls short: sums of weights and offset."""
+"""idx_index_append against the definition in 64 bits where fp32 falls short: sums of weights and offset, squares of small rows."""
 
 import numpy as np
 import pytest
@@ -92,3 +92,58 @@ def test_random_weights_with_an_offset(lib, inter):
     rand = lambda *s: torch.randn(*s, device="cuda", generator=g)
     freq = lib.idx_rope_frequencies(64, 10000.0)[0].numpy()
     run(lib, rand(3000, 8, 128), rand(3000, 128), 0.1 * rand(128), 0.1 * rand(128), 1.0, 1e-6, inter, freq)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-36])
+def test_small_rows(lib, dtype, eps):
+    """Rows whose squares are subnormal or 0 in fp32, with an eps that does not cover them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    size = torch.logspace(-29, -14, 61, base=10.0, device="cuda")
+    q = (size[:, None, None] * torch.randn(61, 5, 128, device="cuda", generator=g)).to(dtype)
+    k = (size[:, None] * torch.randn(61, 128, device="cuda", generator=g)).to(dtype)
+    w = (1 + 0.2 * torch.randn(2, 128, device="cuda", generator=g)).to(dtype)
+    freq = lib.idx_rope_frequencies(32, 10000.0)[0].numpy()
+    run(lib, q, k, w[0], w[1], 0.0, eps, False, freq)
+
+
+def test_rows_of_zeros_without_eps(lib):
+    """0 / 0: scales are NaN, codes 0."""
+    q, k = torch.zeros(1, 1, 128, device="cuda"), torch.zeros(1, 128, device="cuda")
+    w, out, scale = torch.ones(128, device="cuda"), torch.ones(1, 1, 128, dtype=torch.uint8, device="cuda"), torch.zeros(1, 1, device="cuda")
+    pages = torch.ones(1, 128, 72, dtype=torch.uint8, device="cuda")
+    lib.idx_index_append(q, k, w, w, 0.0, torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.float64, device="cuda"), out, scale, pages)
+    flat = pages.view(-1)
+    assert not out.any() and scale.isnan().all() and not flat[:64].any() and flat[128 * 64 : 128 * 64 + 8].eq(0x7F).all()
+
+
+def test_small_rows_in_request_slots(lib):
+    """With request slots and head weights: the flat call's scales at the requests' last slots, the others as they were; captured too."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(13)
+    q = 1e-22 * torch.randn(9, 3, 128, device="cuda", generator=g)
+    q[2] *= 1e22  # a row of ordinary size among them
+    w, hw = 1 + 0.2 * torch.randn(128, device="cuda", generator=g), torch.randn(9, 3, device="cuda", generator=g)
+    pos, freq = torch.arange(9, dtype=torch.int32, device="cuda"), lib.idx_rope_frequencies(32, 10000.0)[0].cuda()
+    flat, flat_scale = torch.zeros(9, 3, 128, dtype=torch.uint8, device="cuda"), torch.zeros(9, 3, device="cuda")
+    lib.idx_index_append(q, None, w, None, 0.0, pos, freq, flat, flat_scale, None, head_weights=hw, scale=0.5)
+    _, want = serve.index_queries(q.double().cpu().numpy(), w.double().cpu().numpy(), 0.0, 0.0, np.arange(9), freq.cpu().numpy(), 1.0, False, 0.5,
+                                  hw.double().cpu().numpy())
+    assert np.all(np.abs(flat_scale.double().cpu().numpy() - want) <= 32 * 2.0**-24 * np.abs(want))
+    cu = torch.tensor([0, 2, 2, 8], dtype=torch.int32, device="cuda")  # the last token is behind the requests, and the third has one too many
+    out, scale = torch.full((3, 5, 3, 128), 0xAB, dtype=torch.uint8, device="cuda"), torch.full((3, 5, 3), -7.0, device="cuda")
+
+    def call():
+        lib.idx_index_append(q, None, w, None, 0.0, pos, freq, out, scale, None, cu_tokens=cu, head_weights=hw, scale=0.5)
+
+    call()
+    for _ in range(2):
+        assert scale[0, :3].eq(-7).all() and scale[1].eq(-7).all()
+        assert torch.equal(scale[0, 3:], flat_scale[:2]) and torch.equal(scale[2], flat_scale[3:8]) and torch.equal(out[2], flat[3:8])
+        scale.fill_(-7.0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graph.replay()
+        torch.cuda.synchronize()
