@@ -167,15 +167,40 @@ class Server:
         self.active = n + m
 
     def release(self, keep):
-        """Pages past the kept lengths (one for each active request) go back; requests that keep nothing end, from the last on."""
-        n = self.active
-        self.keep.zero_()[:n] = torch.tensor(keep, dtype=torch.int32, device=self.cu.device)
+        """Pages past the kept lengths (one for each active request) go back; requests that keep nothing end, from the last on.
+
+        A request cut back into a page that others hold too would write over their tokens in its next step.  It is forked at
+        its kept length into the row behind the active ones, which copies that page, and its child takes its place.
+        """
+        n, spare = self.active, max((i + 1 for i, k in enumerate(keep) if k > 0), default=0)
+        lens = torch.tensor(keep + [0] * (self.rows - n), dtype=torch.int32, device=self.cu.device)
+        shared = self.inside_shared(torch.minimum(self.ctx, lens))
+        if shared and spare == self.rows:
+            raise ValueError(f"requests {shared} end inside pages that others hold, and no row is free to copy them into")
+        self.give_back(lens)
+        self.active = spare
+        for r in self.inside_shared(self.ctx):
+            self.fork([r])
+            self.active = spare
+            lens = self.ctx.clone()
+            lens[r] = 0
+            self.give_back(lens)
+            for a in (self.ctx, self.owned, self.table):
+                a[r] = a[spare]
+            self.ctx[spare], self.owned[spare] = 0, 0
+
+    def inside_shared(self, lens):
+        """Requests whose next token would have its place in a page that others hold too."""
+        page = (lens // PAGE).clamp(max=self.table.shape[1] - 1).long()
+        block = self.table.gather(1, page[:, None])[:, 0].clamp(0, self.blocks - 1).long()
+        return ((lens % PAGE > 0) & (self.refs[block] > 0)).nonzero()[:, 0].tolist()
+
+    def give_back(self, lens):
+        self.keep.copy_(lens)
         idx.idx_release_pages(self.keep, self.owned, self.table, self.refs, self.free, self.cursor, self.cursor_out, self.pages_out, PAGE, status=self.status)
         self.owned.copy_(self.pages_out)
         self.cursor.copy_(self.cursor_out)
         self.ctx.copy_(torch.minimum(self.ctx, self.keep))
-        while self.active > 0 and keep[self.active - 1] == 0:
-            self.active -= 1
 
 
 def timed(server, steps):

@@ -852,6 +852,12 @@ int idx_fork_pages(const idx_cache* caches, int32_t num_caches, int64_t num_bloc
  * blocks than entries the lowest are dropped: IDX_ST_BAD_OUTPUT).  Table
  * entries from pages_out[r] on mean nothing afterwards.  Entries of -1 are
  * skipped, others outside [0, num_blocks) too (IDX_ST_BLOCK_OOR).
+ * A request that is cut back goes on in its last page, behind keep_lens[r].
+ * Where that length ends inside a page with refs above 0 afterwards (a full page
+ * of a fork or its parent), the request must not be given slots there: rows
+ * written to them would replace tokens of the other holders.  Such a request is
+ * forked at its kept length (idx_fork_pages copies the page's first tokens to a
+ * block of its own) and given up for its child.
  *
  *   keep_lens, owned_pages, pages_out   [num_reqs] int32 (a finished request
  *                 keeps 0); pages_out is an array of its own

@@ -857,7 +857,8 @@ def idx_fork_pages(caches, parents, children, ctx_lens, owned_pages, block_table
 def idx_release_pages(keep_lens, owned_pages, block_table, refs, free_blocks, free_cursor, cursor_out, pages_out, page_tokens: int, status=None,
                       stream=None) -> int:
     """Pages past keep_lens [R] i32 given back: refs [nb] i32 less one each, the blocks that nobody holds into free_blocks before the
-    cursor by ascending id; cursor_out, and pages_out [R] i32, the pages that are left."""
+    cursor by ascending id; cursor_out, and pages_out [R] i32, the pages that are left.  A length that ends inside a page with refs
+    above 0 afterwards must not be written on from: such a request is forked there, which copies the page, and given up."""
     lib, T, fn = load_library(), _torch(), "idx_release_pages"
     i32 = T.i32
     reqs, width = block_table.shape
