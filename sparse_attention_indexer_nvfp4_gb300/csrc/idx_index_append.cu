@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreadsI, kCtasI) k_index_append(const __grid
   __shared__ unsigned long long steps[kHeadDim / 2];
   __shared__ float weights[2][2 * kHeadDim];  // offset + w of queries and keys, 1 without, then what its rounding left out
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rd = a.rotary_dim, half = rd / 2, sub = lane / kLanesI, piece = lane % kLanesI;
+  const int rd = a.rotary_dim, sub = lane / kLanesI, piece = lane % kLanesI;
   const Place p = place_of<kInter>(lane, rd);
   const Fours fours = fours_of<kInter>(lane, rd);
   const int at = p.at;
