@@ -650,7 +650,10 @@ int idx_verify_drafts(const float* target, int64_t target_stride, const float* d
  * and n's pairs turn as in idx_rope_append; elements from rotary_dim on are
  * those of n.  Values are not normed.  Computed in 32 bits, rounded once: a row
  * whose squares' sum passes 3e38 becomes 0, one with an infinity or NaN is not
- * finite, nor is one whose mean of squares and eps add up to 0.
+ * finite, nor is one whose mean of squares and eps add up to 0.  Squares below
+ * 2^-126 have fewer bits there, or none: rows of elements below 2^-60 need an eps
+ * that covers them.  With no weights at all the values are idx_rope_append's,
+ * which is the faster call.
  *
  *   q_weight, k_weight   [head_dim] of the type of all tensors, or NULL: that
  *                 side is turned only

@@ -21,8 +21,9 @@
 // 2^-44) and compared with the middle between the codes.  A key whose codes or
 // scales may differ is formed again as a whole, in 64 bits.
 //
-// Bound by the instructions of a row (about 220 a warp for two heads): 8,191
-// tokens of 64 heads take 89 us, 0.35 of HBM; without the look for borders 68,
+// Bound by the instructions of a row (about 220 a warp for two heads) and by their
+// latency: the issue slots are 63% full with 16 warps an SM.  8,191 tokens of 64
+// heads take 90 us, 0.34 of HBM (fp32 87, 0.59); without the look for borders 68,
 // with 64-bit floating point for the elements near one 91, for the angles about
 // 20 more; 4 and 6 CTAs of 128 threads an SM 91 and 95.  512 tokens of 4 heads take
 // 8 us.  A query's row is 16 lanes', both elements of a pair in one (passed between
@@ -124,7 +125,8 @@ __device__ __forceinline__ Eight<T> load4x2(const T* p, const T* q) {
   return x;
 }
 
-// A number as hi + lo, hi the nearest fp32 to it.
+// A number as hi + lo, hi the nearest fp32 to it.  Sums are Dekker's (two_sum) and Knuth's (exact_sum, plus), products take
+// their error from a fused multiply-add.
 struct Two {
   float hi, lo;
 };

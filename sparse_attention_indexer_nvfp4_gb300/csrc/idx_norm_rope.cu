@@ -9,15 +9,22 @@
 // are fp32; each element is rounded once.
 //
 // Bound by HBM, as k_rope_rows is: every element is read once and written once.
-// 30,011 tokens of 64 + 4 heads of 128 in bf16 take 193 us, 0.84 of HBM (180
+// 30,011 tokens of 64 + 4 heads of 128 in bf16 take 191 us, 0.85 of HBM (180
 // without a norm), with the next rows asked for while these are worked on (two a
 // batch, 6 CTAs of 128 threads an SM: 191 to 193; four a batch, 2 of 256: 193;
-// without asking ahead 208 to 225); one token 4.7 us.  k_norm_rows, for heads of at most 32 pieces: a warp takes a token (with few
-// tokens a part of its heads), a group of lanes a head's row, a piece a lane;
-// the sum of squares is a butterfly over the group, which is the pieces'
-// number rounded up to a power of two (lanes past the pieces add 0).
-// k_norm_any, for other heads (single elements by alignment, heads of more
-// than 32 pieces): a warp takes a row through shared memory.
+// without asking ahead 208 to 225); one token 4.8 us.
+//
+// k_norm_rows, for heads of at most 32 pieces: a warp takes a token (with few
+// tokens a part of its heads), a group of lanes a head's row, a piece a lane; the
+// sum of squares is a butterfly over the group, which is the pieces' number rounded
+// up to a power of two (lanes past the pieces add 0).  A side without weights is
+// turned as idx_rope_append does it; where neither has any that call is the faster.
+//
+// k_norm_any, for other heads (single elements by alignment, heads of more than 32
+// pieces): a warp takes a row through shared memory, element by element, and forms
+// its angles for each head again.  It is bound by those instructions: 7,500 tokens
+// of 64 + 4 heads of 512 take 387 us with 64 elements turned, 909 with all, where
+// HBM would take 163.
 #include "idx_internal.h"
 #include "idx_rope.cuh"
 

@@ -21,11 +21,11 @@
 // writes, and the result is the same each time.
 //
 // All three are bound by latency, or, with many layers, by HBM: 64 forks of 16
-// requests over 48 layers take 99 us (their 727 MB, of which a parent's page is
-// read from L2 for the second fork on, at HBM's rate 107), 64 trees of 24 settled
-// over 48 layers 8.2 us (12.7 with eight rows in flight a thread and 256 threads),
-// 187,000 pages of 1,021 requests released 12.5 us (15 with a cluster of 8); the
-// smallest calls 4 to 6 us.
+// requests over 48 layers take 98 us (363 MB written; the parents' pages, 84 MB, are
+// read 2.5 times, the other forks find them in L2: 66 at HBM's rate with one reading
+// each, 107 with one a fork), 64 trees of 24 settled over 48 layers 8.2 us (12.7 with
+// eight rows in flight a thread and 256 threads), 187,000 pages of 1,021 requests
+// released 12.4 us (15 with a cluster of 8); the smallest calls 4 to 6 us.
 #include "idx_common.cuh"
 #include "idx_internal.h"
 

@@ -20,12 +20,16 @@
 // clusters than run at once.
 //
 // HBM bounds it, and the stages of a row: 512 rows of 200,003 bf16 logits with
-// counts, 16 biases a request and masks take 191 us where HBM would take 100 for
+// counts, 16 biases a request and masks take 192 us where HBM would take 100 for
 // their 679 MB.  A row's stages follow one another (in cycles of a CTA, traced
 // when it took 200: left out and summed 3,300, changed entries 2,300, the exchange
-// 5,000, written 4,000, between them 2,500), and two CTAs an SM do not cover all of it.  512 threads a
-// CTA took 272 us, 3 CTAs of 256 with one buffer 219, 128 threads 257; entries
-// kept in fp32, one CTA an SM, 833.  One row of 32,000: 9.1 us, all latency.
+// 5,000, written 4,000, between them 2,500), and two CTAs an SM do not cover all
+// of it.  512 threads a CTA took 272 us, 3 CTAs of 256 with one buffer 219, 128
+// threads 257; entries kept in fp32, one CTA an SM, 833.  Past 200,192 16-bit
+// entries there is one buffer: 202,048 take 197 us, without counts, biases and masks
+// 155 (138 of 200,003).  More than 256 biases a request, or a token with two, are
+// searched for by a warp an entry: 388 us with 300 (192 with 250).  One row of
+// 32,000: 9.4 us, all latency.
 #include <algorithm>
 #include <atomic>
 
