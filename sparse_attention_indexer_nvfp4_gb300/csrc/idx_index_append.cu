@@ -43,6 +43,7 @@ constexpr int kThreadsI = 128;
 constexpr int kCtasI = 5;    // of an SM
 constexpr int kBatchI = 2;  // rows in flight a lane
 constexpr int kLanesI = 16;  // of a row
+constexpr int kLookI = 4;    // rows in flight a lane of k_index_small
 constexpr float kSlack = 9.3e-7f, kSlackSums = 1.07e-6f, kSlackKey = 1.2e-6f;
 constexpr float kSmallI = 0x1p-96f;  // a mean of squares with eps below it is formed again: fp32 holds the squares with fewer bits, or none
 
@@ -484,7 +485,9 @@ __device__ __forceinline__ void turn_token(const IndexArgs& a, int position, con
 }
 
 // The scales of queries whose mean of squares, with eps, is below kSmallI, again: launched after k_index_append where eps is
-// below it.  (In that kernel, whose registers are all taken, it cost 3 to 5 us of 8,191 tokens of 64 heads that need none of it.)
+// below it.  A token's rows are read for their squares first and turned only where one is small: with eps 0 and ordinary rows
+// 8,191 tokens of 64 heads take 122 us, 92 with an eps (209 where each row was turned).  In k_index_append, whose registers are
+// all taken, it cost 3 to 5 us of calls that need none of it.
 template <typename T, bool kInter, bool kWide>
 __global__ void __launch_bounds__(kThreadsI) k_index_small(const __grid_constant__ IndexArgs a) {
   pdl_enter();
@@ -503,13 +506,33 @@ __global__ void __launch_bounds__(kThreadsI) k_index_small(const __grid_constant
       if (t < begin || t >= end || slot < 0) continue;
       out = ((int64_t)r * a.req_slots + slot) * a.heads;
     }
+    auto row_of = [&](int h) { return static_cast<const T*>(a.q) + t * a.q_ts + (int64_t)min(h, a.heads - 1) * a.q_hs; };
+    bool small = false;
+    for (int h0 = 0; h0 < a.heads; h0 += 2 * kLookI) {
+      Eight<T> x[kLookI];
+#pragma unroll
+      for (int u = 0; u < kLookI; ++u) x[u] = load8<T, kWide>(row_of(h0 + lane / kLanesI + 2 * u) + lane % kLanesI * 8);
+#pragma unroll
+      for (int u = 0; u < kLookI; ++u) {
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = Words<T>::get(x[u].w, e);
+          ss = fma2(y, y, ss);
+        }
+        float sum = ss.x + ss.y;
+#pragma unroll
+        for (int o = 1; o < kLanesI; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        small |= fmaf(sum, 1.f / kHeadDim, a.eps) < kSmallI;
+      }
+    }
+    if (!__any_sync(0xFFFFFFFFu, small)) continue;
     __syncwarp();
     turn_token(a, a.positions[t], steps, mine);
     __syncwarp();
     for (int h0 = 0; h0 < a.heads; h0 += 2) {
       const int h = h0 + lane / kLanesI;
-      const T* row = static_cast<const T*>(a.q) + t * a.q_ts + (int64_t)min(h, a.heads - 1) * a.q_hs;
-      const float top = small_top<T, kInter, kWide>(row, weights[0], mine, a.rotary_dim, a.eps);
+      const float top = small_top<T, kInter, kWide>(row_of(h), weights[0], mine, a.rotary_dim, a.eps);
       if (lane % kLanesI == 0 && h < a.heads && top >= 0.f)
         a.q_scale[out + h] = top * (1.f / 448.f) * a.scale * (a.head_weights != nullptr ? a.head_weights[t * a.heads + h] : 1.f);
     }
